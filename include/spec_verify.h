@@ -34,10 +34,14 @@
  * acceptance counters), sv_verify_rows / sv_sample_survivors (its two
  * stages), spec_verify_noalloc (no workspace argument), sv_filter_logits
  * (top-k / top-p), spec_verify_lm_head / sv_lm_head_logits (the target's LM
- * head on the tensor cores, fused with the row statistics), spec_verify_tree
- * (a candidate tree: several drafts per position), sv_workspace_bytes,
- * sv_lm_head_workspace_bytes, sv_tree_workspace_bytes, sv_kernel_launches,
- * sv_status_string.
+ * head on the tensor cores, fused with the row statistics),
+ * spec_verify_lm_head_fp8 / sv_lm_head_logits_fp8 (the same on 8-bit
+ * operands), sv_block_norm (the norms around the target's last block, with
+ * its gate and residual scale), sv_quantize_fp8 (block quantisation),
+ * spec_verify_tree (a candidate tree: several drafts per position),
+ * sv_workspace_bytes, sv_lm_head_workspace_bytes,
+ * sv_lm_head_fp8_workspace_bytes, sv_tree_workspace_bytes,
+ * sv_kernel_launches, sv_status_string.
  *
  * Conventions for every entry point below:
  *   - All tensor pointers are DEVICE pointers (inputs may also be mapped
@@ -73,7 +77,9 @@ typedef enum {
     SV_EUNSUPPORTED = 3
 } sv_status_t;
 
-typedef enum { SV_BF16 = 0, SV_FP32 = 1 } sv_dtype_t;
+/* SV_E4M3 (8-bit floating point, 4 exponent and 3 mantissa bits, no
+ * infinities): only where an entry point names it. */
+typedef enum { SV_BF16 = 0, SV_FP32 = 1, SV_E4M3 = 2 } sv_dtype_t;
 
 /* Device status bits OR-ed into *status_dev. */
 #define SV_BAD_U 1               /* a uniform outside [0, 1) or NaN          */
@@ -89,6 +95,7 @@ typedef enum { SV_BF16 = 0, SV_FP32 = 1 } sv_dtype_t;
 /* Largest vocabulary supported. */
 #define SV_MAX_V (1 << 21)
 #define SV_MAX_TREE_NODES 256  /* nodes of one candidate tree (spec_verify_tree) */
+#define SV_MAX_D 32768         /* widest row of sv_block_norm */
 
 /* Bytes of workspace spec_verify needs for (B, K, V).  The workspace must be
  * zero-filled before its first use.  A completed spec_verify (or the two
@@ -301,6 +308,93 @@ sv_status_t spec_verify_lm_head(const void *hidden, const void *lm_head,
                                 float *accept_prob, float *residual_mass,
                                 int32_t *status_dev, void *workspace,
                                 size_t workspace_bytes, void *stream);
+
+/* The LM head on 8-bit operands: logits and verification as above, with
+ * hidden states and output embedding in e4m3 and one fp32 scale per block of
+ * 128 along the hidden dims (blocks of a row of hidden; of 128 ids of
+ * lm_head), nb = ceil(d / 128):
+ *   logits[m, v] = sum_b hidden_scales[m, b] * lm_head_scales[v / 128, b]
+ *                        * sum_{k in block b} hidden[m, k] * lm_head[v, k]
+ * fp32 accumulation (the scales may be any fp32 numbers), rounded once to
+ * bf16, nearest even.  The pages name quantised targets and drafts as a
+ * deployment measure only ("推测解码采样验证优化策略 —— 深度调研报告", part 1
+ * section 6, 扩展性与安全性).
+ *   hidden          [M, d] (or [B, K+1, d]) e4m3, 16-byte aligned;
+ *   hidden_scales   [M, nb] fp32;
+ *   lm_head         [V, d] e4m3, 16-byte aligned;
+ *   lm_head_scales  [ceil(V / 128), nb] fp32;
+ *   d a multiple of 16 (the rows' 16-byte stride) and at least 16.
+ * sv_block_norm and sv_quantize_fp8 write operands in this form.  A NaN or
+ * infinite scale or value gives NaN logits in the rows and ids it belongs to;
+ * the verification reports such a row as SV_BAD_ROW.  Everything else
+ * (remaining arguments, status_dev, limits, errors, the workspace rule) as
+ * for the bf16 entry points; sv_lm_head_logits_fp8 is one launch,
+ * spec_verify_lm_head_fp8 two plus the draws. */
+size_t sv_lm_head_fp8_workspace_bytes(int64_t B, int32_t K, int32_t V);
+sv_status_t sv_lm_head_logits_fp8(const void *hidden, const float *hidden_scales,
+                                  const void *lm_head,
+                                  const float *lm_head_scales, int64_t M,
+                                  int32_t d, int32_t V, void *logits,
+                                  int32_t *status_dev, void *stream);
+sv_status_t spec_verify_lm_head_fp8(
+    const void *hidden, const float *hidden_scales, const void *lm_head,
+    const float *lm_head_scales, int32_t d, const float *draft_probs,
+    const int32_t *draft_tokens, const float *uniforms, float temperature,
+    int64_t B, int32_t K, int32_t V, void *logits_out, int32_t *out_tokens,
+    int32_t *num_emitted, int8_t *accept_flags, float *accept_prob,
+    float *residual_mass, int32_t *status_dev, void *workspace,
+    size_t workspace_bytes, void *stream);
+
+/* The norms around the target's last block, fused with the block's gate and
+ * the residual scale: from the block's output x and the residual stream to
+ * the LM head's input.  Per row of d values, in fp32:
+ *   a = x * rsqrt(mean(x^2) + eps) * (post_weight + weight_offset)
+ *       (post_weight NULL: a = x)
+ *   r = residual_scale * residual + branch_scale * gate * a
+ *       (gate NULL: 1)
+ *   h = r * rsqrt(mean(r^2) + eps) * (norm_weight + weight_offset)
+ * residual_out = r rounded to the residual's type; hidden = h, formed from
+ * the unrounded r and rounded to its own type.
+ *   x            [M, d] bf16 or fp32 (x_dtype);
+ *   residual     [M, d] bf16 or fp32 (residual_dtype); residual_out has the
+ *                same type and may be the same pointer (in place); other
+ *                overlaps are not allowed;
+ *   post_weight, norm_weight  [d] bf16 or fp32 (weight_dtype); weight_offset
+ *                is 1 for weights stored less one, else 0;
+ *   gate         [gate_rows, d], x's type: gate row i serves the M / gate_rows
+ *                consecutive rows from i * M / gate_rows on (1: one gate for
+ *                all; B: one per sequence; M: one per row); M must be a
+ *                multiple of gate_rows;
+ *   hidden       [M, d] bf16, fp32 or e4m3 (hidden_dtype); for e4m3
+ *                hidden_scales [M, ceil(d / 128)] fp32 receives the scales as
+ *                sv_quantize_fp8 forms them (block_rows 1); NULL otherwise.
+ * eps > 0 and the three scalars finite; d <= SV_MAX_D.  Pointers aligned to
+ * their element; 16-byte aligned rows (d % 8 == 0) take the fast path.  A row
+ * whose mean square exceeds the fp32 range normalises to 0.  One launch on
+ * `stream`; allocates nothing. */
+sv_status_t sv_block_norm(const void *x, sv_dtype_t x_dtype,
+                          const void *residual, sv_dtype_t residual_dtype,
+                          const void *post_weight, const void *gate,
+                          int64_t gate_rows, const void *norm_weight,
+                          sv_dtype_t weight_dtype, float weight_offset,
+                          float residual_scale, float branch_scale, float eps,
+                          int64_t M, int32_t d, void *residual_out,
+                          void *hidden, sv_dtype_t hidden_dtype,
+                          float *hidden_scales, void *stream);
+
+/* Quantisation to e4m3 with one fp32 scale per block of block_rows x 128
+ * values: block_rows 1 for activations, 128 for weights (done once, at load).
+ *   scale = max(largest magnitude of the block, 2^-100) / 448,
+ *   value = x * (1 / scale) rounded to e4m3 (nearest even, at most 448),
+ * each step in fp32.  A block that holds a NaN gets a NaN scale; one that
+ * holds an infinity an infinite scale.
+ *   x       [rows, d] bf16 or fp32;
+ *   values  [rows, d] e4m3 out;
+ *   scales  [ceil(rows / block_rows), ceil(d / 128)] fp32 out.
+ * One launch on `stream`; allocates nothing. */
+sv_status_t sv_quantize_fp8(const void *x, sv_dtype_t x_dtype, int64_t rows,
+                            int32_t d, int32_t block_rows, void *values,
+                            float *scales, void *stream);
 
 /* Verification of a candidate tree: several drafts per position, one path
  * committed.  The pages require that a tree commits one contiguous path and

@@ -7,17 +7,20 @@ import os
 from .build import LIB
 
 SV_OK, SV_EINVAL, SV_ECUDA, SV_EUNSUPPORTED = 0, 1, 2, 3
-SV_BF16, SV_FP32 = 0, 1
+SV_BF16, SV_FP32, SV_E4M3 = 0, 1, 2
 SV_BAD_U, SV_BAD_TOKEN, SV_BAD_Q, SV_BAD_ROW, SV_DEGENERATE_RESIDUAL = 1, 2, 4, 8, 16
 SV_INTERNAL_TIMEOUT = 32
 SV_BAD_TREE = 64
 SV_MAX_TREE_NODES = 256
 SV_MAX_V = 1 << 21
+SV_MAX_D = 32768
 
 # every function the header declares, in declaration order
 EXPORTS = ["sv_workspace_bytes", "spec_verify", "spec_verify_stats", "sv_verify_rows",
            "sv_sample_survivors", "spec_verify_noalloc", "sv_filter_logits", "sv_lm_head_workspace_bytes",
-           "sv_lm_head_logits", "spec_verify_lm_head", "sv_tree_workspace_bytes", "spec_verify_tree",
+           "sv_lm_head_logits", "spec_verify_lm_head", "sv_lm_head_fp8_workspace_bytes",
+           "sv_lm_head_logits_fp8", "spec_verify_lm_head_fp8", "sv_block_norm", "sv_quantize_fp8",
+           "sv_tree_workspace_bytes", "spec_verify_tree",
            "sv_kernel_launches", "sv_status_string"]
 
 
@@ -79,6 +82,19 @@ def lib() -> ctypes.CDLL:
         L.spec_verify_lm_head.restype = ctypes.c_int
         L.spec_verify_lm_head.argtypes = ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32] +
                                           _VERIFY_ARGTYPES[2:9] + [ctypes.c_void_p] + _VERIFY_ARGTYPES[9:])
+        vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+        L.sv_lm_head_fp8_workspace_bytes.restype = ctypes.c_size_t
+        L.sv_lm_head_fp8_workspace_bytes.argtypes = [i64, i32, i32]
+        L.sv_lm_head_logits_fp8.restype = ctypes.c_int
+        L.sv_lm_head_logits_fp8.argtypes = [vp, vp, vp, vp, i64, i32, i32, vp, vp, vp]
+        L.spec_verify_lm_head_fp8.restype = ctypes.c_int
+        L.spec_verify_lm_head_fp8.argtypes = ([vp, vp, vp, vp, i32] + _VERIFY_ARGTYPES[2:9] + [vp] +
+                                              _VERIFY_ARGTYPES[9:])
+        L.sv_block_norm.restype = ctypes.c_int
+        L.sv_block_norm.argtypes = [vp, ctypes.c_int, vp, ctypes.c_int, vp, vp, i64, vp, ctypes.c_int, f32, f32, f32,
+                                    f32, i64, i32, vp, vp, ctypes.c_int, vp, vp]
+        L.sv_quantize_fp8.restype = ctypes.c_int
+        L.sv_quantize_fp8.argtypes = [vp, ctypes.c_int, i64, i32, i32, vp, vp, vp]
         L.sv_status_string.restype = ctypes.c_char_p
         L.sv_status_string.argtypes = [ctypes.c_int]
         _lib = L

@@ -360,6 +360,247 @@ def spec_verify_lm_head(hidden: torch.Tensor, lm_head: torch.Tensor, draft_probs
     return res, logits_out
 
 
+# ------------------------------------------------------------- the last layer in 8-bit floating point
+
+_BLOCK = 128  # values along d (and ids of the output embedding) that share a scale
+_DTYPES = {torch.bfloat16: N.SV_BF16, torch.float32: N.SV_FP32, torch.float8_e4m3fn: N.SV_E4M3}
+
+
+def _dtype(t: torch.Tensor, name: str, fp8: bool = False) -> int:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None or (dt == N.SV_E4M3) != fp8:
+        raise TypeError(f"{name}: expected {'float8_e4m3fn' if fp8 else 'bfloat16 or float32'}, got {t.dtype}")
+    return dt
+
+
+def _cuda(t: torch.Tensor, name: str) -> torch.device:
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return t.device
+
+
+class _on:
+    """Run on `stream` (default: the device's current one): the tensors made
+    inside belong to it, and the launch goes to its device."""
+
+    def __init__(self, dev: torch.device, stream: torch.cuda.Stream | None):
+        self.dev = dev
+        self.stream = stream or torch.cuda.current_stream(dev)
+        if self.stream.device != dev:
+            raise ValueError(f"stream: expected a stream of {dev}, got one of {self.stream.device}")
+        plain = stream is None and torch.cuda.current_device() == dev.index
+        self.ctx = None if plain else torch.cuda.stream(self.stream)
+
+    def __enter__(self) -> int:
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _blocks(n: int) -> int:
+    return -(-n // _BLOCK)
+
+
+def sv_quantize_fp8(x: torch.Tensor, block_rows: int = 1, *, out: torch.Tensor | None = None,
+                    scales: torch.Tensor | None = None,
+                    stream: torch.cuda.Stream | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """e4m3 values of x [..., d] (bf16 / fp32) with one fp32 scale per block
+    of block_rows x 128: 1 for activations (scales [..., ceil(d / 128)]),
+    128 for a weight matrix [V, d] (scales [ceil(V / 128), ceil(d / 128)]).
+    Returns (values, scales); `out` and `scales` may be preallocated."""
+    dt = _dtype(x, "x")
+    dev = _cuda(x, "x")
+    if block_rows not in (1, _BLOCK):
+        raise ValueError("block_rows must be 1 or 128")
+    if x.dim() < 1 or x.shape[-1] < 1 or (block_rows != 1 and x.dim() != 2):
+        raise ValueError("x must be [..., d], and [V, d] for blocks of 128 rows")
+    d = x.shape[-1]
+    rows = x.numel() // d
+    sshape = (x.shape[:-1] if block_rows == 1 else (_blocks(rows),)) + (_blocks(d),)
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+        if scales is None:
+            scales = torch.empty(sshape, dtype=torch.float32, device=dev)
+        _check(out, "out", torch.float8_e4m3fn, x.shape, dev)
+        _check(scales, "scales", torch.float32, sshape, dev)
+        rc = N.lib().sv_quantize_fp8(x.data_ptr(), dt, rows, d, block_rows, out.data_ptr(), scales.data_ptr(), s)
+    if rc != N.SV_OK:
+        raise SpecVerifyError(rc)
+    return out, scales
+
+
+@dataclass
+class BlockNormResult:
+    hidden: torch.Tensor          # [..., d] bf16 / fp32 / e4m3: the LM head's input
+    scales: torch.Tensor | None   # [..., ceil(d / 128)] fp32 (e4m3 hidden)
+    residual: torch.Tensor        # [..., d]: the residual stream after the block
+
+
+def sv_block_norm(x: torch.Tensor, residual: torch.Tensor, norm_weight: torch.Tensor, *,
+                  post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                  residual_scale: float = 1.0, branch_scale: float = 1.0, weight_offset: float = 0.0,
+                  eps: float = 1e-6, hidden_dtype: torch.dtype = torch.bfloat16,
+                  residual_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  scales: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> BlockNormResult:
+    """The norms around the target's last block, from its output x [..., d]
+    and the residual stream [..., d] to the LM head's input:
+
+        a = x (or its RMS norm times post_weight + weight_offset)
+        r = residual_scale * residual + branch_scale * gate * a
+        h = RMS norm of r times norm_weight + weight_offset
+
+    x and residual are bf16 or fp32; the weights [d] share a type, bf16 or
+    fp32; gate has x's type and is [d] or [G, ..., d] with G gate rows in
+    all, each for the same number of consecutive rows of x (one per sequence
+    for [B, 1, d]).  hidden_dtype bfloat16, float32 or float8_e4m3fn (with
+    scales as from sv_quantize_fp8).  residual_out may be `residual` (in
+    place)."""
+    xt, rt, wt = _dtype(x, "x"), _dtype(residual, "residual"), _dtype(norm_weight, "norm_weight")
+    ht = _DTYPES.get(hidden_dtype)
+    if ht is None:
+        raise TypeError("hidden_dtype must be bfloat16, float32 or float8_e4m3fn")
+    dev = _cuda(x, "x")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., d]")
+    d = x.shape[-1]
+    M = x.numel() // d
+    _check(residual, "residual", residual.dtype, x.shape, dev)
+    _check(norm_weight, "norm_weight", norm_weight.dtype, (d,), dev)
+    if post_weight is not None:
+        _check(post_weight, "post_weight", norm_weight.dtype, (d,), dev)
+    gate_rows = 1
+    if gate is not None:
+        if gate.dim() < 1 or gate.shape[-1] != d or gate.numel() == 0:
+            raise ValueError("gate must be [..., d] with at least one row")
+        _check(gate, "gate", x.dtype, gate.shape, dev)
+        gate_rows = gate.numel() // d
+        if M % gate_rows:
+            raise ValueError(f"gate: {gate_rows} rows do not divide the {M} rows of x")
+    if scales is not None and hidden_dtype != torch.float8_e4m3fn:
+        raise ValueError("scales belong to a float8_e4m3fn hidden")
+    with _on(dev, stream) as s:
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        if out is None:
+            out = torch.empty(x.shape, dtype=hidden_dtype, device=dev)
+        if hidden_dtype == torch.float8_e4m3fn:
+            if scales is None:
+                scales = torch.empty(x.shape[:-1] + (_blocks(d),), dtype=torch.float32, device=dev)
+            _check(scales, "scales", torch.float32, x.shape[:-1] + (_blocks(d),), dev)
+        _check(residual_out, "residual_out", residual.dtype, x.shape, dev)
+        _check(out, "out", hidden_dtype, x.shape, dev)
+        rc = N.lib().sv_block_norm(x.data_ptr(), xt, residual.data_ptr(), rt, _ptr(post_weight), _ptr(gate), gate_rows,
+                                   norm_weight.data_ptr(), wt, float(weight_offset), float(residual_scale),
+                                   float(branch_scale), float(eps), M, d, residual_out.data_ptr(), out.data_ptr(), ht,
+                                   _ptr(scales), s)
+    if rc != N.SV_OK:
+        raise SpecVerifyError(rc)
+    return BlockNormResult(out, scales, residual_out)
+
+
+def _lm_fp8_check(hidden, hidden_scales, lm_head, lm_head_scales) -> torch.device:
+    _dtype(hidden, "hidden", fp8=True)
+    _dtype(lm_head, "lm_head", fp8=True)
+    dev = _cuda(hidden, "hidden")
+    if lm_head.dim() != 2 or hidden.dim() < 1 or hidden.shape[-1] != lm_head.shape[1]:
+        raise ValueError("lm_head must be [V, d], d the hidden states' last dimension")
+    V, d = lm_head.shape
+    _check(lm_head, "lm_head", torch.float8_e4m3fn, (V, d), dev)
+    _check(hidden_scales, "hidden_scales", torch.float32, hidden.shape[:-1] + (_blocks(d),), dev)
+    _check(lm_head_scales, "lm_head_scales", torch.float32, (_blocks(V), _blocks(d)), dev)
+    return dev
+
+
+def sv_lm_head_logits_fp8(hidden: torch.Tensor, hidden_scales: torch.Tensor, lm_head: torch.Tensor,
+                          lm_head_scales: torch.Tensor, *, out: torch.Tensor | None = None,
+                          status: torch.Tensor | None = None,
+                          stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """sv_lm_head_logits on e4m3 operands with block scales: hidden [..., d]
+    with hidden_scales [..., ceil(d / 128)], lm_head [V, d] with
+    lm_head_scales [ceil(V / 128), ceil(d / 128)] (sv_block_norm and
+    sv_quantize_fp8 make both) -> [..., V] bf16.  status: optional int32 [1]
+    device tensor that receives SV_INTERNAL_TIMEOUT."""
+    dev = _lm_fp8_check(hidden, hidden_scales, lm_head, lm_head_scales)
+    V, d = lm_head.shape
+    M = hidden.numel() // d if d else 0
+    if status is not None:
+        _check(status, "status", torch.int32, (1,), dev)
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty(hidden.shape[:-1] + (V,), dtype=torch.bfloat16, device=dev)
+        _check(out, "out", torch.bfloat16, hidden.shape[:-1] + (V,), dev)
+        rc = N.lib().sv_lm_head_logits_fp8(hidden.data_ptr(), hidden_scales.data_ptr(), lm_head.data_ptr(),
+                                           lm_head_scales.data_ptr(), M, d, V, out.data_ptr(), _ptr(status), s)
+    if rc != N.SV_OK:
+        raise SpecVerifyError(rc)
+    return out
+
+
+def sv_lm_head_fp8_workspace_bytes(B: int, K: int, V: int) -> int:
+    return int(N.lib().sv_lm_head_fp8_workspace_bytes(int(B), int(K), int(V)))
+
+
+def spec_verify_lm_head_fp8(hidden: torch.Tensor, hidden_scales: torch.Tensor, lm_head: torch.Tensor,
+                            lm_head_scales: torch.Tensor, draft_probs: torch.Tensor | None,
+                            draft_tokens: torch.Tensor, uniforms: torch.Tensor, temperature: float, *,
+                            logits_out: torch.Tensor | None = None, want_probs: bool = True,
+                            workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                            stream: torch.cuda.Stream | None = None):
+    """spec_verify_lm_head on e4m3 operands with block scales: hidden
+    [B, K+1, d], hidden_scales [B, K+1, ceil(d / 128)], lm_head and
+    lm_head_scales as for sv_lm_head_logits_fp8.  Returns (SpecVerifyResult,
+    logits [B, K+1, V] bf16).  A call that is captured into a graph without a
+    workspace of its own gets one that belongs to the graph."""
+    dev = _lm_fp8_check(hidden, hidden_scales, lm_head, lm_head_scales)
+    if hidden.dim() != 3 or hidden.shape[1] < 1:
+        raise ValueError("hidden must be [B, K+1, d]")
+    B, K1, d = hidden.shape
+    K = K1 - 1
+    V = lm_head.shape[0]
+    if draft_probs is not None:
+        _check(draft_probs, "draft_probs", torch.float32, (B, K, V), dev)
+    _check(draft_tokens, "draft_tokens", torch.int32, (B, K), dev)
+    _check(uniforms, "uniforms", torch.float32, (B, K + 1), dev)
+    if status is not None:
+        _check(status, "status", torch.int32, (1,), dev)
+    need = sv_lm_head_fp8_workspace_bytes(B, K, V)
+    if need == 0 and B > 0:
+        raise SpecVerifyError(N.SV_EUNSUPPORTED)
+    with _on(dev, stream) as s:
+        if logits_out is None:
+            logits_out = torch.empty((B, K1, V), dtype=torch.bfloat16, device=dev)
+        _check(logits_out, "logits_out", torch.bfloat16, (B, K1, V), dev)
+        if workspace is None:
+            if torch.cuda.is_current_stream_capturing():
+                workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=dev)
+            else:
+                workspace = default_workspace(dev, need)
+                workspace.record_stream(torch.cuda.current_stream(dev))
+        elif workspace.device != dev or workspace.numel() * workspace.element_size() < need:
+            raise ValueError(f"workspace must hold {need} bytes on {dev}")
+        res = SpecVerifyResult(
+            out_tokens=torch.empty((B, K1), dtype=torch.int32, device=dev),
+            num_emitted=torch.empty((B,), dtype=torch.int32, device=dev),
+            accept_flags=torch.empty((B, K), dtype=torch.int8, device=dev),
+            accept_prob=torch.empty((B, K), dtype=torch.float32, device=dev) if want_probs else None,
+            residual_mass=torch.empty((B,), dtype=torch.float32, device=dev) if want_probs else None,
+            status=status)
+        rc = N.lib().spec_verify_lm_head_fp8(
+            hidden.data_ptr(), hidden_scales.data_ptr(), lm_head.data_ptr(), lm_head_scales.data_ptr(), d,
+            _ptr(draft_probs), draft_tokens.data_ptr(), uniforms.data_ptr(), float(temperature), B, K, V,
+            logits_out.data_ptr(), res.out_tokens.data_ptr(), res.num_emitted.data_ptr(), res.accept_flags.data_ptr(),
+            _ptr(res.accept_prob), _ptr(res.residual_mass), _ptr(status), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), s)
+    if rc != N.SV_OK:
+        raise SpecVerifyError(rc)
+    return res, logits_out
+
+
 # ------------------------------------------------------------- trees
 
 @dataclass

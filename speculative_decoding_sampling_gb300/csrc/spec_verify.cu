@@ -2,8 +2,9 @@
 // workspace layout, and the launches on the caller's stream -- the row
 // pass, the draw stream and, when the draw stream does not fill the GPU,
 // the final draws -- each chained to the one before by programmatic
-// dependent launch; and the top-k / top-p filter.  The operations
-// themselves are documented in spec_verify.h.
+// dependent launch; the top-k / top-p filter; and the target's last layer
+// (norms, quantisation, LM head).  The operations themselves are documented
+// in spec_verify.h.
 #include "spec_verify.h"
 
 #include <cmath>
@@ -12,9 +13,11 @@
 #include <cuda_runtime.h>
 #include <mutex>
 
+#include "sv_block_norm.cuh"
 #include "sv_filter.cuh"
 #include "sv_final.cuh"
 #include "sv_lmhead.cuh"
+#include "sv_lmhead_fp8.cuh"
 #include "sv_tree.cuh"
 #include "sv_rows.cuh"
 
@@ -348,10 +351,12 @@ int32_t lm_tiles(int32_t V) { return static_cast<int32_t>(ceil_div(V, sv::kLmBN)
 
 size_t lm_part_bytes(int64_t M, int32_t V) { return align_up(static_cast<size_t>(M) * lm_tiles(V) * sizeof(float2)); }
 
-// A 2-D tensor map of a row-major bf16 matrix [rows, cols] with boxes of
-// box_rows x 64 elements in the 128-byte swizzle layout; out-of-range
-// elements read as zero.  Reached through the runtime's entry-point lookup.
-bool lm_tensor_map(CUtensorMap *map, const void *base, int64_t rows, int32_t cols, uint32_t box_rows)
+// A 2-D tensor map of a row-major matrix [rows, cols] (bf16, or e4m3 bytes)
+// with boxes of box_rows x 128 bytes in the 128-byte swizzle layout;
+// out-of-range elements read as zero.  Reached through the runtime's
+// entry-point lookup.
+bool lm_tensor_map(CUtensorMap *map, const void *base, int64_t rows, int32_t cols, uint32_t box_rows,
+                   bool fp8 = false)
 {
     using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -370,10 +375,10 @@ bool lm_tensor_map(CUtensorMap *map, const void *base, int64_t rows, int32_t col
     if (!encode)
         return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(sv::kLmBK), box_rows};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * (fp8 ? 1 : 2)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(fp8 ? sv::kL8BK : sv::kLmBK), box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+    return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -482,6 +487,229 @@ cudaError_t lm_launch(const void *hidden, const void *lm_head, int64_t M, int32_
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, sv::lm_head_kernel, ta, tb, L);
 }
+
+// ------------------------------------------------------- LM head on e4m3
+
+constexpr int kNominalSms = 152; // GB300
+
+// How the product is cut: a function of (M, V) only, so that the workspace is.
+struct Lm8Plan {
+    bool pair;
+    int32_t MT, NT, NB, halves;
+};
+
+Lm8Plan lm8_plan(int64_t M, int32_t V)
+{
+    Lm8Plan p;
+    p.pair = M > sv::kLmBM;
+    const int64_t rows = p.pair ? 2 * sv::kLmBM : sv::kLmBM, units = p.pair ? kNominalSms / 2 : kNominalSms;
+    p.MT = static_cast<int32_t>(ceil_div(M > 0 ? M : 1, rows));
+    // ids per tile: the width whose last wave of tiles wastes least (a tile
+    // costs its ids plus about 16 for its start and end); the widest on ties
+    int64_t best = INT64_MAX;
+    for (int32_t nb = sv::kL8MaxNB; nb >= 32; nb -= 32) {
+        const int64_t cost = ceil_div(p.MT * ceil_div(V, nb), units) * (nb + 16);
+        if (cost < best) {
+            best = cost;
+            p.NB = nb;
+        }
+    }
+    p.NT = static_cast<int32_t>(ceil_div(V, p.NB));
+    p.halves = p.NB > 128 ? 2 : 1;
+    return p;
+}
+
+size_t lm8_part_bytes(int64_t M, int32_t V)
+{
+    const Lm8Plan p = lm8_plan(M, V);
+    return align_up(static_cast<size_t>(M) * p.NT * p.halves * sizeof(float2));
+}
+
+sv_status_t lm8_check(const void *hidden, const float *hidden_scales, const void *lm_head, const float *lm_head_scales,
+                      int64_t M, int32_t d, int32_t V, const void *logits)
+{
+    if (M < 0 || d < 16 || d % 16 != 0 || V < 1)
+        return SV_EINVAL;
+    if (V > SV_MAX_V || M > kLmMaxRows)
+        return SV_EUNSUPPORTED;
+    if (M > 0 && (!hidden || !hidden_scales || !lm_head || !lm_head_scales || !logits || !aligned(hidden, 16) ||
+                  !aligned(lm_head, 16) || !aligned(hidden_scales, 4) || !aligned(lm_head_scales, 4) ||
+                  !aligned(logits, 2)))
+        return SV_EINVAL;
+    return SV_OK;
+}
+
+// How many CTAs (or clusters of two) of the e4m3 kernel fit on the current
+// device at once; cached like the bf16 kernel's figure.
+template <bool PAIR> cudaError_t lm8_units(int &units)
+{
+    struct Entry {
+        int units;
+        unsigned long long ctx;
+    };
+    static std::mutex mu;
+    static Entry cache[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= kMaxDevices)
+        return cudaErrorInvalidDevice;
+    const unsigned long long ctx = current_context_id();
+    std::lock_guard<std::mutex> lock(mu);
+    if (cache[dev].units == 0 || cache[dev].ctx == 0 || cache[dev].ctx != ctx) {
+        constexpr int smem = sv::L8Shape<PAIR>::kSmem;
+        e = cudaFuncSetAttribute(sv::lm_head_fp8_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess)
+            return e;
+        int sms = 0, n = 0;
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess)
+            return e;
+        if (PAIR) {
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 2;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(sms > 1 ? sms & ~1 : 2));
+            cfg.blockDim = dim3(sv::kL8Threads);
+            cfg.dynamicSmemBytes = smem;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, sv::lm_head_fp8_kernel<PAIR>, &cfg);
+        } else {
+            n = sms;
+        }
+        if (e != cudaSuccess)
+            return e;
+        if (n < 1)
+            return cudaErrorInvalidConfiguration;
+        cache[dev].units = n;
+        cache[dev].ctx = current_context_id();
+    }
+    units = cache[dev].units;
+    return cudaSuccess;
+}
+
+template <bool PAIR>
+cudaError_t lm8_launch_as(const CUtensorMap &ta, const CUtensorMap &tb, const sv::Lm8Params &L, cudaStream_t stream)
+{
+    int units = 0;
+    const cudaError_t e = lm8_units<PAIR>(units);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t tiles = static_cast<int64_t>(L.MT) * L.NT;
+    const int64_t n = tiles < units ? tiles : units;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = sv::L8Shape<PAIR>::kCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(n * sv::L8Shape<PAIR>::kCtas));
+    cfg.blockDim = dim3(sv::kL8Threads);
+    cfg.dynamicSmemBytes = sv::L8Shape<PAIR>::kSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sv::lm_head_fp8_kernel<PAIR>, ta, tb, L);
+}
+
+// logits (bf16 out) and, with `part`, the row statistics of each half tile.
+cudaError_t lm8_launch(const void *hidden, const float *hidden_scales, const void *lm_head, const float *lm_head_scales,
+                       int64_t M, int32_t d, int32_t V, void *logits, float2 *part, float c, int32_t *status,
+                       cudaStream_t stream)
+{
+    const Lm8Plan p = lm8_plan(M, V);
+    CUtensorMap ta, tb;
+    if (!lm_tensor_map(&ta, hidden, M, d, sv::kLmBM, true) ||
+        !lm_tensor_map(&tb, lm_head, V, d, static_cast<uint32_t>(p.pair ? p.NB / 2 : p.NB), true))
+        return cudaErrorInvalidValue;
+    sv::Lm8Params L;
+    L.M = static_cast<int32_t>(M);
+    L.N = V;
+    L.KB = static_cast<int32_t>(ceil_div(d, sv::kL8BK));
+    L.MT = p.MT;
+    L.NT = p.NT;
+    L.NB = p.NB;
+    L.idesc = sv::l8_idesc(p.pair ? 2 * sv::kLmBM : sv::kLmBM, p.NB);
+    L.hs = hidden_scales;
+    L.ws = lm_head_scales;
+    L.logits = static_cast<uint16_t *>(logits);
+    L.part = part;
+    L.halves = p.halves;
+    L.c = c;
+    L.vec = (V % 8 == 0 && aligned(logits, 16)) ? 1 : 0;
+    L.status = status;
+    L.wait_ns = kWaitLimitNs;
+    return p.pair ? lm8_launch_as<true>(ta, tb, L, stream) : lm8_launch_as<false>(ta, tb, L, stream);
+}
+
+// The statistics of the product's tiles merged per row with the draft data,
+// then the draw stream and the final draws.
+sv_status_t lm_finish(const Plan &plan, float2 *part, int32_t slots, const void *logits, const float *draft_probs,
+                      const int32_t *draft_tokens, const float *uniforms, float temperature, int64_t B, int32_t K,
+                      int32_t V, int32_t *out_tokens, int32_t *num_emitted, int8_t *accept_flags, float *accept_prob,
+                      float *residual_mass, int32_t *status_dev, void *workspace, void *stream)
+{
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    sv::Params P = {};
+    P.logits = logits;
+    P.q = K > 0 ? draft_probs : nullptr;
+    P.tokens = draft_tokens;
+    P.u = uniforms;
+    P.c = static_cast<float>(1.4426950408889634074 / static_cast<double>(temperature));
+    P.B = B;
+    P.K = K;
+    P.V = V;
+    P.row_part = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + plan.off_part);
+    P.row_side = reinterpret_cast<float4 *>(static_cast<char *>(workspace) + plan.off_row_side);
+    P.PM = plan.PM;
+    const unsigned grid = static_cast<unsigned>(ceil_div(plan.R, 8));
+    if (P.q)
+        sv::lm_merge_kernel<true><<<grid, 256, 0, s>>>(P, part, slots);
+    else
+        sv::lm_merge_kernel<false><<<grid, 256, 0, s>>>(P, part, slots);
+    if (cudaGetLastError() != cudaSuccess)
+        return SV_ECUDA;
+    return run(kSurvivors, logits, SV_BF16, draft_probs, draft_tokens, uniforms, temperature, B, K, V, out_tokens,
+               num_emitted, accept_flags, accept_prob, residual_mass, status_dev, workspace, plan.bytes, stream,
+               nullptr, 1);
+}
+
+// ------------------------------------------------- norms and quantisation
+
+size_t elem_size(sv_dtype_t t) { return t == SV_BF16 ? 2 : (t == SV_FP32 ? 4 : 1); }
+
+bool is_bf16_or_fp32(sv_dtype_t t) { return t == SV_BF16 || t == SV_FP32; }
+
+// 16-byte accesses of 8 consecutive values, where the pointer may be NULL
+bool vec_ok(const void *p, sv_dtype_t t) { return aligned(p, t == SV_E4M3 ? 8 : 16); }
+
+template <bool VEC> cudaError_t norm_launch(const sv::NormParams &P, int nseg, unsigned grid, cudaStream_t s)
+{
+    const unsigned threads = static_cast<unsigned>(P.WPR * P.RPC * 32);
+    switch (nseg) {
+    case 1:
+        sv::block_norm_kernel<1, VEC><<<grid, threads, 0, s>>>(P);
+        break;
+    case 2:
+        sv::block_norm_kernel<2, VEC><<<grid, threads, 0, s>>>(P);
+        break;
+    case 4:
+        sv::block_norm_kernel<4, VEC><<<grid, threads, 0, s>>>(P);
+        break;
+    default:
+        sv::block_norm_kernel<8, VEC><<<grid, threads, 0, s>>>(P);
+        break;
+    }
+    return cudaGetLastError();
+}
+
+static_assert(sv::kElemBf16 == SV_BF16 && sv::kElemFp32 == SV_FP32 && sv::kElemE4m3 == SV_E4M3, "element types");
+static_assert(sv::kNormMaxWarps * sv::kNormMaxSegs * sv::kSeg == SV_MAX_D, "widest row of the norms");
 
 static_assert(sv::kTreeMaxNodes == SV_MAX_TREE_NODES, "tree size limit");
 static_assert(sv::kBadTree == SV_BAD_TREE, "status bit");
@@ -681,31 +909,168 @@ sv_status_t spec_verify_lm_head(const void *hidden, const void *lm_head, int32_t
     const float c = static_cast<float>(1.4426950408889634074 / static_cast<double>(temperature));
     if (lm_launch(hidden, lm_head, M, d, V, logits_out, part, c, status_dev, s) != cudaSuccess)
         return SV_ECUDA;
-    // the row statistics and draft data, then the draw stream and final draws
-    {
-        sv::Params P = {};
-        P.logits = logits_out;
-        P.q = K > 0 ? draft_probs : nullptr;
-        P.tokens = draft_tokens;
-        P.u = uniforms;
-        P.c = c;
-        P.B = B;
-        P.K = K;
-        P.V = V;
-        P.row_part = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + plan.off_part);
-        P.row_side = reinterpret_cast<float4 *>(static_cast<char *>(workspace) + plan.off_row_side);
-        P.PM = plan.PM;
-        const unsigned grid = static_cast<unsigned>(ceil_div(M, 8));
-        if (P.q)
-            sv::lm_merge_kernel<true><<<grid, 256, 0, s>>>(P, part, lm_tiles(V));
+    return lm_finish(plan, part, lm_tiles(V), logits_out, draft_probs, draft_tokens, uniforms, temperature, B, K, V,
+                     out_tokens, num_emitted, accept_flags, accept_prob, residual_mass, status_dev, workspace, stream);
+}
+
+size_t sv_lm_head_fp8_workspace_bytes(int64_t B, int32_t K, int32_t V)
+{
+    Plan p;
+    if (!make_plan(B, K, V, p) || p.R > kLmMaxRows)
+        return 0;
+    return p.bytes + lm8_part_bytes(p.R, V);
+}
+
+sv_status_t sv_lm_head_logits_fp8(const void *hidden, const float *hidden_scales, const void *lm_head,
+                                  const float *lm_head_scales, int64_t M, int32_t d, int32_t V, void *logits,
+                                  int32_t *status_dev, void *stream)
+{
+    const sv_status_t st = lm8_check(hidden, hidden_scales, lm_head, lm_head_scales, M, d, V, logits);
+    if (st != SV_OK || M == 0)
+        return st;
+    if (status_dev && !aligned(status_dev, 4))
+        return SV_EINVAL;
+    return lm8_launch(hidden, hidden_scales, lm_head, lm_head_scales, M, d, V, logits, nullptr, 1.0f, status_dev,
+                      static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? SV_OK
+               : SV_ECUDA;
+}
+
+sv_status_t spec_verify_lm_head_fp8(const void *hidden, const float *hidden_scales, const void *lm_head,
+                                    const float *lm_head_scales, int32_t d, const float *draft_probs,
+                                    const int32_t *draft_tokens, const float *uniforms, float temperature, int64_t B,
+                                    int32_t K, int32_t V, void *logits_out, int32_t *out_tokens, int32_t *num_emitted,
+                                    int8_t *accept_flags, float *accept_prob, float *residual_mass,
+                                    int32_t *status_dev, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (B < 0 || K < 0)
+        return SV_EINVAL;
+    if (B > 0 && static_cast<int64_t>(K) + 1 > kLmMaxRows / B)
+        return SV_EUNSUPPORTED;
+    const int64_t M = B * (static_cast<int64_t>(K) + 1);
+    sv_status_t st = lm8_check(hidden, hidden_scales, lm_head, lm_head_scales, M, d, V, logits_out);
+    if (st != SV_OK)
+        return st;
+    Plan plan;
+    if (!make_plan(B, K, V, plan))
+        return SV_EUNSUPPORTED;
+    if (!workspace || workspace_bytes < plan.bytes + lm8_part_bytes(M, V))
+        return SV_EINVAL;
+    // host checks of the verification (nothing launched yet)
+    st = run(0, logits_out, SV_BF16, draft_probs, draft_tokens, uniforms, temperature, B, K, V, out_tokens,
+             num_emitted, accept_flags, accept_prob, residual_mass, status_dev, workspace, plan.bytes, stream);
+    if (st != SV_OK || B == 0)
+        return st;
+    float2 *part = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + plan.bytes);
+    const float c = static_cast<float>(1.4426950408889634074 / static_cast<double>(temperature));
+    if (lm8_launch(hidden, hidden_scales, lm_head, lm_head_scales, M, d, V, logits_out, part, c, status_dev,
+                   static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return SV_ECUDA;
+    const Lm8Plan p = lm8_plan(M, V);
+    return lm_finish(plan, part, p.NT * p.halves, logits_out, draft_probs, draft_tokens, uniforms, temperature, B, K, V,
+                     out_tokens, num_emitted, accept_flags, accept_prob, residual_mass, status_dev, workspace, stream);
+}
+
+sv_status_t sv_block_norm(const void *x, sv_dtype_t x_dtype, const void *residual, sv_dtype_t residual_dtype,
+                          const void *post_weight, const void *gate, int64_t gate_rows, const void *norm_weight,
+                          sv_dtype_t weight_dtype, float weight_offset, float residual_scale, float branch_scale,
+                          float eps, int64_t M, int32_t d, void *residual_out, void *hidden, sv_dtype_t hidden_dtype,
+                          float *hidden_scales, void *stream)
+{
+    if (M < 0 || d < 1 || !is_bf16_or_fp32(x_dtype) || !is_bf16_or_fp32(residual_dtype) ||
+        !is_bf16_or_fp32(weight_dtype) || (!is_bf16_or_fp32(hidden_dtype) && hidden_dtype != SV_E4M3))
+        return SV_EINVAL;
+    if (!std::isfinite(weight_offset) || !std::isfinite(residual_scale) || !std::isfinite(branch_scale) ||
+        !std::isfinite(eps) || !(eps > 0.0f))
+        return SV_EINVAL;
+    if (d > SV_MAX_D || M > INT32_MAX)
+        return SV_EUNSUPPORTED;
+    if (gate && (gate_rows < 1 || M % gate_rows != 0))
+        return SV_EINVAL;
+    if (M == 0)
+        return SV_OK;
+    if (!x || !residual || !norm_weight || !residual_out || !hidden || (hidden_dtype == SV_E4M3) != (hidden_scales != nullptr))
+        return SV_EINVAL;
+    if (!aligned(x, elem_size(x_dtype)) || !aligned(residual, elem_size(residual_dtype)) ||
+        !aligned(residual_out, elem_size(residual_dtype)) || !aligned(hidden, elem_size(hidden_dtype)) ||
+        !aligned(post_weight, elem_size(weight_dtype)) || !aligned(norm_weight, elem_size(weight_dtype)) ||
+        !aligned(gate, elem_size(x_dtype)) || !aligned(hidden_scales, 4))
+        return SV_EINVAL;
+    sv::NormParams P;
+    P.x = x;
+    P.residual = residual;
+    P.post = post_weight;
+    P.gate = gate;
+    P.pre = norm_weight;
+    P.x_type = x_dtype;
+    P.r_type = residual_dtype;
+    P.w_type = weight_dtype;
+    P.h_type = hidden_dtype;
+    P.M = M;
+    P.gate_div = gate ? M / gate_rows : 1;
+    P.d = d;
+    const int segs = static_cast<int>(ceil_div(d, sv::kSeg));
+    P.WPR = 1;
+    while (P.WPR < segs && P.WPR < sv::kNormMaxWarps)
+        P.WPR *= 2;
+    P.RPC = P.WPR < 4 ? 4 / P.WPR : 1;
+    int nseg = 1;
+    while (nseg * P.WPR < segs)
+        nseg *= 2;
+    P.offset = weight_offset;
+    P.rs = residual_scale;
+    P.bs = branch_scale;
+    P.eps = eps;
+    P.inv_d = 1.0f / static_cast<float>(d);
+    P.r_out = residual_out;
+    P.h = hidden;
+    P.scales = hidden_scales;
+    const bool vec = d % 8 == 0 && vec_ok(x, x_dtype) && vec_ok(residual, residual_dtype) &&
+                     vec_ok(residual_out, residual_dtype) && vec_ok(hidden, hidden_dtype) &&
+                     vec_ok(post_weight, weight_dtype) && vec_ok(norm_weight, weight_dtype) && vec_ok(gate, x_dtype);
+    const unsigned grid = static_cast<unsigned>(ceil_div(M, P.RPC));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return (vec ? norm_launch<true>(P, nseg, grid, s) : norm_launch<false>(P, nseg, grid, s)) == cudaSuccess ? SV_OK
+                                                                                                        : SV_ECUDA;
+}
+
+sv_status_t sv_quantize_fp8(const void *x, sv_dtype_t x_dtype, int64_t rows, int32_t d, int32_t block_rows,
+                            void *values, float *scales, void *stream)
+{
+    if (rows < 0 || d < 1 || !is_bf16_or_fp32(x_dtype) || (block_rows != 1 && block_rows != 128))
+        return SV_EINVAL;
+    if (rows > INT32_MAX)
+        return SV_EUNSUPPORTED;
+    if (rows == 0)
+        return SV_OK;
+    if (!x || !values || !scales || !aligned(x, elem_size(x_dtype)) || !aligned(scales, 4))
+        return SV_EINVAL;
+    sv::QuantParams P;
+    P.x = x;
+    P.x_type = x_dtype;
+    P.M = rows;
+    P.d = d;
+    P.v = static_cast<uint8_t *>(values);
+    P.scales = scales;
+    const bool vec = d % 8 == 0 && vec_ok(x, x_dtype) && vec_ok(values, SV_E4M3);
+    P.segs = ceil_div(d, block_rows == 1 ? sv::kSeg : 128);
+    const int64_t grid = block_rows == 1 ? ceil_div(rows * P.segs, sv::kQuantWarps) : ceil_div(rows, 128) * P.segs;
+    if (grid > INT32_MAX)
+        return SV_EUNSUPPORTED;
+    const unsigned g = static_cast<unsigned>(grid);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (block_rows == 1) {
+        if (vec)
+            sv::quantize_rows_kernel<true><<<g, sv::kQuantWarps * 32, 0, s>>>(P);
         else
-            sv::lm_merge_kernel<false><<<grid, 256, 0, s>>>(P, part, lm_tiles(V));
-        if (cudaGetLastError() != cudaSuccess)
-            return SV_ECUDA;
+            sv::quantize_rows_kernel<false><<<g, sv::kQuantWarps * 32, 0, s>>>(P);
+    } else {
+        if (vec)
+            sv::quantize_tiles_kernel<true><<<g, sv::kQuantWarps * 32, 0, s>>>(P);
+        else
+            sv::quantize_tiles_kernel<false><<<g, sv::kQuantWarps * 32, 0, s>>>(P);
     }
-    return run(kSurvivors, logits_out, SV_BF16, draft_probs, draft_tokens, uniforms, temperature, B, K, V, out_tokens,
-               num_emitted, accept_flags, accept_prob, residual_mass, status_dev, workspace, plan.bytes, stream,
-               nullptr, 1);
+    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ECUDA;
 }
 
 size_t sv_tree_workspace_bytes(int64_t B, int32_t N, int32_t V)

@@ -1,0 +1,378 @@
+// sv_block_norm.cuh -- the norms around the target's last block, fused with
+// its gate and residual scale, and e4m3 block quantisation.
+//
+// Per row of d values, all in fp32:
+//   a = x rsqrt(mean(x^2) + eps) (w_post + o)     (a = x without w_post)
+//   r = rs residual + bs g a                      (g = 1 without a gate)
+//   h = r rsqrt(mean(r^2) + eps) (w_pre + o)
+// r is rounded once, to the residual's type, and h once, to its own; h is
+// formed from r before that rounding.  An e4m3 h carries one fp32 scale per
+// 128 values.
+//
+// A row is cut into segments of 256 values, one warp's 8 per lane; WPR warps
+// hold a row in registers from the loads to the stores, so x, residual and
+// gate are read once and r and h written once.  The two row sums are warp
+// sums joined through shared memory in a fixed order.
+#pragma once
+
+#include "sv_device.cuh"
+
+namespace sv {
+
+constexpr int kSeg = 256;         // values of a segment: 8 per lane of a warp
+constexpr int kNormMaxWarps = 16; // warps of a row
+constexpr int kNormMaxSegs = 8;   // segments of a warp
+constexpr float kE4m3Max = 448.0f;
+constexpr float kAmaxFloor = 0x1p-100f; // keeps the scale and its reciprocal normal numbers
+
+enum ElemType { kElemBf16 = 0, kElemFp32 = 1, kElemE4m3 = 2 };
+
+// The 8 values of a lane in a segment starting at `base`: consecutive ones
+// (VEC: 16-byte accesses) or every 32nd (coalesced single accesses, for rows
+// that are not whole 16-byte units).
+template <bool VEC> __device__ __forceinline__ int seg_index(int base, int lane, int i)
+{
+    return VEC ? base + lane * 8 + i : base + i * 32 + lane;
+}
+
+__device__ __forceinline__ float elem_at(const void *p, int type, int64_t e)
+{
+    return type == kElemBf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(p)[e]) << 16)
+                             : static_cast<const float *>(p)[e];
+}
+
+// `row` points at the row's first element; values past d read as 0.  Plain
+// loads, not the read-only path: the residual may be updated in place.
+template <bool VEC>
+__device__ __forceinline__ void seg_load(float (&v)[8], const void *row, int type, int base, int lane, int d)
+{
+    if constexpr (VEC) {
+        const int e = base + lane * 8;
+        if (e < d) { // d is a multiple of 8
+            if (type == kElemBf16) {
+                const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(row) + e);
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[2 * i] = bf16_lo(w[i]);
+                    v[2 * i + 1] = bf16_hi(w[i]);
+                }
+            } else {
+                const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(row) + e);
+                const float4 a = p[0], b = p[1];
+                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+                v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = 0.0f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = seg_index<false>(base, lane, i);
+            v[i] = e >= d ? 0.0f : elem_at(row, type, e);
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// two values as e4m3 bytes, nearest even, magnitudes above 448 to 448, NaN kept
+__device__ __forceinline__ uint32_t e4m3x2_rn(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void seg_store(const float (&v)[8], void *row, int type, int base, int lane, int d)
+{
+    if constexpr (VEC) {
+        const int e = base + lane * 8;
+        if (e >= d)
+            return;
+        if (type == kElemBf16) {
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(row) + e) =
+                make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
+        } else if (type == kElemFp32) {
+            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(row) + e);
+            p[0] = make_float4(v[0], v[1], v[2], v[3]);
+            p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(row) + e) =
+                make_uint2(e4m3x2_rn(v[0], v[1]) | e4m3x2_rn(v[2], v[3]) << 16,
+                           e4m3x2_rn(v[4], v[5]) | e4m3x2_rn(v[6], v[7]) << 16);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = seg_index<false>(base, lane, i);
+            if (e >= d)
+                continue;
+            if (type == kElemBf16)
+                static_cast<uint16_t *>(row)[e] = static_cast<uint16_t>(bf16x2_rn(v[i], 0.0f));
+            else if (type == kElemFp32)
+                static_cast<float *>(row)[e] = v[i];
+            else
+                static_cast<uint8_t *>(row)[e] = static_cast<uint8_t>(e4m3x2_rn(v[i], 0.0f));
+        }
+    }
+}
+
+// the larger one; NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float block_scale(float amax) { return __fdiv_rn(max_nan(amax, kAmaxFloor), kE4m3Max); }
+
+// A segment's two blocks of 128 as e4m3 with their scales.  VEC: lanes 0..15
+// hold the first block, 16..31 the second; otherwise values 0..3 of every
+// lane the first, 4..7 the second.
+template <bool VEC>
+__device__ __forceinline__ void seg_quantize(float (&v)[8], void *row, float *scale_row, int base, int lane, int d)
+{
+    float a0 = 0.0f, a1 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        a0 = max_nan(a0, fabsf(v[i]));
+        a1 = max_nan(a1, fabsf(v[4 + i]));
+    }
+    if constexpr (VEC)
+        a0 = max_nan(a0, a1);
+#pragma unroll
+    for (int o = VEC ? 8 : 16; o > 0; o >>= 1) {
+        a0 = max_nan(a0, __shfl_xor_sync(0xFFFFFFFFu, a0, o));
+        if constexpr (!VEC)
+            a1 = max_nan(a1, __shfl_xor_sync(0xFFFFFFFFu, a1, o));
+    }
+    const float s0 = block_scale(a0), s1 = VEC ? s0 : block_scale(a1);
+    const float i0 = __frcp_rn(s0), i1 = VEC ? i0 : __frcp_rn(s1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = __fmul_rn(v[i], i0);
+        v[4 + i] = __fmul_rn(v[4 + i], i1);
+    }
+    seg_store<VEC>(v, row, kElemE4m3, base, lane, d);
+    const int b = base / 128;
+    if constexpr (VEC) {
+        if ((lane & 15) == 0 && base + lane * 8 < d)
+            scale_row[b + (lane >> 4)] = s0;
+    } else {
+        if (lane == 0 && base < d)
+            scale_row[b] = s0;
+        if (lane == 1 && base + 128 < d)
+            scale_row[b + 1] = s1;
+    }
+}
+
+// ------------------------------------------------------------- the norms
+
+struct NormParams {
+    const void *x, *residual, *post, *gate, *pre;
+    int32_t x_type, r_type, w_type, h_type;
+    int64_t M, gate_div; // row m is gated by row m / gate_div of the gate
+    int32_t d, WPR, RPC; // warps per row, rows per CTA
+    float offset, rs, bs, eps, inv_d;
+    void *r_out, *h;
+    float *scales; // [M, ceil(d / 128)] (e4m3 h)
+};
+
+// sum over the warps of a row; `red` has one float per warp of the CTA
+__device__ __forceinline__ float row_sum(float v, float *red, int warp, int first, int WPR)
+{
+    v = warp_sum_f(v);
+    if (WPR == 1)
+        return v;
+    if ((threadIdx.x & 31) == 0)
+        red[warp] = v;
+    __syncthreads();
+    float s = 0.0f;
+    for (int i = 0; i < WPR; ++i)
+        s = __fadd_rn(s, red[first + i]);
+    return s;
+}
+
+__device__ __forceinline__ const char *row_of(const void *base, int64_t row, int d, int type)
+{
+    return static_cast<const char *>(base) + row * d * (type == kElemBf16 ? 2 : 4);
+}
+
+template <int NSEG, bool VEC>
+__global__ void __launch_bounds__(kNormMaxWarps * 32) block_norm_kernel(const NormParams P)
+{
+    __shared__ float red[2][kNormMaxWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rl = warp / P.WPR, first = rl * P.WPR, wr = warp - first;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * P.RPC + rl;
+    const bool ok = row < P.M; // warps of a missing row still meet the barriers
+    const int d = ok ? P.d : 0;
+    const int64_t rr = ok ? row : 0;
+    float v[NSEG][8], r[NSEG][8];
+#pragma unroll
+    for (int s = 0; s < NSEG; ++s) {
+        const int base = (s * P.WPR + wr) * kSeg;
+        seg_load<VEC>(v[s], row_of(P.x, rr, P.d, P.x_type), P.x_type, base, lane, d);
+        seg_load<VEC>(r[s], row_of(P.residual, rr, P.d, P.r_type), P.r_type, base, lane, d);
+    }
+    if (P.post) {
+        float q = 0.0f;
+#pragma unroll
+        for (int s = 0; s < NSEG; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                q = __fmaf_rn(v[s][i], v[s][i], q);
+        const float f = rsqrtf(__fmaf_rn(row_sum(q, red[0], warp, first, P.WPR), P.inv_d, P.eps));
+#pragma unroll
+        for (int s = 0; s < NSEG; ++s) {
+            float w[8];
+            seg_load<VEC>(w, P.post, P.w_type, (s * P.WPR + wr) * kSeg, lane, d);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[s][i] = v[s][i] * f * (w[i] + P.offset);
+        }
+    }
+    float q = 0.0f;
+#pragma unroll
+    for (int s = 0; s < NSEG; ++s) {
+        const int base = (s * P.WPR + wr) * kSeg;
+        if (P.gate) {
+            float g[8];
+            seg_load<VEC>(g, row_of(P.gate, rr / P.gate_div, P.d, P.x_type), P.x_type, base, lane, d);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[s][i] *= g[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            r[s][i] = __fmaf_rn(P.bs, v[s][i], __fmul_rn(P.rs, r[s][i]));
+            q = __fmaf_rn(r[s][i], r[s][i], q);
+        }
+        seg_store<VEC>(r[s], const_cast<char *>(row_of(P.r_out, rr, P.d, P.r_type)), P.r_type, base, lane, d);
+    }
+    const float f = rsqrtf(__fmaf_rn(row_sum(q, red[1], warp, first, P.WPR), P.inv_d, P.eps));
+#pragma unroll
+    for (int s = 0; s < NSEG; ++s) {
+        const int base = (s * P.WPR + wr) * kSeg;
+        float w[8];
+        seg_load<VEC>(w, P.pre, P.w_type, base, lane, d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            r[s][i] = r[s][i] * f * (w[i] + P.offset);
+        if (P.h_type == kElemE4m3)
+            seg_quantize<VEC>(r[s], static_cast<uint8_t *>(P.h) + rr * P.d,
+                              P.scales + rr * ((P.d + 127) / 128), base, lane, d);
+        else
+            seg_store<VEC>(r[s], const_cast<char *>(row_of(P.h, rr, P.d, P.h_type)), P.h_type, base, lane, d);
+    }
+}
+
+// ------------------------------------------------------------- quantisation
+
+struct QuantParams {
+    const void *x;
+    int32_t x_type;
+    int64_t M;
+    int32_t d;
+    int64_t segs; // segments of a row (1 x 128 blocks) or blocks along a row (128 x 128)
+    uint8_t *v;
+    float *scales;
+};
+
+constexpr int kQuantWarps = 8;
+
+// A scale per row and 128 values: a warp per segment of 256 values.
+template <bool VEC> __global__ void __launch_bounds__(kQuantWarps * 32) quantize_rows_kernel(const QuantParams P)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kQuantWarps + (threadIdx.x >> 5);
+    const int64_t row = i / P.segs;
+    if (row >= P.M) // warp-uniform
+        return;
+    const int base = static_cast<int>(i - row * P.segs) * kSeg;
+    float v[8];
+    seg_load<VEC>(v, row_of(P.x, row, P.d, P.x_type), P.x_type, base, lane, P.d);
+    seg_quantize<VEC>(v, P.v + row * P.d, P.scales + row * ((P.d + 127) / 128), base, lane, P.d);
+}
+
+// A scale per 128 x 128 block: a CTA per block, held in registers (64 values
+// a thread).  VEC: a half-warp per row, 8 consecutive values a lane;
+// otherwise 4 single values of a row per lane.
+template <bool VEC> __global__ void __launch_bounds__(kQuantWarps * 32) quantize_tiles_kernel(const QuantParams P)
+{
+    __shared__ float red[kQuantWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t rb = blockIdx.x / P.segs;
+    const int cb = static_cast<int>(blockIdx.x - rb * P.segs);
+    float v[8][8];
+    float amax = 0.0f;
+    // value (s, i) of this thread: row and column inside the block
+    auto at_row = [&](int s, int i) { return VEC ? s * 16 + warp * 2 + (lane >> 4) : s * 16 + warp * 2 + (i >> 2); };
+    auto at_col = [&](int i) { return VEC ? (lane & 15) * 8 + i : (i & 3) * 32 + lane; };
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+        if constexpr (VEC) {
+            const int64_t row = rb * 128 + at_row(s, 0);
+            // the loader's lane index selects 8 values from `base` on
+            const int base = cb * 128 + (lane & 15) * 8 - lane * 8;
+            seg_load<true>(v[s], row_of(P.x, row < P.M ? row : 0, P.d, P.x_type), P.x_type, base, lane,
+                           row < P.M ? P.d : 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int64_t row = rb * 128 + at_row(s, i);
+                const int e = cb * 128 + at_col(i);
+                v[s][i] = 0.0f;
+                if (row < P.M && e < P.d)
+                    v[s][i] = elem_at(P.x, P.x_type, row * P.d + e);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            amax = max_nan(amax, fabsf(v[s][i]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    if (lane == 0)
+        red[warp] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kQuantWarps; ++w)
+        amax = max_nan(amax, red[w]);
+    const float s = block_scale(amax), inv = __frcp_rn(s);
+    if (threadIdx.x == 0)
+        P.scales[blockIdx.x] = s;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[k][i] = __fmul_rn(v[k][i], inv);
+        if constexpr (VEC) {
+            const int64_t row = rb * 128 + at_row(k, 0);
+            if (row < P.M)
+                seg_store<true>(v[k], P.v + row * P.d, kElemE4m3, cb * 128 + (lane & 15) * 8 - lane * 8, lane, P.d);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int64_t row = rb * 128 + at_row(k, i);
+                const int e = cb * 128 + at_col(i);
+                if (row < P.M && e < P.d)
+                    P.v[row * P.d + e] = static_cast<uint8_t>(e4m3x2_rn(v[k][i], 0.0f));
+            }
+        }
+    }
+}
+
+} // namespace sv
