@@ -708,7 +708,9 @@ template <bool VEC> cudaError_t norm_launch(const sv::NormParams &P, int nseg, u
     return cudaGetLastError();
 }
 
-static_assert(sv::kElemBf16 == SV_BF16 && sv::kElemFp32 == SV_FP32 && sv::kElemE4m3 == SV_E4M3, "element types");
+static_assert(int(sv::kElemBf16) == int(SV_BF16) && int(sv::kElemFp32) == int(SV_FP32) &&
+                  int(sv::kElemE4m3) == int(SV_E4M3),
+              "element types");
 static_assert(sv::kNormMaxWarps * sv::kNormMaxSegs * sv::kSeg == SV_MAX_D, "widest row of the norms");
 
 static_assert(sv::kTreeMaxNodes == SV_MAX_TREE_NODES, "tree size limit");

@@ -22,9 +22,9 @@
 //
 // Warp 0 loads (2-D tensor-memory-accelerator boxes of 128 hidden dims, one
 // 128-byte swizzle row each), warp 1 allocates tensor memory and issues the
-// MMAs, warps 2..9 hold the accumulators: warp w owns the 32 rows of
-// tensor-memory lane quarter w mod 4 and the first (w < 6) or the other
-// columns of the tile from 128 on.  Every wait is bounded as in
+// MMAs, warps 4..11 hold the accumulators: warp w owns the 32 rows of
+// tensor-memory lane quarter w mod 4 and the first 128 columns of the tile
+// (w < 8) or the others.  Every wait is bounded as in
 // lm_head_kernel, with the same teardown.
 #pragma once
 
@@ -36,7 +36,11 @@ constexpr int kL8BK = 128;    // hidden dims per step: one scale block, one swiz
 constexpr int kL8MaxNB = 256; // ids per tile
 constexpr int kL8ABytes = kLmBM * kL8BK;
 constexpr int kL8EpiWarps = 8;
-constexpr int kL8Threads = 64 + 32 * kL8EpiWarps;
+constexpr int kL8Threads = 128 + 32 * kL8EpiWarps;
+// Registers a thread: 168 at launch (64,512 in all); the accumulators' two
+// warpgroups then take 224 and the first warpgroup keeps 40 (62,464).
+constexpr int kL8AccRegs = 224, kL8OtherRegs = 40;
+static_assert(32 * kL8EpiWarps * kL8AccRegs + 128 * kL8OtherRegs <= 168 * kL8Threads, "register split");
 constexpr uint32_t kL8TmemCols = 2 * kL8MaxNB; // two fp32 sums of one step: all 512 columns
 
 template <bool PAIR> struct L8Shape {
@@ -126,6 +130,15 @@ template <bool PAIR> __device__ __forceinline__ void l8_cluster_sync()
         lm_cluster_sync();
     else
         __syncthreads();
+}
+
+// One arrival on a barrier of the leader CTA, behind this warp's reads of
+// tensor memory (tcgen05.wait::ld and the fence order those).  CTA scope: a
+// cluster-scope release waits for every load and store of the warp that is
+// still in flight, on each step.
+__device__ __forceinline__ void l8_arrive(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 // Instruction descriptor: D fp32, A and B e4m3 (format 0), both K-major.
@@ -227,75 +240,80 @@ __global__ void __launch_bounds__(kL8Threads, 1)
         }
     };
 
-    if (warp == 0 && lane == 0) {
-        int s = 0;
-        uint32_t ph = 0;
-        int64_t it = 0;
-        const uint32_t fb0 = PAIR ? lm_mapa(smem_addr(&full[0]), 0) : smem_addr(&full[0]);
-        const uint32_t sbase = smem_addr(smem);
-        const int brows = P.NB / Sh::kCtas; // ids of the tile this CTA loads
-        const uint32_t bytes = static_cast<uint32_t>(Sh::kCtas * (kL8ABytes + brows * kL8BK));
-        for (int64_t t = unit; t < ntiles && !*vstop; t += units) {
-            const int m0 = (static_cast<int>(t % P.MT) * Sh::kCtas + static_cast<int>(rank)) * kLmBM;
-            const int n0 = static_cast<int>(t / P.MT) * P.NB + static_cast<int>(rank) * brows;
-            int kb = 0;
-            for (; kb < P.KB; ++kb, ++it) {
-                if (it >= Sh::kStages && !lm_wait(smem_addr(&empty[s]), ph ^ 1u, vstop, P.wait_ns)) {
-                    fail();
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kL8OtherRegs));
+        if (warp == 0 && lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            int64_t it = 0;
+            const uint32_t fb0 = PAIR ? lm_mapa(smem_addr(&full[0]), 0) : smem_addr(&full[0]);
+            const uint32_t sbase = smem_addr(smem);
+            const int brows = P.NB / Sh::kCtas; // ids of the tile this CTA loads
+            const uint32_t bytes = static_cast<uint32_t>(Sh::kCtas * (kL8ABytes + brows * kL8BK));
+            for (int64_t t = unit; t < ntiles && !*vstop; t += units) {
+                const int m0 = (static_cast<int>(t % P.MT) * Sh::kCtas + static_cast<int>(rank)) * kLmBM;
+                const int n0 = static_cast<int>(t / P.MT) * P.NB + static_cast<int>(rank) * brows;
+                int kb = 0;
+                for (; kb < P.KB; ++kb, ++it) {
+                    if (it >= Sh::kStages && !lm_wait(smem_addr(&empty[s]), ph ^ 1u, vstop, P.wait_ns)) {
+                        fail();
+                        break;
+                    }
+                    const uint32_t sa = sbase + static_cast<uint32_t>(s * Sh::kStageBytes);
+                    const uint32_t fb = fb0 + static_cast<uint32_t>(s * 8);
+                    if (leader)
+                        lm_mbar_expect(smem_addr(&full[s]), bytes);
+                    l8_tma_2d<PAIR>(sa, &tmA, kb * kL8BK, m0, fb);
+                    l8_tma_2d<PAIR>(sa + kL8ABytes, &tmB, kb * kL8BK, n0, fb);
+                    if (++s == Sh::kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (kb < P.KB)
                     break;
-                }
-                const uint32_t sa = sbase + static_cast<uint32_t>(s * Sh::kStageBytes);
-                const uint32_t fb = fb0 + static_cast<uint32_t>(s * 8);
-                if (leader)
-                    lm_mbar_expect(smem_addr(&full[s]), bytes);
-                l8_tma_2d<PAIR>(sa, &tmA, kb * kL8BK, m0, fb);
-                l8_tma_2d<PAIR>(sa + kL8ABytes, &tmB, kb * kL8BK, n0, fb);
-                if (++s == Sh::kStages) {
-                    s = 0;
-                    ph ^= 1u;
-                }
             }
-            if (kb < P.KB)
-                break;
-        }
-    } else if (warp == 1 && lane == 0 && leader) {
-        const uint64_t ad0 = lm_desc(smem_addr(smem)), bd0 = lm_desc(smem_addr(smem + kL8ABytes));
-        int s = 0;
-        uint32_t ph = 0;
-        int64_t it = 0; // steps so far: step `it` forms its sums in tensor-memory half it mod 2
-        for (int64_t t = unit; t < ntiles && !*vstop; t += units) {
-            int kb = 0;
-            for (; kb < P.KB; ++kb, ++it) {
-                const int acc = static_cast<int>(it & 1);
-                if ((it >= 2 && !lm_wait(smem_addr(&tempty[acc]), static_cast<uint32_t>(((it >> 1) & 1) ^ 1), vstop,
-                                         P.wait_ns)) ||
-                    !lm_wait(smem_addr(&full[s]), ph, vstop, P.wait_ns)) {
-                    fail();
-                    break;
-                }
-                lm_tc_after();
-                const uint32_t tacc = tbase + static_cast<uint32_t>(acc * kL8MaxNB);
-                const uint64_t so = static_cast<uint64_t>((s * Sh::kStageBytes) >> 4);
+        } else if (warp == 1 && lane == 0 && leader) {
+            const uint64_t ad0 = lm_desc(smem_addr(smem)), bd0 = lm_desc(smem_addr(smem + kL8ABytes));
+            int s = 0;
+            uint32_t ph = 0;
+            int64_t it = 0; // steps so far: step `it` forms its sums in tensor-memory half it mod 2
+            for (int64_t t = unit; t < ntiles && !*vstop; t += units) {
+                int kb = 0;
+                for (; kb < P.KB; ++kb, ++it) {
+                    const int acc = static_cast<int>(it & 1);
+                    if ((it >= 2 && !lm_wait(smem_addr(&tempty[acc]), static_cast<uint32_t>(((it >> 1) & 1) ^ 1), vstop,
+                                             P.wait_ns)) ||
+                        !lm_wait(smem_addr(&full[s]), ph, vstop, P.wait_ns)) {
+                        fail();
+                        break;
+                    }
+                    lm_tc_after();
+                    const uint32_t tacc = tbase + static_cast<uint32_t>(acc * kL8MaxNB);
+                    const uint64_t so = static_cast<uint64_t>((s * Sh::kStageBytes) >> 4);
 #pragma unroll
-                for (int k = 0; k < kL8BK / 32; ++k)
-                    l8_mma<PAIR>(tacc, ad0 + so + static_cast<uint64_t>(k * 2), bd0 + so + static_cast<uint64_t>(k * 2),
-                                 P.idesc, k ? 1u : 0u);
-                l8_commit<PAIR>(smem_addr(&empty[s]));
-                l8_commit<PAIR>(smem_addr(&tfull[acc]));
-                if (++s == Sh::kStages) {
-                    s = 0;
-                    ph ^= 1u;
+                    for (int k = 0; k < kL8BK / 32; ++k)
+                        l8_mma<PAIR>(tacc, ad0 + so + static_cast<uint64_t>(k * 2), bd0 + so + static_cast<uint64_t>(k * 2),
+                                     P.idesc, k ? 1u : 0u);
+                    l8_commit<PAIR>(smem_addr(&empty[s]));
+                    l8_commit<PAIR>(smem_addr(&tfull[acc]));
+                    if (++s == Sh::kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
+                if (kb < P.KB)
+                    break;
             }
-            if (kb < P.KB)
-                break;
         }
-    } else if (warp >= 2) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kL8AccRegs));
         const int lq = warp & 3;
-        const int half = warp >= 6 ? 1 : 0;
+        const int half = warp >= 8 ? 1 : 0;
         const uint32_t tl0 = tbase + (static_cast<uint32_t>(lq * 32) << 16) + static_cast<uint32_t>(half * 128);
         const int mycols = P.NB - half * 128 < 128 ? P.NB - half * 128 : 128; // <= 0: nothing in this half
         const int wblocks = (P.N + 127) / 128;
+        const uint32_t tempty0 = PAIR ? lm_mapa(smem_addr(&tempty[0]), 0) : smem_addr(&tempty[0]);
         int64_t it = 0;
         bool ok = true;
         for (int64_t t = unit; t < ntiles && ok; t += units) {
@@ -315,14 +333,25 @@ __global__ void __launch_bounds__(kL8Threads, 1)
 #pragma unroll
             for (int i = 0; i < 128; ++i)
                 acc[i] = 0.0f;
+            // a step's scales are loaded one step ahead
+            float hn = 0.0f, wn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (work) {
+                hn = __ldg(hs);
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    wn[g] = __ldg(ws[g]);
+            }
             for (int kb = 0; kb < P.KB; ++kb, ++it) {
                 const int a = static_cast<int>(it & 1);
-                float h = 0.0f, w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (work) { // on their way while the tensor cores finish the step
-                    h = __ldg(hs + kb);
+                float f[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    f[g] = __fmul_rn(hn, wn[g]);
+                if (work && kb + 1 < P.KB) {
+                    hn = __ldg(hs + kb + 1);
 #pragma unroll
                     for (int g = 0; g < 4; ++g)
-                        w[g] = __ldg(ws[g] + kb);
+                        wn[g] = __ldg(ws[g] + kb + 1);
                 }
                 ok = __all_sync(0xFFFFFFFFu, lm_wait(smem_addr(&tfull[a]), static_cast<uint32_t>((it >> 1) & 1), vstop,
                                                      P.wait_ns));
@@ -339,16 +368,15 @@ __global__ void __launch_bounds__(kL8Threads, 1)
                         if (g * 32 < mycols) {
                             uint32_t v[32];
                             lm_tmem_ld32(tl + g * 32, v);
-                            const float f = h * w[g];
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                acc[g * 32 + i] = __fmaf_rn(__uint_as_float(v[i]), f, acc[g * 32 + i]);
+                                acc[g * 32 + i] = __fmaf_rn(__uint_as_float(v[i]), f[g], acc[g * 32 + i]);
                         }
                 }
                 lm_tc_before();
                 __syncwarp();
                 if (lane == 0) // this warp has read the step's sums
-                    lm_mbar_arrive_cluster(PAIR ? lm_mapa(smem_addr(&tempty[a]), 0) : smem_addr(&tempty[a]));
+                    l8_arrive(tempty0 + static_cast<uint32_t>(a * 8));
             }
             if (ok && work && row < P.M) {
                 int ncols = P.N - n;
