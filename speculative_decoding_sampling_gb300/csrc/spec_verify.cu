@@ -506,8 +506,10 @@ Lm8Plan lm8_plan(int64_t M, int32_t V)
     p.MT = static_cast<int32_t>(ceil_div(M > 0 ? M : 1, rows));
     // ids per tile: the width whose last wave of tiles wastes least (a tile
     // costs its ids plus about 16 for its start and end); the widest on ties
+    const int32_t step = p.pair ? 64 : 32;
     int64_t best = INT64_MAX;
-    for (int32_t nb = sv::kL8MaxNB; nb >= 32; nb -= 32) {
+    p.NB = sv::kL8MaxNB;
+    for (int32_t nb = sv::kL8MaxNB; nb >= step; nb -= step) {
         const int64_t cost = ceil_div(p.MT * ceil_div(V, nb), units) * (nb + 16);
         if (cost < best) {
             best = cost;
@@ -531,6 +533,9 @@ sv_status_t lm8_check(const void *hidden, const float *hidden_scales, const void
     if (M < 0 || d < 16 || d % 16 != 0 || V < 1)
         return SV_EINVAL;
     if (V > SV_MAX_V || M > kLmMaxRows)
+        return SV_EUNSUPPORTED;
+    const Lm8Plan p = lm8_plan(M, V);
+    if (static_cast<int64_t>(p.MT) * p.NT > INT32_MAX)
         return SV_EUNSUPPORTED;
     if (M > 0 && (!hidden || !hidden_scales || !lm_head || !lm_head_scales || !logits || !aligned(hidden, 16) ||
                   !aligned(lm_head, 16) || !aligned(hidden_scales, 4) || !aligned(lm_head_scales, 4) ||
@@ -558,7 +563,7 @@ template <bool PAIR> cudaError_t lm8_units(int &units)
     const unsigned long long ctx = current_context_id();
     std::lock_guard<std::mutex> lock(mu);
     if (cache[dev].units == 0 || cache[dev].ctx == 0 || cache[dev].ctx != ctx) {
-        constexpr int smem = sv::L8Shape<PAIR>::kSmem;
+        constexpr int smem = sv::kL8Smem;
         e = cudaFuncSetAttribute(sv::lm_head_fp8_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess)
             return e;
@@ -600,17 +605,17 @@ cudaError_t lm8_launch_as(const CUtensorMap &ta, const CUtensorMap &tb, const sv
     const cudaError_t e = lm8_units<PAIR>(units);
     if (e != cudaSuccess)
         return e;
-    const int64_t tiles = static_cast<int64_t>(L.MT) * L.NT;
+    const int64_t tiles = static_cast<int64_t>(L.MT) * L.NT; // below 2^31 (lm8_check)
     const int64_t n = tiles < units ? tiles : units;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = sv::L8Shape<PAIR>::kCtas;
+    attr[0].val.clusterDim.x = (PAIR ? 2 : 1);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(n * sv::L8Shape<PAIR>::kCtas));
+    cfg.gridDim = dim3(static_cast<unsigned>(n * (PAIR ? 2 : 1)));
     cfg.blockDim = dim3(sv::kL8Threads);
-    cfg.dynamicSmemBytes = sv::L8Shape<PAIR>::kSmem;
+    cfg.dynamicSmemBytes = sv::kL8Smem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -623,18 +628,31 @@ cudaError_t lm8_launch(const void *hidden, const float *hidden_scales, const voi
                        cudaStream_t stream)
 {
     const Lm8Plan p = lm8_plan(M, V);
-    CUtensorMap ta, tb;
-    if (!lm_tensor_map(&ta, hidden, M, d, sv::kLmBM, true) ||
-        !lm_tensor_map(&tb, lm_head, V, d, static_cast<uint32_t>(p.pair ? p.NB / 2 : p.NB), true))
-        return cudaErrorInvalidValue;
+    const int32_t brows = p.pair ? p.NB / 2 : p.NB; // ids of a tile that one CTA loads
     sv::Lm8Params L;
+    // A stage holds the rows of h that exist, in 32s: the MMA's 128 rows then
+    // run on into the stage's ids, and the sums of those rows are not read.
+    // (Only where that leaves 128 rows in the stage.)
+    L.a_rows = static_cast<int32_t>(M < sv::kLmBM ? ceil_div(M, 32) * 32 : sv::kLmBM);
+    if (L.a_rows + brows < sv::kLmBM)
+        L.a_rows = sv::kLmBM;
+    L.stage_bytes = (L.a_rows + brows) * sv::kL8BK;
+    L.stages = sv::kL8RingBytes / L.stage_bytes;
+    if (L.stages > sv::kL8MaxStages)
+        L.stages = sv::kL8MaxStages;
+    CUtensorMap ta, tb;
+    if (!lm_tensor_map(&ta, hidden, M, d, static_cast<uint32_t>(L.a_rows), true) ||
+        !lm_tensor_map(&tb, lm_head, V, d, static_cast<uint32_t>(brows), true))
+        return cudaErrorInvalidValue;
     L.M = static_cast<int32_t>(M);
     L.N = V;
     L.KB = static_cast<int32_t>(ceil_div(d, sv::kL8BK));
     L.MT = p.MT;
     L.NT = p.NT;
     L.NB = p.NB;
-    L.idesc = sv::l8_idesc(p.pair ? 2 * sv::kLmBM : sv::kLmBM, p.NB);
+    const int mma_rows = p.pair ? 2 * sv::kLmBM : sv::kLmBM;
+    L.idesc[0] = sv::l8_idesc(mma_rows, p.NB < 128 ? p.NB : 128);
+    L.idesc[1] = sv::l8_idesc(mma_rows, p.NB - 128); // read only when NB > 128
     L.hs = hidden_scales;
     L.ws = lm_head_scales;
     L.logits = static_cast<uint16_t *>(logits);
@@ -643,7 +661,6 @@ cudaError_t lm8_launch(const void *hidden, const float *hidden_scales, const voi
     L.c = c;
     L.vec = (V % 8 == 0 && aligned(logits, 16)) ? 1 : 0;
     L.status = status;
-    L.wait_ns = kWaitLimitNs;
     return p.pair ? lm8_launch_as<true>(ta, tb, L, stream) : lm8_launch_as<false>(ta, tb, L, stream);
 }
 

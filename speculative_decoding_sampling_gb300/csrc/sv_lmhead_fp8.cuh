@@ -9,8 +9,7 @@
 // (tcgen05, kind f8f6f4) into tensor memory; the scales differ from block to
 // block and are not powers of two, so each block's sums are read back and
 // folded into fp32 accumulators in registers: one fp32 multiply-add per logit
-// and block, while the tensor cores form the next block in the other half of
-// tensor memory.
+// and block, while the tensor cores form the next block's sums.
 //
 // Two shapes of one kernel.  PAIR false (M <= 128): a CTA per SM, tiles of
 // 128 rows x NB ids; few rows leave the tensor cores idle most of the time
@@ -21,11 +20,17 @@
 // running at one time share a few tiles of W.
 //
 // Warp 0 loads (2-D tensor-memory-accelerator boxes of 128 hidden dims, one
-// 128-byte swizzle row each), warp 1 allocates tensor memory and issues the
-// MMAs, warps 4..11 hold the accumulators: warp w owns the 32 rows of
-// tensor-memory lane quarter w mod 4 and the first 128 columns of the tile
-// (w < 8) or the others.  Every wait is bounded as in
-// lm_head_kernel, with the same teardown.
+// 128-byte swizzle row each); warps 1 and 2 issue the MMAs.  A step (128
+// hidden dims) is two MMA groups, the first 128 columns of the tile (warp 1)
+// and the rest (warp 2), each with its own half of one of two tensor-memory
+// buffers and its own barriers: the sums of one half are read while the other
+// half is formed, and neither warp's waits and commits (a few hundred cycles a
+// step) hold up the other's MMAs.  Warp 3 brings the scales of 16 steps at a
+// time into shared memory.  Warps 4..11 hold the accumulators (32 rows x 128 columns a
+// warp, 128 registers a thread); they read the sums 64 columns ahead of the
+// multiply-adds, and hand a buffer back before its last ones.  A finished tile
+// goes through shared memory, so that the logits leave in whole sectors.
+// Every wait is bounded in time (l8_wait), with lm_head_kernel's teardown.
 #pragma once
 
 #include "sv_lmhead.cuh"
@@ -34,27 +39,29 @@ namespace sv {
 
 constexpr int kL8BK = 128;    // hidden dims per step: one scale block, one swizzle row
 constexpr int kL8MaxNB = 256; // ids per tile
-constexpr int kL8ABytes = kLmBM * kL8BK;
-constexpr int kL8EpiWarps = 8;
-constexpr int kL8Threads = 128 + 32 * kL8EpiWarps;
+constexpr int kL8AccWarps = 8;
+constexpr int kL8Threads = 128 + 32 * kL8AccWarps;
 // Registers a thread: 168 at launch (64,512 in all); the accumulators' two
-// warpgroups then take 224 and the first warpgroup keeps 40 (62,464).
-constexpr int kL8AccRegs = 224, kL8OtherRegs = 40;
-static_assert(32 * kL8EpiWarps * kL8AccRegs + 128 * kL8OtherRegs <= 168 * kL8Threads, "register split");
+// warpgroups then take 224 and the first warpgroup keeps 56 (64,512).
+constexpr int kL8AccRegs = 224, kL8OtherRegs = 56;
+static_assert(32 * kL8AccWarps * kL8AccRegs + 128 * kL8OtherRegs <= 168 * kL8Threads, "register split");
 constexpr uint32_t kL8TmemCols = 2 * kL8MaxNB; // two fp32 sums of one step: all 512 columns
-
-template <bool PAIR> struct L8Shape {
-    static constexpr int kCtas = PAIR ? 2 : 1;
-    static constexpr int kBBytes = kL8MaxNB / kCtas * kL8BK;
-    static constexpr int kStageBytes = kL8ABytes + kBBytes;
-    static constexpr int kStages = PAIR ? 6 : 4;
-    static constexpr int kSmem = kStages * kStageBytes + 1024; // + alignment of the swizzled tiles
-};
+constexpr int kL8MaxStages = 8;
+constexpr int kL8Chunk = 16;                                       // steps whose scales are brought in at a time
+constexpr int kL8HsPitch = kLmBM + 1;
+constexpr int kL8TabFloats = kL8Chunk * kL8HsPitch + kL8Chunk * 8; // [step][row], [step][32-column group]
+constexpr int kL8TabBytes = 2 * kL8TabFloats * 4;                  // two chunks
+constexpr int kL8StgBytes = 32 * 64;                               // 32 rows x 32 logits of a warp
+constexpr int kL8RingBytes = 192 * 1024;
+constexpr int kL8Smem = 1024 + kL8RingBytes + kL8TabBytes + kL8AccWarps * kL8StgBytes;
+static_assert(kL8Smem <= 227 * 1024 - 512, "shared memory of a CTA, less the barriers");
 
 struct Lm8Params {
     int32_t M, N, KB;       // rows of h, vocabulary, scale blocks along the hidden dims
-    int32_t MT, NT, NB;     // row tiles, id tiles, ids per tile (a multiple of 32)
-    uint32_t idesc;         // tcgen05 instruction descriptor
+    int32_t MT, NT, NB;     // row tiles, id tiles, ids per tile (a multiple of 32; of 64 on pairs)
+    int32_t a_rows;         // rows of h in a stage (128, or fewer when M is small)
+    int32_t stages, stage_bytes;
+    uint32_t idesc[2];      // tcgen05 instruction descriptors of the two column halves
     const float *hs;        // [M, KB]
     const float *ws;        // [ceil(N / 128), KB]
     uint16_t *logits;       // [M, N] bf16 out
@@ -63,7 +70,6 @@ struct Lm8Params {
     float c;                // log2(e) / T
     int32_t vec;            // N % 8 == 0 and 16-byte aligned logits: vector stores
     int32_t *status;
-    uint64_t wait_ns;
 };
 
 // ------------------------------------------------------------- primitives
@@ -141,6 +147,81 @@ __device__ __forceinline__ void l8_arrive(uint32_t cluster_bar)
     asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// Start loading 32 consecutive fp32 columns of this thread's lane; the values
+// are there after l8_ld_wait on them.
+__device__ __forceinline__ void l8_ld_start(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+}
+
+// Registers of a load that an earlier l8_ld_wait covered.
+__device__ __forceinline__ void l8_ld_tie(uint32_t (&r)[32])
+{
+    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                      "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                      "+r"(r[15]));
+    asm volatile("" : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                      "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                      "+r"(r[30]), "+r"(r[31]));
+}
+
+// Every load started before is done; the registers pass through, so no use of
+// them moves ahead of the wait.
+__device__ __forceinline__ void l8_ld_wait(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(r[30]), "+r"(r[31]));
+}
+
+// One lane of the warp, the same one each time.
+__device__ __forceinline__ bool l8_elect()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Wait for phase `parity` of `bar`: true once it is complete, false after
+// kL8Tries tries, each of which the hardware may suspend for about a
+// microsecond (about a second in all; far less than one step takes if they
+// are not suspended at all would still be 10 ms).  One loop without calls or
+// clock reads: the issuing warps wait several times a step.
+constexpr uint32_t kL8Tries = 1u << 20;
+__device__ __forceinline__ bool l8_wait(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .u32 n;\n\t"
+                 "mov.u32 n, %3;\n\t"
+                 "L8_TRY:\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+                 "@p bra L8_DONE;\n\t"
+                 "sub.u32 n, n, 1;\n\t"
+                 "setp.ne.u32 p, n, 0;\n\t"
+                 "@p bra L8_TRY;\n\t"
+                 "L8_DONE:\n\t"
+                 "setp.ne.u32 p, n, 0;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity), "n"(kL8Tries)
+                 : "memory");
+    return ok != 0;
+}
+
 // Instruction descriptor: D fp32, A and B e4m3 (format 0), both K-major.
 inline uint32_t l8_idesc(int rows, int ids)
 {
@@ -149,47 +230,288 @@ inline uint32_t l8_idesc(int rows, int ids)
 
 // ------------------------------------------------------------- the kernel
 
-// A finished half tile: this lane's row, columns n .. n + 127 of the
-// vocabulary (ncols of them inside it), from the fp32 accumulators.
-__device__ __forceinline__ void l8_store(const Lm8Params &P, const float (&acc)[128], int row, int n, int ncols,
-                                         int slot)
+__device__ __forceinline__ uint32_t l8_round(unsigned long long pair)
 {
-    uint16_t *lrow = P.logits + static_cast<int64_t>(row) * P.N + n;
-    float mx = -INFINITY;
+    float lo, hi;
+    unpack2(pair, lo, hi);
+    return bf16_rn_pair(lo, hi);
+}
+
+// ------------------------------------------------------------- the kernel
+
+// Columns of column half h of a tile.
+__device__ __forceinline__ int l8_half_cols(int NB, int h)
+{
+    return h == 0 ? (NB < 128 ? NB : 128) : (NB > 128 ? NB - 128 : 0);
+}
+
+// First id, relative to the tile's, of the 32 columns from column j of half h
+// on.  On a pair a half's columns are the even CTA's rows of W, then the odd
+// one's, whose rows begin at NB / 2.
+template <bool PAIR> __device__ __forceinline__ int l8_group_id(int NB, int h, int j)
+{
+    if constexpr (!PAIR)
+        return h * 128 + j;
+    const int own = l8_half_cols(NB, h) / 2;
+    return j < own ? h * 64 + j : NB / 2 + h * 64 + j - own;
+}
+
+// 32 finished columns (ids n .. n + 31, ncols of them in the vocabulary) of a
+// warp's 32 rows from the packed logits of this lane's row: through the
+// warp's shared memory (16-byte pieces, swizzled so that neither side
+// conflicts), then out in whole 64-byte rows.
+__device__ __forceinline__ void l8_store(const Lm8Params &P, uint8_t *stg, const uint32_t (&pk)[16], int row0, int n,
+                                         int ncols, int lane)
+{
+    __syncwarp();
 #pragma unroll
-    for (int g = 0; g < 16; ++g) {
-        uint32_t pk[4];
+    for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4 *>(stg + lane * 64 + ((q ^ (lane >> 1)) & 3) * 16) =
+            make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+    __syncwarp();
+    if (P.vec && ncols == 32) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int col = g * 8 + 2 * i;
-            pk[i] = bf16_rn_pair(acc[col], acc[col + 1]);
-            if (col < ncols)
-                mx = fmaxf(mx, bf16_lo(pk[i]));
-            if (col + 1 < ncols)
-                mx = fmaxf(mx, bf16_hi(pk[i]));
+        for (int r = 0; r < 4; ++r) {
+            const int rl = r * 8 + (lane >> 2), q = lane & 3;
+            if (row0 + rl < P.M)
+                *reinterpret_cast<uint4 *>(P.logits + static_cast<int64_t>(row0 + rl) * P.N + n + q * 8) =
+                    *reinterpret_cast<const uint4 *>(stg + rl * 64 + ((q ^ (rl >> 1)) & 3) * 16);
         }
-        if (P.vec && g * 8 + 8 <= ncols) {
-            *reinterpret_cast<uint4 *>(lrow + g * 8) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        } else {
+    } else if (lane < ncols) {
+        const int q = lane >> 3, e = (lane & 7) * 2;
+        for (int rl = 0; rl < 32 && row0 + rl < P.M; ++rl)
+            P.logits[static_cast<int64_t>(row0 + rl) * P.N + n + lane] =
+                *reinterpret_cast<const uint16_t *>(stg + rl * 64 + ((q ^ (rl >> 1)) & 3) * 16 + e);
+    }
+}
+
+// This thread's index, read anew each time: what only a tile's end needs is
+// then not kept in registers through its steps.
+__device__ __forceinline__ uint32_t l8_tid()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ float l8_lds(uint32_t addr)
+{
+    float r;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(addr) : "memory");
+    return r;
+}
+
+__device__ __forceinline__ float2 l8_lds2(uint32_t addr)
+{
+    float2 r;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(addr) : "memory");
+    return r;
+}
+
+// How many tiles a unit has.
+__device__ __forceinline__ uint32_t l8_tiles(uint32_t unit, uint32_t units, uint32_t ntiles)
+{
+    return unit < ntiles ? (ntiles - unit - 1) / units + 1 : 0;
+}
+
+// First row of lane quarter lq of tile t.
+template <bool PAIR>
+__device__ __forceinline__ int l8_row0(const Lm8Params &P, uint32_t t, uint32_t rank, int lq)
+{
+    return static_cast<int>((t % static_cast<uint32_t>(P.MT) * (PAIR ? 2u : 1u) + rank) * kLmBM) + lq * 32;
+}
+
+__device__ __forceinline__ void l8_fail(const Lm8Params &P, int *stop)
+{
+    if (!*static_cast<volatile int *>(stop)) {
+        *static_cast<volatile int *>(stop) = 1;
+        if (P.status)
+            atomicOr(P.status, kTimeout);
+    }
+}
+
+// The scales: step kb's row scales and those of the tile's eight 32-column
+// groups, 16 steps at a time, two chunks in flight.
+template <bool PAIR>
+__device__ __forceinline__ void l8_scales(const Lm8Params &P, float *tab, uint32_t sfull, uint32_t sempty, int *stop,
+                                          uint32_t rank, uint32_t unit, uint32_t units, uint32_t ntiles, int lane)
+{
+    const int k = lane & (kL8Chunk - 1), sub = lane >> 4; // step, and which of 2 rows
+    uint32_t chunk = 0;
+    for (uint32_t t = unit; t < ntiles; t += units) {
+        const int m0 = static_cast<int>((t % static_cast<uint32_t>(P.MT) * (PAIR ? 2u : 1u) + rank) * kLmBM);
+        const int n0 = static_cast<int>(t / static_cast<uint32_t>(P.MT)) * P.NB;
+        const int rows = P.M - m0 < kLmBM ? P.M - m0 : kLmBM;
+        for (int kb0 = 0; kb0 < P.KB; kb0 += kL8Chunk, ++chunk) {
+            const uint32_t b = chunk & 1u;
+            if (chunk >= 2 && !__all_sync(0xFFFFFFFFu, l8_wait(sempty + b * 8, ((chunk >> 1) & 1u) ^ 1u))) {
+                if (lane == 0)
+                    l8_fail(P, stop);
+                return;
+            }
+            if (kb0 + k < P.KB) {
+                float *dst = tab + b * kL8TabFloats + k * kL8HsPitch;
+                const float *src = P.hs + static_cast<int64_t>(m0) * P.KB + kb0 + k;
+#pragma unroll 8
+                for (int r = sub; r < rows; r += 2)
+                    dst[r] = __ldg(src + static_cast<int64_t>(r) * P.KB);
+                float *wd = tab + b * kL8TabFloats + kL8Chunk * kL8HsPitch + k * 8;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (g * 8 + i < ncols)
-                    lrow[g * 8 + i] = static_cast<uint16_t>(i & 1 ? pk[i >> 1] >> 16 : pk[i >> 1] & 0xFFFFu);
+                for (int g = sub; g < 8; g += 2) {
+                    const int n = n0 + l8_group_id<PAIR>(P.NB, g >> 2, (g & 3) * 32);
+                    wd[g] = (g & 3) * 32 < l8_half_cols(P.NB, g >> 2) && n < P.N
+                                ? __ldg(P.ws + static_cast<int64_t>(n >> 7) * P.KB + kb0 + k)
+                                : 0.0f;
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                l8_arrive(sfull + b * 8);
         }
     }
-    if (!P.part)
+}
+
+// acc += f * the 32 columns in v
+__device__ __forceinline__ void l8_fold(unsigned long long *acc, const uint32_t (&v)[32], float f)
+{
+    const unsigned long long ff = pack2(f, f);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        acc[i] = fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), ff, acc[i]);
+}
+
+// The accumulator warps: warp w (from 4 on) holds the tile's rows of
+// tensor-memory lane quarter w mod 4 and column half (w - 4) / 4.
+template <bool PAIR>
+__device__ __forceinline__ void l8_accumulate(const Lm8Params &P, uint32_t tabs, uint8_t *stgs, uint32_t tbase,
+                                              uint32_t tfull, uint32_t tempty, uint32_t sfull, uint32_t sempty,
+                                              int *stop, uint32_t rank, uint32_t unit, uint32_t units, uint32_t ntiles)
+{
+    const int warp = static_cast<int>(l8_tid() >> 5), lane = static_cast<int>(l8_tid() & 31u);
+    const int h = (warp - 4) >> 2, lq = warp & 3;
+    const int groups = l8_half_cols(P.NB, h) / 32; // 32-column groups of this half: 0..4
+    if (groups == 0)
         return;
-    const float mc = mc_of(mx, P.c);
-    float S = 0.0f;
+    const uint32_t tl0 = tbase + (static_cast<uint32_t>(lq) << 21) + static_cast<uint32_t>(h * 128);
+    tfull += static_cast<uint32_t>(h) * 8u;
+    tempty = (PAIR ? lm_mapa(tempty, 0) : tempty) + static_cast<uint32_t>(h) * 8u;
+    uint32_t it = 0, chunk = 0;
+    for (uint32_t t = unit; t < ntiles; t += units) {
+        const int G = l8_row0<PAIR>(P, t, rank, lq) < P.M ? groups : 0; // groups this warp folds
+        unsigned long long acc[64];            // pairs of fp32 sums
 #pragma unroll
-    for (int col = 0; col < 128; col += 2) {
-        const uint32_t pk = bf16_rn_pair(acc[col], acc[col + 1]);
-        if (col < ncols)
-            S += term(bf16_lo(pk), P.c, mc);
-        if (col + 1 < ncols)
-            S += term(bf16_hi(pk), P.c, mc);
+        for (int i = 0; i < 64; ++i)
+            acc[i] = 0;
+        for (int kb0 = 0; kb0 < P.KB; kb0 += kL8Chunk, ++chunk) {
+            const uint32_t sb = chunk & 1u;
+            if (!__all_sync(0xFFFFFFFFu, l8_wait(sfull + sb * 8, (chunk >> 1) & 1u))) {
+                if (lane == 0)
+                    l8_fail(P, stop);
+                return;
+            }
+            uint32_t hsp = tabs + (sb * kL8TabFloats + static_cast<uint32_t>(lq * 32 + lane)) * 4u;
+            uint32_t wsp = tabs + (sb * kL8TabFloats + kL8Chunk * kL8HsPitch + static_cast<uint32_t>(h * 4)) * 4u;
+            const int steps = P.KB - kb0 < kL8Chunk ? P.KB - kb0 : kL8Chunk;
+#pragma unroll 1
+            for (int k = 0; k < steps; ++k, ++it, hsp += kL8HsPitch * 4, wsp += 32) {
+                const float hs = l8_lds(hsp);
+                float2 ws = l8_lds2(wsp);
+                const uint32_t b = it & 1u;
+                if (!__all_sync(0xFFFFFFFFu, l8_wait(tfull + b * 16, (it >> 1) & 1u))) {
+                    if (lane == 0)
+                        l8_fail(P, stop);
+                    return;
+                }
+                lm_tc_after();
+                const uint32_t tl = tl0 + b * kL8MaxNB;
+                auto release = [&]() { // this warp has read the step's sums
+                    lm_tc_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        l8_arrive(tempty + b * 16);
+                };
+                uint32_t v0[32], v1[32];
+                if (G == 0) {
+                    release();
+                    continue;
+                }
+                l8_ld_start(tl, v0);
+                if (G > 1)
+                    l8_ld_start(tl + 32, v1);
+                l8_ld_wait(v0);
+                if (G > 1)
+                    l8_ld_tie(v1);
+                if (G <= 2)
+                    release();
+                l8_fold(acc, v0, __fmul_rn(hs, ws.x));
+                if (G > 2)
+                    l8_ld_start(tl + 64, v0);
+                if (G > 1)
+                    l8_fold(acc + 16, v1, __fmul_rn(hs, ws.y));
+                if (G > 2) {
+                    if (G > 3)
+                        l8_ld_start(tl + 96, v1);
+                    ws = l8_lds2(wsp + 8);
+                    l8_ld_wait(v0);
+                    if (G > 3)
+                        l8_ld_tie(v1);
+                    release();
+                    l8_fold(acc + 32, v0, __fmul_rn(hs, ws.x));
+                    if (G > 3)
+                        l8_fold(acc + 48, v1, __fmul_rn(hs, ws.y));
+                }
+            }
+            __syncwarp();
+            if (lane == 0) // this warp has read the chunk's scales
+                l8_arrive(sempty + sb * 8);
+        }
+        if (G == 0)
+            continue;
+        // ---- the finished half tile: logits and, per row, their statistics
+        const int warp = static_cast<int>(l8_tid() >> 5), lane = static_cast<int>(l8_tid() & 31u);
+        const int h = (warp - 4) >> 2, row0 = l8_row0<PAIR>(P, t, rank, warp & 3);
+        const int n0 = static_cast<int>(t / static_cast<uint32_t>(P.MT)) * P.NB;
+        uint8_t *stg = stgs + (warp - 4) * kL8StgBytes;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int n = n0 + l8_group_id<PAIR>(P.NB, h, 32 * g);
+            const int ncols = g < G ? (P.N - n < 32 ? P.N - n : 32) : 0;
+            if (ncols > 0) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    pk[i] = l8_round(acc[g * 16 + i]);
+                    if (2 * i < ncols)
+                        mx = fmaxf(mx, bf16_lo(pk[i]));
+                    if (2 * i + 1 < ncols)
+                        mx = fmaxf(mx, bf16_hi(pk[i]));
+                }
+                l8_store(P, stg, pk, row0, n, ncols, lane);
+            }
+        }
+        if (P.part) {
+            const float mc = mc_of(mx, P.c);
+            float S = 0.0f;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int n = n0 + l8_group_id<PAIR>(P.NB, h, 32 * g);
+                const int ncols = g < G ? P.N - n : 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint32_t pk = l8_round(acc[g * 16 + i]);
+                    if (2 * i < ncols)
+                        S += term(bf16_lo(pk), P.c, mc);
+                    if (2 * i + 1 < ncols)
+                        S += term(bf16_hi(pk), P.c, mc);
+                }
+            }
+            const int row = row0 + lane;
+            if (row < P.M)
+                P.part[static_cast<int64_t>(row) * (P.NT * P.halves) +
+                       static_cast<int>(t / static_cast<uint32_t>(P.MT)) * P.halves + h] = make_float2(mx, S);
+        }
     }
-    P.part[static_cast<int64_t>(row) * (P.NT * P.halves) + slot] = make_float2(mx, S);
 }
 
 // Unit u (a pair of SMs, or one) takes tiles u, u + units, ...; tile t covers
@@ -197,31 +519,36 @@ __device__ __forceinline__ void l8_store(const Lm8Params &P, const float (&acc)[
 template <bool PAIR>
 __global__ void __launch_bounds__(kL8Threads, 1)
     lm_head_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                       const Lm8Params P)
+                       const __grid_constant__ Lm8Params P)
 {
-    using Sh = L8Shape<PAIR>;
+    constexpr int kCtas = PAIR ? 2 : 1;
     extern __shared__ uint8_t lm_smem_raw[];
-    __shared__ __align__(8) unsigned long long full[Sh::kStages], empty[Sh::kStages], tfull[2], tempty[2], drain;
+    __shared__ __align__(8) unsigned long long full[kL8MaxStages], empty[kL8MaxStages], tfull[4], tempty[4],
+        sfull[2], sempty[2], drain;
     __shared__ uint32_t tmem_base;
     __shared__ int stop;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(lm_smem_raw) + 1023) & ~uintptr_t{1023});
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float *tab = reinterpret_cast<float *>(smem + kL8RingBytes);
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? lm_cluster_rank() : 0u;
     const bool leader = rank == 0;
-    const int64_t unit = blockIdx.x / Sh::kCtas, units = gridDim.x / Sh::kCtas;
-    const int64_t ntiles = static_cast<int64_t>(P.MT) * P.NT;
-    const volatile int *vstop = &stop;
+    const uint32_t unit = blockIdx.x / kCtas, units = gridDim.x / kCtas;
+    const uint32_t ntiles = static_cast<uint32_t>(P.MT) * static_cast<uint32_t>(P.NT);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < Sh::kStages; ++s) {
+        for (int s = 0; s < kL8MaxStages; ++s) {
             lm_mbar_init(smem_addr(&full[s]), 1);  // the leader's arrival with every CTA's bytes
-            lm_mbar_init(smem_addr(&empty[s]), 1); // the MMAs of the stage
+            lm_mbar_init(smem_addr(&empty[s]), static_cast<uint32_t>(P.halves)); // the MMAs of the stage
+        }
+        for (int a = 0; a < 4; ++a) { // buffer a / 2, column half a mod 2
+            lm_mbar_init(smem_addr(&tfull[a]), 1);
+            lm_mbar_init(smem_addr(&tempty[a]), kCtas * kL8AccWarps / 2);
         }
         for (int a = 0; a < 2; ++a) {
-            lm_mbar_init(smem_addr(&tfull[a]), 1);
-            lm_mbar_init(smem_addr(&tempty[a]), Sh::kCtas * kL8EpiWarps);
+            lm_mbar_init(smem_addr(&sfull[a]), 1);
+            lm_mbar_init(smem_addr(&sempty[a]), static_cast<uint32_t>(P.halves) * kL8AccWarps / 2);
         }
-        lm_mbar_init(smem_addr(&drain), 1);
+        lm_mbar_init(smem_addr(&drain), 2);
         stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -231,159 +558,94 @@ __global__ void __launch_bounds__(kL8Threads, 1)
     __syncthreads();
     l8_cluster_sync<PAIR>(); // every CTA's barriers exist before another CTA signals them
     lm_tc_after();
-    const uint32_t tbase = tmem_base;
-    auto fail = [&]() {
-        if (!stop) {
-            stop = 1;
-            if (P.status)
-                atomicOr(P.status, kTimeout);
-        }
-    };
-
+    const uint32_t tbase = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kL8OtherRegs));
-        if (warp == 0 && lane == 0) {
+        // Warps 0 and 1 run their loops as whole warps, so that addresses and
+        // descriptors stay in uniform registers; one lane issues.
+        if (warp == 0) {
             int s = 0;
             uint32_t ph = 0;
-            int64_t it = 0;
+            bool wrapped = false;
             const uint32_t fb0 = PAIR ? lm_mapa(smem_addr(&full[0]), 0) : smem_addr(&full[0]);
             const uint32_t sbase = smem_addr(smem);
-            const int brows = P.NB / Sh::kCtas; // ids of the tile this CTA loads
-            const uint32_t bytes = static_cast<uint32_t>(Sh::kCtas * (kL8ABytes + brows * kL8BK));
-            for (int64_t t = unit; t < ntiles && !*vstop; t += units) {
-                const int m0 = (static_cast<int>(t % P.MT) * Sh::kCtas + static_cast<int>(rank)) * kLmBM;
-                const int n0 = static_cast<int>(t / P.MT) * P.NB + static_cast<int>(rank) * brows;
-                int kb = 0;
-                for (; kb < P.KB; ++kb, ++it) {
-                    if (it >= Sh::kStages && !lm_wait(smem_addr(&empty[s]), ph ^ 1u, vstop, P.wait_ns)) {
-                        fail();
+            const int brows = P.NB / kCtas; // ids of the tile this CTA loads
+            const uint32_t bytes = static_cast<uint32_t>(kCtas * (P.a_rows + brows) * kL8BK);
+            bool ok = true;
+            for (uint32_t t = unit; t < ntiles && ok; t += units) {
+                const int m0 = static_cast<int>((t % static_cast<uint32_t>(P.MT) * kCtas + rank) * kLmBM);
+                const int n0 =
+                    static_cast<int>(t / static_cast<uint32_t>(P.MT)) * P.NB + static_cast<int>(rank) * brows;
+                for (int kb = 0; kb < P.KB; ++kb) {
+                    if (wrapped &&
+                        !__all_sync(0xFFFFFFFFu, l8_wait(smem_addr(&empty[s]), ph ^ 1u))) {
+                        ok = false;
                         break;
                     }
-                    const uint32_t sa = sbase + static_cast<uint32_t>(s * Sh::kStageBytes);
-                    const uint32_t fb = fb0 + static_cast<uint32_t>(s * 8);
-                    if (leader)
-                        lm_mbar_expect(smem_addr(&full[s]), bytes);
-                    l8_tma_2d<PAIR>(sa, &tmA, kb * kL8BK, m0, fb);
-                    l8_tma_2d<PAIR>(sa + kL8ABytes, &tmB, kb * kL8BK, n0, fb);
-                    if (++s == Sh::kStages) {
+                    if (l8_elect()) {
+                        const uint32_t sa = sbase + static_cast<uint32_t>(s * P.stage_bytes);
+                        const uint32_t fb = fb0 + static_cast<uint32_t>(s * 8);
+                        if (leader)
+                            lm_mbar_expect(smem_addr(&full[s]), bytes);
+                        l8_tma_2d<PAIR>(sa, &tmA, kb * kL8BK, m0, fb);
+                        l8_tma_2d<PAIR>(sa + static_cast<uint32_t>(P.a_rows * kL8BK), &tmB, kb * kL8BK, n0, fb);
+                    }
+                    __syncwarp();
+                    if (++s == P.stages) {
                         s = 0;
                         ph ^= 1u;
+                        wrapped = true;
                     }
                 }
-                if (kb < P.KB)
-                    break;
             }
-        } else if (warp == 1 && lane == 0 && leader) {
-            const uint64_t ad0 = lm_desc(smem_addr(smem)), bd0 = lm_desc(smem_addr(smem + kL8ABytes));
+            if (!ok && lane == 0)
+                l8_fail(P, &stop);
+        } else if (warp <= 2) {
+            const int h = warp - 1; // the column half this warp issues
+            const uint32_t idesc = h ? P.idesc[1] : P.idesc[0];
+            const uint64_t ad0 = lm_desc(smem_addr(smem));
+            const uint64_t bd0 = lm_desc(smem_addr(smem) + P.a_rows * kL8BK + h * (128 / kCtas * kL8BK));
+            const uint32_t steps = leader && h < P.halves ? l8_tiles(unit, units, ntiles) * P.KB : 0u;
             int s = 0;
             uint32_t ph = 0;
-            int64_t it = 0; // steps so far: step `it` forms its sums in tensor-memory half it mod 2
-            for (int64_t t = unit; t < ntiles && !*vstop; t += units) {
-                int kb = 0;
-                for (; kb < P.KB; ++kb, ++it) {
-                    const int acc = static_cast<int>(it & 1);
-                    if ((it >= 2 && !lm_wait(smem_addr(&tempty[acc]), static_cast<uint32_t>(((it >> 1) & 1) ^ 1), vstop,
-                                             P.wait_ns)) ||
-                        !lm_wait(smem_addr(&full[s]), ph, vstop, P.wait_ns)) {
-                        fail();
-                        break;
-                    }
-                    lm_tc_after();
-                    const uint32_t tacc = tbase + static_cast<uint32_t>(acc * kL8MaxNB);
-                    const uint64_t so = static_cast<uint64_t>((s * Sh::kStageBytes) >> 4);
-#pragma unroll
-                    for (int k = 0; k < kL8BK / 32; ++k)
-                        l8_mma<PAIR>(tacc, ad0 + so + static_cast<uint64_t>(k * 2), bd0 + so + static_cast<uint64_t>(k * 2),
-                                     P.idesc, k ? 1u : 0u);
-                    l8_commit<PAIR>(smem_addr(&empty[s]));
-                    l8_commit<PAIR>(smem_addr(&tfull[acc]));
-                    if (++s == Sh::kStages) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
-                }
-                if (kb < P.KB)
-                    break;
-            }
-        }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kL8AccRegs));
-        const int lq = warp & 3;
-        const int half = warp >= 8 ? 1 : 0;
-        const uint32_t tl0 = tbase + (static_cast<uint32_t>(lq * 32) << 16) + static_cast<uint32_t>(half * 128);
-        const int mycols = P.NB - half * 128 < 128 ? P.NB - half * 128 : 128; // <= 0: nothing in this half
-        const int wblocks = (P.N + 127) / 128;
-        const uint32_t tempty0 = PAIR ? lm_mapa(smem_addr(&tempty[0]), 0) : smem_addr(&tempty[0]);
-        int64_t it = 0;
-        bool ok = true;
-        for (int64_t t = unit; t < ntiles && ok; t += units) {
-            const int row0 = (static_cast<int>(t % P.MT) * Sh::kCtas + static_cast<int>(rank)) * kLmBM + lq * 32;
-            const int tn = static_cast<int>(t / P.MT);
-            const int n = tn * P.NB + half * 128;
-            const bool work = row0 < P.M && mycols > 0; // warp-uniform
-            const int row = row0 + lane;
-            const float *hs = P.hs + static_cast<int64_t>(row < P.M ? row : P.M - 1) * P.KB;
-            const float *ws[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int wb = (n + g * 32) / 128;
-                ws[g] = P.ws + static_cast<int64_t>(wb < wblocks ? wb : wblocks - 1) * P.KB;
-            }
-            float acc[128];
-#pragma unroll
-            for (int i = 0; i < 128; ++i)
-                acc[i] = 0.0f;
-            // a step's scales are loaded one step ahead
-            float hn = 0.0f, wn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (work) {
-                hn = __ldg(hs);
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    wn[g] = __ldg(ws[g]);
-            }
-            for (int kb = 0; kb < P.KB; ++kb, ++it) {
-                const int a = static_cast<int>(it & 1);
-                float f[4];
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    f[g] = __fmul_rn(hn, wn[g]);
-                if (work && kb + 1 < P.KB) {
-                    hn = __ldg(hs + kb + 1);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        wn[g] = __ldg(ws[g] + kb + 1);
-                }
-                ok = __all_sync(0xFFFFFFFFu, lm_wait(smem_addr(&tfull[a]), static_cast<uint32_t>((it >> 1) & 1), vstop,
-                                                     P.wait_ns));
-                if (!ok) {
-                    if (lane == 0)
-                        fail();
+            bool ok = true;
+            // step `it` forms its sums in tensor-memory buffer it mod 2
+            for (uint32_t it = 0; it < steps; ++it) {
+                const uint32_t b = it & 1u;
+                ok = l8_wait(smem_addr(&full[s]), ph);
+                if (it >= 2)
+                    ok = l8_wait(smem_addr(&tempty[2 * b + h]), ((it >> 1) & 1u) ^ 1u) && ok;
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
                     break;
                 }
                 lm_tc_after();
-                if (work) {
-                    const uint32_t tl = tl0 + static_cast<uint32_t>(a * kL8MaxNB);
+                const uint32_t tacc = tbase + b * kL8MaxNB + static_cast<uint32_t>(h * 128);
+                const uint64_t so = static_cast<uint64_t>((s * P.stage_bytes) >> 4);
+                if (l8_elect()) {
 #pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        if (g * 32 < mycols) {
-                            uint32_t v[32];
-                            lm_tmem_ld32(tl + g * 32, v);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                acc[g * 32 + i] = __fmaf_rn(__uint_as_float(v[i]), f[g], acc[g * 32 + i]);
-                        }
+                    for (int k = 0; k < kL8BK / 32; ++k)
+                        l8_mma<PAIR>(tacc, ad0 + so + static_cast<uint64_t>(k * 2),
+                                     bd0 + so + static_cast<uint64_t>(k * 2), idesc, k ? 1u : 0u);
+                    l8_commit<PAIR>(smem_addr(&tfull[2 * b + h]));
+                    l8_commit<PAIR>(smem_addr(&empty[s]));
                 }
-                lm_tc_before();
                 __syncwarp();
-                if (lane == 0) // this warp has read the step's sums
-                    l8_arrive(tempty0 + static_cast<uint32_t>(a * 8));
+                if (++s == P.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
             }
-            if (ok && work && row < P.M) {
-                int ncols = P.N - n;
-                ncols = ncols < 0 ? 0 : (ncols < mycols ? ncols : mycols);
-                l8_store(P, acc, row, n, ncols, tn * P.halves + half);
-            }
+            if (!ok && lane == 0)
+                l8_fail(P, &stop);
+        } else {
+            l8_scales<PAIR>(P, tab, smem_addr(&sfull[0]), smem_addr(&sempty[0]), &stop, rank, unit, units, ntiles, lane);
         }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kL8AccRegs));
+        l8_accumulate<PAIR>(P, smem_addr(tab), smem + kL8RingBytes + kL8TabBytes, tbase, smem_addr(&tfull[0]),
+                            smem_addr(&tempty[0]), smem_addr(&sfull[0]), smem_addr(&sempty[0]), &stop, rank, unit,
+                            units, ntiles);
     }
     // ---- teardown: copies and MMAs in flight complete before the memory goes
     lm_tc_before();
@@ -394,12 +656,12 @@ __global__ void __launch_bounds__(kL8Threads, 1)
             while (lm_ns() - t0 < 50000ull) {
             }
         }
-        if (warp == 1 && lane == 0 && leader) { // every MMA issued is done
+        if ((warp == 1 || warp == 2) && leader && l8_elect()) { // every MMA issued is done
             if constexpr (PAIR)
                 lm_commit_local(smem_addr(&drain));
             else
                 l8_commit<PAIR>(smem_addr(&drain));
-            (void)lm_wait(smem_addr(&drain), 0u, nullptr, P.wait_ns);
+            (void)l8_wait(smem_addr(&drain), 0u);
         }
     }
     __syncthreads();
