@@ -352,11 +352,12 @@ int32_t lm_tiles(int32_t V) { return static_cast<int32_t>(ceil_div(V, sv::kLmBN)
 size_t lm_part_bytes(int64_t M, int32_t V) { return align_up(static_cast<size_t>(M) * lm_tiles(V) * sizeof(float2)); }
 
 // A 2-D tensor map of a row-major matrix [rows, cols] (bf16, or e4m3 bytes)
-// with boxes of box_rows x 128 bytes in the 128-byte swizzle layout;
-// out-of-range elements read as zero.  Reached through the runtime's
+// with boxes of box_rows x 128 bytes in the 128-byte swizzle layout, or of
+// box_rows x box_cols = 32 bf16 in the 64-byte one; out-of-range elements
+// read as zero and are not written.  Reached through the runtime's
 // entry-point lookup.
 bool lm_tensor_map(CUtensorMap *map, const void *base, int64_t rows, int32_t cols, uint32_t box_rows,
-                   bool fp8 = false)
+                   bool fp8 = false, uint32_t box_cols = 0)
 {
     using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -376,10 +377,11 @@ bool lm_tensor_map(CUtensorMap *map, const void *base, int64_t rows, int32_t col
         return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * (fp8 ? 1 : 2)};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(fp8 ? sv::kL8BK : sv::kLmBK), box_rows};
+    const cuuint32_t box[2] = {box_cols ? box_cols : static_cast<cuuint32_t>(fp8 ? sv::kL8BK : sv::kLmBK), box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -599,7 +601,8 @@ template <bool PAIR> cudaError_t lm8_units(int &units)
 }
 
 template <bool PAIR>
-cudaError_t lm8_launch_as(const CUtensorMap &ta, const CUtensorMap &tb, const sv::Lm8Params &L, cudaStream_t stream)
+cudaError_t lm8_launch_as(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc, const sv::Lm8Params &L,
+                          cudaStream_t stream)
 {
     int units = 0;
     const cudaError_t e = lm8_units<PAIR>(units);
@@ -619,7 +622,7 @@ cudaError_t lm8_launch_as(const CUtensorMap &ta, const CUtensorMap &tb, const sv
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sv::lm_head_fp8_kernel<PAIR>, ta, tb, L);
+    return cudaLaunchKernelEx(&cfg, sv::lm_head_fp8_kernel<PAIR>, ta, tb, tc, L);
 }
 
 // logits (bf16 out) and, with `part`, the row statistics of each half tile.
@@ -640,13 +643,14 @@ cudaError_t lm8_launch(const void *hidden, const float *hidden_scales, const voi
     L.stages = sv::kL8RingBytes / L.stage_bytes;
     if (L.stages > sv::kL8MaxStages)
         L.stages = sv::kL8MaxStages;
-    CUtensorMap ta, tb;
+    CUtensorMap ta, tb, tc = {};
     if (!lm_tensor_map(&ta, hidden, M, d, static_cast<uint32_t>(L.a_rows), true) ||
         !lm_tensor_map(&tb, lm_head, V, d, static_cast<uint32_t>(brows), true))
         return cudaErrorInvalidValue;
     L.M = static_cast<int32_t>(M);
     L.N = V;
     L.KB = static_cast<int32_t>(ceil_div(d, sv::kL8BK));
+    L.mt_inv = p.MT > 1 ? UINT64_MAX / static_cast<uint64_t>(p.MT) + 1 : 0;
     L.MT = p.MT;
     L.NT = p.NT;
     L.NB = p.NB;
@@ -659,9 +663,11 @@ cudaError_t lm8_launch(const void *hidden, const float *hidden_scales, const voi
     L.part = part;
     L.halves = p.halves;
     L.c = c;
-    L.vec = (V % 8 == 0 && aligned(logits, 16)) ? 1 : 0;
+    L.tma = (V % 8 == 0 && aligned(logits, 16)) ? 1 : 0;
+    if (L.tma && !lm_tensor_map(&tc, logits, M, V, 32, false, 32))
+        return cudaErrorInvalidValue;
     L.status = status;
-    return p.pair ? lm8_launch_as<true>(ta, tb, L, stream) : lm8_launch_as<false>(ta, tb, L, stream);
+    return p.pair ? lm8_launch_as<true>(ta, tb, tc, L, stream) : lm8_launch_as<false>(ta, tb, tc, L, stream);
 }
 
 // The statistics of the product's tiles merged per row with the draft data,

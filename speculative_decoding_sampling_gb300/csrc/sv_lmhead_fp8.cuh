@@ -51,13 +51,15 @@ constexpr int kL8Chunk = 16;                                       // steps whos
 constexpr int kL8HsPitch = kLmBM + 1;
 constexpr int kL8TabFloats = kL8Chunk * kL8HsPitch + kL8Chunk * 8; // [step][row], [step][32-column group]
 constexpr int kL8TabBytes = 2 * kL8TabFloats * 4;                  // two chunks
-constexpr int kL8StgBytes = 32 * 64;                               // 32 rows x 32 logits of a warp
-constexpr int kL8RingBytes = 192 * 1024;
-constexpr int kL8Smem = 1024 + kL8RingBytes + kL8TabBytes + kL8AccWarps * kL8StgBytes;
+constexpr int kL8BoxBytes = 32 * 64;                               // 32 rows x 32 logits of a warp
+constexpr int kL8StgBytes = 4 * kL8BoxBytes;                       // a warp's half tile
+constexpr int kL8RingBytes = 144 * 1024;
+constexpr int kL8Smem = 1024 + kL8RingBytes + kL8AccWarps * kL8StgBytes + kL8TabBytes;
 static_assert(kL8Smem <= 227 * 1024 - 512, "shared memory of a CTA, less the barriers");
 
 struct Lm8Params {
     int32_t M, N, KB;       // rows of h, vocabulary, scale blocks along the hidden dims
+    uint64_t mt_inv;        // ceil(2^64 / MT) (0 for MT 1): t / MT is the high word of its product with t
     int32_t MT, NT, NB;     // row tiles, id tiles, ids per tile (a multiple of 32; of 64 on pairs)
     int32_t a_rows;         // rows of h in a stage (128, or fewer when M is small)
     int32_t stages, stage_bytes;
@@ -68,7 +70,7 @@ struct Lm8Params {
     float2 *part;           // [M, NT * halves] (max, normaliser relative to fl(max c)), or nullptr
     int32_t halves;         // column halves of a tile: 1 (NB <= 128) or 2
     float c;                // log2(e) / T
-    int32_t vec;            // N % 8 == 0 and 16-byte aligned logits: vector stores
+    int32_t tma;            // N % 8 == 0 and 16-byte aligned logits: tensor stores
     int32_t *status;
 };
 
@@ -256,44 +258,8 @@ template <bool PAIR> __device__ __forceinline__ int l8_group_id(int NB, int h, i
     return j < own ? h * 64 + j : NB / 2 + h * 64 + j - own;
 }
 
-// 32 finished columns (ids n .. n + 31, ncols of them in the vocabulary) of a
-// warp's 32 rows from the packed logits of this lane's row: through the
-// warp's shared memory (16-byte pieces, swizzled so that neither side
-// conflicts), then out in whole 64-byte rows.
-__device__ __forceinline__ void l8_store(const Lm8Params &P, uint8_t *stg, const uint32_t (&pk)[16], int row0, int n,
-                                         int ncols, int lane)
-{
-    __syncwarp();
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<uint4 *>(stg + lane * 64 + ((q ^ (lane >> 1)) & 3) * 16) =
-            make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
-    __syncwarp();
-    if (P.vec && ncols == 32) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int rl = r * 8 + (lane >> 2), q = lane & 3;
-            if (row0 + rl < P.M)
-                *reinterpret_cast<uint4 *>(P.logits + static_cast<int64_t>(row0 + rl) * P.N + n + q * 8) =
-                    *reinterpret_cast<const uint4 *>(stg + rl * 64 + ((q ^ (rl >> 1)) & 3) * 16);
-        }
-    } else if (lane < ncols) {
-        const int q = lane >> 3, e = (lane & 7) * 2;
-        for (int rl = 0; rl < 32 && row0 + rl < P.M; ++rl)
-            P.logits[static_cast<int64_t>(row0 + rl) * P.N + n + lane] =
-                *reinterpret_cast<const uint16_t *>(stg + rl * 64 + ((q ^ (rl >> 1)) & 3) * 16 + e);
-    }
-}
-
-// This thread's index, read anew each time: what only a tile's end needs is
-// then not kept in registers through its steps.
-__device__ __forceinline__ uint32_t l8_tid()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(r));
-    return r;
-}
-
+// Shared memory by its 32-bit address (a generic pointer would order these
+// accesses with those to global memory).
 __device__ __forceinline__ float l8_lds(uint32_t addr)
 {
     float r;
@@ -308,17 +274,100 @@ __device__ __forceinline__ float2 l8_lds2(uint32_t addr)
     return r;
 }
 
+__device__ __forceinline__ uint16_t l8_lds_u16(uint32_t addr)
+{
+    uint16_t r;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(addr) : "memory");
+    return r;
+}
+
+__device__ __forceinline__ void l8_sts(uint32_t addr, float v)
+{
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void l8_sts4(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// 32 finished columns (ids n .. n + 31, ncols of them in the vocabulary) of a
+// warp's 32 rows from the packed logits of this lane's row, through 2 KiB of
+// shared memory in the 64-byte swizzle layout (neither side conflicts).  A
+// tensor store then takes them out behind the warp's back: plain stores held
+// the accumulator warps up for ~900 cycles per 32 columns.  Rows and ids past
+// the ends are clipped by the map.  Logits whose rows are not whole 16-byte
+// units go out one by one.
+__device__ __forceinline__ void l8_store(const Lm8Params &P, const CUtensorMap *map, uint32_t stg,
+                                         const uint32_t (&pk)[16], int row0, int n, int ncols, int lane)
+{
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        l8_sts4(stg + lane * 64 + ((q ^ (lane >> 1)) & 3) * 16,
+                make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
+    if (P.tma) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (l8_elect()) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                             reinterpret_cast<uint64_t>(map)),
+                         "r"(n), "r"(row0), "r"(stg)
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        return;
+    }
+    __syncwarp();
+    if (lane < ncols) {
+        const int q = lane >> 3, e = (lane & 7) * 2;
+        uint16_t *dst = P.logits + static_cast<int64_t>(row0) * P.N + n + lane;
+#pragma unroll 8
+        for (int rl = 0; rl < 32; ++rl) {
+            const uint16_t v = l8_lds_u16(stg + rl * 64 + ((q ^ (rl >> 1)) & 3) * 16 + e);
+            if (row0 + rl < P.M)
+                *dst = v;
+            dst += P.N;
+        }
+    }
+}
+
+// The tensor stores this lane issued have read their shared memory.
+__device__ __forceinline__ void l8_stores_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
+// This thread's index, read anew each time: what only a tile's end needs is
+// then not kept in registers through its steps.
+__device__ __forceinline__ uint32_t l8_tid()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(r));
+    return r;
+}
+
 // How many tiles a unit has.
 __device__ __forceinline__ uint32_t l8_tiles(uint32_t unit, uint32_t units, uint32_t ntiles)
 {
     return unit < ntiles ? (ntiles - unit - 1) / units + 1 : 0;
 }
 
+// Tile t covers ids NB (t div MT) and row tile t mod MT.
+__device__ __forceinline__ uint32_t l8_tile_n(const Lm8Params &P, uint32_t t)
+{
+    return P.MT == 1 ? t : static_cast<uint32_t>(__umul64hi(P.mt_inv, t));
+}
+
+__device__ __forceinline__ uint32_t l8_tile_m(const Lm8Params &P, uint32_t t)
+{
+    return t - l8_tile_n(P, t) * static_cast<uint32_t>(P.MT);
+}
+
 // First row of lane quarter lq of tile t.
 template <bool PAIR>
 __device__ __forceinline__ int l8_row0(const Lm8Params &P, uint32_t t, uint32_t rank, int lq)
 {
-    return static_cast<int>((t % static_cast<uint32_t>(P.MT) * (PAIR ? 2u : 1u) + rank) * kLmBM) + lq * 32;
+    return static_cast<int>((l8_tile_m(P, t) * (PAIR ? 2u : 1u) + rank) * kLmBM) + lq * 32;
 }
 
 __device__ __forceinline__ void l8_fail(const Lm8Params &P, int *stop)
@@ -333,14 +382,14 @@ __device__ __forceinline__ void l8_fail(const Lm8Params &P, int *stop)
 // The scales: step kb's row scales and those of the tile's eight 32-column
 // groups, 16 steps at a time, two chunks in flight.
 template <bool PAIR>
-__device__ __forceinline__ void l8_scales(const Lm8Params &P, float *tab, uint32_t sfull, uint32_t sempty, int *stop,
+__device__ __forceinline__ void l8_scales(const Lm8Params &P, uint32_t tabs, uint32_t sfull, uint32_t sempty, int *stop,
                                           uint32_t rank, uint32_t unit, uint32_t units, uint32_t ntiles, int lane)
 {
     const int k = lane & (kL8Chunk - 1), sub = lane >> 4; // step, and which of 2 rows
     uint32_t chunk = 0;
     for (uint32_t t = unit; t < ntiles; t += units) {
-        const int m0 = static_cast<int>((t % static_cast<uint32_t>(P.MT) * (PAIR ? 2u : 1u) + rank) * kLmBM);
-        const int n0 = static_cast<int>(t / static_cast<uint32_t>(P.MT)) * P.NB;
+        const int m0 = static_cast<int>((l8_tile_m(P, t) * (PAIR ? 2u : 1u) + rank) * kLmBM);
+        const int n0 = static_cast<int>(l8_tile_n(P, t)) * P.NB;
         const int rows = P.M - m0 < kLmBM ? P.M - m0 : kLmBM;
         for (int kb0 = 0; kb0 < P.KB; kb0 += kL8Chunk, ++chunk) {
             const uint32_t b = chunk & 1u;
@@ -350,18 +399,18 @@ __device__ __forceinline__ void l8_scales(const Lm8Params &P, float *tab, uint32
                 return;
             }
             if (kb0 + k < P.KB) {
-                float *dst = tab + b * kL8TabFloats + k * kL8HsPitch;
+                const uint32_t dst = tabs + (b * kL8TabFloats + static_cast<uint32_t>(k) * kL8HsPitch) * 4u;
                 const float *src = P.hs + static_cast<int64_t>(m0) * P.KB + kb0 + k;
 #pragma unroll 8
                 for (int r = sub; r < rows; r += 2)
-                    dst[r] = __ldg(src + static_cast<int64_t>(r) * P.KB);
-                float *wd = tab + b * kL8TabFloats + kL8Chunk * kL8HsPitch + k * 8;
+                    l8_sts(dst + r * 4, __ldg(src + static_cast<int64_t>(r) * P.KB));
+                const uint32_t wd = tabs + (b * kL8TabFloats + kL8Chunk * kL8HsPitch + static_cast<uint32_t>(k) * 8u) * 4u;
 #pragma unroll
                 for (int g = sub; g < 8; g += 2) {
                     const int n = n0 + l8_group_id<PAIR>(P.NB, g >> 2, (g & 3) * 32);
-                    wd[g] = (g & 3) * 32 < l8_half_cols(P.NB, g >> 2) && n < P.N
-                                ? __ldg(P.ws + static_cast<int64_t>(n >> 7) * P.KB + kb0 + k)
-                                : 0.0f;
+                    l8_sts(wd + g * 4, (g & 3) * 32 < l8_half_cols(P.NB, g >> 2) && n < P.N
+                                           ? __ldg(P.ws + static_cast<int64_t>(n >> 7) * P.KB + kb0 + k)
+                                           : 0.0f);
                 }
             }
             __syncwarp();
@@ -383,7 +432,7 @@ __device__ __forceinline__ void l8_fold(unsigned long long *acc, const uint32_t 
 // The accumulator warps: warp w (from 4 on) holds the tile's rows of
 // tensor-memory lane quarter w mod 4 and column half (w - 4) / 4.
 template <bool PAIR>
-__device__ __forceinline__ void l8_accumulate(const Lm8Params &P, uint32_t tabs, uint8_t *stgs, uint32_t tbase,
+__device__ __forceinline__ void l8_accumulate(const Lm8Params &P, const CUtensorMap *map, uint32_t tabs, uint32_t tbase,
                                               uint32_t tfull, uint32_t tempty, uint32_t sfull, uint32_t sempty,
                                               int *stop, uint32_t rank, uint32_t unit, uint32_t units, uint32_t ntiles)
 {
@@ -470,8 +519,12 @@ __device__ __forceinline__ void l8_accumulate(const Lm8Params &P, uint32_t tabs,
         // ---- the finished half tile: logits and, per row, their statistics
         const int warp = static_cast<int>(l8_tid() >> 5), lane = static_cast<int>(l8_tid() & 31u);
         const int h = (warp - 4) >> 2, row0 = l8_row0<PAIR>(P, t, rank, warp & 3);
-        const int n0 = static_cast<int>(t / static_cast<uint32_t>(P.MT)) * P.NB;
-        uint8_t *stg = stgs + (warp - 4) * kL8StgBytes;
+        const int n0 = static_cast<int>(l8_tile_n(P, t)) * P.NB;
+        const uint32_t stg = tabs - static_cast<uint32_t>(12 - warp) * kL8StgBytes;
+        if (t != unit) { // the last tile's logits have left this warp's shared memory
+            l8_stores_read();
+            __syncwarp();
+        }
         float mx = -INFINITY;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -487,7 +540,7 @@ __device__ __forceinline__ void l8_accumulate(const Lm8Params &P, uint32_t tabs,
                     if (2 * i + 1 < ncols)
                         mx = fmaxf(mx, bf16_hi(pk[i]));
                 }
-                l8_store(P, stg, pk, row0, n, ncols, lane);
+                l8_store(P, map, stg + g * kL8BoxBytes, pk, row0, n, ncols, lane);
             }
         }
         if (P.part) {
@@ -509,9 +562,10 @@ __device__ __forceinline__ void l8_accumulate(const Lm8Params &P, uint32_t tabs,
             const int row = row0 + lane;
             if (row < P.M)
                 P.part[static_cast<int64_t>(row) * (P.NT * P.halves) +
-                       static_cast<int>(t / static_cast<uint32_t>(P.MT)) * P.halves + h] = make_float2(mx, S);
+                       static_cast<int>(l8_tile_n(P, t)) * P.halves + h] = make_float2(mx, S);
         }
     }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); // this lane's stores are done
 }
 
 // Unit u (a pair of SMs, or one) takes tiles u, u + units, ...; tile t covers
@@ -519,7 +573,7 @@ __device__ __forceinline__ void l8_accumulate(const Lm8Params &P, uint32_t tabs,
 template <bool PAIR>
 __global__ void __launch_bounds__(kL8Threads, 1)
     lm_head_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                       const __grid_constant__ Lm8Params P)
+                       const __grid_constant__ CUtensorMap tmC, const __grid_constant__ Lm8Params P)
 {
     constexpr int kCtas = PAIR ? 2 : 1;
     extern __shared__ uint8_t lm_smem_raw[];
@@ -528,7 +582,7 @@ __global__ void __launch_bounds__(kL8Threads, 1)
     __shared__ uint32_t tmem_base;
     __shared__ int stop;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(lm_smem_raw) + 1023) & ~uintptr_t{1023});
-    float *tab = reinterpret_cast<float *>(smem + kL8RingBytes);
+    const uint32_t tabs = smem_addr(smem) + kL8RingBytes + kL8AccWarps * kL8StgBytes;
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? lm_cluster_rank() : 0u;
     const bool leader = rank == 0;
@@ -573,9 +627,9 @@ __global__ void __launch_bounds__(kL8Threads, 1)
             const uint32_t bytes = static_cast<uint32_t>(kCtas * (P.a_rows + brows) * kL8BK);
             bool ok = true;
             for (uint32_t t = unit; t < ntiles && ok; t += units) {
-                const int m0 = static_cast<int>((t % static_cast<uint32_t>(P.MT) * kCtas + rank) * kLmBM);
+                const int m0 = static_cast<int>((l8_tile_m(P, t) * kCtas + rank) * kLmBM);
                 const int n0 =
-                    static_cast<int>(t / static_cast<uint32_t>(P.MT)) * P.NB + static_cast<int>(rank) * brows;
+                    static_cast<int>(l8_tile_n(P, t)) * P.NB + static_cast<int>(rank) * brows;
                 for (int kb = 0; kb < P.KB; ++kb) {
                     if (wrapped &&
                         !__all_sync(0xFFFFFFFFu, l8_wait(smem_addr(&empty[s]), ph ^ 1u))) {
@@ -639,11 +693,11 @@ __global__ void __launch_bounds__(kL8Threads, 1)
             if (!ok && lane == 0)
                 l8_fail(P, &stop);
         } else {
-            l8_scales<PAIR>(P, tab, smem_addr(&sfull[0]), smem_addr(&sempty[0]), &stop, rank, unit, units, ntiles, lane);
+            l8_scales<PAIR>(P, tabs, smem_addr(&sfull[0]), smem_addr(&sempty[0]), &stop, rank, unit, units, ntiles, lane);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kL8AccRegs));
-        l8_accumulate<PAIR>(P, smem_addr(tab), smem + kL8RingBytes + kL8TabBytes, tbase, smem_addr(&tfull[0]),
+        l8_accumulate<PAIR>(P, &tmC, tabs, tbase, smem_addr(&tfull[0]),
                             smem_addr(&tempty[0]), smem_addr(&sfull[0]), smem_addr(&sempty[0]), &stop, rank, unit,
                             units, ntiles);
     }
