@@ -291,43 +291,44 @@ __device__ __forceinline__ void l8_sts4(uint32_t addr, uint4 v)
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// 32 finished columns (ids n .. n + 31, ncols of them in the vocabulary) of a
-// warp's 32 rows from the packed logits of this lane's row, through 2 KiB of
-// shared memory in the 64-byte swizzle layout (neither side conflicts).  A
-// tensor store then takes them out behind the warp's back: plain stores held
-// the accumulator warps up for ~900 cycles per 32 columns.  Rows and ids past
-// the ends are clipped by the map.  Logits whose rows are not whole 16-byte
-// units go out one by one.
-__device__ __forceinline__ void l8_store(const Lm8Params &P, const CUtensorMap *map, uint32_t stg,
-                                         const uint32_t (&pk)[16], int row0, int n, int ncols, int lane)
+// A finished tile leaves through shared memory: boxes of 32 rows x 32 logits,
+// 2 KiB in the 64-byte swizzle layout (neither side conflicts), which tensor
+// stores take out behind the warp's back -- plain stores held the accumulator
+// warps up for ~900 cycles per box.  Rows and ids past the ends are clipped by
+// the map.  Logits whose rows are not whole 16-byte units go out one by one.
+
+// This lane's row of a box, from 16 packed pairs.
+__device__ __forceinline__ void l8_stage(uint32_t box, const uint32_t (&pk)[16], int lane)
 {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-        l8_sts4(stg + lane * 64 + ((q ^ (lane >> 1)) & 3) * 16,
+        l8_sts4(box + lane * 64 + ((q ^ (lane >> 1)) & 3) * 16,
                 make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
-    if (P.tma) {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (l8_elect()) {
-            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                             reinterpret_cast<uint64_t>(map)),
-                         "r"(n), "r"(row0), "r"(stg)
-                         : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
+}
+
+// The box of ids n.. and rows row0.., staged by the whole warp before a proxy
+// fence and a warp barrier; one lane, which commits the group.
+__device__ __forceinline__ void l8_send(const CUtensorMap *map, uint32_t box, int n, int row0)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(n), "r"(row0), "r"(box)
+                 : "memory");
+}
+
+// The same box by plain stores, a logit a lane (ncols of them in the vocabulary).
+__device__ __forceinline__ void l8_store(const Lm8Params &P, uint32_t box, int row0, int n, int ncols, int lane)
+{
+    if (lane >= ncols)
         return;
-    }
-    __syncwarp();
-    if (lane < ncols) {
-        const int q = lane >> 3, e = (lane & 7) * 2;
-        uint16_t *dst = P.logits + static_cast<int64_t>(row0) * P.N + n + lane;
+    const int q = lane >> 3, e = (lane & 7) * 2;
+    uint16_t *dst = P.logits + static_cast<int64_t>(row0) * P.N + n + lane;
 #pragma unroll 8
-        for (int rl = 0; rl < 32; ++rl) {
-            const uint16_t v = l8_lds_u16(stg + rl * 64 + ((q ^ (rl >> 1)) & 3) * 16 + e);
-            if (row0 + rl < P.M)
-                *dst = v;
-            dst += P.N;
-        }
+    for (int rl = 0; rl < 32; ++rl) {
+        const uint16_t v = l8_lds_u16(box + rl * 64 + ((q ^ (rl >> 1)) & 3) * 16 + e);
+        if (row0 + rl < P.M)
+            *dst = v;
+        dst += P.N;
     }
 }
 
@@ -429,6 +430,144 @@ __device__ __forceinline__ void l8_fold(unsigned long long *acc, const uint32_t 
         acc[i] = fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), ff, acc[i]);
 }
 
+// A row's maximum and normaliser over a half tile, from the rounded logits.
+template <bool PAIR>
+__device__ __forceinline__ void l8_statistics(const Lm8Params &P, const unsigned long long (&acc)[64], int n0, int h,
+                                              int G, int row, int slot)
+{
+    float mx = -INFINITY;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const int ncols = g < G ? P.N - n0 - l8_group_id<PAIR>(P.NB, h, 32 * g) : 0;
+        if (ncols >= 32) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t pk = l8_round(acc[g * 16 + i]);
+                mx = fmaxf(mx, fmaxf(bf16_lo(pk), bf16_hi(pk)));
+            }
+        } else if (ncols > 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t pk = l8_round(acc[g * 16 + i]);
+                if (2 * i < ncols)
+                    mx = fmaxf(mx, bf16_lo(pk));
+                if (2 * i + 1 < ncols)
+                    mx = fmaxf(mx, bf16_hi(pk));
+            }
+        }
+    }
+    const float mc = mc_of(mx, P.c);
+    float S = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const int ncols = g < G ? P.N - n0 - l8_group_id<PAIR>(P.NB, h, 32 * g) : 0;
+        if (ncols >= 32) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t pk = l8_round(acc[g * 16 + i]);
+                S += term(bf16_lo(pk), P.c, mc) + term(bf16_hi(pk), P.c, mc);
+            }
+        } else if (ncols > 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t pk = l8_round(acc[g * 16 + i]);
+                if (2 * i < ncols)
+                    S += term(bf16_lo(pk), P.c, mc);
+                if (2 * i + 1 < ncols)
+                    S += term(bf16_hi(pk), P.c, mc);
+            }
+        }
+    }
+    if (row < P.M)
+        P.part[static_cast<int64_t>(row) * (P.NT * P.halves) + slot] = make_float2(mx, S);
+}
+
+// What a warp's steps go by.
+struct L8Steps {
+    uint32_t tl;                     // tensor-memory address of the warp's rows and column half
+    uint32_t tfull, tempty;          // barriers of buffer 0 (buffer 1's are 16 bytes on)
+    uint32_t hsp, wsp;               // this step's scales in shared memory
+    uint32_t it;                     // steps so far
+    bool ok;                         // no wait of this lane has run out
+    __device__ __forceinline__ void wait()
+    {
+        if (ok)
+            ok = l8_wait(tfull + (it & 1u) * 16u, (it >> 1) & 1u);
+        __syncwarp();
+        lm_tc_after();
+    }
+    __device__ __forceinline__ uint32_t buffer() const { return tl + (it & 1u) * kL8MaxNB; }
+    __device__ __forceinline__ void release() const // this warp has read the step's sums
+    {
+        lm_tc_before();
+        __syncwarp();
+        if ((l8_tid() & 31u) == 0)
+            l8_arrive(tempty + (it & 1u) * 16u);
+    }
+    __device__ __forceinline__ void next()
+    {
+        ++it;
+        hsp += kL8HsPitch * 4;
+        wsp += 32;
+    }
+};
+
+// Up to 16 steps of a warp whose half tile has all 128 columns.  The sums are
+// read 64 columns at a time; the next ones are on their way while two 32s are
+// folded in, over the end of a step too.
+__device__ __forceinline__ void l8_steps_full(L8Steps &S, unsigned long long (&acc)[64], int steps)
+{
+    uint32_t v0[32], v1[32];
+    S.wait();
+    l8_ld_start(S.buffer(), v0);
+    l8_ld_start(S.buffer() + 32, v1);
+#pragma unroll 1
+    for (; steps > 0; --steps) {
+        const float hs = l8_lds(S.hsp);
+        float2 ws = l8_lds2(S.wsp);
+        l8_ld_wait(v0);
+        l8_ld_tie(v1);
+        l8_fold(acc, v0, __fmul_rn(hs, ws.x));
+        l8_ld_start(S.buffer() + 64, v0);
+        l8_fold(acc + 16, v1, __fmul_rn(hs, ws.y));
+        l8_ld_start(S.buffer() + 96, v1);
+        ws = l8_lds2(S.wsp + 8);
+        l8_ld_wait(v0);
+        l8_ld_tie(v1);
+        S.release();
+        S.next();
+        l8_fold(acc + 32, v0, __fmul_rn(hs, ws.x));
+        if (steps > 1) {
+            S.wait();
+            l8_ld_start(S.buffer(), v0);
+        }
+        l8_fold(acc + 48, v1, __fmul_rn(hs, ws.y));
+        if (steps > 1)
+            l8_ld_start(S.buffer() + 32, v1);
+    }
+}
+
+// The same for G < 4 32-column groups (none: rows past the end).
+__device__ __forceinline__ void l8_steps_some(L8Steps &S, unsigned long long (&acc)[64], int steps, int G)
+{
+#pragma unroll 1
+    for (; steps > 0; --steps) {
+        S.wait();
+        const float hs = l8_lds(S.hsp);
+#pragma unroll
+        for (int g = 0; g < 3; ++g)
+            if (g < G) {
+                uint32_t v[32];
+                l8_ld_start(S.buffer() + 32 * g, v);
+                const float2 ws = l8_lds2(S.wsp + (g >> 1) * 8);
+                l8_ld_wait(v);
+                l8_fold(acc + 16 * g, v, __fmul_rn(hs, g & 1 ? ws.y : ws.x));
+            }
+        S.release();
+        S.next();
+    }
+}
+
 // The accumulator warps: warp w (from 4 on) holds the tile's rows of
 // tensor-memory lane quarter w mod 4 and column half (w - 4) / 4.
 template <bool PAIR>
@@ -441,130 +580,78 @@ __device__ __forceinline__ void l8_accumulate(const Lm8Params &P, const CUtensor
     const int groups = l8_half_cols(P.NB, h) / 32; // 32-column groups of this half: 0..4
     if (groups == 0)
         return;
-    const uint32_t tl0 = tbase + (static_cast<uint32_t>(lq) << 21) + static_cast<uint32_t>(h * 128);
-    tfull += static_cast<uint32_t>(h) * 8u;
-    tempty = (PAIR ? lm_mapa(tempty, 0) : tempty) + static_cast<uint32_t>(h) * 8u;
-    uint32_t it = 0, chunk = 0;
-    for (uint32_t t = unit; t < ntiles; t += units) {
+    L8Steps S;
+    S.tl = tbase + (static_cast<uint32_t>(lq) << 21) + static_cast<uint32_t>(h * 128);
+    S.tfull = tfull + static_cast<uint32_t>(h) * 8u;
+    S.tempty = (PAIR ? lm_mapa(tempty, 0) : tempty) + static_cast<uint32_t>(h) * 8u;
+    S.it = 0;
+    S.ok = true;
+    uint32_t chunk = 0;
+    bool alive = true;
+    for (uint32_t t = unit; t < ntiles && alive; t += units) {
         const int G = l8_row0<PAIR>(P, t, rank, lq) < P.M ? groups : 0; // groups this warp folds
         unsigned long long acc[64];            // pairs of fp32 sums
 #pragma unroll
         for (int i = 0; i < 64; ++i)
             acc[i] = 0;
-        for (int kb0 = 0; kb0 < P.KB; kb0 += kL8Chunk, ++chunk) {
+        for (int kb0 = 0; kb0 < P.KB && alive; kb0 += kL8Chunk, ++chunk) {
             const uint32_t sb = chunk & 1u;
-            if (!__all_sync(0xFFFFFFFFu, l8_wait(sfull + sb * 8, (chunk >> 1) & 1u))) {
-                if (lane == 0)
-                    l8_fail(P, stop);
-                return;
-            }
-            uint32_t hsp = tabs + (sb * kL8TabFloats + static_cast<uint32_t>(lq * 32 + lane)) * 4u;
-            uint32_t wsp = tabs + (sb * kL8TabFloats + kL8Chunk * kL8HsPitch + static_cast<uint32_t>(h * 4)) * 4u;
+            S.ok = l8_wait(sfull + sb * 8, (chunk >> 1) & 1u);
+            S.hsp = tabs + (sb * kL8TabFloats + static_cast<uint32_t>(lq * 32 + lane)) * 4u;
+            S.wsp = tabs + (sb * kL8TabFloats + kL8Chunk * kL8HsPitch + static_cast<uint32_t>(h * 4)) * 4u;
             const int steps = P.KB - kb0 < kL8Chunk ? P.KB - kb0 : kL8Chunk;
-#pragma unroll 1
-            for (int k = 0; k < steps; ++k, ++it, hsp += kL8HsPitch * 4, wsp += 32) {
-                const float hs = l8_lds(hsp);
-                float2 ws = l8_lds2(wsp);
-                const uint32_t b = it & 1u;
-                if (!__all_sync(0xFFFFFFFFu, l8_wait(tfull + b * 16, (it >> 1) & 1u))) {
-                    if (lane == 0)
-                        l8_fail(P, stop);
-                    return;
-                }
-                lm_tc_after();
-                const uint32_t tl = tl0 + b * kL8MaxNB;
-                auto release = [&]() { // this warp has read the step's sums
-                    lm_tc_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        l8_arrive(tempty + b * 16);
-                };
-                uint32_t v0[32], v1[32];
-                if (G == 0) {
-                    release();
-                    continue;
-                }
-                l8_ld_start(tl, v0);
-                if (G > 1)
-                    l8_ld_start(tl + 32, v1);
-                l8_ld_wait(v0);
-                if (G > 1)
-                    l8_ld_tie(v1);
-                if (G <= 2)
-                    release();
-                l8_fold(acc, v0, __fmul_rn(hs, ws.x));
-                if (G > 2)
-                    l8_ld_start(tl + 64, v0);
-                if (G > 1)
-                    l8_fold(acc + 16, v1, __fmul_rn(hs, ws.y));
-                if (G > 2) {
-                    if (G > 3)
-                        l8_ld_start(tl + 96, v1);
-                    ws = l8_lds2(wsp + 8);
-                    l8_ld_wait(v0);
-                    if (G > 3)
-                        l8_ld_tie(v1);
-                    release();
-                    l8_fold(acc + 32, v0, __fmul_rn(hs, ws.x));
-                    if (G > 3)
-                        l8_fold(acc + 48, v1, __fmul_rn(hs, ws.y));
-                }
-            }
-            __syncwarp();
+            if (G == 4)
+                l8_steps_full(S, acc, steps);
+            else
+                l8_steps_some(S, acc, steps, G);
+            alive = __all_sync(0xFFFFFFFFu, S.ok);
             if (lane == 0) // this warp has read the chunk's scales
                 l8_arrive(sempty + sb * 8);
         }
-        if (G == 0)
+        if (G == 0 || !alive)
             continue;
         // ---- the finished half tile: logits and, per row, their statistics
         const int warp = static_cast<int>(l8_tid() >> 5), lane = static_cast<int>(l8_tid() & 31u);
         const int h = (warp - 4) >> 2, row0 = l8_row0<PAIR>(P, t, rank, warp & 3);
-        const int n0 = static_cast<int>(l8_tile_n(P, t)) * P.NB;
+        const int tn = static_cast<int>(l8_tile_n(P, t)), n0 = tn * P.NB;
         const uint32_t stg = tabs - static_cast<uint32_t>(12 - warp) * kL8StgBytes;
-        if (t != unit) { // the last tile's logits have left this warp's shared memory
+        if (t != unit) // the last tile's logits have left this warp's shared memory
             l8_stores_read();
-            __syncwarp();
-        }
-        float mx = -INFINITY;
+        __syncwarp();
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int n = n0 + l8_group_id<PAIR>(P.NB, h, 32 * g);
-            const int ncols = g < G ? (P.N - n < 32 ? P.N - n : 32) : 0;
-            if (ncols > 0) {
+        for (int g = 0; g < 4; ++g)
+            if (g < G) {
                 uint32_t pk[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < 16; ++i)
                     pk[i] = l8_round(acc[g * 16 + i]);
-                    if (2 * i < ncols)
-                        mx = fmaxf(mx, bf16_lo(pk[i]));
-                    if (2 * i + 1 < ncols)
-                        mx = fmaxf(mx, bf16_hi(pk[i]));
-                }
-                l8_store(P, map, stg + g * kL8BoxBytes, pk, row0, n, ncols, lane);
+                l8_stage(stg + g * kL8BoxBytes, pk, lane);
             }
-        }
-        if (P.part) {
-            const float mc = mc_of(mx, P.c);
-            float S = 0.0f;
+        if (P.tma)
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (P.tma) {
+            if (l8_elect()) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
+                for (int g = 0; g < 4; ++g) {
+                    const int n = n0 + l8_group_id<PAIR>(P.NB, h, 32 * g);
+                    if (g < G && n < P.N)
+                        l8_send(map, stg + g * kL8BoxBytes, n, row0);
+                }
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+        } else {
+#pragma unroll 1
+            for (int g = 0; g < G; ++g) {
                 const int n = n0 + l8_group_id<PAIR>(P.NB, h, 32 * g);
-                const int ncols = g < G ? P.N - n : 0;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const uint32_t pk = l8_round(acc[g * 16 + i]);
-                    if (2 * i < ncols)
-                        S += term(bf16_lo(pk), P.c, mc);
-                    if (2 * i + 1 < ncols)
-                        S += term(bf16_hi(pk), P.c, mc);
-                }
+                l8_store(P, stg + g * kL8BoxBytes, row0, n, P.N - n, lane);
             }
-            const int row = row0 + lane;
-            if (row < P.M)
-                P.part[static_cast<int64_t>(row) * (P.NT * P.halves) +
-                       static_cast<int>(l8_tile_n(P, t)) * P.halves + h] = make_float2(mx, S);
         }
+        if (P.part)
+            l8_statistics<PAIR>(P, acc, n0, h, G, row0 + lane, tn * P.halves + h);
     }
+    if (!alive && lane == 0)
+        l8_fail(P, stop);
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); // this lane's stores are done
 }
 
