@@ -364,6 +364,7 @@ def spec_verify_lm_head(hidden: torch.Tensor, lm_head: torch.Tensor, draft_probs
 
 _BLOCK = 128  # values along d (and ids of the output embedding) that share a scale
 _DTYPES = {torch.bfloat16: N.SV_BF16, torch.float32: N.SV_FP32, torch.float8_e4m3fn: N.SV_E4M3}
+_F8, _F32 = torch.float8_e4m3fn, torch.float32
 
 
 def _dtype(t: torch.Tensor, name: str, fp8: bool = False) -> int:
@@ -379,26 +380,48 @@ def _cuda(t: torch.Tensor, name: str) -> torch.device:
     return t.device
 
 
-class _on:
-    """Run on `stream` (default: the device's current one): the tensors made
-    inside belong to it, and the launch goes to its device."""
+def _need(t: torch.Tensor, name: str, dtype, shape, dev: torch.device):
+    """_check, without its cost where nothing is wrong (these calls are a few
+    microseconds of host time in all)."""
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _check(t, name, dtype, shape, dev)
+
+
+class _Streams:
+    """Enter `stream` and its device: the tensors made inside belong to it."""
 
     def __init__(self, dev: torch.device, stream: torch.cuda.Stream | None):
-        self.dev = dev
-        self.stream = stream or torch.cuda.current_stream(dev)
-        if self.stream.device != dev:
-            raise ValueError(f"stream: expected a stream of {dev}, got one of {self.stream.device}")
-        plain = stream is None and torch.cuda.current_device() == dev.index
-        self.ctx = None if plain else torch.cuda.stream(self.stream)
+        stream = stream or torch.cuda.current_stream(dev)
+        if stream.device != dev:
+            raise ValueError(f"stream: expected a stream of {dev}, got one of {stream.device}")
+        self.raw = stream.cuda_stream
+        self.ctx = torch.cuda.stream(stream)
 
     def __enter__(self) -> int:
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.stream.cuda_stream
+        self.ctx.__enter__()
+        return self.raw
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        self.ctx.__exit__(*exc)
+
+
+class _Current:
+    """The same for the current stream of the current device: nothing to do."""
+
+    def __enter__(self) -> int:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+    def __exit__(self, *exc):
+        pass
+
+
+_CURRENT = _Current()
+
+
+def _on(dev: torch.device, stream: torch.cuda.Stream | None):
+    if stream is None and dev.index == torch.cuda.current_device():
+        return _CURRENT
+    return _Streams(dev, stream)
 
 
 def _blocks(n: int) -> int:
@@ -414,20 +437,23 @@ def sv_quantize_fp8(x: torch.Tensor, block_rows: int = 1, *, out: torch.Tensor |
     Returns (values, scales); `out` and `scales` may be preallocated."""
     dt = _dtype(x, "x")
     dev = _cuda(x, "x")
+    shape = x.shape
     if block_rows not in (1, _BLOCK):
         raise ValueError("block_rows must be 1 or 128")
-    if x.dim() < 1 or x.shape[-1] < 1 or (block_rows != 1 and x.dim() != 2):
+    if len(shape) < 1 or shape[-1] < 1 or (block_rows != 1 and len(shape) != 2):
         raise ValueError("x must be [..., d], and [V, d] for blocks of 128 rows")
-    d = x.shape[-1]
+    d = shape[-1]
     rows = x.numel() // d
-    sshape = (x.shape[:-1] if block_rows == 1 else (_blocks(rows),)) + (_blocks(d),)
+    sshape = (shape[:-1] if block_rows == 1 else (_blocks(rows),)) + (_blocks(d),)
     with _on(dev, stream) as s:
         if out is None:
-            out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+            out = torch.empty(shape, dtype=_F8, device=dev)
+        else:
+            _need(out, "out", _F8, shape, dev)
         if scales is None:
-            scales = torch.empty(sshape, dtype=torch.float32, device=dev)
-        _check(out, "out", torch.float8_e4m3fn, x.shape, dev)
-        _check(scales, "scales", torch.float32, sshape, dev)
+            scales = torch.empty(sshape, dtype=_F32, device=dev)
+        else:
+            _need(scales, "scales", _F32, sshape, dev)
         rc = N.lib().sv_quantize_fp8(x.data_ptr(), dt, rows, d, block_rows, out.data_ptr(), scales.data_ptr(), s)
     if rc != N.SV_OK:
         raise SpecVerifyError(rc)
@@ -465,39 +491,45 @@ def sv_block_norm(x: torch.Tensor, residual: torch.Tensor, norm_weight: torch.Te
     if ht is None:
         raise TypeError("hidden_dtype must be bfloat16, float32 or float8_e4m3fn")
     dev = _cuda(x, "x")
-    if x.dim() < 1 or x.shape[-1] < 1:
+    shape = x.shape
+    if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("x must be [..., d]")
-    d = x.shape[-1]
+    d = shape[-1]
     M = x.numel() // d
-    _check(residual, "residual", residual.dtype, x.shape, dev)
-    _check(norm_weight, "norm_weight", norm_weight.dtype, (d,), dev)
+    _need(residual, "residual", residual.dtype, shape, dev)
+    _need(norm_weight, "norm_weight", norm_weight.dtype, (d,), dev)
     if post_weight is not None:
-        _check(post_weight, "post_weight", norm_weight.dtype, (d,), dev)
+        _need(post_weight, "post_weight", norm_weight.dtype, (d,), dev)
     gate_rows = 1
     if gate is not None:
         if gate.dim() < 1 or gate.shape[-1] != d or gate.numel() == 0:
             raise ValueError("gate must be [..., d] with at least one row")
-        _check(gate, "gate", x.dtype, gate.shape, dev)
+        _need(gate, "gate", x.dtype, gate.shape, dev)
         gate_rows = gate.numel() // d
         if M % gate_rows:
             raise ValueError(f"gate: {gate_rows} rows do not divide the {M} rows of x")
-    if scales is not None and hidden_dtype != torch.float8_e4m3fn:
+    if scales is not None and ht != N.SV_E4M3:
         raise ValueError("scales belong to a float8_e4m3fn hidden")
     with _on(dev, stream) as s:
         if residual_out is None:
             residual_out = torch.empty_like(residual)
+        else:
+            _need(residual_out, "residual_out", residual.dtype, shape, dev)
         if out is None:
-            out = torch.empty(x.shape, dtype=hidden_dtype, device=dev)
-        if hidden_dtype == torch.float8_e4m3fn:
+            out = torch.empty(shape, dtype=hidden_dtype, device=dev)
+        else:
+            _need(out, "out", hidden_dtype, shape, dev)
+        sp = None
+        if ht == N.SV_E4M3:
+            sshape = shape[:-1] + (_blocks(d),)
             if scales is None:
-                scales = torch.empty(x.shape[:-1] + (_blocks(d),), dtype=torch.float32, device=dev)
-            _check(scales, "scales", torch.float32, x.shape[:-1] + (_blocks(d),), dev)
-        _check(residual_out, "residual_out", residual.dtype, x.shape, dev)
-        _check(out, "out", hidden_dtype, x.shape, dev)
+                scales = torch.empty(sshape, dtype=_F32, device=dev)
+            else:
+                _need(scales, "scales", _F32, sshape, dev)
+            sp = scales.data_ptr()
         rc = N.lib().sv_block_norm(x.data_ptr(), xt, residual.data_ptr(), rt, _ptr(post_weight), _ptr(gate), gate_rows,
-                                   norm_weight.data_ptr(), wt, float(weight_offset), float(residual_scale),
-                                   float(branch_scale), float(eps), M, d, residual_out.data_ptr(), out.data_ptr(), ht,
-                                   _ptr(scales), s)
+                                   norm_weight.data_ptr(), wt, weight_offset, residual_scale, branch_scale, eps, M, d,
+                                   residual_out.data_ptr(), out.data_ptr(), ht, sp, s)
     if rc != N.SV_OK:
         raise SpecVerifyError(rc)
     return BlockNormResult(out, scales, residual_out)
@@ -507,12 +539,14 @@ def _lm_fp8_check(hidden, hidden_scales, lm_head, lm_head_scales) -> torch.devic
     _dtype(hidden, "hidden", fp8=True)
     _dtype(lm_head, "lm_head", fp8=True)
     dev = _cuda(hidden, "hidden")
-    if lm_head.dim() != 2 or hidden.dim() < 1 or hidden.shape[-1] != lm_head.shape[1]:
+    shape, wshape = hidden.shape, lm_head.shape
+    if len(wshape) != 2 or len(shape) < 1 or shape[-1] != wshape[1]:
         raise ValueError("lm_head must be [V, d], d the hidden states' last dimension")
-    V, d = lm_head.shape
-    _check(lm_head, "lm_head", torch.float8_e4m3fn, (V, d), dev)
-    _check(hidden_scales, "hidden_scales", torch.float32, hidden.shape[:-1] + (_blocks(d),), dev)
-    _check(lm_head_scales, "lm_head_scales", torch.float32, (_blocks(V), _blocks(d)), dev)
+    V, d = wshape
+    nb = _blocks(d)
+    _need(lm_head, "lm_head", _F8, wshape, dev)
+    _need(hidden_scales, "hidden_scales", _F32, shape[:-1] + (nb,), dev)
+    _need(lm_head_scales, "lm_head_scales", _F32, (_blocks(V), nb), dev)
     return dev
 
 
@@ -528,12 +562,14 @@ def sv_lm_head_logits_fp8(hidden: torch.Tensor, hidden_scales: torch.Tensor, lm_
     dev = _lm_fp8_check(hidden, hidden_scales, lm_head, lm_head_scales)
     V, d = lm_head.shape
     M = hidden.numel() // d if d else 0
+    oshape = hidden.shape[:-1] + (V,)
     if status is not None:
-        _check(status, "status", torch.int32, (1,), dev)
+        _need(status, "status", torch.int32, (1,), dev)
     with _on(dev, stream) as s:
         if out is None:
-            out = torch.empty(hidden.shape[:-1] + (V,), dtype=torch.bfloat16, device=dev)
-        _check(out, "out", torch.bfloat16, hidden.shape[:-1] + (V,), dev)
+            out = torch.empty(oshape, dtype=torch.bfloat16, device=dev)
+        else:
+            _need(out, "out", torch.bfloat16, oshape, dev)
         rc = N.lib().sv_lm_head_logits_fp8(hidden.data_ptr(), hidden_scales.data_ptr(), lm_head.data_ptr(),
                                            lm_head_scales.data_ptr(), M, d, V, out.data_ptr(), _ptr(status), s)
     if rc != N.SV_OK:
@@ -563,18 +599,18 @@ def spec_verify_lm_head_fp8(hidden: torch.Tensor, hidden_scales: torch.Tensor, l
     K = K1 - 1
     V = lm_head.shape[0]
     if draft_probs is not None:
-        _check(draft_probs, "draft_probs", torch.float32, (B, K, V), dev)
-    _check(draft_tokens, "draft_tokens", torch.int32, (B, K), dev)
-    _check(uniforms, "uniforms", torch.float32, (B, K + 1), dev)
+        _need(draft_probs, "draft_probs", torch.float32, (B, K, V), dev)
+    _need(draft_tokens, "draft_tokens", torch.int32, (B, K), dev)
+    _need(uniforms, "uniforms", torch.float32, (B, K + 1), dev)
     if status is not None:
-        _check(status, "status", torch.int32, (1,), dev)
+        _need(status, "status", torch.int32, (1,), dev)
     need = sv_lm_head_fp8_workspace_bytes(B, K, V)
     if need == 0 and B > 0:
         raise SpecVerifyError(N.SV_EUNSUPPORTED)
     with _on(dev, stream) as s:
         if logits_out is None:
             logits_out = torch.empty((B, K1, V), dtype=torch.bfloat16, device=dev)
-        _check(logits_out, "logits_out", torch.bfloat16, (B, K1, V), dev)
+        _need(logits_out, "logits_out", torch.bfloat16, (B, K1, V), dev)
         if workspace is None:
             if torch.cuda.is_current_stream_capturing():
                 workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=dev)
