@@ -506,14 +506,19 @@ Lm8Plan lm8_plan(int64_t M, int32_t V)
     p.pair = M > sv::kLmBM;
     const int64_t rows = p.pair ? 2 * sv::kLmBM : sv::kLmBM, units = p.pair ? kNominalSms / 2 : kNominalSms;
     p.MT = static_cast<int32_t>(ceil_div(M > 0 ? M : 1, rows));
-    // ids per tile: the width whose last wave of tiles wastes least (a tile
-    // costs its ids plus about 16 for its start and end); the widest on ties
-    const int32_t step = p.pair ? 64 : 32;
+    // Ids per tile: the width for which the waves of tiles cost least.  A step
+    // of a tile (128 hidden dims) costs at least the accumulator warps' chain
+    // of about 640 cycles, whatever its width, or the time its weights take from memory when every step brings
+    // new ones (one row tile: 128 bytes an id at 23 bytes a cycle and SM).
+    // Narrower tiles on ties: they reach more SMs.  A pair's tiles are 64, 128
+    // or 256 wide (two whole halves, each in boxes of one size).
+    const int64_t per_id = p.pair ? 11 : 22; // quarter cycles an id
     int64_t best = INT64_MAX;
     p.NB = sv::kL8MaxNB;
-    for (int32_t nb = sv::kL8MaxNB; nb >= step; nb -= step) {
-        const int64_t cost = ceil_div(p.MT * ceil_div(V, nb), units) * (nb + 16);
-        if (cost < best) {
+    for (int32_t nb = sv::kL8MaxNB; nb >= (p.pair ? 64 : 32); nb = p.pair ? nb / 2 : nb - 32) {
+        const int64_t bytes = p.MT == 1 ? per_id * nb / 4 : 0;
+        const int64_t cost = ceil_div(p.MT * ceil_div(V, nb), units) * ((bytes > 640 ? bytes : 640) + 40);
+        if (cost <= best) {
             best = cost;
             p.NB = nb;
         }
@@ -525,8 +530,7 @@ Lm8Plan lm8_plan(int64_t M, int32_t V)
 
 size_t lm8_part_bytes(int64_t M, int32_t V)
 {
-    const Lm8Plan p = lm8_plan(M, V);
-    return align_up(static_cast<size_t>(M) * p.NT * p.halves * sizeof(float2));
+    return align_up(static_cast<size_t>(M) * lm8_plan(M, V).NT * sizeof(float2));
 }
 
 sv_status_t lm8_check(const void *hidden, const float *hidden_scales, const void *lm_head, const float *lm_head_scales,
@@ -645,7 +649,7 @@ cudaError_t lm8_launch(const void *hidden, const float *hidden_scales, const voi
         L.stages = sv::kL8MaxStages;
     CUtensorMap ta, tb, tc = {};
     if (!lm_tensor_map(&ta, hidden, M, d, static_cast<uint32_t>(L.a_rows), true) ||
-        !lm_tensor_map(&tb, lm_head, V, d, static_cast<uint32_t>(brows), true))
+        !lm_tensor_map(&tb, lm_head, V, d, static_cast<uint32_t>(p.pair && p.halves == 2 ? brows / 2 : brows), true))
         return cudaErrorInvalidValue;
     L.M = static_cast<int32_t>(M);
     L.N = V;
@@ -991,9 +995,8 @@ sv_status_t spec_verify_lm_head_fp8(const void *hidden, const float *hidden_scal
     if (lm8_launch(hidden, hidden_scales, lm_head, lm_head_scales, M, d, V, logits_out, part, c, status_dev,
                    static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return SV_ECUDA;
-    const Lm8Plan p = lm8_plan(M, V);
-    return lm_finish(plan, part, p.NT * p.halves, logits_out, draft_probs, draft_tokens, uniforms, temperature, B, K, V,
-                     out_tokens, num_emitted, accept_flags, accept_prob, residual_mass, status_dev, workspace, stream);
+    return lm_finish(plan, part, lm8_plan(M, V).NT, logits_out, draft_probs, draft_tokens, uniforms, temperature, B, K,
+                     V, out_tokens, num_emitted, accept_flags, accept_prob, residual_mass, status_dev, workspace, stream);
 }
 
 sv_status_t sv_block_norm(const void *x, sv_dtype_t x_dtype, const void *residual, sv_dtype_t residual_dtype,

@@ -29,7 +29,11 @@
 // time into shared memory.  Warps 4..11 hold the accumulators (32 rows x 128 columns a
 // warp, 128 registers a thread); they read the sums 64 columns ahead of the
 // multiply-adds, and hand a buffer back before its last ones.  A finished tile
-// goes through shared memory, so that the logits leave in whole sectors.
+// goes through shared memory: tensor stores take it out behind the
+// accumulator warps' backs, and warps 12..15 form each row's statistics from
+// it (the fused verification), or store it where the logits' rows are not
+// whole 16-byte units -- an SM gets rid of about 16 bytes a cycle while all of
+// them write, so a warp that stores itself waits thousands of cycles a tile.
 // Every wait is bounded in time (l8_wait), with lm_head_kernel's teardown.
 #pragma once
 
@@ -40,11 +44,11 @@ namespace sv {
 constexpr int kL8BK = 128;    // hidden dims per step: one scale block, one swizzle row
 constexpr int kL8MaxNB = 256; // ids per tile
 constexpr int kL8AccWarps = 8;
-constexpr int kL8Threads = 128 + 32 * kL8AccWarps;
-// Registers a thread: 168 at launch (64,512 in all); the accumulators' two
-// warpgroups then take 224 and the first warpgroup keeps 56 (64,512).
-constexpr int kL8AccRegs = 224, kL8OtherRegs = 56;
-static_assert(32 * kL8AccWarps * kL8AccRegs + 128 * kL8OtherRegs <= 168 * kL8Threads, "register split");
+constexpr int kL8Threads = 256 + 32 * kL8AccWarps;
+// Registers a thread: 128 at launch (65,536 in all); the accumulators' two
+// warpgroups then take 224 and the others keep 32 (65,536).
+constexpr int kL8AccRegs = 224, kL8OtherRegs = 32;
+static_assert(32 * kL8AccWarps * kL8AccRegs + 256 * kL8OtherRegs <= 128 * kL8Threads, "register split");
 constexpr uint32_t kL8TmemCols = 2 * kL8MaxNB; // two fp32 sums of one step: all 512 columns
 constexpr int kL8MaxStages = 8;
 constexpr int kL8Chunk = 16;                                       // steps whose scales are brought in at a time
@@ -67,7 +71,7 @@ struct Lm8Params {
     const float *hs;        // [M, KB]
     const float *ws;        // [ceil(N / 128), KB]
     uint16_t *logits;       // [M, N] bf16 out
-    float2 *part;           // [M, NT * halves] (max, normaliser relative to fl(max c)), or nullptr
+    float2 *part;           // [M, NT] (max, normaliser relative to fl(max c)) per tile, or nullptr
     int32_t halves;         // column halves of a tile: 1 (NB <= 128) or 2
     float c;                // log2(e) / T
     int32_t tma;            // N % 8 == 0 and 16-byte aligned logits: tensor stores
@@ -247,17 +251,6 @@ __device__ __forceinline__ int l8_half_cols(int NB, int h)
     return h == 0 ? (NB < 128 ? NB : 128) : (NB > 128 ? NB - 128 : 0);
 }
 
-// First id, relative to the tile's, of the 32 columns from column j of half h
-// on.  On a pair a half's columns are the even CTA's rows of W, then the odd
-// one's, whose rows begin at NB / 2.
-template <bool PAIR> __device__ __forceinline__ int l8_group_id(int NB, int h, int j)
-{
-    if constexpr (!PAIR)
-        return h * 128 + j;
-    const int own = l8_half_cols(NB, h) / 2;
-    return j < own ? h * 64 + j : NB / 2 + h * 64 + j - own;
-}
-
 // Shared memory by its 32-bit address (a generic pointer would order these
 // accesses with those to global memory).
 __device__ __forceinline__ float l8_lds(uint32_t addr)
@@ -274,6 +267,16 @@ __device__ __forceinline__ float2 l8_lds2(uint32_t addr)
     return r;
 }
 
+__device__ __forceinline__ uint4 l8_lds4(uint32_t addr)
+{
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "r"(addr)
+                 : "memory");
+    return r;
+}
+
 __device__ __forceinline__ uint16_t l8_lds_u16(uint32_t addr)
 {
     uint16_t r;
@@ -281,9 +284,11 @@ __device__ __forceinline__ uint16_t l8_lds_u16(uint32_t addr)
     return r;
 }
 
-__device__ __forceinline__ void l8_sts(uint32_t addr, float v)
+// Four bytes from global memory (zero where `in` is false), without registers
+// in between.
+__device__ __forceinline__ void l8_copy4(uint32_t dst, const float *src, bool in)
 {
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
 
 __device__ __forceinline__ void l8_sts4(uint32_t addr, uint4 v)
@@ -295,7 +300,7 @@ __device__ __forceinline__ void l8_sts4(uint32_t addr, uint4 v)
 // 2 KiB in the 64-byte swizzle layout (neither side conflicts), which tensor
 // stores take out behind the warp's back -- plain stores held the accumulator
 // warps up for ~900 cycles per box.  Rows and ids past the ends are clipped by
-// the map.  Logits whose rows are not whole 16-byte units go out one by one.
+// the map.
 
 // This lane's row of a box, from 16 packed pairs.
 __device__ __forceinline__ void l8_stage(uint32_t box, const uint32_t (&pk)[16], int lane)
@@ -314,22 +319,6 @@ __device__ __forceinline__ void l8_send(const CUtensorMap *map, uint32_t box, in
                      reinterpret_cast<uint64_t>(map)),
                  "r"(n), "r"(row0), "r"(box)
                  : "memory");
-}
-
-// The same box by plain stores, a logit a lane (ncols of them in the vocabulary).
-__device__ __forceinline__ void l8_store(const Lm8Params &P, uint32_t box, int row0, int n, int ncols, int lane)
-{
-    if (lane >= ncols)
-        return;
-    const int q = lane >> 3, e = (lane & 7) * 2;
-    uint16_t *dst = P.logits + static_cast<int64_t>(row0) * P.N + n + lane;
-#pragma unroll 8
-    for (int rl = 0; rl < 32; ++rl) {
-        const uint16_t v = l8_lds_u16(box + rl * 64 + ((q ^ (rl >> 1)) & 3) * 16 + e);
-        if (row0 + rl < P.M)
-            *dst = v;
-        dst += P.N;
-    }
 }
 
 // The tensor stores this lane issued have read their shared memory.
@@ -381,7 +370,8 @@ __device__ __forceinline__ void l8_fail(const Lm8Params &P, int *stop)
 }
 
 // The scales: step kb's row scales and those of the tile's eight 32-column
-// groups, 16 steps at a time, two chunks in flight.
+// groups, 16 steps at a time, two chunks in flight, by asynchronous copies (a
+// warp that waits for loads of 68 values a lane in turn is too slow).
 template <bool PAIR>
 __device__ __forceinline__ void l8_scales(const Lm8Params &P, uint32_t tabs, uint32_t sfull, uint32_t sempty, int *stop,
                                           uint32_t rank, uint32_t unit, uint32_t units, uint32_t ntiles, int lane)
@@ -400,20 +390,20 @@ __device__ __forceinline__ void l8_scales(const Lm8Params &P, uint32_t tabs, uin
                 return;
             }
             if (kb0 + k < P.KB) {
-                const uint32_t dst = tabs + (b * kL8TabFloats + static_cast<uint32_t>(k) * kL8HsPitch) * 4u;
-                const float *src = P.hs + static_cast<int64_t>(m0) * P.KB + kb0 + k;
+                uint32_t dst = tabs + (b * kL8TabFloats + static_cast<uint32_t>(k * kL8HsPitch + sub)) * 4u;
+                const float *src = P.hs + static_cast<int64_t>(m0 + sub) * P.KB + kb0 + k;
 #pragma unroll 8
-                for (int r = sub; r < rows; r += 2)
-                    l8_sts(dst + r * 4, __ldg(src + static_cast<int64_t>(r) * P.KB));
+                for (int r = sub; r < rows; r += 2, dst += 8, src += 2 * static_cast<int64_t>(P.KB))
+                    l8_copy4(dst, src, true);
                 const uint32_t wd = tabs + (b * kL8TabFloats + kL8Chunk * kL8HsPitch + static_cast<uint32_t>(k) * 8u) * 4u;
 #pragma unroll
                 for (int g = sub; g < 8; g += 2) {
-                    const int n = n0 + l8_group_id<PAIR>(P.NB, g >> 2, (g & 3) * 32);
-                    l8_sts(wd + g * 4, (g & 3) * 32 < l8_half_cols(P.NB, g >> 2) && n < P.N
-                                           ? __ldg(P.ws + static_cast<int64_t>(n >> 7) * P.KB + kb0 + k)
-                                           : 0.0f);
+                    const int n = n0 + g * 32;
+                    const bool in = g * 32 < P.NB && n < P.N;
+                    l8_copy4(wd + g * 4, P.ws + static_cast<int64_t>(in ? n >> 7 : 0) * P.KB + kb0 + k, in);
                 }
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
             if (lane == 0)
                 l8_arrive(sfull + b * 8);
@@ -430,56 +420,130 @@ __device__ __forceinline__ void l8_fold(unsigned long long *acc, const uint32_t 
         acc[i] = fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), ff, acc[i]);
 }
 
-// A row's maximum and normaliser over a half tile, from the rounded logits.
-template <bool PAIR>
-__device__ __forceinline__ void l8_statistics(const Lm8Params &P, const unsigned long long (&acc)[64], int n0, int h,
-                                              int G, int row, int slot)
+// Whether warps 12..15 have work: logits that tensor stores can not write, or
+// the rows' statistics.
+__device__ __forceinline__ bool l8_helpers(const Lm8Params &P) { return !P.tma || P.part; }
+
+// Where column c of a staged row r is.
+__device__ __forceinline__ uint32_t l8_staged_at(uint32_t boxes, int r, int c)
+{
+    return boxes + static_cast<uint32_t>((c >> 5) * kL8BoxBytes + r * 64 + (((c >> 3) ^ (r >> 1)) & 3) * 16 + (c & 7) * 2);
+}
+
+// 8 halfwords from halfword a (0..7) on of the 16 in u, v.
+__device__ __forceinline__ uint4 l8_shift(uint4 u, uint4 v, int a)
+{
+    uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i)
+        w[i] = a & 4 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+        w[i] = a & 2 ? w[i + 1] : w[i];
+    const uint32_t sel = a & 1 ? 0x5432u : 0x3210u;
+    return make_uint4(__byte_perm(w[0], w[1], sel), __byte_perm(w[1], w[2], sel), __byte_perm(w[2], w[3], sel),
+                      __byte_perm(w[3], w[4], sel));
+}
+
+// A half tile's staged rows (ncols <= 128 ids from n on) by plain stores, at
+// whatever alignment they have: first their whole 16-byte units, 16 lanes a
+// row, each shifted out of two staged units; then the logits before the first
+// and behind the last unit (8 a row, or up to 14 where the vocabulary ends),
+// 8 lanes a row.
+__device__ __forceinline__ void l8_store_rows(const Lm8Params &P, uint32_t boxes, int row0, int n, int ncols, int lane)
+{
+    const int rows = P.M - row0 < 32 ? P.M - row0 : 32;
+    uint16_t *const dst0 = P.logits + static_cast<int64_t>(row0) * P.N + n;
+    {
+        const int u = (lane & 15) * 8;
+#pragma unroll 2
+        for (int r = lane >> 4; r < rows; r += 2) {
+            uint16_t *dst = dst0 + static_cast<int64_t>(r) * P.N;
+            const int lead = (8 - static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 1)) & 7; // columns before the first unit
+            const uint4 lo = l8_lds4(l8_staged_at(boxes, r, u));
+            const uint4 hi = l8_lds4(l8_staged_at(boxes, r, u < 120 ? u + 8 : u));
+            if (u + lead + 8 <= ncols)
+                *reinterpret_cast<uint4 *>(dst + u + lead) = l8_shift(lo, hi, lead);
+        }
+    }
+    const int c = lane & 7;
+#pragma unroll 4
+    for (int r = lane >> 3; r < rows; r += 4) {
+        uint16_t *dst = dst0 + static_cast<int64_t>(r) * P.N;
+        const int lead = (8 - static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 1)) & 7;
+        const int units = ncols > lead ? (ncols - lead) >> 3 : 0; // whole units
+        const int first = lead < ncols ? lead : ncols, edges = ncols - units * 8;
+        if (c < edges) {
+            const int p = c < first ? c : units * 8 + c;
+            dst[p] = l8_lds_u16(l8_staged_at(boxes, r, p));
+        }
+        if (c + 8 < edges) {
+            const int p = c + 8 < first ? c + 8 : units * 8 + c + 8;
+            dst[p] = l8_lds_u16(l8_staged_at(boxes, r, p));
+        }
+    }
+}
+
+// The maximum and normaliser of staged row r over the tile's first ncols ids:
+// the maximum, then the softmax terms against it, four sums side by side.
+__device__ __forceinline__ float2 l8_statistics(const Lm8Params &P, uint32_t half0, uint32_t half1, int r, int ncols)
 {
     float mx = -INFINITY;
+    for (int c = 0; c < ncols; c += 8) {
+        const uint4 v = l8_lds4(l8_staged_at(c < 128 ? half0 : half1, r, c & 127));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const int ncols = g < G ? P.N - n0 - l8_group_id<PAIR>(P.NB, h, 32 * g) : 0;
-        if (ncols >= 32) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint32_t pk = l8_round(acc[g * 16 + i]);
-                mx = fmaxf(mx, fmaxf(bf16_lo(pk), bf16_hi(pk)));
-            }
-        } else if (ncols > 0) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint32_t pk = l8_round(acc[g * 16 + i]);
-                if (2 * i < ncols)
-                    mx = fmaxf(mx, bf16_lo(pk));
-                if (2 * i + 1 < ncols)
-                    mx = fmaxf(mx, bf16_hi(pk));
-            }
+        for (int i = 0; i < 4; ++i) {
+            mx = c + 2 * i < ncols ? fmaxf(mx, bf16_lo(w[i])) : mx;
+            mx = c + 2 * i + 1 < ncols ? fmaxf(mx, bf16_hi(w[i])) : mx;
         }
     }
     const float mc = mc_of(mx, P.c);
-    float S = 0.0f;
+    float S[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = 0; c < ncols; c += 8) {
+        const uint4 v = l8_lds4(l8_staged_at(c < 128 ? half0 : half1, r, c & 127));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const int ncols = g < G ? P.N - n0 - l8_group_id<PAIR>(P.NB, h, 32 * g) : 0;
-        if (ncols >= 32) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint32_t pk = l8_round(acc[g * 16 + i]);
-                S += term(bf16_lo(pk), P.c, mc) + term(bf16_hi(pk), P.c, mc);
-            }
-        } else if (ncols > 0) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint32_t pk = l8_round(acc[g * 16 + i]);
-                if (2 * i < ncols)
-                    S += term(bf16_lo(pk), P.c, mc);
-                if (2 * i + 1 < ncols)
-                    S += term(bf16_hi(pk), P.c, mc);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float a = term(bf16_lo(w[i]), P.c, mc), b = term(bf16_hi(w[i]), P.c, mc);
+            S[i] += (c + 2 * i < ncols ? a : 0.0f) + (c + 2 * i + 1 < ncols ? b : 0.0f);
         }
     }
-    if (row < P.M)
-        P.part[static_cast<int64_t>(row) * (P.NT * P.halves) + slot] = make_float2(mx, S);
+    return make_float2(mx, (S[0] + S[1]) + (S[2] + S[3]));
+}
+
+// Warps 12..15: warp 12 + lq works on the staged rows of lane quarter lq.
+template <bool PAIR>
+__device__ __forceinline__ void l8_finish(const Lm8Params &P, uint32_t tabs, uint32_t staged, uint32_t sfree, int *stop,
+                                          uint32_t rank, uint32_t unit, uint32_t units, uint32_t ntiles, int lq, int lane)
+{
+    uint32_t odd = 0;
+    const uint32_t half0 = tabs - static_cast<uint32_t>(8 - lq) * kL8StgBytes;
+    const uint32_t half1 = half0 + 4 * kL8StgBytes;
+    for (uint32_t t = unit; t < ntiles; t += units, odd ^= 1u) {
+        if (!__all_sync(0xFFFFFFFFu, l8_wait(staged, odd))) {
+            if (lane == 0)
+                l8_fail(P, stop);
+            return;
+        }
+        const int row0 = l8_row0<PAIR>(P, t, rank, lq), tn = static_cast<int>(l8_tile_n(P, t)), n0 = tn * P.NB;
+        const int ncols = P.N - n0 < P.NB ? P.N - n0 : P.NB; // at least 1
+        if (row0 < P.M) {
+            if (!P.tma) {
+                l8_store_rows(P, half0, row0, n0, ncols < 128 ? ncols : 128, lane);
+                if (ncols > 128)
+                    l8_store_rows(P, half1, row0, n0 + 128, ncols - 128, lane);
+            }
+            if (P.part) {
+                const float2 ms = l8_statistics(P, half0, half1, lane, ncols);
+                if (row0 + lane < P.M)
+                    P.part[static_cast<int64_t>(row0 + lane) * P.NT + tn] = ms;
+            }
+        }
+        __syncwarp();
+        if (lane == 0)
+            l8_arrive(sfree);
+    }
 }
 
 // What a warp's steps go by.
@@ -573,7 +637,8 @@ __device__ __forceinline__ void l8_steps_some(L8Steps &S, unsigned long long (&a
 template <bool PAIR>
 __device__ __forceinline__ void l8_accumulate(const Lm8Params &P, const CUtensorMap *map, uint32_t tabs, uint32_t tbase,
                                               uint32_t tfull, uint32_t tempty, uint32_t sfull, uint32_t sempty,
-                                              int *stop, uint32_t rank, uint32_t unit, uint32_t units, uint32_t ntiles)
+                                              uint32_t staged, uint32_t sfree, int *stop, uint32_t rank, uint32_t unit,
+                                              uint32_t units, uint32_t ntiles)
 {
     const int warp = static_cast<int>(l8_tid() >> 5), lane = static_cast<int>(l8_tid() & 31u);
     const int h = (warp - 4) >> 2, lq = warp & 3;
@@ -586,7 +651,7 @@ __device__ __forceinline__ void l8_accumulate(const Lm8Params &P, const CUtensor
     S.tempty = (PAIR ? lm_mapa(tempty, 0) : tempty) + static_cast<uint32_t>(h) * 8u;
     S.it = 0;
     S.ok = true;
-    uint32_t chunk = 0;
+    uint32_t chunk = 0, odd = 0;
     bool alive = true;
     for (uint32_t t = unit; t < ntiles && alive; t += units) {
         const int G = l8_row0<PAIR>(P, t, rank, lq) < P.M ? groups : 0; // groups this warp folds
@@ -608,16 +673,21 @@ __device__ __forceinline__ void l8_accumulate(const Lm8Params &P, const CUtensor
             if (lane == 0) // this warp has read the chunk's scales
                 l8_arrive(sempty + sb * 8);
         }
-        if (G == 0 || !alive)
-            continue;
-        // ---- the finished half tile: logits and, per row, their statistics
+        if (!alive)
+            break;
+        // ---- the finished half tile
         const int warp = static_cast<int>(l8_tid() >> 5), lane = static_cast<int>(l8_tid() & 31u);
-        const int h = (warp - 4) >> 2, row0 = l8_row0<PAIR>(P, t, rank, warp & 3);
-        const int tn = static_cast<int>(l8_tile_n(P, t)), n0 = tn * P.NB;
         const uint32_t stg = tabs - static_cast<uint32_t>(12 - warp) * kL8StgBytes;
-        if (t != unit) // the last tile's logits have left this warp's shared memory
-            l8_stores_read();
-        __syncwarp();
+        if (t != unit) { // the last tile's has left this warp's shared memory
+            if (P.tma)
+                l8_stores_read();
+            if (l8_helpers(P))
+                alive = l8_wait(sfree, odd ^ 1u);
+        }
+        if (!__all_sync(0xFFFFFFFFu, alive)) {
+            alive = false;
+            break;
+        }
 #pragma unroll
         for (int g = 0; g < 4; ++g)
             if (g < G) {
@@ -630,25 +700,20 @@ __device__ __forceinline__ void l8_accumulate(const Lm8Params &P, const CUtensor
         if (P.tma)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (P.tma) {
-            if (l8_elect()) {
+        if (l8_elect()) {
+            if (P.tma) {
+                const int n = static_cast<int>(l8_tile_n(P, t)) * P.NB + ((warp - 4) >> 2) * 128;
+                const int row0 = l8_row0<PAIR>(P, t, rank, warp & 3);
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int n = n0 + l8_group_id<PAIR>(P.NB, h, 32 * g);
-                    if (g < G && n < P.N)
-                        l8_send(map, stg + g * kL8BoxBytes, n, row0);
-                }
+                for (int g = 0; g < 4; ++g)
+                    if (g < G && n + 32 * g < P.N)
+                        l8_send(map, stg + g * kL8BoxBytes, n + 32 * g, row0);
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
-        } else {
-#pragma unroll 1
-            for (int g = 0; g < G; ++g) {
-                const int n = n0 + l8_group_id<PAIR>(P.NB, h, 32 * g);
-                l8_store(P, stg + g * kL8BoxBytes, row0, n, P.N - n, lane);
-            }
+            if (l8_helpers(P))
+                l8_arrive(staged);
         }
-        if (P.part)
-            l8_statistics<PAIR>(P, acc, n0, h, G, row0 + lane, tn * P.halves + h);
+        odd ^= 1u;
     }
     if (!alive && lane == 0)
         l8_fail(P, stop);
@@ -665,7 +730,7 @@ __global__ void __launch_bounds__(kL8Threads, 1)
     constexpr int kCtas = PAIR ? 2 : 1;
     extern __shared__ uint8_t lm_smem_raw[];
     __shared__ __align__(8) unsigned long long full[kL8MaxStages], empty[kL8MaxStages], tfull[4], tempty[4],
-        sfull[2], sempty[2], drain;
+        sfull[2], sempty[2], staged, sfree, drain;
     __shared__ uint32_t tmem_base;
     __shared__ int stop;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(lm_smem_raw) + 1023) & ~uintptr_t{1023});
@@ -689,6 +754,8 @@ __global__ void __launch_bounds__(kL8Threads, 1)
             lm_mbar_init(smem_addr(&sfull[a]), 1);
             lm_mbar_init(smem_addr(&sempty[a]), static_cast<uint32_t>(P.halves) * kL8AccWarps / 2);
         }
+        lm_mbar_init(smem_addr(&staged), static_cast<uint32_t>(P.halves) * kL8AccWarps / 2);
+        lm_mbar_init(smem_addr(&sfree), 4);
         lm_mbar_init(smem_addr(&drain), 2);
         stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -710,13 +777,13 @@ __global__ void __launch_bounds__(kL8Threads, 1)
             bool wrapped = false;
             const uint32_t fb0 = PAIR ? lm_mapa(smem_addr(&full[0]), 0) : smem_addr(&full[0]);
             const uint32_t sbase = smem_addr(smem);
-            const int brows = P.NB / kCtas; // ids of the tile this CTA loads
+            const int brows = P.NB / kCtas; // ids of the tile this CTA loads: its share of each half
+            const int box = l8_half_cols(P.NB, 0) / kCtas;
             const uint32_t bytes = static_cast<uint32_t>(kCtas * (P.a_rows + brows) * kL8BK);
             bool ok = true;
             for (uint32_t t = unit; t < ntiles && ok; t += units) {
                 const int m0 = static_cast<int>((l8_tile_m(P, t) * kCtas + rank) * kLmBM);
-                const int n0 =
-                    static_cast<int>(l8_tile_n(P, t)) * P.NB + static_cast<int>(rank) * brows;
+                const int n0 = static_cast<int>(l8_tile_n(P, t)) * P.NB + static_cast<int>(rank) * box;
                 for (int kb = 0; kb < P.KB; ++kb) {
                     if (wrapped &&
                         !__all_sync(0xFFFFFFFFu, l8_wait(smem_addr(&empty[s]), ph ^ 1u))) {
@@ -729,7 +796,10 @@ __global__ void __launch_bounds__(kL8Threads, 1)
                         if (leader)
                             lm_mbar_expect(smem_addr(&full[s]), bytes);
                         l8_tma_2d<PAIR>(sa, &tmA, kb * kL8BK, m0, fb);
-                        l8_tma_2d<PAIR>(sa + static_cast<uint32_t>(P.a_rows * kL8BK), &tmB, kb * kL8BK, n0, fb);
+                        const uint32_t sb = sa + static_cast<uint32_t>(P.a_rows * kL8BK);
+                        l8_tma_2d<PAIR>(sb, &tmB, kb * kL8BK, n0, fb);
+                        if (PAIR && P.halves == 2)
+                            l8_tma_2d<PAIR>(sb + static_cast<uint32_t>(box * kL8BK), &tmB, kb * kL8BK, n0 + 128, fb);
                     }
                     __syncwarp();
                     if (++s == P.stages) {
@@ -782,11 +852,16 @@ __global__ void __launch_bounds__(kL8Threads, 1)
         } else {
             l8_scales<PAIR>(P, tabs, smem_addr(&sfull[0]), smem_addr(&sempty[0]), &stop, rank, unit, units, ntiles, lane);
         }
-    } else {
+    } else if (warp < 12) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kL8AccRegs));
-        l8_accumulate<PAIR>(P, &tmC, tabs, tbase, smem_addr(&tfull[0]),
-                            smem_addr(&tempty[0]), smem_addr(&sfull[0]), smem_addr(&sempty[0]), &stop, rank, unit,
-                            units, ntiles);
+        l8_accumulate<PAIR>(P, &tmC, tabs, tbase, smem_addr(&tfull[0]), smem_addr(&tempty[0]), smem_addr(&sfull[0]),
+                            smem_addr(&sempty[0]), smem_addr(&staged), smem_addr(&sfree), &stop, rank, unit, units,
+                            ntiles);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kL8OtherRegs));
+        if (l8_helpers(P))
+            l8_finish<PAIR>(P, tabs, smem_addr(&staged), smem_addr(&sfree), &stop, rank, unit, units, ntiles, warp - 12,
+                            lane);
     }
     // ---- teardown: copies and MMAs in flight complete before the memory goes
     lm_tc_before();

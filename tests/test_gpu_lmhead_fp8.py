@@ -37,7 +37,9 @@ def _bits(t):
 # stores), d below one block, ending inside a block, wrapping the ring
 SHAPES = [(1, 256, 128), (1, 1, 16), (5, 7, 16), (31, 33, 112), (33, 300, 144), (45, 1001, 1040), (127, 520, 256),
           (128, 5000, 272), (129, 2056, 512), (130, 31, 128), (200, 9999, 144), (256, 777, 1024), (257, 1000, 384),
-          (300, 4097, 640), (513, 512, 2048), (40, 20000, 4096), (3, 45000, 64)]
+          (300, 4097, 640), (513, 512, 2048), (40, 20000, 4096), (3, 45000, 64),
+          # wide tiles whose rows start at every alignment: vocabularies 3, 1, 6, 4 and 7 above a multiple of 8
+          (131, 32003, 144), (260, 40001, 128), (50, 36006, 128), (7, 44004, 16), (129, 65527, 32)]
 
 
 @pytest.mark.parametrize("M,V,d", SHAPES, ids=[f"M{m}_V{v}_d{d}" for m, v, d in SHAPES])
@@ -106,6 +108,20 @@ def test_logits_write_only_their_buffer():
         torch.cuda.synchronize()
         assert o.guards_intact() and st.guards_intact() and int(st.t.item()) == 0
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(ops, keep))
+
+
+@pytest.mark.parametrize("shift", [1, 2, 5])
+@pytest.mark.parametrize("M,V", [(5, 40008), (140, 32008), (3, 77)])
+def test_logits_at_any_alignment(M, V, shift):
+    """An output that starts between 16-byte boundaries (a slice of a larger
+    buffer): the same logits, and nothing around them."""
+    ops = _dev(R.head_operands(M, V, 80, seed=shift))
+    want = sv.sv_lm_head_logits_fp8(*ops)
+    buf = torch.full((M * V + 16,), -7.0, dtype=torch.bfloat16, device=DEV)
+    out = buf[shift:shift + M * V].view(M, V)
+    sv.sv_lm_head_logits_fp8(*ops, out=out)
+    assert torch.equal(out, want)
+    assert (buf[:shift] == -7).all() and (buf[shift + M * V:] == -7).all()
 
 
 def test_offsets_past_32_bits():
