@@ -228,6 +228,19 @@ __device__ __forceinline__ bool l8_wait(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
+// Whether phase `parity` of `bar` is complete, without waiting.
+__device__ __forceinline__ uint32_t l8_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok;
+}
+
 // Instruction descriptor: D fp32, A and B e4m3 (format 0), both K-major.
 inline uint32_t l8_idesc(int rows, int ids)
 {
@@ -560,6 +573,20 @@ struct L8Steps {
         __syncwarp();
         lm_tc_after();
     }
+    // A wait costs ~180 cycles even where nothing is to be waited for, so the
+    // next step's sums are asked for early, and waited for only if they were
+    // not there.
+    __device__ __forceinline__ uint32_t next_there() const
+    {
+        return l8_test(tfull + ((it + 1u) & 1u) * 16u, ((it + 1u) >> 1) & 1u);
+    }
+    __device__ __forceinline__ void wait_unless(uint32_t there)
+    {
+        if (!__all_sync(0xFFFFFFFFu, there != 0))
+            wait();
+        else
+            lm_tc_after();
+    }
     __device__ __forceinline__ uint32_t buffer() const { return tl + (it & 1u) * kL8MaxNB; }
     __device__ __forceinline__ void release() const // this warp has read the step's sums
     {
@@ -595,6 +622,7 @@ __device__ __forceinline__ void l8_steps_full(L8Steps &S, unsigned long long (&a
         l8_ld_start(S.buffer() + 64, v0);
         l8_fold(acc + 16, v1, __fmul_rn(hs, ws.y));
         l8_ld_start(S.buffer() + 96, v1);
+        const uint32_t there = S.next_there();
         ws = l8_lds2(S.wsp + 8);
         l8_ld_wait(v0);
         l8_ld_tie(v1);
@@ -602,7 +630,7 @@ __device__ __forceinline__ void l8_steps_full(L8Steps &S, unsigned long long (&a
         S.next();
         l8_fold(acc + 32, v0, __fmul_rn(hs, ws.x));
         if (steps > 1) {
-            S.wait();
+            S.wait_unless(there);
             l8_ld_start(S.buffer(), v0);
         }
         l8_fold(acc + 48, v1, __fmul_rn(hs, ws.y));
