@@ -708,6 +708,8 @@ sv_status_t lm_finish(const Plan &plan, float2 *part, int32_t slots, const void 
 
 // ------------------------------------------------- norms and quantisation
 
+constexpr int64_t kNormManyRows = 4 * kNominalSms;
+
 size_t elem_size(sv_dtype_t t) { return t == SV_BF16 ? 2 : (t == SV_FP32 ? 4 : 1); }
 
 bool is_bf16_or_fp32(sv_dtype_t t) { return t == SV_BF16 || t == SV_FP32; }
@@ -1035,11 +1037,15 @@ sv_status_t sv_block_norm(const void *x, sv_dtype_t x_dtype, const void *residua
     P.w_type = weight_dtype;
     P.h_type = hidden_dtype;
     P.M = M;
-    P.gate_div = gate ? M / gate_rows : 1;
+    P.gate_div = static_cast<uint32_t>(gate ? M / gate_rows : 1);
     P.d = d;
     const int segs = static_cast<int>(ceil_div(d, sv::kSeg));
+    // One segment a warp gives a few rows the shortest chain; enough rows to
+    // fill the GPU take two, for half the instructions spent on sums and
+    // addresses.
+    const int per_warp = M >= kNormManyRows ? 2 : 1;
     P.WPR = 1;
-    while (P.WPR < segs && P.WPR < sv::kNormMaxWarps)
+    while (P.WPR * per_warp < segs && P.WPR < sv::kNormMaxWarps)
         P.WPR *= 2;
     P.RPC = P.WPR < 4 ? 4 / P.WPR : 1;
     int nseg = 1;
@@ -1093,7 +1099,9 @@ sv_status_t sv_quantize_fp8(const void *x, sv_dtype_t x_dtype, int64_t rows, int
         else
             sv::quantize_rows_kernel<false><<<g, sv::kQuantWarps * 32, 0, s>>>(P);
     } else {
-        if (vec)
+        if (!vec)
+            sv::quantize_tiles_odd_kernel<<<g, sv::kQuantWarps * 32, 0, s>>>(P);
+        else if (x_dtype == SV_FP32)
             sv::quantize_tiles_kernel<true><<<g, sv::kQuantWarps * 32, 0, s>>>(P);
         else
             sv::quantize_tiles_kernel<false><<<g, sv::kQuantWarps * 32, 0, s>>>(P);

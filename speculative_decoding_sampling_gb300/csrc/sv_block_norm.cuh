@@ -182,25 +182,28 @@ __device__ __forceinline__ void seg_quantize(float (&v)[8], void *row, float *sc
 struct NormParams {
     const void *x, *residual, *post, *gate, *pre;
     int32_t x_type, r_type, w_type, h_type;
-    int64_t M, gate_div; // row m is gated by row m / gate_div of the gate
-    int32_t d, WPR, RPC; // warps per row, rows per CTA
+    int64_t M;
+    uint32_t gate_div;   // row m is gated by row m / gate_div of the gate
+    int32_t d, WPR, RPC; // warps per row (a power of two), rows per CTA
     float offset, rs, bs, eps, inv_d;
     void *r_out, *h;
     float *scales; // [M, ceil(d / 128)] (e4m3 h)
 };
 
-// sum over the warps of a row; `red` has one float per warp of the CTA
+// Sum over the warps of a row; `red` has one float per warp of the CTA.  Every
+// lane forms the same sum in the same order.
 __device__ __forceinline__ float row_sum(float v, float *red, int warp, int first, int WPR)
 {
     v = warp_sum_f(v);
     if (WPR == 1)
         return v;
-    if ((threadIdx.x & 31) == 0)
+    const int lane = threadIdx.x & 31;
+    if (lane == 0)
         red[warp] = v;
     __syncthreads();
-    float s = 0.0f;
-    for (int i = 0; i < WPR; ++i)
-        s = __fadd_rn(s, red[first + i]);
+    float s = red[first + (lane & (WPR - 1))];
+    for (int o = WPR >> 1; o > 0; o >>= 1)
+        s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
     return s;
 }
 
@@ -226,7 +229,31 @@ __global__ void __launch_bounds__(kNormMaxWarps * 32) block_norm_kernel(const No
         seg_load<VEC>(v[s], row_of(P.x, rr, P.d, P.x_type), P.x_type, base, lane, d);
         seg_load<VEC>(r[s], row_of(P.residual, rr, P.d, P.r_type), P.r_type, base, lane, d);
     }
-    if (P.post) {
+    // g: the gate, times the post norm's weight where there is one; on its way
+    // while the first sum is formed
+    float g[NSEG][8];
+    const bool post = P.post != nullptr, gated = P.gate != nullptr;
+    if (post || gated) {
+        const char *grow = gated ? row_of(P.gate, static_cast<uint32_t>(rr) / P.gate_div, P.d, P.x_type) : nullptr;
+#pragma unroll
+        for (int s = 0; s < NSEG; ++s) {
+            const int base = (s * P.WPR + wr) * kSeg;
+            if (post) {
+                seg_load<VEC>(g[s], P.post, P.w_type, base, lane, d);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    g[s][i] += P.offset;
+            }
+            if (gated) {
+                float w[8];
+                seg_load<VEC>(w, grow, P.x_type, base, lane, d);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    g[s][i] = post ? g[s][i] * w[i] : w[i];
+            }
+        }
+    }
+    if (post) {
         float q = 0.0f;
 #pragma unroll
         for (int s = 0; s < NSEG; ++s)
@@ -235,41 +262,37 @@ __global__ void __launch_bounds__(kNormMaxWarps * 32) block_norm_kernel(const No
                 q = __fmaf_rn(v[s][i], v[s][i], q);
         const float f = rsqrtf(__fmaf_rn(row_sum(q, red[0], warp, first, P.WPR), P.inv_d, P.eps));
 #pragma unroll
-        for (int s = 0; s < NSEG; ++s) {
-            float w[8];
-            seg_load<VEC>(w, P.post, P.w_type, (s * P.WPR + wr) * kSeg, lane, d);
+        for (int s = 0; s < NSEG; ++s)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[s][i] = v[s][i] * f * (w[i] + P.offset);
-        }
+                v[s][i] *= f;
     }
     float q = 0.0f;
 #pragma unroll
     for (int s = 0; s < NSEG; ++s) {
-        const int base = (s * P.WPR + wr) * kSeg;
-        if (P.gate) {
-            float g[8];
-            seg_load<VEC>(g, row_of(P.gate, rr / P.gate_div, P.d, P.x_type), P.x_type, base, lane, d);
+        if (post || gated) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[s][i] *= g[i];
+                v[s][i] *= g[s][i];
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             r[s][i] = __fmaf_rn(P.bs, v[s][i], __fmul_rn(P.rs, r[s][i]));
             q = __fmaf_rn(r[s][i], r[s][i], q);
         }
-        seg_store<VEC>(r[s], const_cast<char *>(row_of(P.r_out, rr, P.d, P.r_type)), P.r_type, base, lane, d);
+        seg_store<VEC>(r[s], const_cast<char *>(row_of(P.r_out, rr, P.d, P.r_type)), P.r_type,
+                       (s * P.WPR + wr) * kSeg, lane, d);
     }
+#pragma unroll
+    for (int s = 0; s < NSEG; ++s) // the norm's weight, before the second sum
+        seg_load<VEC>(g[s], P.pre, P.w_type, (s * P.WPR + wr) * kSeg, lane, d);
     const float f = rsqrtf(__fmaf_rn(row_sum(q, red[1], warp, first, P.WPR), P.inv_d, P.eps));
 #pragma unroll
     for (int s = 0; s < NSEG; ++s) {
         const int base = (s * P.WPR + wr) * kSeg;
-        float w[8];
-        seg_load<VEC>(w, P.pre, P.w_type, base, lane, d);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            r[s][i] = r[s][i] * f * (w[i] + P.offset);
+            r[s][i] = r[s][i] * f * (g[s][i] + P.offset);
         if (P.h_type == kElemE4m3)
             seg_quantize<VEC>(r[s], static_cast<uint8_t *>(P.h) + rr * P.d,
                               P.scales + rr * ((P.d + 127) / 128), base, lane, d);
@@ -307,72 +330,124 @@ template <bool VEC> __global__ void __launch_bounds__(kQuantWarps * 32) quantize
 }
 
 // A scale per 128 x 128 block: a CTA per block, held in registers (64 values
-// a thread).  VEC: a half-warp per row, 8 consecutive values a lane;
-// otherwise 4 single values of a row per lane.
-template <bool VEC> __global__ void __launch_bounds__(kQuantWarps * 32) quantize_tiles_kernel(const QuantParams P)
+// a thread; bf16 ones stay packed until they are scaled, so that more CTAs are
+// resident).  VEC: a half-warp per row, 8 consecutive values a lane; otherwise
+// 4 single values of a row per lane.
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b)
 {
-    __shared__ float red[kQuantWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t rb = blockIdx.x / P.segs;
-    const int cb = static_cast<int>(blockIdx.x - rb * P.segs);
-    float v[8][8];
-    float amax = 0.0f;
-    // value (s, i) of this thread: row and column inside the block
-    auto at_row = [&](int s, int i) { return VEC ? s * 16 + warp * 2 + (lane >> 4) : s * 16 + warp * 2 + (i >> 2); };
-    auto at_col = [&](int i) { return VEC ? (lane & 15) * 8 + i : (i & 3) * 32 + lane; };
-#pragma unroll
-    for (int s = 0; s < 8; ++s) {
-        if constexpr (VEC) {
-            const int64_t row = rb * 128 + at_row(s, 0);
-            // the loader's lane index selects 8 values from `base` on
-            const int base = cb * 128 + (lane & 15) * 8 - lane * 8;
-            seg_load<true>(v[s], row_of(P.x, row < P.M ? row : 0, P.d, P.x_type), P.x_type, base, lane,
-                           row < P.M ? P.d : 0);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t row = rb * 128 + at_row(s, i);
-                const int e = cb * 128 + at_col(i);
-                v[s][i] = 0.0f;
-                if (row < P.M && e < P.d)
-                    v[s][i] = elem_at(P.x, P.x_type, row * P.d + e);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            amax = max_nan(amax, fabsf(v[s][i]));
-    }
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// The block's scale and its reciprocal, from every thread's largest magnitude.
+__device__ __forceinline__ float tile_scale(float amax, float *red, float *scale_out)
+{
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    if (lane == 0)
-        red[warp] = amax;
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = amax;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kQuantWarps; ++w)
         amax = max_nan(amax, red[w]);
-    const float s = block_scale(amax), inv = __frcp_rn(s);
+    const float s = block_scale(amax);
     if (threadIdx.x == 0)
-        P.scales[blockIdx.x] = s;
+        *scale_out = s;
+    return __frcp_rn(s);
+}
+
+__device__ __forceinline__ uint32_t e4m3x4_scaled(float a, float b, float c, float d, float inv)
+{
+    return e4m3x2_rn(__fmul_rn(a, inv), __fmul_rn(b, inv)) | e4m3x2_rn(__fmul_rn(c, inv), __fmul_rn(d, inv)) << 16;
+}
+
+template <bool FP32> __global__ void __launch_bounds__(kQuantWarps * 32) quantize_tiles_kernel(const QuantParams P)
+{
+    __shared__ float red[kQuantWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t segs = static_cast<uint32_t>(P.segs), rb = blockIdx.x / segs, cb = blockIdx.x - rb * segs;
+    const int64_t row0 = static_cast<int64_t>(rb) * 128 + warp * 2 + (lane >> 4); // rows row0, row0 + 16, ...
+    const int e = static_cast<int>(cb) * 128 + (lane & 15) * 8;
+    const int rows = P.M - row0 <= 0 || e >= P.d ? 0 : P.M - row0 < 128 ? static_cast<int>(P.M - row0 + 15) / 16 : 8;
+    uint4 v[8][FP32 ? 2 : 1];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int s = 0; s < 8; ++s) {
+        const int64_t at = (row0 + s * 16) * P.d + e;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[k][i] = __fmul_rn(v[k][i], inv);
-        if constexpr (VEC) {
-            const int64_t row = rb * 128 + at_row(k, 0);
-            if (row < P.M)
-                seg_store<true>(v[k], P.v + row * P.d, kElemE4m3, cb * 128 + (lane & 15) * 8 - lane * 8, lane, P.d);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t row = rb * 128 + at_row(k, i);
-                const int e = cb * 128 + at_col(i);
-                if (row < P.M && e < P.d)
-                    P.v[row * P.d + e] = static_cast<uint8_t>(e4m3x2_rn(v[k][i], 0.0f));
-            }
-        }
+        for (int i = 0; i < (FP32 ? 2 : 1); ++i)
+            v[s][i] = s < rows ? *reinterpret_cast<const uint4 *>(static_cast<const char *>(P.x) +
+                                                                  at * (FP32 ? 4 : 2) + i * 16)
+                               : make_uint4(0, 0, 0, 0);
     }
+    float amax = 0.0f;
+    if constexpr (FP32) {
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                amax = max_nan(max_nan(max_nan(amax, fabsf(__uint_as_float(v[s][i].x))),
+                                       fabsf(__uint_as_float(v[s][i].y))),
+                               max_nan(fabsf(__uint_as_float(v[s][i].z)), fabsf(__uint_as_float(v[s][i].w))));
+    } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            m = max_nan_bf16x2(m, v[s][0].x & 0x7FFF7FFFu);
+            m = max_nan_bf16x2(m, v[s][0].y & 0x7FFF7FFFu);
+            m = max_nan_bf16x2(m, v[s][0].z & 0x7FFF7FFFu);
+            m = max_nan_bf16x2(m, v[s][0].w & 0x7FFF7FFFu);
+        }
+        amax = max_nan(bf16_lo(m), bf16_hi(m));
+    }
+    const float inv = tile_scale(amax, red, P.scales + blockIdx.x);
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+        uint2 o;
+        if constexpr (FP32) {
+            const uint4 a = v[s][0], b = v[s][1];
+            o.x = e4m3x4_scaled(__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w), inv);
+            o.y = e4m3x4_scaled(__uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w), inv);
+        } else {
+            const uint4 a = v[s][0];
+            o.x = e4m3x4_scaled(bf16_lo(a.x), bf16_hi(a.x), bf16_lo(a.y), bf16_hi(a.y), inv);
+            o.y = e4m3x4_scaled(bf16_lo(a.z), bf16_hi(a.z), bf16_lo(a.w), bf16_hi(a.w), inv);
+        }
+        if (s < rows)
+            *reinterpret_cast<uint2 *>(P.v + (row0 + s * 16) * P.d + e) = o;
+    }
+}
+
+// Rows that are not whole 16-byte units.
+__global__ void __launch_bounds__(kQuantWarps * 32) quantize_tiles_odd_kernel(const QuantParams P)
+{
+    __shared__ float red[kQuantWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t segs = static_cast<uint32_t>(P.segs), rb = blockIdx.x / segs, cb = blockIdx.x - rb * segs;
+    const int64_t row0 = static_cast<int64_t>(rb) * 128 + warp; // rows row0, row0 + 8, ...
+    const int e0 = static_cast<int>(cb) * 128 + lane;           // columns e0, e0 + 32, ...
+    float v[16][4];
+    float amax = 0.0f;
+#pragma unroll
+    for (int s = 0; s < 16; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t row = row0 + s * 8;
+            const int e = e0 + i * 32;
+            v[s][i] = row < P.M && e < P.d ? elem_at(P.x, P.x_type, row * P.d + e) : 0.0f;
+            amax = max_nan(amax, fabsf(v[s][i]));
+        }
+    const float inv = tile_scale(amax, red, P.scales + blockIdx.x);
+#pragma unroll
+    for (int s = 0; s < 16; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t row = row0 + s * 8;
+            const int e = e0 + i * 32;
+            if (row < P.M && e < P.d)
+                P.v[row * P.d + e] = static_cast<uint8_t>(e4m3x2_rn(__fmul_rn(v[s][i], inv), 0.0f));
+        }
 }
 
 } // namespace sv
