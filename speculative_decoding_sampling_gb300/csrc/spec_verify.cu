@@ -737,6 +737,31 @@ template <bool VEC> cudaError_t norm_launch(const sv::NormParams &P, int nseg, u
     return cudaGetLastError();
 }
 
+template <bool XF32, bool RF32> cudaError_t norm_rows_launch(sv::NormParams P, cudaStream_t s)
+{
+    auto *kernel = sv::block_norm_rows_kernel<XF32, RF32>;
+    P.WPR = 1;
+    while (P.WPR * sv::kNormCols < P.d)
+        P.WPR *= 2;
+    const int threads = P.WPR * 32;
+    const size_t smem = static_cast<size_t>(sv::kNormRing) * 16 * ((XF32 ? 4 : 2) + (RF32 ? 4 : 2)) * threads;
+    int dev = 0, sms = 0, per_sm = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && smem > 48 * 1024)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess)
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+    if (e != cudaSuccess)
+        return e;
+    if (per_sm < 1)
+        return cudaErrorInvalidConfiguration;
+    const int64_t resident = static_cast<int64_t>(sms > 0 ? sms : 1) * per_sm;
+    kernel<<<static_cast<unsigned>(P.M < resident ? P.M : resident), threads, smem, s>>>(P);
+    return cudaGetLastError();
+}
+
 static_assert(int(sv::kElemBf16) == int(SV_BF16) && int(sv::kElemFp32) == int(SV_FP32) &&
                   int(sv::kElemE4m3) == int(SV_E4M3),
               "element types");
@@ -1040,12 +1065,8 @@ sv_status_t sv_block_norm(const void *x, sv_dtype_t x_dtype, const void *residua
     P.gate_div = static_cast<uint32_t>(gate ? M / gate_rows : 1);
     P.d = d;
     const int segs = static_cast<int>(ceil_div(d, sv::kSeg));
-    // One segment a warp gives a few rows the shortest chain; enough rows to
-    // fill the GPU take two, for half the instructions spent on sums and
-    // addresses.
-    const int per_warp = M >= kNormManyRows ? 2 : 1;
     P.WPR = 1;
-    while (P.WPR * per_warp < segs && P.WPR < sv::kNormMaxWarps)
+    while (P.WPR < segs && P.WPR < sv::kNormMaxWarps)
         P.WPR *= 2;
     P.RPC = P.WPR < 4 ? 4 / P.WPR : 1;
     int nseg = 1;
@@ -1064,6 +1085,13 @@ sv_status_t sv_block_norm(const void *x, sv_dtype_t x_dtype, const void *residua
                      vec_ok(post_weight, weight_dtype) && vec_ok(norm_weight, weight_dtype) && vec_ok(gate, x_dtype);
     const unsigned grid = static_cast<unsigned>(ceil_div(M, P.RPC));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // rows enough for every SM to walk several: CTAs that stay
+    if (vec && d <= sv::kNormRowsMaxD && M >= kNormManyRows) {
+        const bool xf = x_dtype == SV_FP32, rf = residual_dtype == SV_FP32;
+        const cudaError_t e = xf ? (rf ? norm_rows_launch<true, true>(P, s) : norm_rows_launch<true, false>(P, s))
+                                 : (rf ? norm_rows_launch<false, true>(P, s) : norm_rows_launch<false, false>(P, s));
+        return e == cudaSuccess ? SV_OK : SV_ECUDA;
+    }
     return (vec ? norm_launch<true>(P, nseg, grid, s) : norm_launch<false>(P, nseg, grid, s)) == cudaSuccess ? SV_OK
                                                                                                         : SV_ECUDA;
 }

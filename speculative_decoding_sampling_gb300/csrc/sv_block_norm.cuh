@@ -137,6 +137,11 @@ __device__ __forceinline__ float max_nan(float a, float b)
 
 __device__ __forceinline__ float block_scale(float amax) { return __fdiv_rn(max_nan(amax, kAmaxFloor), kE4m3Max); }
 
+__device__ __forceinline__ uint32_t e4m3x4_scaled(float a, float b, float c, float d, float inv)
+{
+    return e4m3x2_rn(__fmul_rn(a, inv), __fmul_rn(b, inv)) | e4m3x2_rn(__fmul_rn(c, inv), __fmul_rn(d, inv)) << 16;
+}
+
 // A segment's two blocks of 128 as e4m3 with their scales.  VEC: lanes 0..15
 // hold the first block, 16..31 the second; otherwise values 0..3 of every
 // lane the first, 4..7 the second.
@@ -202,8 +207,10 @@ __device__ __forceinline__ float row_sum(float v, float *red, int warp, int firs
         red[warp] = v;
     __syncthreads();
     float s = red[first + (lane & (WPR - 1))];
-    for (int o = WPR >> 1; o > 0; o >>= 1)
-        s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
+#pragma unroll
+    for (int o = kNormMaxWarps / 2; o > 0; o >>= 1)
+        if (o < WPR)
+            s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
     return s;
 }
 
@@ -301,6 +308,218 @@ __global__ void __launch_bounds__(kNormMaxWarps * 32) block_norm_kernel(const No
     }
 }
 
+// Many rows: CTAs that stay, each with a run of consecutive rows.  A lane has
+// the same 16 columns in every row, so the norm's weight is read and converted
+// once and the branch's factors (gate, post norm's weight) once per gate row;
+// its pieces of the next rows' x and residual are on their way into its own
+// slots of shared memory (asynchronous copies that no other thread waits for)
+// while this row's sums are formed.  A warp has 512 columns, lane l the four
+// from 4 l on of each 128: every access covers whole sectors (a lane's 16
+// consecutive columns would write fp32 rows in half sectors, twice as many
+// transactions), and a block's largest magnitude is one warp-wide maximum of
+// its bits, above which NaNs lie.  Pairs of values go through the packed fp32
+// instructions.  Rows of whole 16-byte units, up to 512 columns a warp.
+constexpr int kNormRing = 4; // rows in flight, this one included
+constexpr int kNormCols = 512;
+constexpr int kNormRowsMaxD = kNormMaxWarps * kNormCols;
+
+template <bool FP32> __device__ __forceinline__ void lane_fetch(uint8_t *slot, int pitch, const char *src, int left)
+{
+    constexpr int size = FP32 ? 4 : 2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i * 128 < left)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(slot + i * pitch)),
+                         "l"(src + i * 128 * size), "n"(4 * size)
+                         : "memory");
+}
+
+template <bool FP32>
+__device__ __forceinline__ void lane_take(unsigned long long (&v)[8], const uint8_t *slot, int pitch, int left)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = v[2 * i + 1] = 0;
+        if (i * 128 < left) {
+            if constexpr (FP32) {
+                const uint4 a = lds_v4(slot + i * pitch);
+                v[2 * i] = pack2(__uint_as_float(a.x), __uint_as_float(a.y));
+                v[2 * i + 1] = pack2(__uint_as_float(a.z), __uint_as_float(a.w));
+            } else {
+                uint32_t x, y;
+                asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x), "=r"(y) : "r"(smem_addr(slot + i * pitch)));
+                v[2 * i] = pack2(bf16_lo(x), bf16_hi(x));
+                v[2 * i + 1] = pack2(bf16_lo(y), bf16_hi(y));
+            }
+        }
+    }
+}
+
+// A lane's values of a weight or gate row (`row` at the lane's first column),
+// plus `offset`; 1 past the row's end.
+__device__ __forceinline__ void lane_weights(unsigned long long (&w)[8], const char *row, int type, int left,
+                                             float offset)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float t[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+        if (i * 128 < left) {
+            if (type == kElemBf16) {
+                const uint2 q = *reinterpret_cast<const uint2 *>(row + i * 256);
+                t[0] = bf16_lo(q.x), t[1] = bf16_hi(q.x), t[2] = bf16_lo(q.y), t[3] = bf16_hi(q.y);
+            } else {
+                const float4 q = *reinterpret_cast<const float4 *>(row + i * 512);
+                t[0] = q.x, t[1] = q.y, t[2] = q.z, t[3] = q.w;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                t[k] += offset;
+        }
+        w[2 * i] = pack2(t[0], t[1]);
+        w[2 * i + 1] = pack2(t[2], t[3]);
+    }
+}
+
+// A lane's values to a row of bf16 or fp32 (`row` at the lane's first column).
+__device__ __forceinline__ void lane_store(const unsigned long long (&v)[8], char *row, bool fp32, int left)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i * 128 < left) {
+            float a, b, c, d;
+            unpack2(v[2 * i], a, b);
+            unpack2(v[2 * i + 1], c, d);
+            if (fp32)
+                *reinterpret_cast<float4 *>(row + i * 512) = make_float4(a, b, c, d);
+            else
+                *reinterpret_cast<uint2 *>(row + i * 256) = make_uint2(bf16x2_rn(a, b), bf16x2_rn(c, d));
+        }
+}
+
+__device__ __forceinline__ float sum_squares(const unsigned long long (&v)[8])
+{
+    unsigned long long q = mul2(v[0], v[0]), p = mul2(v[1], v[1]);
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) {
+        q = fma2(v[i], v[i], q);
+        p = fma2(v[i + 1], v[i + 1], p);
+    }
+    float a, b;
+    unpack2(add2(q, p), a, b);
+    return __fadd_rn(a, b);
+}
+
+template <bool XF32, bool RF32>
+__global__ void __launch_bounds__(kNormMaxWarps * 32, 1) block_norm_rows_kernel(const NormParams P)
+{
+    constexpr int kXSize = XF32 ? 4 : 2, kRSize = RF32 ? 4 : 2;
+    constexpr int kXType = XF32 ? kElemFp32 : kElemBf16;
+    extern __shared__ __align__(16) uint8_t norm_smem[]; // [ring][x's 4 pieces, then the residual's][thread]
+    __shared__ float red[2][2][kNormMaxWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = P.d;
+    const int e = warp * kNormCols + lane * 4, left = d - e; // first column; piece i is in the row where 128 i < left
+    const int threads = static_cast<int>(blockDim.x), slot_bytes = threads * 16 * (kXSize + kRSize);
+    uint8_t *own_x = norm_smem + threadIdx.x * 4 * kXSize;
+    uint8_t *own_r = norm_smem + threads * 16 * kXSize + threadIdx.x * 4 * kRSize;
+    const bool post = P.post != nullptr, gated = P.gate != nullptr;
+    const int64_t begin = P.M * blockIdx.x / gridDim.x, end = P.M * (blockIdx.x + 1) / gridDim.x;
+    const int wsize = P.w_type == kElemBf16 ? 2 : 4, hsize = P.h_type == kElemE4m3 ? 1 : P.h_type == kElemBf16 ? 2 : 4;
+    const char *wpost = static_cast<const char *>(P.post) + e * wsize;
+    const unsigned long long rs = pack2(P.rs, P.rs);
+    unsigned long long wpre[8], branch[8];
+    lane_weights(wpre, static_cast<const char *>(P.pre) + e * wsize, P.w_type, left, P.offset);
+    lane_weights(branch, wpost, P.w_type, post ? left : 0, P.offset);
+    // where this lane's columns of the next row to fetch, and of this row, are
+    const char *x = static_cast<const char *>(P.x) + (begin * d + e) * kXSize;
+    const char *res = static_cast<const char *>(P.residual) + (begin * d + e) * kRSize;
+    char *r_out = static_cast<char *>(P.r_out) + (begin * d + e) * kRSize;
+    char *h = static_cast<char *>(P.h) + (begin * d + e) * hsize;
+    float *scales = P.scales + begin * ((d + 127) / 128) + warp * 4 + (lane & 3);
+    int to_fetch = static_cast<int>(end - begin);
+    auto fetch = [&](int slot) {
+        if (to_fetch-- > 0) {
+            lane_fetch<XF32>(own_x + slot * slot_bytes, threads * 4 * kXSize, x, left);
+            lane_fetch<RF32>(own_r + slot * slot_bytes, threads * 4 * kRSize, res, left);
+            x += static_cast<int64_t>(d) * kXSize;
+            res += static_cast<int64_t>(d) * kRSize;
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kNormRing - 1; ++i)
+        fetch(i);
+    uint32_t gate_left = 0; // rows that the factors in `branch` still serve
+    int slot = 0, odd = 0;
+#pragma unroll 1
+    for (int64_t row = begin; row < end; ++row, odd ^= 1) {
+        fetch(slot == 0 ? kNormRing - 1 : slot - 1); // the slot this lane has read last
+        if (gated && gate_left == 0) {
+            const uint32_t g = static_cast<uint32_t>(row) / P.gate_div;
+            gate_left = (g + 1) * P.gate_div - static_cast<uint32_t>(row);
+            lane_weights(branch, static_cast<const char *>(P.gate) + (static_cast<int64_t>(g) * d + e) * kXSize, kXType,
+                         left, 0.0f);
+            if (post) {
+                unsigned long long w[8];
+                lane_weights(w, wpost, P.w_type, left, P.offset);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    branch[i] = mul2(branch[i], w[i]);
+            }
+        }
+        --gate_left;
+        cp_async_wait<kNormRing - 1>();
+        unsigned long long v[8], r[8];
+        lane_take<XF32>(v, own_x + slot * slot_bytes, threads * 4 * kXSize, left);
+        lane_take<RF32>(r, own_r + slot * slot_bytes, threads * 4 * kRSize, left);
+        slot = slot == kNormRing - 1 ? 0 : slot + 1;
+        float f = P.bs;
+        if (post)
+            f *= rsqrtf(__fmaf_rn(row_sum(sum_squares(v), red[0][odd], warp, 0, P.WPR), P.inv_d, P.eps));
+        const unsigned long long ff = pack2(f, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            r[i] = fma2(mul2(v[i], branch[i]), ff, mul2(r[i], rs));
+        lane_store(r, r_out, RF32, left);
+        r_out += static_cast<int64_t>(d) * kRSize;
+        const float fh =
+            rsqrtf(__fmaf_rn(row_sum(sum_squares(r), red[1][odd], warp, 0, P.WPR), P.inv_d, P.eps));
+        const unsigned long long hh = pack2(fh, fh);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            r[i] = mul2(mul2(r[i], hh), wpre[i]);
+        if (P.h_type == kElemE4m3) {
+            uint32_t amax = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float a, b, c, t;
+                unpack2(r[2 * i], a, b);
+                unpack2(r[2 * i + 1], c, t);
+                const uint32_t m = max(max(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(b) & 0x7FFFFFFFu),
+                                       max(__float_as_uint(c) & 0x7FFFFFFFu, __float_as_uint(t) & 0x7FFFFFFFu));
+                const uint32_t block = __reduce_max_sync(0xFFFFFFFFu, m);
+                amax = (lane & 3) == i ? block : amax;
+            }
+            // lane l has the scale of block l mod 4 of the warp's columns
+            const float scale = block_scale(__uint_as_float(amax)), inv = __frcp_rn(scale);
+            if (lane < 4 && warp * kNormCols + lane * 128 < d)
+                *scales = scale;
+            scales += (d + 127) / 128;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float s = __shfl_sync(0xFFFFFFFFu, inv, i);
+                float a, b, c, t;
+                unpack2(mul2(r[2 * i], pack2(s, s)), a, b);
+                unpack2(mul2(r[2 * i + 1], pack2(s, s)), c, t);
+                if (i * 128 < left)
+                    *reinterpret_cast<uint32_t *>(h + i * 128) = e4m3x2_rn(a, b) | e4m3x2_rn(c, t) << 16;
+            }
+        } else {
+            lane_store(r, h, P.h_type == kElemFp32, left);
+        }
+        h += static_cast<int64_t>(d) * hsize;
+    }
+}
+
 // ------------------------------------------------------------- quantisation
 
 struct QuantParams {
@@ -356,11 +575,6 @@ __device__ __forceinline__ float tile_scale(float amax, float *red, float *scale
     if (threadIdx.x == 0)
         *scale_out = s;
     return __frcp_rn(s);
-}
-
-__device__ __forceinline__ uint32_t e4m3x4_scaled(float a, float b, float c, float d, float inv)
-{
-    return e4m3x2_rn(__fmul_rn(a, inv), __fmul_rn(b, inv)) | e4m3x2_rn(__fmul_rn(c, inv), __fmul_rn(d, inv)) << 16;
 }
 
 template <bool FP32> __global__ void __launch_bounds__(kQuantWarps * 32) quantize_tiles_kernel(const QuantParams P)
