@@ -739,7 +739,8 @@ template <bool VEC> cudaError_t norm_launch(const sv::NormParams &P, int nseg, u
 
 template <bool XF32, bool RF32> cudaError_t norm_rows_launch(sv::NormParams P, cudaStream_t s)
 {
-    auto *kernel = sv::block_norm_rows_kernel<XF32, RF32>;
+    auto *kernel = P.d % sv::kNormCols == 0 ? sv::block_norm_rows_kernel<XF32, RF32, true>
+                                            : sv::block_norm_rows_kernel<XF32, RF32, false>;
     P.WPR = 1;
     while (P.WPR * sv::kNormCols < P.d)
         P.WPR *= 2;

@@ -135,7 +135,17 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
-__device__ __forceinline__ float block_scale(float amax) { return __fdiv_rn(max_nan(amax, kAmaxFloor), kE4m3Max); }
+// amax / 448, correctly rounded: the product with the rounded reciprocal, then
+// one correction by its exact remainder (Markstein's theorem: the quotient's
+// estimate is within one unit of it, and no operand here is near the range's
+// ends, thanks to the floor; infinite and NaN amax give themselves).
+__device__ __forceinline__ float block_scale(float amax)
+{
+    const float a = max_nan(amax, kAmaxFloor), r = 1.0f / kE4m3Max;
+    const float q = __fmul_rn(a, r);
+    const float s = __fmaf_rn(__fmaf_rn(-kE4m3Max, q, a), r, q);
+    return a < INFINITY ? s : a;
+}
 
 __device__ __forceinline__ uint32_t e4m3x4_scaled(float a, float b, float c, float d, float inv)
 {
@@ -318,29 +328,31 @@ __global__ void __launch_bounds__(kNormMaxWarps * 32) block_norm_kernel(const No
 // consecutive columns would write fp32 rows in half sectors, twice as many
 // transactions), and a block's largest magnitude is one warp-wide maximum of
 // its bits, above which NaNs lie.  Pairs of values go through the packed fp32
-// instructions.  Rows of whole 16-byte units, up to 512 columns a warp.
+// instructions.  Rows of whole 16-byte units, up to 512 columns a warp (FULL:
+// exactly 512).
 constexpr int kNormRing = 4; // rows in flight, this one included
 constexpr int kNormCols = 512;
 constexpr int kNormRowsMaxD = kNormMaxWarps * kNormCols;
 
-template <bool FP32> __device__ __forceinline__ void lane_fetch(uint8_t *slot, int pitch, const char *src, int left)
+template <bool FP32, bool FULL>
+__device__ __forceinline__ void lane_fetch(uint8_t *slot, int pitch, const char *src, int left)
 {
     constexpr int size = FP32 ? 4 : 2;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (i * 128 < left)
+        if (FULL || i * 128 < left)
             asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(slot + i * pitch)),
                          "l"(src + i * 128 * size), "n"(4 * size)
                          : "memory");
 }
 
-template <bool FP32>
+template <bool FP32, bool FULL>
 __device__ __forceinline__ void lane_take(unsigned long long (&v)[8], const uint8_t *slot, int pitch, int left)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         v[2 * i] = v[2 * i + 1] = 0;
-        if (i * 128 < left) {
+        if (FULL || i * 128 < left) {
             if constexpr (FP32) {
                 const uint4 a = lds_v4(slot + i * pitch);
                 v[2 * i] = pack2(__uint_as_float(a.x), __uint_as_float(a.y));
@@ -381,11 +393,12 @@ __device__ __forceinline__ void lane_weights(unsigned long long (&w)[8], const c
 }
 
 // A lane's values to a row of bf16 or fp32 (`row` at the lane's first column).
+template <bool FULL>
 __device__ __forceinline__ void lane_store(const unsigned long long (&v)[8], char *row, bool fp32, int left)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (i * 128 < left) {
+        if (FULL || i * 128 < left) {
             float a, b, c, d;
             unpack2(v[2 * i], a, b);
             unpack2(v[2 * i + 1], c, d);
@@ -409,7 +422,7 @@ __device__ __forceinline__ float sum_squares(const unsigned long long (&v)[8])
     return __fadd_rn(a, b);
 }
 
-template <bool XF32, bool RF32>
+template <bool XF32, bool RF32, bool FULL>
 __global__ void __launch_bounds__(kNormMaxWarps * 32, 1) block_norm_rows_kernel(const NormParams P)
 {
     constexpr int kXSize = XF32 ? 4 : 2, kRSize = RF32 ? 4 : 2;
@@ -438,8 +451,8 @@ __global__ void __launch_bounds__(kNormMaxWarps * 32, 1) block_norm_rows_kernel(
     int to_fetch = static_cast<int>(end - begin);
     auto fetch = [&](int slot) {
         if (to_fetch-- > 0) {
-            lane_fetch<XF32>(own_x + slot * slot_bytes, threads * 4 * kXSize, x, left);
-            lane_fetch<RF32>(own_r + slot * slot_bytes, threads * 4 * kRSize, res, left);
+            lane_fetch<XF32, FULL>(own_x + slot * slot_bytes, threads * 4 * kXSize, x, left);
+            lane_fetch<RF32, FULL>(own_r + slot * slot_bytes, threads * 4 * kRSize, res, left);
             x += static_cast<int64_t>(d) * kXSize;
             res += static_cast<int64_t>(d) * kRSize;
         }
@@ -469,8 +482,8 @@ __global__ void __launch_bounds__(kNormMaxWarps * 32, 1) block_norm_rows_kernel(
         --gate_left;
         cp_async_wait<kNormRing - 1>();
         unsigned long long v[8], r[8];
-        lane_take<XF32>(v, own_x + slot * slot_bytes, threads * 4 * kXSize, left);
-        lane_take<RF32>(r, own_r + slot * slot_bytes, threads * 4 * kRSize, left);
+        lane_take<XF32, FULL>(v, own_x + slot * slot_bytes, threads * 4 * kXSize, left);
+        lane_take<RF32, FULL>(r, own_r + slot * slot_bytes, threads * 4 * kRSize, left);
         slot = slot == kNormRing - 1 ? 0 : slot + 1;
         float f = P.bs;
         if (post)
@@ -479,7 +492,7 @@ __global__ void __launch_bounds__(kNormMaxWarps * 32, 1) block_norm_rows_kernel(
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             r[i] = fma2(mul2(v[i], branch[i]), ff, mul2(r[i], rs));
-        lane_store(r, r_out, RF32, left);
+        lane_store<FULL>(r, r_out, RF32, left);
         r_out += static_cast<int64_t>(d) * kRSize;
         const float fh =
             rsqrtf(__fmaf_rn(row_sum(sum_squares(r), red[1][odd], warp, 0, P.WPR), P.inv_d, P.eps));
@@ -501,7 +514,7 @@ __global__ void __launch_bounds__(kNormMaxWarps * 32, 1) block_norm_rows_kernel(
             }
             // lane l has the scale of block l mod 4 of the warp's columns
             const float scale = block_scale(__uint_as_float(amax)), inv = __frcp_rn(scale);
-            if (lane < 4 && warp * kNormCols + lane * 128 < d)
+            if (lane < 4 && (FULL || warp * kNormCols + lane * 128 < d))
                 *scales = scale;
             scales += (d + 127) / 128;
 #pragma unroll
@@ -510,11 +523,11 @@ __global__ void __launch_bounds__(kNormMaxWarps * 32, 1) block_norm_rows_kernel(
                 float a, b, c, t;
                 unpack2(mul2(r[2 * i], pack2(s, s)), a, b);
                 unpack2(mul2(r[2 * i + 1], pack2(s, s)), c, t);
-                if (i * 128 < left)
+                if (FULL || i * 128 < left)
                     *reinterpret_cast<uint32_t *>(h + i * 128) = e4m3x2_rn(a, b) | e4m3x2_rn(c, t) << 16;
             }
         } else {
-            lane_store(r, h, P.h_type == kElemFp32, left);
+            lane_store<FULL>(r, h, P.h_type == kElemFp32, left);
         }
         h += static_cast<int64_t>(d) * hsize;
     }
