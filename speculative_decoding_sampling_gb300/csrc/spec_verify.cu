@@ -614,7 +614,9 @@ cudaError_t lm8_launch_as(const CUtensorMap &ta, const CUtensorMap &tb, const CU
         return e;
     const int64_t tiles = static_cast<int64_t>(L.MT) * L.NT; // below 2^31 (lm8_check)
     const int64_t n = tiles < units ? tiles : units;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (PAIR ? 2 : 1);
     attr[0].val.clusterDim.y = 1;
@@ -625,7 +627,7 @@ cudaError_t lm8_launch_as(const CUtensorMap &ta, const CUtensorMap &tb, const CU
     cfg.dynamicSmemBytes = sv::kL8Smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, sv::lm_head_fp8_kernel<PAIR>, ta, tb, tc, L);
 }
 
@@ -694,12 +696,18 @@ sv_status_t lm_finish(const Plan &plan, float2 *part, int32_t slots, const void 
     P.row_part = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + plan.off_part);
     P.row_side = reinterpret_cast<float4 *>(static_cast<char *>(workspace) + plan.off_row_side);
     P.PM = plan.PM;
-    const unsigned grid = static_cast<unsigned>(ceil_div(plan.R, 8));
-    if (P.q)
-        sv::lm_merge_kernel<true><<<grid, 256, 0, s>>>(P, part, slots);
-    else
-        sv::lm_merge_kernel<false><<<grid, 256, 0, s>>>(P, part, slots);
-    if (cudaGetLastError() != cudaSuccess)
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(plan.R, 8)));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = P.q ? cudaLaunchKernelEx(&cfg, sv::lm_merge_kernel<true>, P, part, slots)
+                              : cudaLaunchKernelEx(&cfg, sv::lm_merge_kernel<false>, P, part, slots);
+    if (e != cudaSuccess)
         return SV_ECUDA;
     return run(kSurvivors, logits, SV_BF16, draft_probs, draft_tokens, uniforms, temperature, B, K, V, out_tokens,
                num_emitted, accept_flags, accept_prob, residual_mass, status_dev, workspace, plan.bytes, stream,
@@ -709,6 +717,23 @@ sv_status_t lm_finish(const Plan &plan, float2 *part, int32_t slots, const void 
 // ------------------------------------------------- norms and quantisation
 
 constexpr int64_t kNormManyRows = 4 * kNominalSms;
+
+// A launch as programmatic dependent of the kernel before on the stream.
+template <typename Kernel, typename Args>
+cudaError_t launch_behind(Kernel kernel, unsigned grid, unsigned threads, size_t smem, cudaStream_t s, const Args &args)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args);
+}
 
 size_t elem_size(sv_dtype_t t) { return t == SV_BF16 ? 2 : (t == SV_FP32 ? 4 : 1); }
 
@@ -722,19 +747,14 @@ template <bool VEC> cudaError_t norm_launch(const sv::NormParams &P, int nseg, u
     const unsigned threads = static_cast<unsigned>(P.WPR * P.RPC * 32);
     switch (nseg) {
     case 1:
-        sv::block_norm_kernel<1, VEC><<<grid, threads, 0, s>>>(P);
-        break;
+        return launch_behind(sv::block_norm_kernel<1, VEC>, grid, threads, 0, s, P);
     case 2:
-        sv::block_norm_kernel<2, VEC><<<grid, threads, 0, s>>>(P);
-        break;
+        return launch_behind(sv::block_norm_kernel<2, VEC>, grid, threads, 0, s, P);
     case 4:
-        sv::block_norm_kernel<4, VEC><<<grid, threads, 0, s>>>(P);
-        break;
+        return launch_behind(sv::block_norm_kernel<4, VEC>, grid, threads, 0, s, P);
     default:
-        sv::block_norm_kernel<8, VEC><<<grid, threads, 0, s>>>(P);
-        break;
+        return launch_behind(sv::block_norm_kernel<8, VEC>, grid, threads, 0, s, P);
     }
-    return cudaGetLastError();
 }
 
 template <bool XF32, bool RF32> cudaError_t norm_rows_launch(sv::NormParams P, cudaStream_t s)
@@ -759,8 +779,8 @@ template <bool XF32, bool RF32> cudaError_t norm_rows_launch(sv::NormParams P, c
     if (per_sm < 1)
         return cudaErrorInvalidConfiguration;
     const int64_t resident = static_cast<int64_t>(sms > 0 ? sms : 1) * per_sm;
-    kernel<<<static_cast<unsigned>(P.M < resident ? P.M : resident), threads, smem, s>>>(P);
-    return cudaGetLastError();
+    return launch_behind(kernel, static_cast<unsigned>(P.M < resident ? P.M : resident),
+                         static_cast<unsigned>(threads), smem, s, P);
 }
 
 static_assert(int(sv::kElemBf16) == int(SV_BF16) && int(sv::kElemFp32) == int(SV_FP32) &&
@@ -1122,20 +1142,16 @@ sv_status_t sv_quantize_fp8(const void *x, sv_dtype_t x_dtype, int64_t rows, int
         return SV_EUNSUPPORTED;
     const unsigned g = static_cast<unsigned>(grid);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (block_rows == 1) {
-        if (vec)
-            sv::quantize_rows_kernel<true><<<g, sv::kQuantWarps * 32, 0, s>>>(P);
-        else
-            sv::quantize_rows_kernel<false><<<g, sv::kQuantWarps * 32, 0, s>>>(P);
-    } else {
-        if (!vec)
-            sv::quantize_tiles_odd_kernel<<<g, sv::kQuantWarps * 32, 0, s>>>(P);
-        else if (x_dtype == SV_FP32)
-            sv::quantize_tiles_kernel<true><<<g, sv::kQuantWarps * 32, 0, s>>>(P);
-        else
-            sv::quantize_tiles_kernel<false><<<g, sv::kQuantWarps * 32, 0, s>>>(P);
-    }
-    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ECUDA;
+    constexpr unsigned threads = sv::kQuantWarps * 32;
+    cudaError_t e;
+    if (block_rows == 1)
+        e = launch_behind(vec ? sv::quantize_rows_kernel<true> : sv::quantize_rows_kernel<false>, g, threads, 0, s, P);
+    else if (!vec)
+        e = launch_behind(sv::quantize_tiles_odd_kernel, g, threads, 0, s, P);
+    else
+        e = launch_behind(x_dtype == SV_FP32 ? sv::quantize_tiles_kernel<true> : sv::quantize_tiles_kernel<false>, g,
+                          threads, 0, s, P);
+    return e == cudaSuccess ? SV_OK : SV_ECUDA;
 }
 
 size_t sv_tree_workspace_bytes(int64_t B, int32_t N, int32_t V)

@@ -27,6 +27,15 @@ constexpr float kAmaxFloor = 0x1p-100f; // keeps the scale and its reciprocal no
 
 enum ElemType { kElemBf16 = 0, kElemFp32 = 1, kElemE4m3 = 2 };
 
+// Launched as a programmatic dependent: the CTAs are placed while the kernel
+// before drains, and wait here for its memory; the next kernel may be placed in
+// turn.
+__device__ __forceinline__ void follow_primary()
+{
+    pdl_wait_primary();
+    pdl_launch_dependents();
+}
+
 // The 8 values of a lane in a segment starting at `base`: consecutive ones
 // (VEC: 16-byte accesses) or every 32nd (coalesced single accesses, for rows
 // that are not whole 16-byte units).
@@ -233,6 +242,7 @@ template <int NSEG, bool VEC>
 __global__ void __launch_bounds__(kNormMaxWarps * 32) block_norm_kernel(const NormParams P)
 {
     __shared__ float red[2][kNormMaxWarps];
+    follow_primary();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rl = warp / P.WPR, first = rl * P.WPR, wr = warp - first;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * P.RPC + rl;
@@ -429,6 +439,7 @@ __global__ void __launch_bounds__(kNormMaxWarps * 32, 1) block_norm_rows_kernel(
     constexpr int kXType = XF32 ? kElemFp32 : kElemBf16;
     extern __shared__ __align__(16) uint8_t norm_smem[]; // [ring][x's 4 pieces, then the residual's][thread]
     __shared__ float red[2][2][kNormMaxWarps];
+    follow_primary();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = P.d;
     const int e = warp * kNormCols + lane * 4, left = d - e; // first column; piece i is in the row where 128 i < left
     const int threads = static_cast<int>(blockDim.x), slot_bytes = threads * 16 * (kXSize + kRSize);
@@ -550,6 +561,7 @@ constexpr int kQuantWarps = 8;
 // A scale per row and 128 values: a warp per segment of 256 values.
 template <bool VEC> __global__ void __launch_bounds__(kQuantWarps * 32) quantize_rows_kernel(const QuantParams P)
 {
+    follow_primary();
     const int lane = threadIdx.x & 31;
     const int64_t i = static_cast<int64_t>(blockIdx.x) * kQuantWarps + (threadIdx.x >> 5);
     const int64_t row = i / P.segs;
@@ -593,6 +605,7 @@ __device__ __forceinline__ float tile_scale(float amax, float *red, float *scale
 template <bool FP32> __global__ void __launch_bounds__(kQuantWarps * 32) quantize_tiles_kernel(const QuantParams P)
 {
     __shared__ float red[kQuantWarps];
+    follow_primary();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t segs = static_cast<uint32_t>(P.segs), rb = blockIdx.x / segs, cb = blockIdx.x - rb * segs;
     const int64_t row0 = static_cast<int64_t>(rb) * 128 + warp * 2 + (lane >> 4); // rows row0, row0 + 16, ...
@@ -650,6 +663,7 @@ template <bool FP32> __global__ void __launch_bounds__(kQuantWarps * 32) quantiz
 __global__ void __launch_bounds__(kQuantWarps * 32) quantize_tiles_odd_kernel(const QuantParams P)
 {
     __shared__ float red[kQuantWarps];
+    follow_primary();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t segs = static_cast<uint32_t>(P.segs), rb = blockIdx.x / segs, cb = blockIdx.x - rb * segs;
     const int64_t row0 = static_cast<int64_t>(rb) * 128 + warp; // rows row0, row0 + 8, ...

@@ -470,6 +470,7 @@ __global__ void __launch_bounds__(kLmThreads, 1)
 template <bool DENSE>
 __global__ void __launch_bounds__(256) lm_merge_kernel(const Params P, float2 *part, int32_t NT)
 {
+    pdl_wait_primary(); // behind the e4m3 product it is launched as a programmatic dependent
     const int lane = threadIdx.x & 31;
     const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int64_t R = P.B * (static_cast<int64_t>(P.K) + 1);

@@ -799,6 +799,11 @@ __global__ void __launch_bounds__(kL8Threads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kL8OtherRegs));
         // Warps 0 and 1 run their loops as whole warps, so that addresses and
         // descriptors stay in uniform registers; one lane issues.
+        // Launched as a programmatic dependent: all of the above ran while the
+        // kernel before drained; only warps 0 (operands) and the scales' read
+        // what it may have written, and every write here follows from theirs.
+        pdl_wait_primary();
+        pdl_launch_dependents();
         if (warp == 0) {
             int s = 0;
             uint32_t ph = 0;
