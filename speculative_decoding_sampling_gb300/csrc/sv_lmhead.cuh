@@ -476,10 +476,20 @@ __global__ void __launch_bounds__(256) lm_merge_kernel(const Params P, float2 *p
     const int64_t R = P.B * (static_cast<int64_t>(P.K) + 1);
     if (r < R) { // warp-uniform
         float M = -INFINITY, S = 0.0f;
-        for (int32_t i = lane; i < NT; i += 32) {
-            const float2 pr = part[r * NT + i];
-            part[r * NT + i] = make_float2(0.0f, 0.0f); // the workspace goes back to zero once read
-            merge_ms(M, S, pr.x, pr.y, P.c);
+        // eight pairs a lane on their way at a time, merged in order
+        float2 *row = part + r * NT;
+        for (int32_t i0 = lane; i0 < NT; i0 += 32 * 8) {
+            float2 pr[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i0 + 32 * k < NT)
+                    pr[k] = row[i0 + 32 * k];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i0 + 32 * k < NT) {
+                    row[i0 + 32 * k] = make_float2(0.0f, 0.0f); // the workspace goes back to zero once read
+                    merge_ms(M, S, pr[k].x, pr[k].y, P.c);
+                }
         }
         warp_merge_ms(M, S, P.c);
         if (lane == 0) {
