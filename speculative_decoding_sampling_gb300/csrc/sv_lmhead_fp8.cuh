@@ -46,8 +46,8 @@ constexpr int kL8MaxNB = 256; // ids per tile
 constexpr int kL8AccWarps = 8;
 constexpr int kL8Threads = 256 + 32 * kL8AccWarps;
 // Registers a thread: 128 at launch (65,536 in all); the accumulators' two
-// warpgroups then take 224 and the others keep 32 (65,536).
-constexpr int kL8AccRegs = 224, kL8OtherRegs = 32;
+// warpgroups then take 216 and the others keep 40 (65,536).
+constexpr int kL8AccRegs = 216, kL8OtherRegs = 40;
 static_assert(32 * kL8AccWarps * kL8AccRegs + 256 * kL8OtherRegs <= 128 * kL8Threads, "register split");
 constexpr uint32_t kL8TmemCols = 2 * kL8MaxNB; // two fp32 sums of one step: all 512 columns
 constexpr int kL8MaxStages = 8;
@@ -280,23 +280,6 @@ __device__ __forceinline__ float2 l8_lds2(uint32_t addr)
     return r;
 }
 
-__device__ __forceinline__ uint4 l8_lds4(uint32_t addr)
-{
-    uint4 r;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "r"(addr)
-                 : "memory");
-    return r;
-}
-
-__device__ __forceinline__ uint16_t l8_lds_u16(uint32_t addr)
-{
-    uint16_t r;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(addr) : "memory");
-    return r;
-}
-
 // Four bytes from global memory (zero where `in` is false), without registers
 // in between.
 __device__ __forceinline__ void l8_copy4(uint32_t dst, const float *src, bool in)
@@ -437,6 +420,24 @@ __device__ __forceinline__ void l8_fold(unsigned long long *acc, const uint32_t 
 // the rows' statistics.
 __device__ __forceinline__ bool l8_helpers(const Lm8Params &P) { return !P.tma || P.part; }
 
+// Loads of staged logits that the compiler may batch and move, but not above
+// l8_staged_now, which a finished wait for them is followed by.
+__device__ __forceinline__ void l8_staged_now(uint32_t &boxes) { asm volatile("" : "+r"(boxes)::"memory"); }
+
+__device__ __forceinline__ uint4 l8_staged4(uint32_t addr)
+{
+    uint4 r;
+    asm("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr));
+    return r;
+}
+
+__device__ __forceinline__ uint16_t l8_staged1(uint32_t addr)
+{
+    uint16_t r;
+    asm("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(addr));
+    return r;
+}
+
 // Where column c of a staged row r is.
 __device__ __forceinline__ uint32_t l8_staged_at(uint32_t boxes, int r, int c)
 {
@@ -467,32 +468,52 @@ __device__ __forceinline__ void l8_store_rows(const Lm8Params &P, uint32_t boxes
 {
     const int rows = P.M - row0 < 32 ? P.M - row0 : 32;
     uint16_t *const dst0 = P.logits + static_cast<int64_t>(row0) * P.N + n;
+    auto columns_before_unit = [&](const uint16_t *dst) {
+        return (8 - static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 1)) & 7;
+    };
     {
         const int u = (lane & 15) * 8;
-#pragma unroll 2
-        for (int r = lane >> 4; r < rows; r += 2) {
-            uint16_t *dst = dst0 + static_cast<int64_t>(r) * P.N;
-            const int lead = (8 - static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 1)) & 7; // columns before the first unit
-            const uint4 lo = l8_lds4(l8_staged_at(boxes, r, u));
-            const uint4 hi = l8_lds4(l8_staged_at(boxes, r, u < 120 ? u + 8 : u));
-            if (u + lead + 8 <= ncols)
-                *reinterpret_cast<uint4 *>(dst + u + lead) = l8_shift(lo, hi, lead);
+#pragma unroll 1
+        for (int r0 = lane >> 4; r0 < rows; r0 += 4) {
+            uint4 lo[2], hi[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                lo[i] = l8_staged4(l8_staged_at(boxes, (r0 + 2 * i) & 31, u));
+                hi[i] = l8_staged4(l8_staged_at(boxes, (r0 + 2 * i) & 31, u < 120 ? u + 8 : u));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint16_t *dst = dst0 + static_cast<int64_t>(r0 + 2 * i) * P.N;
+                const int lead = columns_before_unit(dst);
+                if (r0 + 2 * i < rows && u + lead + 8 <= ncols)
+                    *reinterpret_cast<uint4 *>(dst + u + lead) = l8_shift(lo[i], hi[i], lead);
+            }
         }
     }
     const int c = lane & 7;
-#pragma unroll 4
-    for (int r = lane >> 3; r < rows; r += 4) {
-        uint16_t *dst = dst0 + static_cast<int64_t>(r) * P.N;
-        const int lead = (8 - static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 1)) & 7;
-        const int units = ncols > lead ? (ncols - lead) >> 3 : 0; // whole units
-        const int first = lead < ncols ? lead : ncols, edges = ncols - units * 8;
-        if (c < edges) {
-            const int p = c < first ? c : units * 8 + c;
-            dst[p] = l8_lds_u16(l8_staged_at(boxes, r, p));
+#pragma unroll 1
+    for (int r0 = lane >> 3; r0 < rows; r0 += 16) {
+        uint16_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int lead = columns_before_unit(dst0 + static_cast<int64_t>(r0 + 4 * i) * P.N);
+            const int units = ncols > lead ? (ncols - lead) >> 3 : 0; // whole units
+            const int first = lead < ncols ? lead : ncols, p = c < first ? c : units * 8 + c;
+            v[i] = l8_staged1(l8_staged_at(boxes, (r0 + 4 * i) & 31, p < 128 ? p : 0));
         }
-        if (c + 8 < edges) {
-            const int p = c + 8 < first ? c + 8 : units * 8 + c + 8;
-            dst[p] = l8_lds_u16(l8_staged_at(boxes, r, p));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + 4 * i;
+            uint16_t *dst = dst0 + static_cast<int64_t>(r) * P.N;
+            const int lead = columns_before_unit(dst);
+            const int units = ncols > lead ? (ncols - lead) >> 3 : 0, edges = ncols - units * 8;
+            const int first = lead < ncols ? lead : ncols;
+            if (r < rows && c < edges)
+                dst[c < first ? c : units * 8 + c] = v[i];
+            if (r < rows && c + 8 < edges) {
+                const int p = c + 8 < first ? c + 8 : units * 8 + c + 8;
+                dst[p] = l8_staged1(l8_staged_at(boxes, r, p));
+            }
         }
     }
 }
@@ -502,8 +523,9 @@ __device__ __forceinline__ void l8_store_rows(const Lm8Params &P, uint32_t boxes
 __device__ __forceinline__ float2 l8_statistics(const Lm8Params &P, uint32_t half0, uint32_t half1, int r, int ncols)
 {
     float mx = -INFINITY;
+#pragma unroll 4
     for (int c = 0; c < ncols; c += 8) {
-        const uint4 v = l8_lds4(l8_staged_at(c < 128 ? half0 : half1, r, c & 127));
+        const uint4 v = l8_staged4(l8_staged_at(c < 128 ? half0 : half1, r, c & 127));
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -513,8 +535,9 @@ __device__ __forceinline__ float2 l8_statistics(const Lm8Params &P, uint32_t hal
     }
     const float mc = mc_of(mx, P.c);
     float S[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
     for (int c = 0; c < ncols; c += 8) {
-        const uint4 v = l8_lds4(l8_staged_at(c < 128 ? half0 : half1, r, c & 127));
+        const uint4 v = l8_staged4(l8_staged_at(c < 128 ? half0 : half1, r, c & 127));
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -531,14 +554,15 @@ __device__ __forceinline__ void l8_finish(const Lm8Params &P, uint32_t tabs, uin
                                           uint32_t rank, uint32_t unit, uint32_t units, uint32_t ntiles, int lq, int lane)
 {
     uint32_t odd = 0;
-    const uint32_t half0 = tabs - static_cast<uint32_t>(8 - lq) * kL8StgBytes;
-    const uint32_t half1 = half0 + 4 * kL8StgBytes;
+    uint32_t half0 = tabs - static_cast<uint32_t>(8 - lq) * kL8StgBytes;
     for (uint32_t t = unit; t < ntiles; t += units, odd ^= 1u) {
         if (!__all_sync(0xFFFFFFFFu, l8_wait(staged, odd))) {
             if (lane == 0)
                 l8_fail(P, stop);
             return;
         }
+        l8_staged_now(half0);
+        const uint32_t half1 = half0 + 4 * kL8StgBytes;
         const int row0 = l8_row0<PAIR>(P, t, rank, lq), tn = static_cast<int>(l8_tile_n(P, t)), n0 = tn * P.NB;
         const int ncols = P.N - n0 < P.NB ? P.N - n0 : P.NB; // at least 1
         if (row0 < P.M) {
