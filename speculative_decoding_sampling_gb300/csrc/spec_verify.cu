@@ -540,8 +540,9 @@ sv_status_t lm8_check(const void *hidden, const float *hidden_scales, const void
         return SV_EINVAL;
     if (V > SV_MAX_V || M > kLmMaxRows)
         return SV_EUNSUPPORTED;
-    const Lm8Plan p = lm8_plan(M, V);
-    if (static_cast<int64_t>(p.MT) * p.NT > INT32_MAX)
+    const Lm8Plan p = lm8_plan(M, V); // tiles, and steps of all tiles, are counted in 32 bits
+    const int64_t tiles = static_cast<int64_t>(p.MT) * p.NT;
+    if (tiles > INT32_MAX || tiles > INT32_MAX / ceil_div(d, sv::kL8BK) * (kNominalSms / 2))
         return SV_EUNSUPPORTED;
     if (M > 0 && (!hidden || !hidden_scales || !lm_head || !lm_head_scales || !logits || !aligned(hidden, 16) ||
                   !aligned(lm_head, 16) || !aligned(hidden_scales, 4) || !aligned(lm_head_scales, 4) ||
@@ -757,15 +758,27 @@ template <bool VEC> cudaError_t norm_launch(const sv::NormParams &P, int nseg, u
     }
 }
 
+// The staying CTAs: warps of a row, and the bytes of their rows in flight.
+int norm_rows_warps(int32_t d)
+{
+    int w = 1;
+    while (w * sv::kNormCols < d)
+        w *= 2;
+    return w;
+}
+
+size_t norm_rows_smem(int32_t d, size_t x_size, size_t r_size)
+{
+    return static_cast<size_t>(sv::kNormRing) * norm_rows_warps(d) * sv::kNormCols * (x_size + r_size);
+}
+
 template <bool XF32, bool RF32> cudaError_t norm_rows_launch(sv::NormParams P, cudaStream_t s)
 {
-    auto *kernel = P.d % sv::kNormCols == 0 ? sv::block_norm_rows_kernel<XF32, RF32, true>
-                                            : sv::block_norm_rows_kernel<XF32, RF32, false>;
-    P.WPR = 1;
-    while (P.WPR * sv::kNormCols < P.d)
-        P.WPR *= 2;
+    P.WPR = norm_rows_warps(P.d);
+    auto *kernel = P.WPR * sv::kNormCols == P.d ? sv::block_norm_rows_kernel<XF32, RF32, true>
+                                                : sv::block_norm_rows_kernel<XF32, RF32, false>;
     const int threads = P.WPR * 32;
-    const size_t smem = static_cast<size_t>(sv::kNormRing) * 16 * ((XF32 ? 4 : 2) + (RF32 ? 4 : 2)) * threads;
+    const size_t smem = norm_rows_smem(P.d, XF32 ? 4 : 2, RF32 ? 4 : 2);
     int dev = 0, sms = 0, per_sm = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
@@ -1106,8 +1119,10 @@ sv_status_t sv_block_norm(const void *x, sv_dtype_t x_dtype, const void *residua
                      vec_ok(post_weight, weight_dtype) && vec_ok(norm_weight, weight_dtype) && vec_ok(gate, x_dtype);
     const unsigned grid = static_cast<unsigned>(ceil_div(M, P.RPC));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // rows enough for every SM to walk several: CTAs that stay
-    if (vec && d <= sv::kNormRowsMaxD && M >= kNormManyRows) {
+    // rows enough for every SM to walk several (and not too wide for several to
+    // be in flight in shared memory): CTAs that stay
+    if (vec && d <= sv::kNormRowsMaxD && M >= kNormManyRows &&
+        norm_rows_smem(d, elem_size(x_dtype), elem_size(residual_dtype)) <= 224 * 1024) {
         const bool xf = x_dtype == SV_FP32, rf = residual_dtype == SV_FP32;
         const cudaError_t e = xf ? (rf ? norm_rows_launch<true, true>(P, s) : norm_rows_launch<true, false>(P, s))
                                  : (rf ? norm_rows_launch<false, true>(P, s) : norm_rows_launch<false, false>(P, s));

@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kNormMaxWarps * 32) block_norm_kernel(const No
 // transactions), and a block's largest magnitude is one warp-wide maximum of
 // its bits, above which NaNs lie.  Pairs of values go through the packed fp32
 // instructions.  Rows of whole 16-byte units, up to 512 columns a warp (FULL:
-// exactly 512).
+// all of the CTA's warps have 512).
 constexpr int kNormRing = 4; // rows in flight, this one included
 constexpr int kNormCols = 512;
 constexpr int kNormRowsMaxD = kNormMaxWarps * kNormCols;

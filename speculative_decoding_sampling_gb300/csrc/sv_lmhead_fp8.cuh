@@ -34,7 +34,7 @@
 // it (the fused verification), or store it where the logits' rows are not
 // whole 16-byte units -- an SM gets rid of about 16 bytes a cycle while all of
 // them write, so a warp that stores itself waits thousands of cycles a tile.
-// Every wait is bounded in time (l8_wait), with lm_head_kernel's teardown.
+// Every wait is bounded (l8_wait), with lm_head_kernel's teardown.
 #pragma once
 
 #include "sv_lmhead.cuh"
@@ -204,9 +204,9 @@ __device__ __forceinline__ bool l8_elect()
 
 // Wait for phase `parity` of `bar`: true once it is complete, false after
 // kL8Tries tries, each of which the hardware may suspend for about a
-// microsecond (about a second in all; far less than one step takes if they
-// are not suspended at all would still be 10 ms).  One loop without calls or
-// clock reads: the issuing warps wait several times a step.
+// microsecond (a second in all; tens of milliseconds if it never suspends,
+// against microseconds that a step takes).  One loop without calls or clock
+// reads: some warps wait several times a step.
 constexpr uint32_t kL8Tries = 1u << 20;
 __device__ __forceinline__ bool l8_wait(uint32_t bar, uint32_t parity)
 {
@@ -819,15 +819,15 @@ __global__ void __launch_bounds__(kL8Threads, 1)
     l8_cluster_sync<PAIR>(); // every CTA's barriers exist before another CTA signals them
     lm_tc_after();
     const uint32_t tbase = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);
+    // Launched as a programmatic dependent: all of the above ran while the
+    // kernel before drained.  Every thread waits for it here, so that no bounded
+    // wait below counts the time that kernel still takes.
+    pdl_wait_primary();
+    pdl_launch_dependents();
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kL8OtherRegs));
         // Warps 0 and 1 run their loops as whole warps, so that addresses and
         // descriptors stay in uniform registers; one lane issues.
-        // Launched as a programmatic dependent: all of the above ran while the
-        // kernel before drained; only warps 0 (operands) and the scales' read
-        // what it may have written, and every write here follows from theirs.
-        pdl_wait_primary();
-        pdl_launch_dependents();
         if (warp == 0) {
             int s = 0;
             uint32_t ph = 0;

@@ -66,6 +66,57 @@ def test_block_norm(M, d, hidden, xt, rt, wt):
         assert R.within(got.hidden.cpu(), h, eh, hidden)
 
 
+# rows enough for CTAs that stay: whole warps of 512 columns and ragged ones, one
+# warp a row and sixteen, runs of rows that begin and end inside a gate's rows
+MANY = [(608, 512), (1001, 4096), (700, 1000), (611, 8), (640, 136), (616, 8192), (900, 5136), (1520, 1536)]
+
+
+@pytest.mark.parametrize("M,d", MANY, ids=[f"M{m}_d{d}" for m, d in MANY])
+@pytest.mark.parametrize("xt,rt,hidden", [(BF, FP, E4), (BF, BF, BF), (FP, FP, FP), (FP, BF, E4)])
+@pytest.mark.parametrize("form", ["plain", "post", "gate", "both"])
+def test_block_norm_many_rows(M, d, xt, rt, hidden, form):
+    seed = 7 * M + d
+    x, res = R.rand((M, d), seed, xt, 1.5), R.rand((M, d), seed + 1, rt, 4.0)
+    wt = BF if form in ("plain", "both") else FP
+    pre = R.rand((d,), seed + 2, wt, 0.3)
+    post = R.rand((d,), seed + 3, wt, 0.3) if form in ("post", "both") else None
+    G = next(g for g in (17, 16, 13, 11, 10, 9, 7) if M % g == 0)
+    gate = R.rand((G, d), seed + 4, xt) if form in ("gate", "both") else None
+    kw = dict(rs=0.5, bs=0.22, offset=1.0) if form == "both" else {}
+    h, r, eh, er = R.norm64(x, res, pre, post, gate, **kw)
+    dv = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    o = {k: Guarded(sh, t) for k, sh, t in (("out", (M, d), hidden), ("residual_out", (M, d), rt))}
+    got = sv.sv_block_norm(dv(x), dv(res), dv(pre), post_weight=dv(post), gate=dv(gate),
+                           residual_scale=kw.get("rs", 1.0), branch_scale=kw.get("bs", 1.0),
+                           weight_offset=kw.get("offset", 0.0), hidden_dtype=hidden, **{k: g.t for k, g in o.items()})
+    torch.cuda.synchronize()
+    assert all(g.guards_intact() for g in o.values())
+    assert R.within(got.residual.cpu(), r, er, rt)
+    if hidden == E4:
+        _check_e4m3(got.hidden.cpu(), got.scales.cpu(), h, eh)
+    else:
+        assert R.within(got.hidden.cpu(), h, eh, hidden)
+
+
+def test_block_norm_many_rows_in_place_and_bad_rows():
+    """In place, with rows of zeros, a NaN and an infinity among them: those
+    stay in their rows."""
+    M, d = 650, 1024
+    x, res, pre = R.rand((M, d), 1, BF), R.rand((M, d), 2, BF), R.rand((d,), 3, BF)
+    x[5], res[5] = 0, 0
+    clean = sv.sv_block_norm(x.to(DEV), res.to(DEV), pre.to(DEV), hidden_dtype=E4)
+    x[100, 17], x[300, 1000] = float("nan"), float("inf")
+    buf = res.to(DEV)
+    got = sv.sv_block_norm(x.to(DEV), buf, pre.to(DEV), hidden_dtype=E4, residual_out=buf)
+    keep = torch.ones(M, dtype=torch.bool)
+    keep[100] = keep[300] = False
+    for k in ("hidden", "scales", "residual"):
+        assert torch.equal(_bits(getattr(got, k))[keep], _bits(getattr(clean, k))[keep]), k
+    assert (got.hidden[5].float() == 0).all() and (got.scales[5].cpu() == torch.tensor(R.AMAX_FLOOR) / 448).all()
+    assert got.scales[100].isnan().all() and got.hidden[100].float().isnan().all()
+    assert got.residual[300, 1000].isinf() and got.hidden[300].float()[1000].isnan()
+
+
 @pytest.mark.parametrize("shape,gshape", [((4, 3, 96), (96,)), ((4, 3, 96), (4, 1, 96)), ((4, 3, 96), (4, 3, 96)),
                                           ((4, 3, 95), (4, 1, 95)), ((6, 64), (2, 64))])
 def test_gate_rows_serve_consecutive_rows(shape, gshape):
@@ -190,6 +241,18 @@ def test_offsets_past_32_bits():
     ref = sv.sv_block_norm(tail, tail, w)
     assert torch.equal(_bits(got.hidden[-3:]), _bits(ref.hidden))
     assert torch.equal(_bits(got.residual[-3:]), _bits(ref.residual))
+
+
+def test_many_rows_offsets_past_32_bits():
+    """More than 2^31 values through the CTAs that stay."""
+    M, d = 300001, 8192
+    x = torch.zeros((M, d), dtype=BF, device=DEV)
+    tail, w = R.rand((3, d), 4, BF), R.rand((d,), 5, BF)
+    x[-3:] = tail.to(DEV)
+    got = sv.sv_block_norm(x, x, w.to(DEV))
+    h, r, eh, er = R.norm64(tail, tail, w)
+    assert R.within(got.residual[-3:].cpu(), r, er, BF) and R.within(got.hidden[-3:].cpu(), h, eh, BF)
+    assert int(got.hidden[:-3].count_nonzero()) == 0
 
 
 def test_other_stream_and_captured_graph():

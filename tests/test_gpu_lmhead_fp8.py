@@ -162,7 +162,7 @@ def _fused(ops, B, K, q, tokens, u, T, **kw):
 
 
 FUSED = [(24, 3, 1000, 256), (24, 0, 4097, 128), (17, 8, 32000, 256), (5, 4, 130, 64), (40, 3, 257, 192),
-         (1, 0, 500, 128), (1, 4, 32003, 144)]
+         (1, 0, 500, 128), (1, 4, 32003, 144), (30, 4, 32001, 64), (64, 4, 40000, 64)]
 
 
 @pytest.mark.parametrize("onehot", [False, True], ids=["dense", "onehot"])
