@@ -39,7 +39,10 @@ SHAPES = [(1, 256, 128), (1, 1, 16), (5, 7, 16), (31, 33, 112), (33, 300, 144), 
           (128, 5000, 272), (129, 2056, 512), (130, 31, 128), (200, 9999, 144), (256, 777, 1024), (257, 1000, 384),
           (300, 4097, 640), (513, 512, 2048), (40, 20000, 4096), (3, 45000, 64),
           # wide tiles whose rows start at every alignment: vocabularies 3, 1, 6, 4 and 7 above a multiple of 8
-          (131, 32003, 144), (260, 40001, 128), (50, 36006, 128), (7, 44004, 16), (129, 65527, 32)]
+          (131, 32003, 144), (260, 40001, 128), (50, 36006, 128), (7, 44004, 16), (129, 65527, 32),
+          # a last row tile of at most 128 rows: 1, 33, 64, 65, 128 of them, and 129 (not one)
+          (257, 9000, 256), (289, 9001, 384), (320, 12000, 128), (577, 20003, 64), (384, 9504, 640), (641, 30000, 272),
+          (385, 9000, 128), (896, 20000, 2176)]
 
 
 @pytest.mark.parametrize("M,V,d", SHAPES, ids=[f"M{m}_V{v}_d{d}" for m, v, d in SHAPES])
@@ -58,11 +61,11 @@ def test_logits_dyadic_bit_exact(M, V, d):
     assert torch.equal(_logits(ops), z.float().to(torch.bfloat16))
 
 
-@pytest.mark.parametrize("M", [3, 200])
-def test_every_value_and_scale_reaches_its_place(M):
+@pytest.mark.parametrize("M,V", [(3, 1500), (200, 1500), (300, 9000), (384, 9002)])
+def test_every_value_and_scale_reaches_its_place(M, V):
     """One non-zero per operand row and scales that differ everywhere: each
     logit is a single product, so an index that is off shows as a wrong one."""
-    V, d = 1500, 1168
+    d = 1168
     nb = R.blocks(d)
     g = torch.Generator().manual_seed(M)
     kk = torch.randint(0, d, (V,), generator=g)
@@ -162,7 +165,8 @@ def _fused(ops, B, K, q, tokens, u, T, **kw):
 
 
 FUSED = [(24, 3, 1000, 256), (24, 0, 4097, 128), (17, 8, 32000, 256), (5, 4, 130, 64), (40, 3, 257, 192),
-         (1, 0, 500, 128), (1, 4, 32003, 144), (30, 4, 32001, 64), (64, 4, 40000, 64)]
+         (1, 0, 500, 128), (1, 4, 32003, 144), (30, 4, 32001, 64), (64, 4, 40000, 64),
+         (60, 4, 9000, 128), (96, 3, 9003, 64)]
 
 
 @pytest.mark.parametrize("onehot", [False, True], ids=["dense", "onehot"])
