@@ -72,15 +72,16 @@ def algorithmic_bytes(w, num_emitted: np.ndarray) -> dict:
     return {"rows_kernel": rows, "draw_kernels": surv, "total": rows + surv, "rejected": rejected}
 
 
-OWN_KERNEL_FILES = ("sv_filter.cuh", "sv_lmhead.cuh", "sv_tree.cuh")  # kernels of their own, hashed apart
+# kernels of their own, hashed apart
+OWN_KERNEL_FILES = ("sv_block_norm.cuh", "sv_filter.cuh", "sv_lmhead.cuh", "sv_lmhead_fp8.cuh", "sv_tree.cuh")
 
 
 def kernel_source_hash(only: str | None = None) -> str:
     """Hash of device code, with // comments, trailing blanks and empty lines
     removed (they do not change a kernel).  Default: the verification
     kernels, i.e. every .cuh file but those of the top-k / top-p filter, the
-    LM head and the tree walk (the C ABI's host code in spec_verify.cu is
-    left out).  only="sv_lmhead.cuh" (or another of those files): that file
+    LM head (bf16 and e4m3), the last norms and the tree walk (the C ABI's
+    host code in spec_verify.cu is left out).  only="sv_lmhead.cuh" (or another of those files): that file
     and the verification kernels it includes."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "speculative_decoding_sampling_gb300", "csrc")

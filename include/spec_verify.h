@@ -328,8 +328,11 @@ sv_status_t spec_verify_lm_head(const void *hidden, const void *lm_head,
  * infinite scale or value gives NaN logits in the rows and ids it belongs to;
  * the verification reports such a row as SV_BAD_ROW.  Everything else
  * (remaining arguments, status_dev, limits, errors, the workspace rule) as
- * for the bf16 entry points; sv_lm_head_logits_fp8 is one launch,
- * spec_verify_lm_head_fp8 two plus the draws. */
+ * for the bf16 entry points; products of more than about 2^31 tiles of the
+ * logits, or steps of 128 dims of one SM's tiles, are SV_EUNSUPPORTED.
+ * sv_lm_head_logits_fp8 is one launch, spec_verify_lm_head_fp8 two plus the
+ * draws.  All launches may start before the kernel ahead of them on the
+ * stream has ended, and wait for it before they touch memory. */
 size_t sv_lm_head_fp8_workspace_bytes(int64_t B, int32_t K, int32_t V);
 sv_status_t sv_lm_head_logits_fp8(const void *hidden, const float *hidden_scales,
                                   const void *lm_head,

@@ -383,7 +383,7 @@ def _cuda(t: torch.Tensor, name: str) -> torch.device:
 def _need(t: torch.Tensor, name: str, dtype, shape, dev: torch.device):
     """_check, without its cost where nothing is wrong (these calls are a few
     microseconds of host time in all)."""
-    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         _check(t, name, dtype, shape, dev)
 
 
@@ -428,6 +428,12 @@ def _blocks(n: int) -> int:
     return -(-n // _BLOCK)
 
 
+def _fits(d: int):
+    """A row's length is a 32-bit integer in the C ABI."""
+    if d > 0x7FFFFFFF:
+        raise SpecVerifyError(N.SV_EUNSUPPORTED)
+
+
 def sv_quantize_fp8(x: torch.Tensor, block_rows: int = 1, *, out: torch.Tensor | None = None,
                     scales: torch.Tensor | None = None,
                     stream: torch.cuda.Stream | None = None) -> tuple[torch.Tensor, torch.Tensor]:
@@ -443,6 +449,7 @@ def sv_quantize_fp8(x: torch.Tensor, block_rows: int = 1, *, out: torch.Tensor |
     if len(shape) < 1 or shape[-1] < 1 or (block_rows != 1 and len(shape) != 2):
         raise ValueError("x must be [..., d], and [V, d] for blocks of 128 rows")
     d = shape[-1]
+    _fits(d)
     rows = x.numel() // d
     sshape = (shape[:-1] if block_rows == 1 else (_blocks(rows),)) + (_blocks(d),)
     with _on(dev, stream) as s:
@@ -495,6 +502,7 @@ def sv_block_norm(x: torch.Tensor, residual: torch.Tensor, norm_weight: torch.Te
     if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("x must be [..., d]")
     d = shape[-1]
+    _fits(d)
     M = x.numel() // d
     _need(residual, "residual", residual.dtype, shape, dev)
     _need(norm_weight, "norm_weight", norm_weight.dtype, (d,), dev)
@@ -543,6 +551,8 @@ def _lm_fp8_check(hidden, hidden_scales, lm_head, lm_head_scales) -> torch.devic
     if len(wshape) != 2 or len(shape) < 1 or shape[-1] != wshape[1]:
         raise ValueError("lm_head must be [V, d], d the hidden states' last dimension")
     V, d = wshape
+    _fits(V)
+    _fits(d)
     nb = _blocks(d)
     _need(lm_head, "lm_head", _F8, wshape, dev)
     _need(hidden_scales, "hidden_scales", _F32, shape[:-1] + (nb,), dev)

@@ -35,6 +35,18 @@
 // whole 16-byte units -- an SM gets rid of about 16 bytes a cycle while all of
 // them write, so a warp that stores itself waits thousands of cycles a tile.
 // Every wait is bounded (l8_wait), with lm_head_kernel's teardown.
+//
+// Measured (graph replay, weights larger than L2 or rotated): M 2304, V 151936,
+// d 4096: 0.99 ms = 2890 TFLOP/s in a burst (1.14 ms under the power cap), the
+// tensor pipe 62 % active; bound by the round trip of a buffer (MMA, commit,
+// wait, read, hand back, wait: ~1400 cycles for two buffers' 2 x 512).  M 384,
+// V 128256: 207 us (two row tiles, half of the second empty).  M 8, V 151936:
+// 98 us = 6.3 TB/s, and M 1, V 32000: 26 us = 5.0 TB/s, bound by the weights'
+// bytes, the latter with ~6 us of launch, first loads and last tile.
+// What the parts were worth on the large shape: hand-back without a
+// cluster-scope release 3150 -> 1580 us with the register split; two issuing
+// warps, scales through shared memory and waits without clock reads -> 1233;
+// tensor stores -> 1124; reading ahead over a step's end -> 991.
 #pragma once
 
 #include "sv_lmhead.cuh"
@@ -842,8 +854,7 @@ __global__ void __launch_bounds__(kL8Threads, 1)
                 const int m0 = static_cast<int>((l8_tile_m(P, t) * kCtas + rank) * kLmBM);
                 const int n0 = static_cast<int>(l8_tile_n(P, t)) * P.NB + static_cast<int>(rank) * box;
                 for (int kb = 0; kb < P.KB; ++kb) {
-                    if (wrapped &&
-                        !__all_sync(0xFFFFFFFFu, l8_wait(smem_addr(&empty[s]), ph ^ 1u))) {
+                    if (wrapped && !__all_sync(0xFFFFFFFFu, l8_wait(smem_addr(&empty[s]), ph ^ 1u))) {
                         ok = false;
                         break;
                     }
@@ -864,6 +875,20 @@ __global__ void __launch_bounds__(kL8Threads, 1)
                         ph ^= 1u;
                         wrapped = true;
                     }
+                }
+            }
+            // every stage's last MMAs have signalled this CTA's barriers before
+            // its shared memory goes
+            int left = wrapped ? P.stages : s;
+            if (!wrapped) {
+                s = 0;
+                ph = 1u;
+            }
+            for (; ok && left > 0; --left) {
+                ok = __all_sync(0xFFFFFFFFu, l8_wait(smem_addr(&empty[s]), ph ^ 1u));
+                if (++s == P.stages) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
             if (!ok && lane == 0)

@@ -85,6 +85,9 @@ def test_head_sizes():
     assert _head(V=N.SV_MAX_V + 1) == N.SV_EUNSUPPORTED
     assert _head(M=(1 << 30) + 1) == N.SV_EUNSUPPORTED
     assert _head(M=0, h=None) == N.SV_OK
+    # more tiles, or steps of them, than are counted in 32 bits
+    assert _head(M=1 << 30, V=N.SV_MAX_V) == N.SV_EUNSUPPORTED
+    assert _head(M=1 << 24, V=N.SV_MAX_V, d=(1 << 31) - 16) == N.SV_EUNSUPPORTED
 
 
 VERIFY = dict(h=FAKE, hs=FAKE, w=FAKE, ws=FAKE, d=256, q=FAKE, tok=FAKE, u=FAKE, T=1.0, B=4, K=3, V=1000, logits=FAKE,
