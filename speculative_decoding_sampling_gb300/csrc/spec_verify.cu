@@ -502,25 +502,43 @@ struct Lm8Plan {
 
 Lm8Plan lm8_plan(int64_t M, int32_t V)
 {
-    Lm8Plan p;
-    p.pair = M > sv::kLmBM;
-    const int64_t rows = p.pair ? 2 * sv::kLmBM : sv::kLmBM, units = p.pair ? kNominalSms / 2 : kNominalSms;
-    p.MT = static_cast<int32_t>(ceil_div(M > 0 ? M : 1, rows));
-    // Ids per tile: the width for which the waves of tiles cost least.  A step
-    // of a tile (128 hidden dims) costs at least the accumulator warps' chain
-    // of about 640 cycles, whatever its width, or the time its weights take from memory when every step brings
-    // new ones (one row tile: 128 bytes an id at 23 bytes a cycle and SM).
+    // Row tiles of 128 by CTAs alone or of 256 by pairs, and ids per tile: the
+    // cut for which the waves of tiles cost least.  A step of a tile (128
+    // hidden dims) costs at least the accumulator warps' chain of about 640
+    // cycles, whatever its width, or the time its weights take from memory when
+    // every step brings new ones (one row tile: 128 bytes an id at 23 bytes a
+    // cycle and SM).  Lone CTAs over several row tiles load each weight tile
+    // twice as often as pairs do; that makes a wave 1.17 times a pair's
+    // (measured 1.13 to 1.24 at d 2048 and 4096), so they are taken where a pair
+    // would leave enough of its rows or of its last wave empty:
+    //   M 384, V 128256, d 4096: 10 waves 181 us, pairs 14 waves 207 us;
+    //   M 257, V 50000, d 2048: 4 waves 41 us, pairs 6 waves 50 us;
+    //   M 2304, V 151936, d 4096: 71 waves 1095 us, pairs 71 waves 993 us;
+    //   M 896, V 151936, d 4096: 28 waves 467 us, pairs 32 waves 456 us.
     // Narrower tiles on ties: they reach more SMs.  A pair's tiles are 64, 128
     // or 256 wide (two whole halves, each in boxes of one size).
-    const int64_t per_id = p.pair ? 11 : 22; // quarter cycles an id
+    Lm8Plan p = {};
     int64_t best = INT64_MAX;
-    p.NB = sv::kL8MaxNB;
-    for (int32_t nb = sv::kL8MaxNB; nb >= (p.pair ? 64 : 32); nb = p.pair ? nb / 2 : nb - 32) {
-        const int64_t bytes = p.MT == 1 ? per_id * nb / 4 : 0;
-        const int64_t cost = ceil_div(p.MT * ceil_div(V, nb), units) * ((bytes > 640 ? bytes : 640) + 40);
-        if (cost <= best) {
-            best = cost;
-            p.NB = nb;
+    for (int pair = M > sv::kLmBM ? 1 : 0; pair >= 0; --pair) {
+        const int64_t rows = pair ? 2 * sv::kLmBM : sv::kLmBM, units = pair ? kNominalSms / 2 : kNominalSms;
+        const int32_t mt = static_cast<int32_t>(ceil_div(M > 0 ? M : 1, rows));
+        const int64_t chain = pair || mt == 1 ? 640 : 755;
+        const int64_t per_id = pair ? 11 : 22; // quarter cycles an id
+        int64_t low = INT64_MAX;
+        int32_t NB = sv::kL8MaxNB;
+        for (int32_t nb = sv::kL8MaxNB; nb >= (pair ? 64 : 32); nb = pair ? nb / 2 : nb - 32) {
+            const int64_t bytes = mt == 1 ? per_id * nb / 4 : 0;
+            const int64_t cost = ceil_div(mt * ceil_div(V, nb), units) * ((bytes > chain ? bytes : chain) + 40);
+            if (cost <= low) {
+                low = cost;
+                NB = nb;
+            }
+        }
+        if (low < best) { // a pair on ties
+            best = low;
+            p.pair = pair != 0;
+            p.MT = mt;
+            p.NB = NB;
         }
     }
     p.NT = static_cast<int32_t>(ceil_div(V, p.NB));

@@ -11,13 +11,14 @@
 // folded into fp32 accumulators in registers: one fp32 multiply-add per logit
 // and block, while the tensor cores form the next block's sums.
 //
-// Two shapes of one kernel.  PAIR false (M <= 128): a CTA per SM, tiles of
-// 128 rows x NB ids; few rows leave the tensor cores idle most of the time
-// and the kernel streams W.  PAIR true: a cluster of two CTAs on a pair of
-// SMs, tiles of 256 rows x NB ids, each CTA loading its 128 rows of h and
-// half of the tile of W (one tcgen05.mma of M 256 reads both), which halves
-// what each SM takes from L2.  Tiles are walked rows fastest, so the CTAs
-// running at one time share a few tiles of W.
+// Two shapes of one kernel.  PAIR false (M <= 128, and the row counts of
+// several tiles that fill pairs badly: lm8_plan): a CTA per SM, tiles of 128
+// rows x NB ids; few rows leave the tensor cores idle most of the time and the
+// kernel streams W.  PAIR true: a cluster of two CTAs on a pair of SMs, tiles
+// of 256 rows x NB ids, each CTA loading its 128 rows of h and half of the
+// tile of W (one tcgen05.mma of M 256 reads both), which halves what each SM
+// takes from L2.  Tiles are walked rows fastest, so the CTAs running at one
+// time share a few tiles of W.
 //
 // Warp 0 loads (2-D tensor-memory-accelerator boxes of 128 hidden dims, one
 // 128-byte swizzle row each); warps 1 and 2 issue the MMAs.  A step (128
@@ -40,7 +41,7 @@
 // d 4096: 0.99 ms = 2890 TFLOP/s in a burst (1.14 ms under the power cap), the
 // tensor pipe 62 % active; bound by the round trip of a buffer (MMA, commit,
 // wait, read, hand back, wait: ~1400 cycles for two buffers' 2 x 512).  M 384,
-// V 128256: 207 us (two row tiles, half of the second empty).  M 8, V 151936:
+// V 128256: 181 us (three row tiles on single CTAs).  M 8, V 151936:
 // 98 us = 6.3 TB/s, and M 1, V 32000: 26 us = 5.0 TB/s, bound by the weights'
 // bytes, the latter with ~6 us of launch, first loads and last tile.
 // What the parts were worth on the large shape: hand-back without a

@@ -80,6 +80,20 @@ def test_every_value_and_scale_reaches_its_place(M, V):
     assert R.within(_logits(ops), z, 3 * R.U * z.abs(), torch.bfloat16)
 
 
+# row counts of several 128-row tiles whose waves cost less on single CTAs than
+# on pairs, and the same ids a wave below, where pairs take them
+@pytest.mark.parametrize("M,V,d", [(257, 20003, 128), (288, 32000, 272), (321, 24006, 1040), (384, 50001, 64),
+                                   (513, 20008, 144), (640, 35000, 128), (384, 9700, 272), (384, 12960, 144),
+                                   (384, 12961, 144), (1100, 33001, 32)])
+def test_logits_over_several_row_tiles(M, V, d):
+    test_logits(M, V, d)
+
+
+@pytest.mark.parametrize("M,V", [(300, 20010), (513, 20003)])
+def test_places_over_several_row_tiles(M, V):
+    test_every_value_and_scale_reaches_its_place(M, V)
+
+
 def test_leading_dims_and_empty():
     h, hs, w, ws = _dev(R.head_operands(12, 300, 144, seed=1))
     flat = sv.sv_lm_head_logits_fp8(h, hs, w, ws)
