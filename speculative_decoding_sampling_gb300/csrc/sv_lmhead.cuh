@@ -470,12 +470,14 @@ __global__ void __launch_bounds__(kLmThreads, 1)
 template <bool DENSE>
 __global__ void __launch_bounds__(256) lm_merge_kernel(const Params P, float2 *part, int32_t NT)
 {
-    pdl_wait_primary(); // behind the e4m3 product it is launched as a programmatic dependent
     const int lane = threadIdx.x & 31;
     const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int64_t R = P.B * (static_cast<int64_t>(P.K) + 1);
+    pdl_wait_primary(); // behind the e4m3 product it is launched as a programmatic dependent
+    pdl_launch_dependents(); // the draw stream's CTAs are placed meanwhile, and wait for this kernel's end
     if (r < R) { // warp-uniform
         float M = -INFINITY, S = 0.0f;
+        RowSide sd = {-1, 0.0f, 1.0f, 0.0f};
         // eight pairs a lane on their way at a time, merged in order
         float2 *row = part + r * NT;
         for (int32_t i0 = lane; i0 < NT; i0 += 32 * 8) {
@@ -484,6 +486,8 @@ __global__ void __launch_bounds__(256) lm_merge_kernel(const Params P, float2 *p
             for (int k = 0; k < 8; ++k)
                 if (i0 + 32 * k < NT)
                     pr[k] = row[i0 + 32 * k];
+            if (i0 == 0) // the draft data's two loads behind each other, while the pairs are on their way
+                sd = fetch_side<uint16_t, DENSE>(P, r);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 if (i0 + 32 * k < NT) {
@@ -494,11 +498,9 @@ __global__ void __launch_bounds__(256) lm_merge_kernel(const Params P, float2 *p
         warp_merge_ms(M, S, P.c);
         if (lane == 0) {
             P.row_part[r * P.PM] = make_float2(M, S);
-            const RowSide sd = fetch_side<uint16_t, DENSE>(P, r);
             P.row_side[r] = make_float4(__int_as_float(sd.x), sd.zx, sd.qx, sd.u);
         }
     }
-    pdl_launch_dependents();
 }
 
 } // namespace sv
