@@ -64,6 +64,12 @@ constexpr int kL8AccRegs = 216, kL8OtherRegs = 40;
 static_assert(32 * kL8AccWarps * kL8AccRegs + 256 * kL8OtherRegs <= 128 * kL8Threads, "register split");
 constexpr uint32_t kL8TmemCols = 2 * kL8MaxNB; // two fp32 sums of one step: all 512 columns
 constexpr int kL8MaxStages = 8;
+// Several row tiles share each tile of W and ask for it at about the same time,
+// so all of them wait for memory; the unit with the first row tile asks for it
+// this many steps earlier (4 to 12 time the same, 24 worse): 282 -> 268 us at
+// M 576, V 128256, d 4096.  With one row tile asking early is slower (98 us
+// became 112 or more at M 8, V 151936).
+constexpr int kL8Ahead = 8;
 constexpr int kL8Chunk = 16;                                       // steps whose scales are brought in at a time
 constexpr int kL8HsPitch = kLmBM + 1;
 constexpr int kL8TabFloats = kL8Chunk * kL8HsPitch + kL8Chunk * 8; // [step][row], [step][32-column group]
@@ -103,6 +109,15 @@ __device__ __forceinline__ void l8_tma_2d(uint32_t dst, const CUtensorMap *map, 
                      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
                      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
                      : "memory");
+}
+
+// The box into L2.
+__device__ __forceinline__ void l8_prefetch_2d(const CUtensorMap *map, int32_t c0, int32_t c1)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1)
+                 : "memory");
 }
 
 template <bool PAIR> __device__ __forceinline__ void l8_tmem_alloc(uint32_t dst_smem, uint32_t ncols)
@@ -851,10 +866,30 @@ __global__ void __launch_bounds__(kL8Threads, 1)
             const int box = l8_half_cols(P.NB, 0) / kCtas;
             const uint32_t bytes = static_cast<uint32_t>(kCtas * (P.a_rows + brows) * kL8BK);
             bool ok = true;
+            uint32_t pt = unit; // kL8Ahead steps on: tile, step and first id (-1: not this unit's to ask for)
+            int pkb = kL8Ahead, pn = -1;
+            auto settle = [&]() {
+                while (pkb >= P.KB && pt < ntiles) {
+                    pkb -= P.KB;
+                    pt += units;
+                }
+                pn = P.MT > 1 && pt < ntiles && l8_tile_m(P, pt) == 0
+                         ? static_cast<int>(l8_tile_n(P, pt)) * P.NB + static_cast<int>(rank) * box
+                         : -1;
+            };
+            settle();
             for (uint32_t t = unit; t < ntiles && ok; t += units) {
                 const int m0 = static_cast<int>((l8_tile_m(P, t) * kCtas + rank) * kLmBM);
                 const int n0 = static_cast<int>(l8_tile_n(P, t)) * P.NB + static_cast<int>(rank) * box;
                 for (int kb = 0; kb < P.KB; ++kb) {
+                    if (pn >= 0 && l8_elect()) {
+                        l8_prefetch_2d(&tmB, pkb * kL8BK, pn);
+                        if (PAIR && P.halves == 2)
+                            l8_prefetch_2d(&tmB, pkb * kL8BK, pn + 128);
+                    }
+                    __syncwarp();
+                    if (++pkb >= P.KB)
+                        settle();
                     if (wrapped && !__all_sync(0xFFFFFFFFu, l8_wait(smem_addr(&empty[s]), ph ^ 1u))) {
                         ok = false;
                         break;
