@@ -41,7 +41,7 @@
 // d 4096: 0.99 ms = 2890 TFLOP/s in a burst (1.14 ms under the power cap), the
 // tensor pipe 62 % active; bound by the round trip of a buffer (MMA, commit,
 // wait, read, hand back, wait: ~1400 cycles for two buffers' 2 x 512).  M 384,
-// V 128256: 181 us (three row tiles on single CTAs).  M 8, V 151936:
+// V 128256: 176 us (three row tiles on single CTAs).  M 8, V 151936:
 // 98 us = 6.3 TB/s, and M 1, V 32000: 26 us = 5.0 TB/s, bound by the weights'
 // bytes, the latter with ~6 us of launch, first loads and last tile.
 // What the parts were worth on the large shape: hand-back without a
