@@ -790,28 +790,72 @@ size_t norm_rows_smem(int32_t d, size_t x_size, size_t r_size)
     return static_cast<size_t>(sv::kNormRing) * norm_rows_warps(d) * sv::kNormCols * (x_size + r_size);
 }
 
+// The most that a call may ask for; a multiprocessor has 227 KB, less the
+// kernel's own.
+constexpr size_t kNormRowsMaxSmem = 224 * 1024;
+
+// How many staying CTAs of `warps` warps are resident at once on the current
+// device; cached like lm8_units.  The kernel's limit on shared memory belongs
+// to all of its callers, whatever their width and host thread, so it is raised
+// once, to the most that any width may ask for, and never lowered: a limit
+// fitted to each call's width would make a wider call that another thread is
+// just launching fail.
+template <bool XF32, bool RF32, bool FULL> cudaError_t norm_rows_resident(int warps, size_t smem, int64_t &ctas)
+{
+    struct Entry {
+        int ctas[sv::kNormMaxWarps + 1]; // by warps of a row
+        unsigned long long ctx;
+    };
+    static std::mutex mu;
+    static Entry cache[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= kMaxDevices)
+        return cudaErrorInvalidDevice;
+    const unsigned long long ctx = current_context_id();
+    std::lock_guard<std::mutex> lock(mu);
+    Entry &c = cache[dev];
+    if (c.ctx == 0 || c.ctx != ctx)
+        c = {};
+    if (c.ctas[warps] == 0) {
+        auto *kernel = sv::block_norm_rows_kernel<XF32, RF32, FULL>;
+        int sms = 0, per_sm = 0;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kNormRowsMaxSmem));
+        if (e == cudaSuccess)
+            e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, warps * 32, smem);
+        if (e != cudaSuccess)
+            return e;
+        if (per_sm < 1)
+            return cudaErrorInvalidConfiguration;
+        c.ctas[warps] = (sms > 0 ? sms : 1) * per_sm;
+        c.ctx = current_context_id();
+    }
+    ctas = c.ctas[warps];
+    return cudaSuccess;
+}
+
+template <bool XF32, bool RF32, bool FULL> cudaError_t norm_rows_launch_as(const sv::NormParams &P, cudaStream_t s)
+{
+    const size_t smem = norm_rows_smem(P.d, XF32 ? 4 : 2, RF32 ? 4 : 2);
+    int64_t resident = 0;
+    const cudaError_t e = norm_rows_resident<XF32, RF32, FULL>(P.WPR, smem, resident);
+    if (e != cudaSuccess)
+        return e;
+    return launch_behind(sv::block_norm_rows_kernel<XF32, RF32, FULL>,
+                         static_cast<unsigned>(P.M < resident ? P.M : resident), static_cast<unsigned>(P.WPR * 32), smem,
+                         s, P);
+}
+
 template <bool XF32, bool RF32> cudaError_t norm_rows_launch(sv::NormParams P, cudaStream_t s)
 {
     P.WPR = norm_rows_warps(P.d);
-    auto *kernel = P.WPR * sv::kNormCols == P.d ? sv::block_norm_rows_kernel<XF32, RF32, true>
-                                                : sv::block_norm_rows_kernel<XF32, RF32, false>;
-    const int threads = P.WPR * 32;
-    const size_t smem = norm_rows_smem(P.d, XF32 ? 4 : 2, RF32 ? 4 : 2);
-    int dev = 0, sms = 0, per_sm = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess)
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e == cudaSuccess)
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
-    if (e != cudaSuccess)
-        return e;
-    if (per_sm < 1)
-        return cudaErrorInvalidConfiguration;
-    const int64_t resident = static_cast<int64_t>(sms > 0 ? sms : 1) * per_sm;
-    return launch_behind(kernel, static_cast<unsigned>(P.M < resident ? P.M : resident),
-                         static_cast<unsigned>(threads), smem, s, P);
+    return P.WPR * sv::kNormCols == P.d ? norm_rows_launch_as<XF32, RF32, true>(P, s)
+                                        : norm_rows_launch_as<XF32, RF32, false>(P, s);
 }
 
 static_assert(int(sv::kElemBf16) == int(SV_BF16) && int(sv::kElemFp32) == int(SV_FP32) &&
@@ -1140,7 +1184,7 @@ sv_status_t sv_block_norm(const void *x, sv_dtype_t x_dtype, const void *residua
     // rows enough for every SM to walk several (and not too wide for several to
     // be in flight in shared memory): CTAs that stay
     if (vec && d <= sv::kNormRowsMaxD && M >= kNormManyRows &&
-        norm_rows_smem(d, elem_size(x_dtype), elem_size(residual_dtype)) <= 224 * 1024) {
+        norm_rows_smem(d, elem_size(x_dtype), elem_size(residual_dtype)) <= kNormRowsMaxSmem) {
         const bool xf = x_dtype == SV_FP32, rf = residual_dtype == SV_FP32;
         const cudaError_t e = xf ? (rf ? norm_rows_launch<true, true>(P, s) : norm_rows_launch<true, false>(P, s))
                                  : (rf ? norm_rows_launch<false, true>(P, s) : norm_rows_launch<false, false>(P, s));

@@ -1,0 +1,95 @@
+"""The last layer's operators where their callers or their numbers leave the
+ordinary: several widths of one kernel, from several host threads and in one
+graph."""
+import ctypes
+import threading
+
+import pytest
+import torch
+
+import last_layer_ref as R
+import speculative_decoding_sampling_gb300 as sv
+from speculative_decoding_sampling_gb300 import _native as N
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+BF = torch.bfloat16
+
+
+def _bits(t):
+    t = t.cpu().contiguous()
+    return t.view({1: torch.uint8, 2: torch.int16, 4: torch.int32}[t.element_size()])
+
+
+# ------------------------------------------------------------- one kernel, several widths
+
+def _norm_args(x, res, pre, out, res_out, stream):
+    """sv_block_norm's arguments, converted once (bf16 all round)."""
+    M, d = x.shape
+    vp, f = ctypes.c_void_p, ctypes.c_float
+    return (vp(x.data_ptr()), N.SV_BF16, vp(res.data_ptr()), N.SV_BF16, None, None, ctypes.c_int64(1),
+            vp(pre.data_ptr()), N.SV_BF16, f(0.0), f(1.0), f(1.0), f(1e-6), ctypes.c_int64(M), d,
+            vp(res_out.data_ptr()), vp(out.data_ptr()), N.SV_BF16, None, vp(stream.cuda_stream))
+
+
+def test_norm_widths_on_several_host_threads():
+    """Rows of 4096, 1024 and 8192 values need different amounts of shared
+    memory of one kernel: calls from three host threads at once, each on its
+    own stream, all succeed and give what the same calls give alone."""
+    jobs = []
+    for i, d in enumerate((4096, 1024, 8192)):
+        x, res, pre = (R.rand(s, 10 * i + k, BF).to(DEV) for k, s in enumerate(((700, d), (700, d), (d,))))
+        jobs.append((x, res, pre, sv.sv_block_norm(x, res, pre), torch.empty_like(x), torch.empty_like(x),
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    start, codes = threading.Barrier(len(jobs)), [set() for _ in jobs]
+
+    def work(job, seen):
+        x, res, pre, _, out, res_out, stream = job
+        fn, args = N.lib().sv_block_norm, _norm_args(x, res, pre, out, res_out, stream)
+        start.wait()
+        for _ in range(4000):
+            seen.add(fn(*args))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(jobs, codes)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert codes == [{N.SV_OK}] * len(jobs)
+    for _, _, _, want, out, res_out, _ in jobs:
+        assert torch.equal(_bits(out), _bits(want.hidden)) and torch.equal(_bits(res_out), _bits(want.residual))
+
+
+def test_norm_widths_in_one_graph():
+    """Both widths captured into one graph, the second branch on a stream of
+    its own that joins before the quantisation; replayed with new inputs."""
+    xs = [R.rand((700, d), d, BF).to(DEV) for d in (4096, 1024)]
+    ws = [R.rand((d,), d + 1, BF).to(DEV) for d in (4096, 1024)]
+    call = lambda i: sv.sv_block_norm(xs[i], xs[i], ws[i], hidden_dtype=BF)  # noqa: E731
+    want = [call(0), call(1)]
+    sv.sv_quantize_fp8(want[0].hidden)
+    torch.cuda.synchronize()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        a = call(0)
+        with torch.cuda.stream(side):
+            b = call(1)
+        main.wait_stream(side)
+        q = sv.sv_quantize_fp8(a.hidden)
+        c = call(1)
+    for k in range(3):
+        for i, x in enumerate(xs):
+            x.copy_(R.rand(x.shape, 50 + 2 * k + i, BF))
+        g.replay()
+        want = [call(0), call(1)]
+        wq = sv.sv_quantize_fp8(want[0].hidden)
+        torch.cuda.synchronize()
+        for got, ref in ((a, want[0]), (b, want[1]), (c, want[1])):
+            assert torch.equal(_bits(got.hidden), _bits(ref.hidden))
+            assert torch.equal(_bits(got.residual), _bits(ref.residual))
+        assert torch.equal(_bits(q[0]), _bits(wq[0])) and torch.equal(q[1], wq[1])
