@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kNormMaxWarps * 32, 1) block_norm_rows_kernel(
     const int64_t begin = P.M * blockIdx.x / gridDim.x, end = P.M * (blockIdx.x + 1) / gridDim.x;
     const int wsize = P.w_type == kElemBf16 ? 2 : 4, hsize = P.h_type == kElemE4m3 ? 1 : P.h_type == kElemBf16 ? 2 : 4;
     const char *wpost = static_cast<const char *>(P.post) + e * wsize;
-    const unsigned long long rs = pack2(P.rs, P.rs);
+    const unsigned long long rs = pack2(P.rs, P.rs), bs = pack2(P.bs, P.bs);
     unsigned long long wpre[8], branch[8];
     lane_weights(wpre, static_cast<const char *>(P.pre) + e * wsize, P.w_type, left, P.offset);
     lane_weights(branch, wpost, P.w_type, post ? left : 0, P.offset);
@@ -502,13 +502,17 @@ __global__ void __launch_bounds__(kNormMaxWarps * 32, 1) block_norm_rows_kernel(
         lane_take<XF32, FULL>(v, own_x + slot * slot_bytes, threads * 4 * kXSize, left);
         lane_take<RF32, FULL>(r, own_r + slot * slot_bytes, threads * 4 * kRSize, left);
         slot = slot == kNormRing - 1 ? 0 : slot + 1;
-        float f = P.bs;
-        if (post)
-            f *= rsqrtf(__fmaf_rn(row_sum(sum_squares(v), red[0][odd], warp, 0, P.WPR), P.inv_d, P.eps));
-        const unsigned long long ff = pack2(f, f);
+        if (post) { // before gate and weight, whose products with x may leave the fp32 range
+            const float f =
+                rsqrtf(__fmaf_rn(row_sum(sum_squares(v), red[0][odd], warp, 0, P.WPR), P.inv_d, P.eps));
+            const unsigned long long ff = pack2(f, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = mul2(v[i], ff);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            r[i] = fma2(mul2(v[i], branch[i]), ff, mul2(r[i], rs));
+            r[i] = fma2(mul2(v[i], branch[i]), bs, mul2(r[i], rs));
         lane_store<FULL>(r, r_out, RF32, left);
         r_out += static_cast<int64_t>(d) * kRSize;
         const float fh =

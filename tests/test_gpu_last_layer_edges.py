@@ -1,6 +1,6 @@
 """The last layer's operators where their callers or their numbers leave the
 ordinary: several widths of one kernel, from several host threads and in one
-graph."""
+graph; values near the ends of the fp32 range."""
 import ctypes
 import threading
 
@@ -14,7 +14,7 @@ from speculative_decoding_sampling_gb300 import _native as N
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda:0"
-BF = torch.bfloat16
+BF, FP = torch.bfloat16, torch.float32
 
 
 def _bits(t):
@@ -93,3 +93,31 @@ def test_norm_widths_in_one_graph():
             assert torch.equal(_bits(got.hidden), _bits(ref.hidden))
             assert torch.equal(_bits(got.residual), _bits(ref.residual))
         assert torch.equal(_bits(q[0]), _bits(wq[0])) and torch.equal(q[1], wq[1])
+
+
+# ------------------------------------------------------------- ends of the range
+
+def _norm(x, res, pre, post=None, gate=None, hidden=FP, **kw):
+    dv = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    return sv.sv_block_norm(dv(x), dv(res), dv(pre), post_weight=dv(post), gate=dv(gate), hidden_dtype=hidden,
+                            branch_scale=kw.get("bs", 1.0))
+
+
+@pytest.mark.parametrize("M", [5, 700])
+@pytest.mark.parametrize("d", [1024, 1000])
+def test_norm_factor_before_gate_and_weight(M, d):
+    """x times gate times weight past the fp32 range, their product with the
+    norm's factor well inside it; and a row whose mean square is past the
+    range, which normalises to 0 before the gate."""
+    x, res, pre = R.rand((M, d), 1), R.rand((M, d), 2), R.rand((d,), 3)
+    post, gate = R.rand((d,), 4) * 1e11, R.rand((M, d), 5) * 1e11
+    x[1] *= 1e17
+    bs = 1e-16
+    h, r, eh, er = R.norm64(x, res, pre, post, gate, bs=bs)
+    got = _norm(x, res, pre, post, gate, bs=bs)
+    assert R.within(got.residual.cpu(), r, er, FP) and R.within(got.hidden.cpu(), h, eh, FP)
+    x[2] = 1e38
+    post, gate = post * 1e-11, gate * 1e-11
+    got = _norm(x, res, pre, post, gate * 16)
+    assert torch.equal(got.residual[2].cpu(), res[2])
+    assert got.hidden.isfinite().all()
