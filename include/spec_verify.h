@@ -373,8 +373,9 @@ sv_status_t spec_verify_lm_head_fp8(
  *                sv_quantize_fp8 forms them (block_rows 1); NULL otherwise.
  * eps > 0 and the three scalars finite; d <= SV_MAX_D.  Pointers aligned to
  * their element; 16-byte aligned rows (d % 8 == 0) take the fast path.  A row
- * whose mean square exceeds the fp32 range normalises to 0.  One launch on
- * `stream`; allocates nothing. */
+ * whose mean square exceeds the fp32 range normalises to 0 (with eps below
+ * 2^-100: whose sum of squares does).  One launch on `stream`; allocates
+ * nothing. */
 sv_status_t sv_block_norm(const void *x, sv_dtype_t x_dtype,
                           const void *residual, sv_dtype_t residual_dtype,
                           const void *post_weight, const void *gate,

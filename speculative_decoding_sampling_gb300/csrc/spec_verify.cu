@@ -1172,7 +1172,13 @@ sv_status_t sv_block_norm(const void *x, sv_dtype_t x_dtype, const void *residua
     P.rs = residual_scale;
     P.bs = branch_scale;
     P.eps = eps;
-    P.inv_d = 1.0f / static_cast<float>(d);
+    // An eps this small does not cover what the smallest squares lose by the
+    // scale (4 d 2^-150 of the mean): they are then added as they are.
+    int half = 0;
+    while (eps >= 0x1p-100f && (int64_t{1} << (2 * half)) < d)
+        ++half;
+    P.sq_scale = std::ldexp(1.0f, -half);
+    P.sq_inv_d = std::ldexp(1.0f / static_cast<float>(d), 2 * half);
     P.r_out = residual_out;
     P.h = hidden;
     P.scales = hidden_scales;

@@ -121,3 +121,39 @@ def test_norm_factor_before_gate_and_weight(M, d):
     got = _norm(x, res, pre, post, gate * 16)
     assert torch.equal(got.residual[2].cpu(), res[2])
     assert got.hidden.isfinite().all()
+
+
+@pytest.mark.parametrize("M", [5, 700])
+@pytest.mark.parametrize("d", [8192, 4096, 1000, 300, 96, 20000, 4101])
+def test_norm_of_large_rows(M, d):
+    """Rows whose sum of squares is past the fp32 range while their mean
+    square is inside it, beside ordinary rows, as x (under a post norm) and as
+    residual; past the mean square's own range a row normalises to 0."""
+    if M == 700 and d > 8192:
+        pytest.skip("few rows cover the width")
+    x, res, pre, post = R.rand((M, d), 1), R.rand((M, d), 2), R.rand((d,), 3), R.rand((d,), 4)
+    sign = torch.where(torch.arange(d) % 3 == 0, -1.0, 1.0)
+    # mean square 3e37: the sum is past 3.4e38 from 12 values on
+    x[1], res[3] = 5.5e18 * sign, 5.5e18 * sign.flip(0)
+    x[4], res[4] = 4e18 * sign, -4e18 * sign
+    h, r, eh, er = R.norm64(x, res, pre, post)
+    got = _norm(x, res, pre, post)
+    assert R.within(got.residual.cpu(), r, er, FP) and R.within(got.hidden.cpu(), h, eh, FP)
+    assert got.hidden[1].count_nonzero() > 0 and got.hidden[3].count_nonzero() > 0
+    res[0] = 3e19 * sign                                    # mean square 9e38
+    clean = got.hidden[1:].clone()
+    got = _norm(x, res, pre, post)
+    assert (got.hidden[0] == 0).all() and got.residual[0].isfinite().all()
+    assert torch.equal(_bits(got.hidden[1:]), _bits(clean))
+
+
+@pytest.mark.parametrize("M", [5, 700])
+def test_norm_of_tiny_rows_under_a_tiny_eps(M):
+    """Values whose squares are near the smallest normal number, with an eps
+    that does not hide them."""
+    d, eps = 8192, 1e-38
+    x, res, pre = torch.zeros(M, d), R.rand((M, d), 2) * 2.0 ** -60, R.rand((d,), 3)
+    eps32 = float(torch.tensor(eps))
+    h, r, eh, er = R.norm64(x, res, pre, eps=eps32)
+    got = sv.sv_block_norm(x.to(DEV), res.to(DEV), pre.to(DEV), eps=eps, hidden_dtype=FP)
+    assert R.within(got.residual.cpu(), r, er, FP) and R.within(got.hidden.cpu(), h, eh, FP)
