@@ -324,9 +324,10 @@ sv_status_t spec_verify_lm_head(const void *hidden, const void *lm_head,
  *   lm_head         [V, d] e4m3, 16-byte aligned;
  *   lm_head_scales  [ceil(V / 128), nb] fp32;
  *   d a multiple of 16 (the rows' 16-byte stride) and at least 16.
- * sv_block_norm and sv_quantize_fp8 write operands in this form.  A NaN or
- * infinite scale or value gives NaN logits in the rows and ids it belongs to;
- * the verification reports such a row as SV_BAD_ROW.  Everything else
+ * sv_block_norm and sv_quantize_fp8 write operands in this form.  A NaN
+ * value or a NaN or infinite scale gives NaN logits in the rows and ids it
+ * belongs to, and so do two scales whose product exceeds the fp32 range (it is
+ * formed in fp32); the verification reports such a row as SV_BAD_ROW.  Everything else
  * (remaining arguments, status_dev, limits, errors, the workspace rule) as
  * for the bf16 entry points; products of more than about 2^31 tiles of the
  * logits, or steps of 128 dims of one SM's tiles, are SV_EUNSUPPORTED.

@@ -435,6 +435,15 @@ __device__ __forceinline__ void l8_scales(const Lm8Params &P, uint32_t tabs, uin
     }
 }
 
+// The scale of a block's sums.  One that is infinite becomes NaN (f + 0 f): a
+// block's sum times an infinity would be an infinity of either sign, and -inf
+// is a masked token to what reads the logits.
+__device__ __forceinline__ float l8_scale(float hs, float ws)
+{
+    const float f = __fmul_rn(hs, ws);
+    return __fmaf_rn(f, 0.0f, f);
+}
+
 // acc += f * the 32 columns in v
 __device__ __forceinline__ void l8_fold(unsigned long long *acc, const uint32_t (&v)[32], float f)
 {
@@ -670,9 +679,9 @@ __device__ __forceinline__ void l8_steps_full(L8Steps &S, unsigned long long (&a
         float2 ws = l8_lds2(S.wsp);
         l8_ld_wait(v0);
         l8_ld_tie(v1);
-        l8_fold(acc, v0, __fmul_rn(hs, ws.x));
+        l8_fold(acc, v0, l8_scale(hs, ws.x));
         l8_ld_start(S.buffer() + 64, v0);
-        l8_fold(acc + 16, v1, __fmul_rn(hs, ws.y));
+        l8_fold(acc + 16, v1, l8_scale(hs, ws.y));
         l8_ld_start(S.buffer() + 96, v1);
         const uint32_t there = S.next_there();
         ws = l8_lds2(S.wsp + 8);
@@ -680,12 +689,12 @@ __device__ __forceinline__ void l8_steps_full(L8Steps &S, unsigned long long (&a
         l8_ld_tie(v1);
         S.release();
         S.next();
-        l8_fold(acc + 32, v0, __fmul_rn(hs, ws.x));
+        l8_fold(acc + 32, v0, l8_scale(hs, ws.x));
         if (steps > 1) {
             S.wait_unless(there);
             l8_ld_start(S.buffer(), v0);
         }
-        l8_fold(acc + 48, v1, __fmul_rn(hs, ws.y));
+        l8_fold(acc + 48, v1, l8_scale(hs, ws.y));
         if (steps > 1)
             l8_ld_start(S.buffer() + 32, v1);
     }
@@ -705,7 +714,7 @@ __device__ __forceinline__ void l8_steps_some(L8Steps &S, unsigned long long (&a
                 l8_ld_start(S.buffer() + 32 * g, v);
                 const float2 ws = l8_lds2(S.wsp + (g >> 1) * 8);
                 l8_ld_wait(v);
-                l8_fold(acc + 16 * g, v, __fmul_rn(hs, g & 1 ? ws.y : ws.x));
+                l8_fold(acc + 16 * g, v, l8_scale(hs, g & 1 ? ws.y : ws.x));
             }
         S.release();
         S.next();

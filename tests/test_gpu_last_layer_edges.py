@@ -1,6 +1,6 @@
 """The last layer's operators where their callers or their numbers leave the
 ordinary: several widths of one kernel, from several host threads and in one
-graph; values near the ends of the fp32 range."""
+graph; values near the ends of the fp32 range; infinite scales."""
 import ctypes
 import threading
 
@@ -157,3 +157,53 @@ def test_norm_of_tiny_rows_under_a_tiny_eps(M):
     h, r, eh, er = R.norm64(x, res, pre, eps=eps32)
     got = sv.sv_block_norm(x.to(DEV), res.to(DEV), pre.to(DEV), eps=eps, hidden_dtype=FP)
     assert R.within(got.residual.cpu(), r, er, FP) and R.within(got.hidden.cpu(), h, eh, FP)
+
+
+# ------------------------------------------------------------- infinite scales
+
+@pytest.mark.parametrize("M,V,d", [(6, 700, 256), (140, 700, 256), (300, 20003, 144), (1, 130, 64)])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_infinite_scales_give_nan_logits(M, V, d, value):
+    """A scale that is not finite makes NaN of the logits it belongs to, and
+    of no other; so do two scales whose product is past the fp32 range."""
+    h, hs, w, ws = R.head_operands(M, V, d, seed=2)
+    clean = sv.sv_lm_head_logits_fp8(*(t.to(DEV) for t in (h, hs, w, ws))).cpu()
+    nb, vb = R.blocks(d), R.blocks(V)
+    row, wb = M // 2, vb - 1
+    hs[row, nb - 1] = value
+    ws[wb, 0] = value
+    got = sv.sv_lm_head_logits_fp8(*(t.to(DEV) for t in (h, hs, w, ws))).cpu()
+    bad = torch.zeros(M, V, dtype=torch.bool)
+    bad[row] = True
+    bad[:, wb * 128:] = True
+    assert got[bad].isnan().all() and torch.equal(got[~bad], clean[~bad])
+    hs[row, nb - 1], ws[wb, 0] = 3e30, 1.0
+    ws[0, nb - 1] = 3e30
+    got = sv.sv_lm_head_logits_fp8(*(t.to(DEV) for t in (h, hs, w, ws))).cpu()
+    assert got[row, :128].isnan().all()
+
+
+@pytest.mark.parametrize("B", [4, 60])
+@pytest.mark.parametrize("where", ["weights", "hidden"])
+def test_fused_reports_infinite_scales(B, where):
+    """An infinite scale of a weight block with a single id reaches every
+    sequence, one of a hidden row its own: SV_BAD_ROW, nothing emitted."""
+    K, V, d = 3, 257, 256
+    h, hs, w, ws = R.head_operands(B * (K + 1), V, d, seed=3, dyadic=True)
+    if where == "weights":
+        ws[2, 1] = float("inf")
+    else:
+        hs[(K + 1) * 1, 0] = float("inf")
+    g = torch.Generator().manual_seed(1)
+    tokens = torch.randint(0, V, (B, K), generator=g, dtype=torch.int32)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    res, logits = sv.spec_verify_lm_head_fp8(h.view(B, K + 1, d).to(DEV), hs.view(B, K + 1, 2).to(DEV), w.to(DEV),
+                                             ws.to(DEV), None, tokens.to(DEV),
+                                             torch.rand((B, K + 1), generator=g).to(DEV), 0.9, status=status)
+    assert int(status.item()) == sv.SV_BAD_ROW
+    if where == "weights":
+        assert logits[..., 256].isnan().all() and logits[..., :256].isfinite().all()
+        assert (res.num_emitted == 0).all() and (res.out_tokens == -1).all()
+    else:
+        assert logits[1, 0].isnan().all()
+        assert int(res.num_emitted[1]) == 0 and (res.num_emitted[torch.arange(B) != 1] >= 1).all()
