@@ -77,22 +77,37 @@ def sv_filter_logits(logits: torch.Tensor, temperature: float, top_k: int = 0, t
     return out, kept
 
 
-_ws_lock = threading.Lock()
-_ws_cache: dict[int, torch.Tensor] = {}
+_ws_local = threading.local()  # of each host thread: {(device index, raw stream): workspace}
 
 
-def default_workspace(device: torch.device, nbytes: int) -> torch.Tensor:
-    """A zero-filled workspace of at least `nbytes` on `device`, shared by the
-    calls that do not pass their own.  The kernels leave it zero-filled, so
-    calls ordered on one stream may reuse it; calls that may overlap (other
-    streams) must pass distinct workspaces."""
+def default_workspace(device: torch.device, nbytes: int, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """A zero-filled workspace of at least `nbytes` on `device` for the calls
+    on `stream` (default: the current one) that do not pass their own.  Each
+    stream and host thread has one, allocated, cleared and used on that stream
+    only: the kernels leave it zero-filled, so calls in the stream's order may
+    share it, and calls that may overlap never do (a call is several launches,
+    which another thread's may come between).  While the stream is being
+    captured, a new one that belongs to the graph, which clears it."""
     idx = device.index if device.index is not None else torch.cuda.current_device()
-    with _ws_lock:
-        ws = _ws_cache.get(idx)
-        if ws is None or ws.numel() < nbytes:
-            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=f"cuda:{idx}")
-            _ws_cache[idx] = ws
-        return ws
+    current = torch.cuda.current_stream(idx)
+    if stream is None:
+        stream = current
+    if stream != current or idx != torch.cuda.current_device():
+        with torch.cuda.stream(stream):
+            return _workspace_here(idx, stream.cuda_stream, nbytes)
+    return _workspace_here(idx, stream.cuda_stream, nbytes)
+
+
+def _workspace_here(idx: int, raw_stream: int, nbytes: int) -> torch.Tensor:
+    """default_workspace of the current stream and device."""
+    capturing = torch.cuda.is_current_stream_capturing()
+    mine, key = _ws_local.__dict__, (idx, raw_stream)
+    ws = None if capturing else mine.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=f"cuda:{idx}")
+        if not capturing:
+            mine[key] = ws
+    return ws
 
 
 @dataclass
@@ -177,13 +192,9 @@ def _call(fn_name: str, target_logits, draft_probs, draft_tokens, uniforms,
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     if workspace is None:
-        workspace = default_workspace(dev, need)
-        # the shared workspace was allocated on the stream current at the time;
-        # when this call runs on another one, the caching allocator must not
-        # hand the memory out again (after a larger workspace replaces it)
-        # before this call's kernels are done with it
-        if stream != torch.cuda.current_stream(dev):
-            workspace.record_stream(stream)
+        if fn_name != "spec_verify" and torch.cuda.is_current_stream_capturing():
+            raise ValueError("workspace: the two stages of a captured call need one that both are given")
+        workspace = default_workspace(dev, need, stream)
     elif workspace.device != dev or workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must hold {need} bytes on {dev}")
     args = [target_logits.data_ptr(), dt, _ptr(draft_probs), _ptr(draft_tokens),
@@ -236,7 +247,10 @@ def spec_verify(target_logits: torch.Tensor, draft_probs: torch.Tensor | None,
     [1] device tensor that receives SV_BAD_* bits; `stats` an int64
     [SV_STATS_WORDS(K)] device tensor the verdicts add the call's acceptance
     counters to (spec_verify_stats).  Runs asynchronously on `stream`
-    (default: the current stream)."""
+    (default: the current stream).  Without a `workspace` the call takes
+    default_workspace's, which calls on other streams or from other host
+    threads do not share; in a captured graph that is one of the graph's own,
+    which every replay clears."""
     o = _outputs(target_logits, want_probs, out)
     if status is not None:
         o["status"] = status
@@ -314,7 +328,8 @@ def spec_verify_lm_head(hidden: torch.Tensor, lm_head: torch.Tensor, draft_probs
                         stream: torch.cuda.Stream | None = None):
     """spec_verify on logits computed in the same step by the target's LM
     head: hidden [B, K+1, d] bf16, lm_head [V, d] bf16.  Returns
-    (SpecVerifyResult, logits [B, K+1, V] bf16)."""
+    (SpecVerifyResult, logits [B, K+1, V] bf16).  workspace as for
+    spec_verify."""
     _lm_check(hidden, lm_head)
     if hidden.dim() != 3:
         raise ValueError("hidden must be [B, K+1, d]")
@@ -335,9 +350,7 @@ def spec_verify_lm_head(hidden: torch.Tensor, lm_head: torch.Tensor, draft_probs
         raise SpecVerifyError(N.SV_EUNSUPPORTED)
     stream = stream or torch.cuda.current_stream(dev)
     if workspace is None:
-        workspace = default_workspace(dev, need)
-        if stream != torch.cuda.current_stream(dev):
-            workspace.record_stream(stream)
+        workspace = default_workspace(dev, need, stream)
     elif workspace.device != dev or workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must hold {need} bytes on {dev}")
     res = SpecVerifyResult(
@@ -600,8 +613,7 @@ def spec_verify_lm_head_fp8(hidden: torch.Tensor, hidden_scales: torch.Tensor, l
     """spec_verify_lm_head on e4m3 operands with block scales: hidden
     [B, K+1, d], hidden_scales [B, K+1, ceil(d / 128)], lm_head and
     lm_head_scales as for sv_lm_head_logits_fp8.  Returns (SpecVerifyResult,
-    logits [B, K+1, V] bf16).  A call that is captured into a graph without a
-    workspace of its own gets one that belongs to the graph."""
+    logits [B, K+1, V] bf16).  workspace as for spec_verify."""
     dev = _lm_fp8_check(hidden, hidden_scales, lm_head, lm_head_scales)
     if hidden.dim() != 3 or hidden.shape[1] < 1:
         raise ValueError("hidden must be [B, K+1, d]")
@@ -622,11 +634,7 @@ def spec_verify_lm_head_fp8(hidden: torch.Tensor, hidden_scales: torch.Tensor, l
             logits_out = torch.empty((B, K1, V), dtype=torch.bfloat16, device=dev)
         _need(logits_out, "logits_out", torch.bfloat16, (B, K1, V), dev)
         if workspace is None:
-            if torch.cuda.is_current_stream_capturing():
-                workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=dev)
-            else:
-                workspace = default_workspace(dev, need)
-                workspace.record_stream(torch.cuda.current_stream(dev))
+            workspace = _workspace_here(dev.index, s, need)
         elif workspace.device != dev or workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace must hold {need} bytes on {dev}")
         res = SpecVerifyResult(
@@ -669,7 +677,8 @@ def spec_verify_tree(logits: torch.Tensor, draft_probs: torch.Tensor, parent: to
     """Verification of a candidate tree (multi-step speculative sampling):
     logits [B, N, V] bf16 / fp32 (row i: the target after node i's path),
     draft_probs [B, N, V] fp32 (row i: the draft distribution of node i's
-    children), parent / tokens [B, N] int32, uniforms [B, N] fp32."""
+    children), parent / tokens [B, N] int32, uniforms [B, N] fp32.  workspace
+    as for spec_verify."""
     if logits.dim() != 3:
         raise ValueError("logits must be [B, N, V]")
     B, Nn, V = logits.shape
@@ -687,9 +696,7 @@ def spec_verify_tree(logits: torch.Tensor, draft_probs: torch.Tensor, parent: to
         raise SpecVerifyError(N.SV_EUNSUPPORTED)
     stream = stream or torch.cuda.current_stream(dev)
     if workspace is None:
-        workspace = default_workspace(dev, need)
-        if stream != torch.cuda.current_stream(dev):
-            workspace.record_stream(stream)
+        workspace = default_workspace(dev, need, stream)
     elif workspace.device != dev or workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must hold {need} bytes on {dev}")
     if status is not None:
