@@ -593,7 +593,8 @@ template <bool VEC> __global__ void __launch_bounds__(kQuantWarps * 32) quantize
     const int base = static_cast<int>(i - row * P.segs) * kSeg;
     float v[8];
     seg_load<VEC>(v, row_of(P.x, row, P.d, P.x_type), P.x_type, base, lane, P.d);
-    seg_quantize<VEC>(v, P.v + row * P.d, P.scales + row * ((P.d + 127) / 128), base, lane, P.d);
+    const int64_t blocks = (static_cast<int64_t>(P.d) + 127) / 128; // d may be the largest 32-bit number
+    seg_quantize<VEC>(v, P.v + row * P.d, P.scales + row * blocks, base, lane, P.d);
 }
 
 // A scale per 128 x 128 block: a CTA per block, held in registers (64 values

@@ -207,3 +207,26 @@ def test_fused_reports_infinite_scales(B, where):
     else:
         assert logits[1, 0].isnan().all()
         assert int(res.num_emitted[1]) == 0 and (res.num_emitted[torch.arange(B) != 1] >= 1).all()
+
+
+# ------------------------------------------------------------- the widest rows
+
+@pytest.mark.parametrize("d", [2 ** 31 - 8, 2 ** 31 - 1, 2 ** 31 - 129])
+@pytest.mark.parametrize("rows", [1, 128])
+def test_quantize_rows_as_wide_as_an_int(d, rows):
+    """Widths at the end of 32 bits, three rows: the ends of every row are
+    quantised as they are alone, and the scales lie where they belong."""
+    nb = R.blocks(d)
+    n = d - (nb - 3) * 128                                  # the last three blocks, the last one short
+    x = torch.zeros((3, d), dtype=BF, device=DEV)
+    head, tail = R.rand((3, 256), 1, BF).to(DEV), R.rand((3, n), 2, BF).to(DEV)
+    x[:, :256], x[:, -n:] = head, tail
+    v, s = sv.sv_quantize_fp8(x, rows)
+    hv, hs = sv.sv_quantize_fp8(head, rows)
+    tv, ts = sv.sv_quantize_fp8(tail, rows)
+    assert s.shape == (3 if rows == 1 else 1, nb)
+    assert torch.equal(s[:, :2], hs) and torch.equal(s[:, -3:], ts)
+    assert torch.equal(_bits(v[:, :256]), _bits(hv)) and torch.equal(_bits(v[:, -n:]), _bits(tv))
+    mid = v.view(torch.uint8)[:, 256:d - n]
+    assert all(int(mid[i].count_nonzero()) == 0 for i in range(3))
+    assert (s[:, 2:-3] == torch.tensor(R.AMAX_FLOOR, device=DEV) / 448).all()
