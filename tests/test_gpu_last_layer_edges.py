@@ -95,6 +95,20 @@ def test_norm_widths_in_one_graph():
         assert torch.equal(_bits(q[0]), _bits(wq[0])) and torch.equal(q[1], wq[1])
 
 
+@pytest.mark.parametrize("M", [64, 351, 607, 608])
+@pytest.mark.parametrize("d", [1536, 1537])
+def test_norm_row_counts_up_to_the_staying_ctas(M, d):
+    """Row counts on both sides of the change of kernel, and a width that
+    never changes: the same rows within the same bounds."""
+    x, res, pre = R.rand((M, d), 1, BF), R.rand((M, d), 2, FP, 3.0), R.rand((d,), 3, BF, 0.3)
+    post, gate = R.rand((d,), 4, BF, 0.3), R.rand((1, d), 5, BF)
+    h, r, eh, er = R.norm64(x, res, pre, post, gate, offset=1.0)
+    dv = lambda t: t.to(DEV)  # noqa: E731
+    got = sv.sv_block_norm(dv(x), dv(res), dv(pre), post_weight=dv(post), gate=dv(gate), weight_offset=1.0,
+                           hidden_dtype=FP)
+    assert R.within(got.residual.cpu(), r, er, FP) and R.within(got.hidden.cpu(), h, eh, FP)
+
+
 # ------------------------------------------------------------- ends of the range
 
 def _norm(x, res, pre, post=None, gate=None, hidden=FP, **kw):
@@ -123,14 +137,11 @@ def test_norm_factor_before_gate_and_weight(M, d):
     assert got.hidden.isfinite().all()
 
 
-@pytest.mark.parametrize("M", [5, 700])
-@pytest.mark.parametrize("d", [8192, 4096, 1000, 300, 96, 20000, 4101])
+@pytest.mark.parametrize("M,d", [(M, d) for M in (5, 700) for d in (8192, 4096, 1000, 300, 96, 4101)] + [(5, 20000)])
 def test_norm_of_large_rows(M, d):
     """Rows whose sum of squares is past the fp32 range while their mean
     square is inside it, beside ordinary rows, as x (under a post norm) and as
     residual; past the mean square's own range a row normalises to 0."""
-    if M == 700 and d > 8192:
-        pytest.skip("few rows cover the width")
     x, res, pre, post = R.rand((M, d), 1), R.rand((M, d), 2), R.rand((d,), 3), R.rand((d,), 4)
     sign = torch.where(torch.arange(d) % 3 == 0, -1.0, 1.0)
     # mean square 3e37: the sum is past 3.4e38 from 12 values on
