@@ -375,8 +375,10 @@ sv_status_t spec_verify_lm_head_fp8(
  * eps > 0 and the three scalars finite; d <= SV_MAX_D.  Pointers aligned to
  * their element; 16-byte aligned rows (d % 8 == 0) take the fast path.  A row
  * whose mean square exceeds the fp32 range normalises to 0 (with eps below
- * 2^-100: whose sum of squares does).  One launch on `stream`; allocates
- * nothing. */
+ * 2^-100: whose sum of squares does).  A row's squares are added in an order
+ * that depends on M, d and the pointers' alignment, so the last bits of its
+ * hidden values may differ between calls with other row counts.  One launch on
+ * `stream`; allocates nothing. */
 sv_status_t sv_block_norm(const void *x, sv_dtype_t x_dtype,
                           const void *residual, sv_dtype_t residual_dtype,
                           const void *post_weight, const void *gate,
@@ -389,7 +391,9 @@ sv_status_t sv_block_norm(const void *x, sv_dtype_t x_dtype,
 
 /* Quantisation to e4m3 with one fp32 scale per block of block_rows x 128
  * values: block_rows 1 for activations, 128 for weights (done once, at load).
- *   scale = max(largest magnitude of the block, 2^-100) / 448,
+ *   scale = max(largest magnitude of the block, 2^-100) / 448 (the quotient
+ *           correctly rounded; a product with a rounded 1 / 448 is one step
+ *           off for about half of all blocks),
  *   value = x * (1 / scale) rounded to e4m3 (nearest even, at most 448),
  * each step in fp32.  A block that holds a NaN gets a NaN scale; one that
  * holds an infinity an infinite scale.

@@ -379,9 +379,9 @@ bool lm_tensor_map(CUtensorMap *map, const void *base, int64_t rows, int32_t col
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * (fp8 ? 1 : 2)};
     const cuuint32_t box[2] = {box_cols ? box_cols : static_cast<cuuint32_t>(fp8 ? sv::kL8BK : sv::kLmBK), box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                  const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  box_cols ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -508,13 +508,13 @@ Lm8Plan lm8_plan(int64_t M, int32_t V)
     // cycles, whatever its width, or the time its weights take from memory when
     // every step brings new ones (one row tile: 128 bytes an id at 23 bytes a
     // cycle and SM).  Lone CTAs over several row tiles load each weight tile
-    // twice as often as pairs do; that makes a wave 1.17 times a pair's
-    // (measured 1.13 to 1.24 at d 2048 and 4096), so they are taken where a pair
-    // would leave enough of its rows or of its last wave empty:
-    //   M 384, V 128256, d 4096: 10 waves 181 us, pairs 14 waves 207 us;
-    //   M 257, V 50000, d 2048: 4 waves 41 us, pairs 6 waves 50 us;
-    //   M 2304, V 151936, d 4096: 71 waves 1095 us, pairs 71 waves 993 us;
-    //   M 896, V 151936, d 4096: 28 waves 467 us, pairs 32 waves 456 us.
+    // twice as often as pairs do; the rule takes a wave of theirs as 1.17 times a
+    // pair's (measured 1.06 to 1.22 at d 2048 and 4096), so they are taken where a
+    // pair would leave enough of its rows or of its last wave empty:
+    //   M 384, V 128256, d 4096: 10 waves 179 us, pairs 14 waves 205 us;
+    //   M 257, V 50000, d 2048: 4 waves 40 us, pairs 6 waves 52 us;
+    //   M 2304, V 151936, d 4096: 71 waves 1072 us, pairs 71 waves 1010 us;
+    //   M 896, V 151936, d 4096: 28 waves 439 us, pairs 32 waves 457 us (taken).
     // Narrower tiles on ties: they reach more SMs.  A pair's tiles are 64, 128
     // or 256 wide (two whole halves, each in boxes of one size).
     Lm8Plan p = {};
@@ -650,7 +650,7 @@ cudaError_t lm8_launch_as(const CUtensorMap &ta, const CUtensorMap &tb, const CU
     return cudaLaunchKernelEx(&cfg, sv::lm_head_fp8_kernel<PAIR>, ta, tb, tc, L);
 }
 
-// logits (bf16 out) and, with `part`, the row statistics of each half tile.
+// logits (bf16 out) and, with `part`, the row statistics of each tile.
 cudaError_t lm8_launch(const void *hidden, const float *hidden_scales, const void *lm_head, const float *lm_head_scales,
                        int64_t M, int32_t d, int32_t V, void *logits, float2 *part, float c, int32_t *status,
                        cudaStream_t stream)

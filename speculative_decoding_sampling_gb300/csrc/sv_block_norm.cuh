@@ -11,10 +11,14 @@
 //
 // A row is cut into segments of 256 values, one warp's 8 per lane; WPR warps
 // hold a row in registers from the loads to the stores, so x, residual and
-// gate are read once and r and h written once.  The two row sums are warp
-// sums joined through shared memory in a fixed order.  A few rows are bound by
-// one launch's latency (5 rows of 4096: 4.0 us), so a row takes as many warps
-// as it has segments; many rows take block_norm_rows_kernel.
+// gate are read once and r and h written once.  (Above 16384 values a lane has
+// 64 of each, more than its registers hold, and some wait in local memory: 5
+// rows of 32768 take 22.7 us, of 16384 9.2.)  The two row sums are warp sums
+// joined through shared memory in a fixed order.  A few rows are bound by one
+// launch's latency (5 rows of 4096: 4.0 us), so a row takes as many warps as it
+// has segments; many rows take block_norm_rows_kernel, which adds a row's
+// squares in another order, so h may differ from the same row's among few in
+// its last bits.
 #pragma once
 
 #include "sv_device.cuh"
@@ -349,11 +353,13 @@ __global__ void __launch_bounds__(kNormMaxWarps * 32) block_norm_kernel(const No
 // transactions), and a block's largest magnitude is one warp-wide maximum of
 // its bits, above which NaNs lie.  Pairs of values go through the packed fp32
 // instructions.  2304 rows of 4096 (bf16 x, fp32 residual, gate, e4m3 out,
-// 106 MB): 24.8 us = 4.3 TB/s, bound by the ~400 instructions a warp issues per
+// 106 MB): 25.0 us = 4.25 TB/s, bound by the ~440 instructions a warp issues per
 // row, each behind the last (33 us with one row per CTA and 8 values a lane,
 // half of it half-sector stores; a third CTA per SM at 80 registers was slower,
 // 28 us).  Rows of whole 16-byte units, up to 512 columns a warp (FULL:
-// all of the CTA's warps have 512).
+// all of the CTA's warps have 512).  Warps and slots are rounded up to a power
+// of two, so a width between two costs as much as the wider one (5120: 41 us,
+// 8192: 44 us).
 constexpr int kNormRing = 4; // rows in flight, this one included
 constexpr int kNormCols = 512;
 constexpr int kNormRowsMaxD = kNormMaxWarps * kNormCols;
@@ -599,8 +605,9 @@ template <bool VEC> __global__ void __launch_bounds__(kQuantWarps * 32) quantize
 
 // A scale per 128 x 128 block: a CTA per block, held in registers (64 values
 // a thread; bf16 ones stay packed until they are scaled, so that more CTAs are
-// resident: 88 -> 58 us for 32003 x 4112, 6.8 TB/s, bound by its bytes).  VEC: a half-warp per row, 8 consecutive values a lane; otherwise
-// 4 single values of a row per lane.
+// resident: 88 -> 58 us for 32003 x 4112, 6.8 TB/s, bound by its bytes; fp32
+// 97 us, 6.7 TB/s).  A half-warp per row, 8 consecutive values a lane; rows that
+// are not whole 16-byte units take quantize_tiles_odd_kernel.
 __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b)
 {
     uint32_t r;
@@ -683,7 +690,9 @@ template <bool FP32> __global__ void __launch_bounds__(kQuantWarps * 32) quantiz
     }
 }
 
-// Rows that are not whole 16-byte units.
+// Rows that are not whole 16-byte units: 4 single values of a row per lane, 64
+// in all (32003 x 4111: 234 us from bf16, bound by its 2-byte loads, 99 from
+// fp32).
 __global__ void __launch_bounds__(kQuantWarps * 32) quantize_tiles_odd_kernel(const QuantParams P)
 {
     __shared__ float red[kQuantWarps];

@@ -5,7 +5,7 @@
 //
 // h e4m3 [M, d] with a scale per row and 128 hidden dims, W e4m3 [V, d] with
 // a scale per 128 ids x 128 hidden dims; z is rounded once to bf16.  The
-// inner sums (128 products, each exact in fp32) run on the tensor cores
+// inner sums (fp32 sums of 128 products, each exact) run on the tensor cores
 // (tcgen05, kind f8f6f4) into tensor memory; the scales differ from block to
 // block and are not powers of two, so each block's sums are read back and
 // folded into fp32 accumulators in registers: one fp32 multiply-add per logit
@@ -38,8 +38,8 @@
 // Every wait is bounded (l8_wait), with lm_head_kernel's teardown.
 //
 // Measured (graph replay, weights larger than L2 or rotated): M 2304, V 151936,
-// d 4096: 0.99 ms = 2890 TFLOP/s in a burst (1.14 ms under the power cap), the
-// tensor pipe 62 % active; bound by the round trip of a buffer (MMA, commit,
+// d 4096: 1.00 ms = 2870 TFLOP/s in a burst (1.14 ms under the power cap), the
+// tensor pipe 61 % active; bound by the round trip of a buffer (MMA, commit,
 // wait, read, hand back, wait: ~1400 cycles for two buffers' 2 x 512).  M 384,
 // V 128256: 176 us (three row tiles on single CTAs).  M 8, V 151936:
 // 98 us = 6.3 TB/s, and M 1, V 32000: 26 us = 5.0 TB/s, bound by the weights'
@@ -275,7 +275,7 @@ inline uint32_t l8_idesc(int rows, int ids)
     return (1u << 4) | ((static_cast<uint32_t>(ids) >> 3) << 17) | ((static_cast<uint32_t>(rows) >> 4) << 24);
 }
 
-// ------------------------------------------------------------- the kernel
+// ------------------------------------------------------------- the parts
 
 __device__ __forceinline__ uint32_t l8_round(unsigned long long pair)
 {
