@@ -73,7 +73,8 @@ def algorithmic_bytes(w, num_emitted: np.ndarray) -> dict:
 
 
 # kernels of their own, hashed apart
-OWN_KERNEL_FILES = ("sv_block_norm.cuh", "sv_filter.cuh", "sv_lmhead.cuh", "sv_lmhead_fp8.cuh", "sv_tree.cuh")
+OWN_KERNEL_FILES = ("sv_block_norm.cuh", "sv_filter.cuh", "sv_fp4.cuh", "sv_lmhead.cuh", "sv_lmhead_fp4.cuh",
+                    "sv_lmhead_fp8.cuh", "sv_sample.cuh", "sv_tree.cuh")
 
 
 def kernel_source_hash(only: str | None = None) -> str:

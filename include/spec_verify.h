@@ -38,6 +38,9 @@
  * spec_verify_lm_head_fp8 / sv_lm_head_logits_fp8 (the same on 8-bit
  * operands), sv_block_norm (the norms around the target's last block, with
  * its gate and residual scale), sv_quantize_fp8 (block quantisation),
+ * sv_quantize_fp4 / sv_dequantize_fp4 (microscaled 4-bit floating point),
+ * sv_lm_head_logits_fp4 (the LM head on such operands), sv_sample_logits (the
+ * draft's tokens and its q: temperature, top-k, top-p, min-p),
  * spec_verify_tree (a candidate tree: several drafts per position),
  * sv_workspace_bytes, sv_lm_head_workspace_bytes,
  * sv_lm_head_fp8_workspace_bytes, sv_tree_workspace_bytes,
@@ -404,6 +407,111 @@ sv_status_t sv_block_norm(const void *x, sv_dtype_t x_dtype,
 sv_status_t sv_quantize_fp8(const void *x, sv_dtype_t x_dtype, int64_t rows,
                             int32_t d, int32_t block_rows, void *values,
                             float *scales, void *stream);
+
+/* Microscaled 4-bit floating point, for a draft's or a target's last layer:
+ * x [rows, d] as e2m1 values (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives)
+ * with a scale for each `block` consecutive values of a row.  The pages name
+ * quantised drafts and targets as a deployment measure only
+ * ("推测解码采样验证优化策略 —— 深度调研报告", part 1 section 6, 扩展性与安全性).
+ *   block 16: row_scales[r] = 2^k, the least with
+ *             (row's largest magnitude) / 2^k <= 6 * 448 (1 for a row of zeros,
+ *             at least 2^-126);
+ *             scale = (block's largest magnitude) / (6 * row_scales[r]) rounded
+ *             to e4m3, at least 2^-9 unless the block is all zeros;
+ *             value = x / (scale * row_scales[r]) rounded to e2m1.
+ *   block 32: scale = 2^(floor(log2(block's largest magnitude)) - 2), at least
+ *             2^-127 (e8m0: exponent + 127 in a byte); value = x / scale rounded
+ *             to e2m1; no row scales.
+ * Roundings go to the nearest value, ties to an even last bit, magnitudes over 6
+ * to 6; quotients are rounded to fp32 first.  A block that holds a NaN or an
+ * infinity gets a NaN scale and values of 0, and does not count in its row's
+ * largest magnitude.
+ *   x          [rows, d] bf16 or fp32, d even; d a multiple of 8 with 16-byte
+ *              aligned x takes the fast path;
+ *   values     [rows, d / 2] bytes out: column 2i in the low half of byte i;
+ *   scales     sv_fp4_scale_bytes(rows, d, block) bytes out, 16-byte aligned:
+ *              tiles of 128 rows x 4 blocks, [ceil(rows / 128),
+ *              ceil(d / (4 block)), 32, 4, 4], element [i, j, l, a, b] of row
+ *              128 i + 32 a + l and block 4 j + b, zeros behind the ends (the
+ *              layout the tensor cores read);
+ *   row_scales [rows] fp32 out (block 16), NULL for block 32.
+ * sv_dequantize_fp4 reads the form back: value * scale * row scale, in fp32,
+ * rounded to out_dtype (bf16 or fp32); row_scales there may be any numbers.
+ * sv_fp4_scale_bytes is 0 for sizes that are refused.  One launch each on
+ * `stream`; allocate nothing. */
+size_t sv_fp4_scale_bytes(int64_t rows, int32_t d, int32_t block);
+sv_status_t sv_quantize_fp4(const void *x, sv_dtype_t x_dtype, int64_t rows,
+                            int32_t d, int32_t block, void *values,
+                            void *scales, float *row_scales, void *stream);
+sv_status_t sv_dequantize_fp4(const void *values, const void *scales,
+                              const float *row_scales, int64_t rows, int32_t d,
+                              int32_t block, void *out, sv_dtype_t out_dtype,
+                              void *stream);
+
+/* The LM head on 4-bit operands, both in the form above with the same `block`:
+ *   logits[m, v] = hidden_row_scales[m] * lm_head_row_scales[v]
+ *       * sum_k (hidden * its scale)[m, k] * (lm_head * its scale)[v, k]
+ * The sum over all of d is formed by the tensor cores in fp32 (products and
+ * block scales exact, the order of summation theirs), the row scales (any fp32
+ * numbers; NULL for block 32) multiplied to it in fp32, and the result rounded
+ * once to bf16, nearest even.  A NaN scale gives NaN logits in the rows or ids
+ * it belongs to, and a result outside the fp32 range is NaN, never infinite (-inf
+ * is a masked token); verification and draw report such a row as SV_BAD_ROW.
+ *   hidden         [M, d / 2] bytes, hidden_scales its tiles, both 16-byte
+ *                  aligned; lm_head [V, d / 2] and lm_head_scales likewise;
+ *   logits         [M, V] bf16 out (16-byte aligned with V % 8 == 0 for the
+ *                  fast stores);
+ *   status_dev     as for sv_lm_head_logits;
+ *   d a multiple of 32 (the rows' 16-byte stride).
+ * M <= 2^30, V <= SV_MAX_V.  Returns SV_EINVAL / SV_EUNSUPPORTED on bad sizes or
+ * pointers, SV_ECUDA when a launch (or the tensor-map set-up) fails.  One launch
+ * on `stream`; allocates nothing. */
+sv_status_t sv_lm_head_logits_fp4(
+    const void *hidden, const void *hidden_scales,
+    const float *hidden_row_scales, const void *lm_head,
+    const void *lm_head_scales, const float *lm_head_row_scales, int32_t block,
+    int64_t M, int32_t d, int32_t V, void *logits, int32_t *status_dev,
+    void *stream);
+
+/* One token a row from its logits, as a draft (or a target without drafts)
+ * samples it, and the distribution it came from: q must be what the draft
+ * actually used ("推测解码：草稿、验证与实际加速", section 接受与拒绝怎样保住分布),
+ * so that probs goes to spec_verify as draft_probs as it is.  The ids of a row
+ * are ordered by p = softmax(z / T) descending, equal p by ascending id, and kept
+ * are, in this order:
+ *   top-k  the first min(top_k, #finite) ids (top_k <= 0: all);
+ *   top-p  the shortest prefix of those whose mass reaches top_p times theirs,
+ *          the crossing id included (top_p >= 1: all);
+ *   min-p  of those, the ids with p >= min_p * max p (min_p 0: all; 1: the
+ *          largest alone and its equals).
+ * The token is the smallest id i with u * sum(w) < w_0 + ... + w_i, w the kept
+ * ids' masses in id order and u the row's uniform.
+ *   logits    [rows, V] bf16 or fp32 (-inf: a masked id);
+ *   uniforms  [rows] fp32 in [0, 1);
+ *   tokens    [rows] int32 out;
+ *   prob      [rows] fp32 out, the token's probability; may be NULL;
+ *   kept      [rows] int32 out, ids kept; may be NULL;
+ *   probs     [rows, V] fp32 out, the processed distribution (0 for ids that are
+ *             not kept); may be NULL.  No output may overlap the logits.
+ *   status_dev  SV_BAD_ROW for a row with NaN, +inf or no finite logit (token
+ *             -1, prob and kept 0, probs zeros), SV_BAD_U for a uniform outside
+ *             [0, 1) (token -1, prob 0; kept and probs are the row's); may be
+ *             NULL.
+ * Masses are whole multiples of 2^-45 of the largest (2^-40 at V = SV_MAX_V), right to about 2^-28 of
+ * themselves and summed exactly: an id below half a unit may be kept but
+ * is never drawn.  A cut or a draw differs from exact arithmetic only where it
+ * lies within about 2^-30 of an id's boundary.  Results do not depend on the other
+ * rows of a call.
+ * Returns SV_EINVAL (NULL or misaligned pointer, rows < 0, V < 1, T not finite or
+ * <= 0 or too far from 1, top_p <= 0 or NaN, min_p outside [0, 1], unknown
+ * dtype), SV_EUNSUPPORTED (V > SV_MAX_V, rows > 2^31 / 8) or SV_ECUDA.  One
+ * launch on `stream`; allocates nothing. */
+sv_status_t sv_sample_logits(const void *logits, sv_dtype_t logits_dtype,
+                             const float *uniforms, float temperature,
+                             int32_t top_k, float top_p, float min_p,
+                             int64_t rows, int32_t V, int32_t *tokens,
+                             float *prob, int32_t *kept, float *probs,
+                             int32_t *status_dev, void *stream);
 
 /* Verification of a candidate tree: several drafts per position, one path
  * committed.  The pages require that a tree commits one contiguous path and

@@ -18,6 +18,8 @@ from .binding import (SpecVerifyError, SpecVerifyResult, default_workspace,
                       spec_verify_lm_head, sv_lm_head_logits, sv_lm_head_workspace_bytes,
                       BlockNormResult, sv_block_norm, sv_quantize_fp8, spec_verify_lm_head_fp8,
                       sv_lm_head_logits_fp8, sv_lm_head_fp8_workspace_bytes,
+                      Fp4Tensor, sv_quantize_fp4, sv_dequantize_fp4, sv_lm_head_logits_fp4,
+                      SampleResult, sv_sample_logits,
                       TreeResult, spec_verify_tree, sv_tree_workspace_bytes)
 from . import adaptive
 
@@ -26,6 +28,8 @@ __all__ = [
     "spec_verify_lm_head", "sv_lm_head_logits", "sv_lm_head_workspace_bytes",
     "spec_verify_lm_head_fp8", "sv_lm_head_logits_fp8", "sv_lm_head_fp8_workspace_bytes",
     "sv_block_norm", "BlockNormResult", "sv_quantize_fp8",
+    "sv_quantize_fp4", "sv_dequantize_fp4", "Fp4Tensor", "sv_lm_head_logits_fp4",
+    "sv_sample_logits", "SampleResult",
     "spec_verify_tree", "sv_tree_workspace_bytes", "TreeResult",
     "sv_workspace_bytes", "sv_filter_logits", "sv_kernel_launches", "sv_status_string", "default_workspace",
     "SpecVerifyResult", "SpecVerifyError", "NativeLibraryMissing",

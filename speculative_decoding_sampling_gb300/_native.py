@@ -20,6 +20,7 @@ EXPORTS = ["sv_workspace_bytes", "spec_verify", "spec_verify_stats", "sv_verify_
            "sv_sample_survivors", "spec_verify_noalloc", "sv_filter_logits", "sv_lm_head_workspace_bytes",
            "sv_lm_head_logits", "spec_verify_lm_head", "sv_lm_head_fp8_workspace_bytes",
            "sv_lm_head_logits_fp8", "spec_verify_lm_head_fp8", "sv_block_norm", "sv_quantize_fp8",
+           "sv_fp4_scale_bytes", "sv_quantize_fp4", "sv_dequantize_fp4", "sv_lm_head_logits_fp4", "sv_sample_logits",
            "sv_tree_workspace_bytes", "spec_verify_tree",
            "sv_kernel_launches", "sv_status_string"]
 
@@ -95,6 +96,16 @@ def lib() -> ctypes.CDLL:
                                     f32, i64, i32, vp, vp, ctypes.c_int, vp, vp]
         L.sv_quantize_fp8.restype = ctypes.c_int
         L.sv_quantize_fp8.argtypes = [vp, ctypes.c_int, i64, i32, i32, vp, vp, vp]
+        L.sv_fp4_scale_bytes.restype = ctypes.c_size_t
+        L.sv_fp4_scale_bytes.argtypes = [i64, i32, i32]
+        L.sv_quantize_fp4.restype = ctypes.c_int
+        L.sv_quantize_fp4.argtypes = [vp, ctypes.c_int, i64, i32, i32, vp, vp, vp, vp]
+        L.sv_dequantize_fp4.restype = ctypes.c_int
+        L.sv_dequantize_fp4.argtypes = [vp, vp, vp, i64, i32, i32, vp, ctypes.c_int, vp]
+        L.sv_lm_head_logits_fp4.restype = ctypes.c_int
+        L.sv_lm_head_logits_fp4.argtypes = [vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, vp, vp, vp]
+        L.sv_sample_logits.restype = ctypes.c_int
+        L.sv_sample_logits.argtypes = [vp, ctypes.c_int, vp, f32, i32, f32, f32, i64, i32, vp, vp, vp, vp, vp, vp]
         L.sv_status_string.restype = ctypes.c_char_p
         L.sv_status_string.argtypes = [ctypes.c_int]
         _lib = L

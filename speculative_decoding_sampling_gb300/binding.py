@@ -655,6 +655,178 @@ def spec_verify_lm_head_fp8(hidden: torch.Tensor, hidden_scales: torch.Tensor, l
     return res, logits_out
 
 
+# ------------------------------------------------------------- the draft's step in 4-bit floating point
+
+_SCALE_TYPES = {torch.float8_e4m3fn: 16, torch.float8_e8m0fnu: 32}  # values of a block, by its scales' type
+
+
+@dataclass
+class Fp4Tensor:
+    """A tensor [..., d] in microscaled 4-bit form.  The scales' type says
+    which: float8_e4m3fn (a scale for 16 values, and row_scales) or
+    float8_e8m0fnu (a scale for 32 values, no row_scales)."""
+    values: torch.Tensor              # uint8 [..., d / 2]: column 2i in the low half of byte i
+    scales: torch.Tensor              # [ceil(rows / 128), ceil(blocks / 4), 32, 4, 4]: tiles of 128 rows x 4 blocks
+    row_scales: torch.Tensor | None   # fp32 [...]
+
+
+def _fp4_check(t: Fp4Tensor, name: str) -> tuple[torch.device, int, int, int]:
+    """(device, block, rows, d) of t."""
+    block = _SCALE_TYPES.get(t.scales.dtype)
+    if block is None:
+        raise TypeError(f"{name}.scales: expected float8_e4m3fn or float8_e8m0fnu, got {t.scales.dtype}")
+    if t.values.dtype is not torch.uint8:
+        raise TypeError(f"{name}.values: expected uint8, got {t.values.dtype}")
+    dev = _cuda(t.values, f"{name}.values")
+    shape = t.values.shape
+    if len(shape) < 1 or shape[-1] < 1:
+        raise ValueError(f"{name}.values must be [..., d / 2]")
+    d = 2 * shape[-1]
+    _fits(d)
+    rows = t.values.numel() // shape[-1]
+    _need(t.scales, f"{name}.scales", t.scales.dtype, _fp4_scale_shape(rows, d, block), dev)
+    if (t.row_scales is None) != (block == 32):
+        raise ValueError(f"{name}.row_scales: blocks of 16 have them, blocks of 32 do not")
+    if block == 16:
+        _need(t.row_scales, f"{name}.row_scales", _F32, shape[:-1], dev)
+    return dev, block, rows, d
+
+
+def _fp4_scale_shape(rows: int, d: int, block: int) -> tuple[int, ...]:
+    return -(-rows // 128), -(-d // (4 * block)), 32, 4, 4
+
+
+def sv_quantize_fp4(x: torch.Tensor, block: int = 16, *, out: Fp4Tensor | None = None,
+                    stream: torch.cuda.Stream | None = None) -> Fp4Tensor:
+    """x [..., d] (bf16 / fp32, d even) in microscaled 4-bit form: e2m1
+    values, a scale for each block of 16 (e4m3, beside a power of two for
+    each row) or 32 consecutive values (a power of two, e8m0).  `out`: one of
+    the same shape and block to write into."""
+    dt = _dtype(x, "x")
+    dev = _cuda(x, "x")
+    shape = x.shape
+    if block not in (16, 32):
+        raise ValueError("block must be 16 or 32")
+    if len(shape) < 1 or shape[-1] < 2 or shape[-1] % 2:
+        raise ValueError("x must be [..., d], d even")
+    d = shape[-1]
+    _fits(d)
+    rows = x.numel() // d
+    with _on(dev, stream) as s:
+        if out is None:
+            st = torch.float8_e4m3fn if block == 16 else torch.float8_e8m0fnu
+            out = Fp4Tensor(torch.empty(shape[:-1] + (d // 2,), dtype=torch.uint8, device=dev),
+                            torch.empty(_fp4_scale_shape(rows, d, block), dtype=st, device=dev),
+                            torch.empty(shape[:-1], dtype=_F32, device=dev) if block == 16 else None)
+        else:
+            odev, oblock, _, _ = _fp4_check(out, "out")
+            if odev != dev or oblock != block or out.values.shape != shape[:-1] + (d // 2,):
+                raise ValueError("out must be of x's shape and device and of this block")
+        rc = N.lib().sv_quantize_fp4(x.data_ptr(), dt, rows, d, block, out.values.data_ptr(), out.scales.data_ptr(),
+                                     _ptr(out.row_scales), s)
+    if rc != N.SV_OK:
+        raise SpecVerifyError(rc)
+    return out
+
+
+def sv_dequantize_fp4(t: Fp4Tensor, dtype: torch.dtype = torch.bfloat16, *, out: torch.Tensor | None = None,
+                      stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """What t stands for, [..., d] in bfloat16 or float32."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("dtype must be bfloat16 or float32")
+    dev, block, rows, d = _fp4_check(t, "t")
+    shape = t.values.shape[:-1] + (d,)
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            _need(out, "out", dtype, shape, dev)
+        rc = N.lib().sv_dequantize_fp4(t.values.data_ptr(), t.scales.data_ptr(), _ptr(t.row_scales), rows, d, block,
+                                       out.data_ptr(), _DTYPES[dtype], s)
+    if rc != N.SV_OK:
+        raise SpecVerifyError(rc)
+    return out
+
+
+def sv_lm_head_logits_fp4(hidden: Fp4Tensor, lm_head: Fp4Tensor, *, out: torch.Tensor | None = None,
+                          status: torch.Tensor | None = None,
+                          stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """sv_lm_head_logits on operands in microscaled 4-bit form, both of the
+    same block: hidden [..., d], lm_head [V, d] -> [..., V] bf16; d a
+    multiple of 32.  status: optional int32 [1] device tensor that receives
+    SV_INTERNAL_TIMEOUT."""
+    dev, block, M, d = _fp4_check(hidden, "hidden")
+    wdev, wblock, V, wd = _fp4_check(lm_head, "lm_head")
+    if wdev != dev or wblock != block or wd != d or lm_head.values.dim() != 2:
+        raise ValueError("lm_head must be [V, d] on the hidden states' device, d their last dimension, of the same block")
+    _fits(V)
+    oshape = hidden.values.shape[:-1] + (V,)
+    if status is not None:
+        _need(status, "status", torch.int32, (1,), dev)
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty(oshape, dtype=torch.bfloat16, device=dev)
+        else:
+            _need(out, "out", torch.bfloat16, oshape, dev)
+        rc = N.lib().sv_lm_head_logits_fp4(hidden.values.data_ptr(), hidden.scales.data_ptr(), _ptr(hidden.row_scales),
+                                           lm_head.values.data_ptr(), lm_head.scales.data_ptr(), _ptr(lm_head.row_scales),
+                                           block, M, d, V, out.data_ptr(), _ptr(status), s)
+    if rc != N.SV_OK:
+        raise SpecVerifyError(rc)
+    return out
+
+
+@dataclass
+class SampleResult:
+    tokens: torch.Tensor              # int32 [...]
+    prob: torch.Tensor                # fp32 [...]: the tokens' probabilities
+    kept: torch.Tensor                # int32 [...]: ids the filters kept
+    probs: torch.Tensor | None        # fp32 [..., V]: the processed distribution
+    status: torch.Tensor | None       # int32 [1], OR of SV_BAD_ROW and SV_BAD_U
+
+
+def sv_sample_logits(logits: torch.Tensor, uniforms: torch.Tensor, temperature: float, top_k: int = 0,
+                     top_p: float = 1.0, min_p: float = 0.0, *, want_probs: bool = False,
+                     out: dict | None = None, status: torch.Tensor | None = None,
+                     stream: torch.cuda.Stream | None = None) -> SampleResult:
+    """One token for each row of logits [..., V] (bf16 / fp32) at
+    `temperature`, by inverse CDF from uniforms [...] (fp32 in [0, 1)), among
+    the ids that top-k, top-p (of the top-k set's mass) and min-p (of the
+    largest probability) keep.  want_probs: also the processed distribution,
+    spec_verify's draft_probs.  `out` may supply preallocated outputs by
+    name (tokens, prob, kept, probs); `status` an int32 [1] device tensor that
+    receives SV_BAD_* bits."""
+    dt = _dtype(logits, "logits")
+    dev = _cuda(logits, "logits")
+    shape = logits.shape
+    if len(shape) < 1 or shape[-1] < 1:
+        raise ValueError("logits must be [..., V]")
+    V = shape[-1]
+    _fits(V)
+    lead = shape[:-1]
+    rows = logits.numel() // V
+    _need(uniforms, "uniforms", _F32, lead, dev)
+    if status is not None:
+        _need(status, "status", torch.int32, (1,), dev)
+    top_k = min(max(int(top_k), 0), 0x7FFFFFFF)
+    with _on(dev, stream) as s:
+        o = {}
+        for name, dtype, oshape in (("tokens", torch.int32, lead), ("prob", _F32, lead), ("kept", torch.int32, lead),
+                                    ("probs", _F32, shape)):
+            given = out.get(name) if out else None
+            if given is not None:
+                _need(given, name, dtype, oshape, dev)
+            elif name != "probs" or want_probs:
+                given = torch.empty(oshape, dtype=dtype, device=dev)
+            o[name] = given
+        rc = N.lib().sv_sample_logits(logits.data_ptr(), dt, uniforms.data_ptr(), float(temperature), top_k,
+                                      float(top_p), float(min_p), rows, V, o["tokens"].data_ptr(), o["prob"].data_ptr(),
+                                      o["kept"].data_ptr(), _ptr(o["probs"]), _ptr(status), s)
+    if rc != N.SV_OK:
+        raise SpecVerifyError(rc)
+    return SampleResult(o["tokens"], o["prob"], o["kept"], o["probs"], status)
+
+
 # ------------------------------------------------------------- trees
 
 @dataclass

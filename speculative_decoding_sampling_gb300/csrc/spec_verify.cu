@@ -2,9 +2,10 @@
 // workspace layout, and the launches on the caller's stream -- the row
 // pass, the draw stream and, when the draw stream does not fill the GPU,
 // the final draws -- each chained to the one before by programmatic
-// dependent launch; the top-k / top-p filter; and the target's last layer
-// (norms, quantisation, LM head).  The operations themselves are documented
-// in spec_verify.h.
+// dependent launch; the top-k / top-p filter; the target's last layer (norms,
+// quantisation, LM head); and the draft's step (4-bit quantisation and LM head,
+// the draw of tokens).  The operations themselves are documented in
+// spec_verify.h.
 #include "spec_verify.h"
 
 #include <cmath>
@@ -16,8 +17,11 @@
 #include "sv_block_norm.cuh"
 #include "sv_filter.cuh"
 #include "sv_final.cuh"
+#include "sv_fp4.cuh"
 #include "sv_lmhead.cuh"
+#include "sv_lmhead_fp4.cuh"
 #include "sv_lmhead_fp8.cuh"
+#include "sv_sample.cuh"
 #include "sv_tree.cuh"
 #include "sv_rows.cuh"
 
@@ -356,8 +360,8 @@ size_t lm_part_bytes(int64_t M, int32_t V) { return align_up(static_cast<size_t>
 // box_rows x box_cols = 32 bf16 in the 64-byte one; out-of-range elements
 // read as zero and are not written.  Reached through the runtime's
 // entry-point lookup.
-bool lm_tensor_map(CUtensorMap *map, const void *base, int64_t rows, int32_t cols, uint32_t box_rows,
-                   bool fp8 = false, uint32_t box_cols = 0)
+bool lm_tensor_map_of(CUtensorMap *map, CUtensorMapDataType type, const void *base, int64_t rows, int64_t cols,
+                      int64_t pitch, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle)
 {
     using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -376,13 +380,20 @@ bool lm_tensor_map(CUtensorMap *map, const void *base, int64_t rows, int32_t col
     if (!encode)
         return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * (fp8 ? 1 : 2)};
-    const cuuint32_t box[2] = {box_cols ? box_cols : static_cast<cuuint32_t>(fp8 ? sv::kL8BK : sv::kLmBK), box_rows};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+    const cuuint32_t box[2] = {box_cols, box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                  const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  box_cols ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(map, type, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool lm_tensor_map(CUtensorMap *map, const void *base, int64_t rows, int32_t cols, uint32_t box_rows,
+                   bool fp8 = false, uint32_t box_cols = 0)
+{
+    return lm_tensor_map_of(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rows, cols,
+                            static_cast<int64_t>(cols) * (fp8 ? 1 : 2),
+                            box_cols ? box_cols : static_cast<uint32_t>(fp8 ? sv::kL8BK : sv::kLmBK), box_rows,
+                            box_cols ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 sv_status_t lm_check(const void *hidden, const void *lm_head, int64_t M, int32_t d, int32_t V, const void *logits)
@@ -760,6 +771,231 @@ bool is_bf16_or_fp32(sv_dtype_t t) { return t == SV_BF16 || t == SV_FP32; }
 
 // 16-byte accesses of 8 consecutive values, where the pointer may be NULL
 bool vec_ok(const void *p, sv_dtype_t t) { return aligned(p, t == SV_E4M3 ? 8 : 16); }
+
+// dynamic shared memory a CTA of sample_kernel may have, beside its own structures
+constexpr size_t kSampleSmem = 227 * 1024 - sizeof(sv::SampleShared) - 1024;
+
+// ------------------------------------------------------- 4-bit operands
+
+// Scale tiles (128 rows x 4 blocks) along d.
+int32_t fp4_tiles(int32_t d, int32_t block) { return static_cast<int32_t>(ceil_div(d, 4 * static_cast<int64_t>(block))); }
+
+// A matrix's scale tiles, 512 bytes each, `box` of them a copy.
+bool lm4_scale_map(CUtensorMap *map, const void *base, int64_t tiles, uint32_t box)
+{
+    return lm_tensor_map_of(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, base, tiles, 128, 512, 128, box,
+                            CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// How a product is cut: a function of (M, V).  A stage (256 hidden dims) of a tile
+// costs an SM the largest of
+//   the MMAs' time, 2 cycles an id (4 steps of 64 dims);
+//   what it loads: a row of h or of W is 128 bytes with 16 of scales, at about 50
+//   bytes a cycle from L2 -- and with one row tile, where W comes from memory
+//   once, 23 bytes a cycle and SM for W.
+// Narrower tiles on ties: they reach more SMs.
+struct Lm4Plan {
+    bool pair;
+    int32_t MT, NT, NB;
+};
+
+Lm4Plan lm4_plan(int64_t M, int32_t V)
+{
+    Lm4Plan p = {};
+    p.pair = M > sv::kLmBM;
+    const int64_t units = p.pair ? kNominalSms / 2 : kNominalSms;
+    p.MT = static_cast<int32_t>(ceil_div(M > 0 ? M : 1, p.pair ? 2 * sv::kLmBM : sv::kLmBM));
+    const int64_t rows = M < sv::kLmBM ? M : sv::kLmBM;
+    int64_t best = INT64_MAX;
+    for (int32_t nb = sv::kL4MaxNB; nb >= 64; nb -= 64) {
+        const int64_t w = 144 * (p.pair ? nb / 2 : nb), loads = (144 * rows + w) / 50;
+        int64_t stage = p.MT == 1 ? w / 23 : 0;
+        stage = stage > loads ? stage : loads;
+        stage = stage > 2 * nb ? stage : 2 * nb;
+        const int64_t cost = ceil_div(p.MT * ceil_div(V, nb), units) * (stage + 40);
+        if (cost <= best) {
+            best = cost;
+            p.NB = nb;
+        }
+    }
+    p.NT = static_cast<int32_t>(ceil_div(V, p.NB));
+    return p;
+}
+
+template <bool PAIR, int BLOCK> cudaError_t lm4_units(int &units)
+{
+    struct Entry {
+        int units;
+        unsigned long long ctx;
+    };
+    static std::mutex mu;
+    static Entry cache[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= kMaxDevices)
+        return cudaErrorInvalidDevice;
+    const unsigned long long ctx = current_context_id();
+    std::lock_guard<std::mutex> lock(mu);
+    if (cache[dev].units == 0 || cache[dev].ctx == 0 || cache[dev].ctx != ctx) {
+        const auto kernel = sv::lm_head_fp4_kernel<PAIR, BLOCK>;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sv::kL4Smem);
+        if (e != cudaSuccess)
+            return e;
+        int sms = 0, n = 0;
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess)
+            return e;
+        n = sms;
+        if (PAIR) {
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 2;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(sms > 1 ? sms & ~1 : 2));
+            cfg.blockDim = dim3(sv::kL4Threads);
+            cfg.dynamicSmemBytes = sv::kL4Smem;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+            if (e != cudaSuccess)
+                return e;
+        }
+        if (n < 1)
+            return cudaErrorInvalidConfiguration;
+        cache[dev].units = n;
+        cache[dev].ctx = current_context_id();
+    }
+    units = cache[dev].units;
+    return cudaSuccess;
+}
+
+template <bool PAIR, int BLOCK>
+cudaError_t lm4_launch_as(const CUtensorMap (&m)[5], const sv::Lm4Params &L, cudaStream_t stream)
+{
+    int units = 0;
+    const cudaError_t e = lm4_units<PAIR, BLOCK>(units);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t tiles = static_cast<int64_t>(L.t.MT) * L.t.NT; // below 2^31 (sv_lm_head_logits_fp4)
+    const int64_t n = tiles < units ? tiles : units;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = PAIR ? 2 : 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(n * (PAIR ? 2 : 1)));
+    cfg.blockDim = dim3(sv::kL4Threads);
+    cfg.dynamicSmemBytes = sv::kL4Smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, sv::lm_head_fp4_kernel<PAIR, BLOCK>, m[0], m[1], m[2], m[3], m[4], L);
+}
+
+cudaError_t lm4_launch(const void *hidden, const void *hidden_scales, const float *gh, const void *lm_head,
+                       const void *lm_head_scales, const float *gw, int32_t block, int64_t M, int32_t d, int32_t V,
+                       void *logits, int32_t *status, cudaStream_t stream)
+{
+    const Lm4Plan p = lm4_plan(M, V);
+    sv::Lm4Params L = {};
+    const int32_t brows = p.pair ? p.NB / 2 : p.NB; // ids of a tile that one CTA loads
+    // A stage holds the rows of h that exist, in 8s (a swizzle group): the MMA's
+    // 128 rows then run on into what lies behind, and those sums are not read.
+    L.t.a_rows = static_cast<int32_t>(M < sv::kLmBM ? ceil_div(M, 8) * 8 : sv::kLmBM);
+    L.KT = fp4_tiles(d, block);
+    const int32_t per_stage = sv::kL4BK / (4 * block); // scale tiles
+    L.blocks = p.NB > 128 ? 2 : 1;
+    L.t.stage_bytes = static_cast<int32_t>((L.t.a_rows + brows) * 128 + per_stage * 512 * (1 + L.blocks));
+    L.t.stage_bytes = (L.t.stage_bytes + 1023) / 1024 * 1024;
+    L.t.stages = sv::kL4RingBytes / L.t.stage_bytes;
+    if (L.t.stages > sv::kL4MaxStages)
+        L.t.stages = sv::kL4MaxStages;
+    CUtensorMap m[5] = {};
+    if (!lm_tensor_map(&m[0], hidden, M, d / 2, static_cast<uint32_t>(L.t.a_rows), true) ||
+        !lm_tensor_map(&m[1], lm_head, V, d / 2, static_cast<uint32_t>(brows), true) ||
+        !lm4_scale_map(&m[2], hidden_scales, ceil_div(M, 128) * L.KT, static_cast<uint32_t>(per_stage)) ||
+        !lm4_scale_map(&m[3], lm_head_scales, ceil_div(V, 128) * L.KT, static_cast<uint32_t>(per_stage)))
+        return cudaErrorInvalidValue;
+    L.t.M = static_cast<int32_t>(M);
+    L.t.N = V;
+    L.t.KB = static_cast<int32_t>(ceil_div(d, sv::kL4BK));
+    L.t.mt_inv = p.MT > 1 ? UINT64_MAX / static_cast<uint64_t>(p.MT) + 1 : 0;
+    L.t.MT = p.MT;
+    L.t.NT = p.NT;
+    L.t.NB = p.NB;
+    L.t.logits = static_cast<uint16_t *>(logits);
+    L.t.tma = (V % 8 == 0 && aligned(logits, 16)) ? 1 : 0;
+    if (L.t.tma && !lm_tensor_map(&m[4], logits, M, V, 32, false, 32))
+        return cudaErrorInvalidValue;
+    L.t.status = status;
+    L.d = d;
+    L.idesc = sv::l4_idesc(p.pair ? 2 * sv::kLmBM : sv::kLmBM, p.NB, block);
+    L.gh = gh;
+    L.gw = gw;
+    if (block == 16)
+        return p.pair ? lm4_launch_as<true, 16>(m, L, stream) : lm4_launch_as<false, 16>(m, L, stream);
+    return p.pair ? lm4_launch_as<true, 32>(m, L, stream) : lm4_launch_as<false, 32>(m, L, stream);
+}
+
+// Warps of a row of `octets` octets: as many as it takes for each lane to keep
+// its share in registers, up to 8.
+int32_t fp4_warps(int32_t octets)
+{
+    int32_t w = 1;
+    while (w < 8 && octets > w * 32 * sv::kF4Regs)
+        w *= 2;
+    return w;
+}
+
+template <int BLOCK, typename XT>
+cudaError_t quantize_fp4_launch(const sv::Fp4Params &P, bool vec, cudaStream_t s)
+{
+    const unsigned grid = static_cast<unsigned>(ceil_div(P.Mpad, sv::kF4Threads / 32 / P.WPR));
+    return launch_behind(vec ? sv::quantize_fp4_kernel<BLOCK, XT, true> : sv::quantize_fp4_kernel<BLOCK, XT, false>, grid,
+                         sv::kF4Threads, 0, s, P);
+}
+
+template <int BLOCK, bool F32>
+cudaError_t dequantize_fp4_launch(const sv::Fp4BackParams &P, bool vec, cudaStream_t s)
+{
+    const unsigned grid = static_cast<unsigned>(ceil_div(P.M, sv::kF4Threads / 32 / P.WPR));
+    return launch_behind(vec ? sv::dequantize_fp4_kernel<BLOCK, F32, true> : sv::dequantize_fp4_kernel<BLOCK, F32, false>,
+                         grid, sv::kF4Threads, 0, s, P);
+}
+
+// ------------------------------------------------------- the draw of tokens
+
+template <typename LT> cudaError_t sample_launch(const sv::SampleParams &P, size_t smem, cudaStream_t stream)
+{
+    if (smem + sizeof(sv::SampleShared) > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(sv::sample_kernel<LT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(kSampleSmem));
+        if (e != cudaSuccess)
+            return e;
+    }
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(P.C);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(P.rows * P.C));
+    cfg.blockDim = dim3(sv::kSmThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, sv::sample_kernel<LT>, P);
+}
 
 template <bool VEC> cudaError_t norm_launch(const sv::NormParams &P, int nseg, unsigned grid, cudaStream_t s)
 {
@@ -1234,6 +1470,178 @@ sv_status_t sv_quantize_fp8(const void *x, sv_dtype_t x_dtype, int64_t rows, int
     else
         e = launch_behind(x_dtype == SV_FP32 ? sv::quantize_tiles_kernel<true> : sv::quantize_tiles_kernel<false>, g,
                           threads, 0, s, P);
+    return e == cudaSuccess ? SV_OK : SV_ECUDA;
+}
+
+size_t sv_fp4_scale_bytes(int64_t rows, int32_t d, int32_t block)
+{
+    if (rows < 0 || rows > INT32_MAX || d < 2 || d % 2 != 0 || (block != 16 && block != 32))
+        return 0;
+    return static_cast<size_t>(ceil_div(rows, 128)) * static_cast<size_t>(fp4_tiles(d, block)) * 512;
+}
+
+sv_status_t sv_quantize_fp4(const void *x, sv_dtype_t x_dtype, int64_t rows, int32_t d, int32_t block, void *values,
+                            void *scales, float *row_scales, void *stream)
+{
+    if (rows < 0 || d < 2 || d % 2 != 0 || !is_bf16_or_fp32(x_dtype) || (block != 16 && block != 32))
+        return SV_EINVAL;
+    if (rows > INT32_MAX - 127 || d > INT32_MAX - 1024)
+        return SV_EUNSUPPORTED;
+    if (rows == 0)
+        return SV_OK;
+    if (!x || !values || !scales || (block == 16) != (row_scales != nullptr) || !aligned(x, elem_size(x_dtype)) ||
+        !aligned(scales, 16) || !aligned(row_scales, 4))
+        return SV_EINVAL;
+    sv::Fp4Params P;
+    P.x = x;
+    P.M = rows;
+    P.Mpad = ceil_div(rows, 128) * 128;
+    P.d = d;
+    P.KT = fp4_tiles(d, block);
+    P.octets = static_cast<int32_t>(P.KT * (block / 2)); // 4 blocks a tile
+    P.WPR = fp4_warps(P.octets);
+    P.v = static_cast<uint8_t *>(values);
+    P.s = static_cast<uint8_t *>(scales);
+    P.g = row_scales;
+    const bool vec = d % 8 == 0 && aligned(x, 16) && aligned(values, 4);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (block == 16)
+        e = x_dtype == SV_BF16 ? quantize_fp4_launch<16, uint16_t>(P, vec, s) : quantize_fp4_launch<16, float>(P, vec, s);
+    else
+        e = x_dtype == SV_BF16 ? quantize_fp4_launch<32, uint16_t>(P, vec, s) : quantize_fp4_launch<32, float>(P, vec, s);
+    return e == cudaSuccess ? SV_OK : SV_ECUDA;
+}
+
+sv_status_t sv_dequantize_fp4(const void *values, const void *scales, const float *row_scales, int64_t rows, int32_t d,
+                              int32_t block, void *out, sv_dtype_t out_dtype, void *stream)
+{
+    if (rows < 0 || d < 2 || d % 2 != 0 || !is_bf16_or_fp32(out_dtype) || (block != 16 && block != 32))
+        return SV_EINVAL;
+    if (rows > INT32_MAX - 127 || d > INT32_MAX - 1024)
+        return SV_EUNSUPPORTED;
+    if (rows == 0)
+        return SV_OK;
+    if (!values || !scales || !out || (block == 16) != (row_scales != nullptr) || !aligned(out, elem_size(out_dtype)) ||
+        !aligned(row_scales, 4))
+        return SV_EINVAL;
+    sv::Fp4BackParams P;
+    P.v = static_cast<const uint8_t *>(values);
+    P.s = static_cast<const uint8_t *>(scales);
+    P.g = row_scales;
+    P.M = rows;
+    P.d = d;
+    P.octets = static_cast<int32_t>(ceil_div(d, 8));
+    P.KT = fp4_tiles(d, block);
+    P.WPR = fp4_warps(P.octets);
+    P.out = out;
+    const bool vec = d % 8 == 0 && aligned(values, 4) && aligned(out, 16);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (block == 16)
+        e = out_dtype == SV_BF16 ? dequantize_fp4_launch<16, false>(P, vec, s) : dequantize_fp4_launch<16, true>(P, vec, s);
+    else
+        e = out_dtype == SV_BF16 ? dequantize_fp4_launch<32, false>(P, vec, s) : dequantize_fp4_launch<32, true>(P, vec, s);
+    return e == cudaSuccess ? SV_OK : SV_ECUDA;
+}
+
+sv_status_t sv_lm_head_logits_fp4(const void *hidden, const void *hidden_scales, const float *hidden_row_scales,
+                                  const void *lm_head, const void *lm_head_scales, const float *lm_head_row_scales,
+                                  int32_t block, int64_t M, int32_t d, int32_t V, void *logits, int32_t *status_dev,
+                                  void *stream)
+{
+    if (M < 0 || d < 32 || d % 32 != 0 || V < 1 || (block != 16 && block != 32) || !aligned(status_dev, 4))
+        return SV_EINVAL;
+    if (V > SV_MAX_V || M > kLmMaxRows)
+        return SV_EUNSUPPORTED;
+    // tiles, their steps and the scale tiles are counted in 32 bits
+    const Lm4Plan p = lm4_plan(M, V);
+    const int64_t tiles = static_cast<int64_t>(p.MT) * p.NT, kt = fp4_tiles(d, block);
+    if (tiles > INT32_MAX || ceil_div(M, 128) > INT32_MAX / kt - 4 || ceil_div(V, 128) > INT32_MAX / kt - 4)
+        return SV_EUNSUPPORTED;
+    if (M == 0)
+        return SV_OK;
+    if (!hidden || !hidden_scales || !lm_head || !lm_head_scales || !logits || !aligned(hidden, 16) ||
+        !aligned(hidden_scales, 16) || !aligned(lm_head, 16) || !aligned(lm_head_scales, 16) || !aligned(logits, 2) ||
+        (block == 16) != (hidden_row_scales != nullptr) || (block == 16) != (lm_head_row_scales != nullptr) ||
+        !aligned(hidden_row_scales, 4) || !aligned(lm_head_row_scales, 4))
+        return SV_EINVAL;
+    return lm4_launch(hidden, hidden_scales, hidden_row_scales, lm_head, lm_head_scales, lm_head_row_scales, block, M, d, V,
+                      logits, status_dev, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? SV_OK
+               : SV_ECUDA;
+}
+
+sv_status_t sv_sample_logits(const void *logits, sv_dtype_t logits_dtype, const float *uniforms, float temperature,
+                             int32_t top_k, float top_p, float min_p, int64_t rows, int32_t V, int32_t *tokens,
+                             float *prob, int32_t *kept, float *probs, int32_t *status_dev, void *stream)
+{
+    if (rows < 0 || V < 1 || !is_bf16_or_fp32(logits_dtype))
+        return SV_EINVAL;
+    if (V > SV_MAX_V)
+        return SV_EUNSUPPORTED;
+    if (!std::isfinite(temperature) || !(temperature > 0.0f) || !(top_p > 0.0f) || !(min_p >= 0.0f && min_p <= 1.0f))
+        return SV_EINVAL;
+    const double c = 32 * 1.4426950408889634074 / static_cast<double>(temperature);
+    sv::SampleParams P = {};
+    P.c_hi = static_cast<float>(c);
+    P.c_lo = static_cast<float>(c - static_cast<double>(P.c_hi));
+    P.cq = static_cast<float>(c / 32);
+    P.dmin = static_cast<float>(-48 * 32 / c);
+    P.window = static_cast<float>(10 * 32 / c);
+    // (a temperature this far from 1 leaves no fp32 number for its window)
+    if (!std::isfinite(P.c_hi) || !std::isfinite(P.dmin) || !(P.cq > 0x1p-100f) || !(P.cq < 0x1p100f))
+        return SV_EINVAL;
+    if (rows > 0 && (!logits || !uniforms || !tokens))
+        return SV_EINVAL;
+    if (!aligned(logits, elem_size(logits_dtype)) || !aligned(uniforms, 4) || !aligned(tokens, 4) || !aligned(prob, 4) ||
+        !aligned(kept, 4) || !aligned(probs, 4) || !aligned(status_dev, 4))
+        return SV_EINVAL;
+    if (rows > INT32_MAX / sv::kSmMaxCtas)
+        return SV_EUNSUPPORTED;
+    if (rows == 0)
+        return SV_OK;
+    P.in = logits;
+    P.rows = rows;
+    P.V = V;
+    P.u = uniforms;
+    P.min_p = min_p > 0.0f;
+    P.min_off = min_p > 0.0f ? std::log(static_cast<double>(min_p)) * static_cast<double>(temperature) : 0.0;
+    P.top_k = top_k;
+    P.top_p = top_p;
+    P.tokens = tokens;
+    P.prob = prob;
+    P.kept = kept;
+    P.probs = probs;
+    P.status = status_dev;
+    P.vec_q = aligned(logits, 16) && aligned(probs, 16);
+    const int fb = 62 - ceil_log2_u64(static_cast<uint64_t>(V) + 1);
+    P.fix = fb < 45 ? fb : 45;
+    // a CTA's ids of a bin add up in 32 bits: 15 bits of up to 2^16 ids each, or (rows
+    // of more than 2^19, up to 2^18 a CTA, and then fix <= 42) 14
+    P.piece = V <= (1 << 19) ? 15 : 14;
+    // CTAs of a row: enough that two of them fit an SM with their slices (one loads
+    // while the other works), and, for few rows, that the rows' clusters reach every
+    // SM, down to 2048 ids a CTA.
+    const int32_t es = static_cast<int32_t>(elem_size(logits_dtype)), pv = 16 / es;
+    auto cut = [&](int32_t C) {
+        P.C = C;
+        P.slice = static_cast<int32_t>(ceil_div(ceil_div(static_cast<int64_t>(V) + pv, C), pv) * pv);
+        const int32_t part = static_cast<int32_t>(ceil_div(P.slice / pv, sv::kSmWarps)) * pv;
+        P.cap = part / 4 > 256 ? part / 4 : (part < 256 ? part : 256);
+        if (P.slice > 65536)
+            P.cap = 0; // a list's entries have 16 bits
+        return static_cast<size_t>(P.slice) * static_cast<size_t>(es) + static_cast<size_t>(P.cap) * 2 * sv::kSmWarps;
+    };
+    int32_t C = 1;
+    while (C < sv::kSmMaxCtas && (cut(C) > 88 * 1024 || (rows * C * 2 <= 2 * kNominalSms && V / (2 * C) >= 2048)))
+        C *= 2;
+    size_t smem = cut(C);
+    P.staged = smem <= kSampleSmem;
+    if (!P.staged)
+        smem = static_cast<size_t>(P.cap) * 2 * sv::kSmWarps;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = logits_dtype == SV_BF16 ? sample_launch<uint16_t>(P, smem, s) : sample_launch<float>(P, smem, s);
     return e == cudaSuccess ? SV_OK : SV_ECUDA;
 }
 

@@ -1,0 +1,399 @@
+// sv_lmhead_fp4.cuh -- the LM head on microscaled 4-bit operands.
+//
+//   z[m, v] = gh[m] gw[v] sum_b sh[m, b] sw[v, b] sum_{k in block b} h[m, k] W[v, k]
+//
+// h [M, d] and W [V, d] as sv_fp4.cuh writes them: e2m1 values with a scale for
+// each 16 of them (e4m3, and a factor gh, gw for each row) or each 32 (e8m0, no
+// factors); z is rounded once to bf16.  The tensor cores multiply the blocks'
+// scales in (tcgen05, kind mxf4nvf4, block_scale), so the whole sum over d stays
+// in tensor memory in fp32 and only the rows' factors are left to the epilogue.
+//
+// Two shapes of one kernel, as for e4m3.  PAIR false (M <= 128): a CTA per SM,
+// tiles of 128 rows x NB ids; W streams through.  PAIR true: a cluster of two
+// CTAs on a pair of SMs, tiles of 256 rows x NB ids, each CTA loading its 128
+// rows of h and half of the tile of W.  Tiles are walked rows fastest.
+//
+// Warp 0 loads: a stage is 256 hidden dims, one 128-byte swizzle row of 4-bit
+// values, with the 512-byte scale tiles that belong to it (both CTAs of a pair
+// take the scales of all NB ids: each forms all columns of its rows).  Warp 1
+// issues: the stage's scale tiles from shared into tensor memory (tcgen05.cp,
+// the four lane quarters get copies), then an MMA for each 64 dims.  Copies and
+// MMAs of one thread run in order, and two sets of scale columns alternate.
+// Warps 2..5 are the epilogue: two accumulators, so that a tile is read, scaled
+// and stored (through shared memory, as for e4m3) while the next is formed.
+// 512 tensor-memory columns: 2 x 192 of sums, 2 x 64 of scales, hence NB <= 192.
+// Ids start at a multiple of 64 of their scale tile: two columns.
+// Every wait is bounded (l8_wait), with lm_head_kernel's teardown.
+#pragma once
+
+#include "sv_lmhead_fp8.cuh"
+
+namespace sv {
+
+constexpr int kL4BK = 256;                 // hidden dims of a stage
+constexpr int kL4MaxNB = 192;
+constexpr int kL4Threads = 192;
+constexpr int kL4MaxStages = 8;
+constexpr uint32_t kL4TmemCols = 512;
+constexpr uint32_t kL4ScaleCol = 2 * kL4MaxNB; // first of 2 x 64 scale columns
+constexpr int kL4StgBytes = kL4MaxNB / 32 * kL8BoxBytes; // an epilogue warp's 32 rows of a tile
+constexpr int kL4RingBytes = 172 * 1024;
+// l8_store_rows reads whole half tiles of 4 boxes (what lies past a tile's ids is
+// not used): the last warp's second half ends past its boxes and the factors.
+constexpr int kL4Behind = 4 * kL4MaxNB * 4 + 1024;
+static_assert(3 * kL4StgBytes + 8 * kL8BoxBytes <= 4 * kL4StgBytes + kL4Behind, "staged rows read behind the boxes");
+constexpr int kL4Smem = 1024 + kL4RingBytes + 4 * kL4StgBytes + kL4Behind;
+static_assert(kL4Smem <= 227 * 1024 - 512, "shared memory of a CTA, less the barriers");
+// the MMA's 128 rows may run past the rows a stage has: never past the memory
+static_assert(4 * kL4StgBytes >= kLmBM * 128, "rows read behind the ring");
+
+struct Lm4Params {
+    Lm8Params t;              // M, N, tiles, logits, status (its own scales and sums unused)
+    int32_t d;                // hidden dims
+    int32_t KT;               // scale tiles along d
+    int32_t blocks;           // scale tiles across a tile's ids: 1 or 2
+    uint32_t idesc;
+    const float *gh, *gw;     // [M], [N] factors, or nullptr
+};
+
+// Tensor map coordinates and copies ---------------------------------------
+
+// 16-byte rows without swizzle, 8-row groups 128 bytes apart: a 512-byte scale
+// tile as tcgen05.cp reads it (32 rows x 128 bits).
+__device__ __forceinline__ uint64_t l4_scale_desc(uint32_t saddr)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(1u) << 16;          // leading byte offset (one column of 16 bytes: unused)
+    d |= static_cast<uint64_t>(128u >> 4) << 32;   // stride byte offset
+    d |= static_cast<uint64_t>(1u) << 46;          // descriptor version
+    return d;                                      // no swizzle
+}
+
+template <bool PAIR> __device__ __forceinline__ void l4_copy_scales(uint32_t taddr, uint64_t desc)
+{
+    if constexpr (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+template <bool PAIR, int BLOCK>
+__device__ __forceinline__ void l4_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sa,
+                                       uint32_t sb, uint32_t acc)
+{
+#define SV_L4_MMA(GROUP, VEC)                                                                                          \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                                     \
+                 "tcgen05.mma.cta_group::" GROUP ".kind::mxf4nvf4.block_scale.scale_vec::" VEC                         \
+                 " [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem),                                               \
+                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(sa), "r"(sb)                                        \
+                 : "memory")
+    if constexpr (PAIR && BLOCK == 16)
+        SV_L4_MMA("2", "4X");
+    else if constexpr (PAIR)
+        SV_L4_MMA("2", "2X");
+    else if constexpr (BLOCK == 16)
+        SV_L4_MMA("1", "4X");
+    else
+        SV_L4_MMA("1", "2X");
+#undef SV_L4_MMA
+}
+
+// Instruction descriptor: D fp32, A and B e2m1, both K-major, scales e4m3
+// (block 16) or e8m0; the scale bytes used are the word's first.
+inline uint32_t l4_idesc(int rows, int ids, int block)
+{
+    return (1u << 7) | (1u << 10) | ((static_cast<uint32_t>(ids) >> 3) << 17) | (block == 32 ? 1u << 23 : 0u) |
+           ((static_cast<uint32_t>(rows) >> 4) << 24);
+}
+
+__device__ __forceinline__ float4 l4_lds4(uint32_t addr)
+{
+    float4 r;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "r"(addr) : "memory");
+    return r;
+}
+
+// x, NaN if it is infinite: -inf is a masked token to what reads the logits.
+__device__ __forceinline__ float l4_finite(float x) { return __fmaf_rn(x, 0.0f, x); }
+
+// The epilogue warps: warp w holds the tile's rows of tensor-memory lane
+// quarter w mod 4.
+template <bool PAIR>
+__device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMap *map, uint32_t stg0, uint32_t gws0,
+                                            uint32_t tbase, uint32_t tfull, uint32_t tempty, int *stop, uint32_t rank,
+                                            uint32_t unit, uint32_t units, uint32_t ntiles)
+{
+    const Lm8Params &T = P.t;
+    const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31u), lq = warp & 3;
+    const uint32_t stg = stg0 + static_cast<uint32_t>(lq) * kL4StgBytes;
+    const uint32_t gws = gws0 + static_cast<uint32_t>(lq) * (kL4MaxNB * 4);
+    const int G = T.NB / 32;
+    const uint32_t te = PAIR ? lm_mapa(tempty, 0) : tempty;
+    bool alive = true;
+    uint32_t i = 0;
+    for (uint32_t t = unit; t < ntiles; t += units, ++i) {
+        const uint32_t a = i & 1u;
+        const int row0 = l8_row0<PAIR>(T, t, rank, lq), n0 = static_cast<int>(l8_tile_n(T, t)) * T.NB;
+        // the rows' and ids' factors, while the tile is formed
+        float gh = 1.0f;
+        if (P.gh) {
+            gh = row0 + lane < T.M ? __ldg(P.gh + row0 + lane) : 0.0f;
+            __syncwarp();
+            for (int c = lane; c < T.NB; c += 32) {
+                const float g = n0 + c < T.N ? __ldg(P.gw + n0 + c) : 0.0f;
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(gws + static_cast<uint32_t>(c) * 4u), "f"(g) : "memory");
+            }
+            __syncwarp();
+        }
+        alive = __all_sync(0xFFFFFFFFu, l8_wait(tfull + a * 8u, (i >> 1) & 1u));
+        if (!alive)
+            break;
+        lm_tc_after();
+        if (T.tma && i > 0) // the last tile's stores have read this warp's shared memory
+            l8_stores_read();
+        __syncwarp();
+        const bool rows_in = row0 < T.M;
+        const uint32_t tl = tbase + (static_cast<uint32_t>(lq) << 21) + a * kL4MaxNB;
+#pragma unroll 1
+        for (int g = 0; g < G; ++g) {
+            if (rows_in) {
+                uint32_t v[32];
+                l8_ld_start(tl + 32 * g, v);
+                l8_ld_wait(v);
+                uint32_t pk[16];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    float4 w = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+                    if (P.gh)
+                        w = l4_lds4(gws + static_cast<uint32_t>(32 * g + 4 * k) * 4u);
+                    const float x0 = l4_finite(__fmul_rn(__uint_as_float(v[4 * k]), __fmul_rn(gh, w.x)));
+                    const float x1 = l4_finite(__fmul_rn(__uint_as_float(v[4 * k + 1]), __fmul_rn(gh, w.y)));
+                    const float x2 = l4_finite(__fmul_rn(__uint_as_float(v[4 * k + 2]), __fmul_rn(gh, w.z)));
+                    const float x3 = l4_finite(__fmul_rn(__uint_as_float(v[4 * k + 3]), __fmul_rn(gh, w.w)));
+                    pk[2 * k] = bf16_rn_pair(x0, x1);
+                    pk[2 * k + 1] = bf16_rn_pair(x2, x3);
+                }
+                l8_stage(stg + g * kL8BoxBytes, pk, lane);
+            }
+        }
+        lm_tc_before();
+        __syncwarp();
+        if (lane == 0) // this warp has read the accumulator
+            l8_arrive(te + a * 8u);
+        if (!rows_in)
+            continue;
+        if (T.tma) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (l8_elect()) {
+                for (int g = 0; g < G; ++g)
+                    if (n0 + 32 * g < T.N)
+                        l8_send(map, stg + g * kL8BoxBytes, n0 + 32 * g, row0);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+        } else {
+            const int ncols = T.N - n0 < T.NB ? T.N - n0 : T.NB;
+            uint32_t boxes = stg;
+            l8_staged_now(boxes);
+            l8_store_rows(T, boxes, row0, n0, ncols < 128 ? ncols : 128, lane);
+            if (ncols > 128)
+                l8_store_rows(T, boxes + 4 * kL8BoxBytes, row0, n0 + 128, ncols - 128, lane);
+            __syncwarp();
+        }
+    }
+    if (!alive && lane == 0)
+        l8_fail(T, stop);
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); // this lane's stores are done
+}
+
+// Unit u (a pair of SMs, or one) takes tiles u, u + units, ...
+template <bool PAIR, int BLOCK>
+__global__ void __launch_bounds__(kL4Threads, 1)
+    lm_head_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                       const __grid_constant__ CUtensorMap tmC, const __grid_constant__ Lm4Params P)
+{
+    constexpr int kCtas = PAIR ? 2 : 1;
+    constexpr int kDimsPerTile = 4 * BLOCK;            // hidden dims of a scale tile
+    constexpr int kTiles = kL4BK / kDimsPerTile;       // scale tiles of a stage: 4 or 2
+    extern __shared__ uint8_t lm_smem_raw[];
+    __shared__ __align__(8) unsigned long long full[kL4MaxStages], empty[kL4MaxStages], tfull[2], tempty[2], drain;
+    __shared__ uint32_t tmem_base;
+    __shared__ int stop;
+    const Lm8Params &T = P.t;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(lm_smem_raw) + 1023) & ~uintptr_t{1023});
+    const uint32_t sbase = smem_addr(smem);
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? lm_cluster_rank() : 0u;
+    const bool leader = rank == 0;
+    const uint32_t unit = blockIdx.x / kCtas, units = gridDim.x / kCtas;
+    const uint32_t ntiles = static_cast<uint32_t>(T.MT) * static_cast<uint32_t>(T.NT);
+    const uint32_t abytes = static_cast<uint32_t>(T.a_rows) * 128u, bbytes = static_cast<uint32_t>(T.NB / kCtas) * 128u;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kL4MaxStages; ++s) {
+            lm_mbar_init(smem_addr(&full[s]), 1);  // the leader's arrival with every CTA's bytes
+            lm_mbar_init(smem_addr(&empty[s]), 1); // the MMAs of the stage
+        }
+        for (int a = 0; a < 2; ++a) {
+            lm_mbar_init(smem_addr(&tfull[a]), 1);
+            lm_mbar_init(smem_addr(&tempty[a]), kCtas * 4);
+        }
+        lm_mbar_init(smem_addr(&drain), 1);
+        stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1)
+        l8_tmem_alloc<PAIR>(smem_addr(&tmem_base), kL4TmemCols);
+    lm_tc_before();
+    __syncthreads();
+    l8_cluster_sync<PAIR>(); // every CTA's barriers exist before another CTA signals them
+    lm_tc_after();
+    const uint32_t tbase = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);
+    pdl_wait_primary();
+    pdl_launch_dependents();
+
+    if (warp == 0) {
+        int s = 0;
+        uint32_t ph = 0;
+        bool wrapped = false, ok = true;
+        const uint32_t fb0 = PAIR ? lm_mapa(smem_addr(&full[0]), 0) : smem_addr(&full[0]);
+        const uint32_t bytes = kCtas * (abytes + bbytes + static_cast<uint32_t>(kTiles * 512 * (1 + P.blocks)));
+        for (uint32_t t = unit; t < ntiles && ok; t += units) {
+            const int mt = static_cast<int>(l8_tile_m(T, t) * kCtas + rank);
+            const int n0 = static_cast<int>(l8_tile_n(T, t)) * T.NB;
+            const int sa0 = mt * P.KT, sb0 = (n0 >> 7) * P.KT;
+            for (int kb = 0; kb < T.KB; ++kb) {
+                if (wrapped && !__all_sync(0xFFFFFFFFu, l8_wait(smem_addr(&empty[s]), ph ^ 1u))) {
+                    ok = false;
+                    break;
+                }
+                if (l8_elect()) {
+                    uint32_t dst = sbase + static_cast<uint32_t>(s * T.stage_bytes);
+                    const uint32_t fb = fb0 + static_cast<uint32_t>(s * 8);
+                    if (leader)
+                        lm_mbar_expect(smem_addr(&full[s]), bytes);
+                    l8_tma_2d<PAIR>(dst, &tmA, kb * 128, mt * kLmBM, fb);
+                    dst += abytes;
+                    l8_tma_2d<PAIR>(dst, &tmB, kb * 128, n0 + static_cast<int>(rank) * (T.NB / kCtas), fb);
+                    dst += bbytes;
+                    l8_tma_2d<PAIR>(dst, &tmSA, 0, sa0 + kb * kTiles, fb);
+                    dst += kTiles * 512;
+                    l8_tma_2d<PAIR>(dst, &tmSB, 0, sb0 + kb * kTiles, fb);
+                    if (P.blocks == 2)
+                        l8_tma_2d<PAIR>(dst + kTiles * 512, &tmSB, 0, sb0 + P.KT + kb * kTiles, fb);
+                }
+                __syncwarp();
+                if (++s == T.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                    wrapped = true;
+                }
+            }
+        }
+        // every stage's last MMAs have signalled this CTA's barriers before
+        // its shared memory goes
+        int left = wrapped ? T.stages : s;
+        if (!wrapped) {
+            s = 0;
+            ph = 1u;
+        }
+        for (; ok && left > 0; --left) {
+            ok = __all_sync(0xFFFFFFFFu, l8_wait(smem_addr(&empty[s]), ph ^ 1u));
+            if (++s == T.stages) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+        if (!ok && lane == 0)
+            l8_fail(T, &stop);
+    } else if (warp == 1) {
+        if (leader) {
+            const uint64_t ad0 = lm_desc(sbase), bd0 = lm_desc(sbase + abytes);
+            const uint64_t sd0 = l4_scale_desc(sbase + abytes + bbytes);
+            int s = 0;
+            uint32_t ph = 0, i = 0, set = 0;
+            bool ok = true;
+            for (uint32_t t = unit; t < ntiles && ok; t += units, ++i) {
+                const uint32_t a = i & 1u;
+                if (i >= 2 && !__all_sync(0xFFFFFFFFu, l8_wait(smem_addr(&tempty[a]), ((i >> 1) & 1u) ^ 1u))) {
+                    ok = false;
+                    break;
+                }
+                lm_tc_after();
+                const uint32_t tacc = tbase + a * kL4MaxNB;
+                const uint32_t shift = ((l8_tile_n(T, t) * static_cast<uint32_t>(T.NB)) & 127u) >> 5; // 0 or 2 columns
+                for (int kb = 0; kb < T.KB; ++kb) {
+                    if (!__all_sync(0xFFFFFFFFu, l8_wait(smem_addr(&full[s]), ph))) {
+                        ok = false;
+                        break;
+                    }
+                    lm_tc_after();
+                    if (l8_elect()) {
+                        const uint64_t so = static_cast<uint64_t>((s * T.stage_bytes) >> 4);
+                        const uint32_t sa = tbase + kL4ScaleCol + set * 64u, sb = sa + kTiles * 4u;
+                        const int left = P.d - kb * kL4BK; // hidden dims from here on
+#pragma unroll
+                        for (int k = 0; k < kTiles; ++k) {
+                            l4_copy_scales<PAIR>(sa + 4 * k, sd0 + so + static_cast<uint64_t>(k * 32));
+                            l4_copy_scales<PAIR>(sb + 4 * P.blocks * k, sd0 + so + static_cast<uint64_t>((kTiles + k) * 32));
+                            if (P.blocks == 2)
+                                l4_copy_scales<PAIR>(sb + 8 * k + 4, sd0 + so + static_cast<uint64_t>((2 * kTiles + k) * 32));
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (k * 64 >= left)
+                                break;
+                            const int tile = k * 64 / kDimsPerTile; // of the stage's scale tiles
+                            // two scales a row and MMA: the first or the second half of the word
+                            const uint32_t half = BLOCK == 32 && (k & 1) ? (2u << 29) | (2u << 4) : 0u;
+                            l4_mma<PAIR, BLOCK>(tacc, ad0 + so + static_cast<uint64_t>(k * 2),
+                                                bd0 + so + static_cast<uint64_t>(k * 2), P.idesc | half, sa + 4 * tile,
+                                                sb + 4 * P.blocks * tile + shift, (kb | k) ? 1u : 0u);
+                        }
+                        l8_commit<PAIR>(smem_addr(&empty[s]));
+                        if (kb == T.KB - 1)
+                            l8_commit<PAIR>(smem_addr(&tfull[a]));
+                    }
+                    __syncwarp();
+                    set ^= 1u;
+                    if (++s == T.stages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (!ok && lane == 0)
+                l8_fail(T, &stop);
+        }
+    } else {
+        l4_epilogue<PAIR>(P, &tmC, sbase + kL4RingBytes, sbase + kL4RingBytes + 4 * kL4StgBytes, tbase,
+                          smem_addr(&tfull[0]), smem_addr(&tempty[0]), &stop, rank, unit, units, ntiles);
+    }
+    // ---- teardown: copies and MMAs in flight complete before the memory goes
+    lm_tc_before();
+    __syncthreads();
+    if (stop) {
+        if (threadIdx.x == 0) { // copies issued before the stop land within microseconds
+            const uint64_t t0 = lm_ns();
+            while (lm_ns() - t0 < 50000ull) {
+            }
+        }
+        if (warp == 1 && leader && l8_elect()) { // every MMA issued is done
+            if constexpr (PAIR)
+                lm_commit_local(smem_addr(&drain));
+            else
+                l8_commit<PAIR>(smem_addr(&drain));
+            (void)l8_wait(smem_addr(&drain), 0u);
+        }
+    }
+    __syncthreads();
+    l8_cluster_sync<PAIR>(); // no CTA's memory goes while the MMAs or signals may still use it
+    if (warp == 1) {
+        lm_tc_after();
+        l8_tmem_dealloc<PAIR>(tbase, kL4TmemCols);
+    }
+}
+
+} // namespace sv
