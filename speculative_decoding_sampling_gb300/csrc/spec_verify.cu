@@ -972,11 +972,13 @@ cudaError_t dequantize_fp4_launch(const sv::Fp4BackParams &P, bool vec, cudaStre
 
 // ------------------------------------------------------- the draw of tokens
 
-template <typename LT> cudaError_t sample_launch(const sv::SampleParams &P, size_t smem, cudaStream_t stream)
+template <typename LT, bool CUTS>
+cudaError_t sample_launch(const sv::SampleParams &P, size_t smem, cudaStream_t stream)
 {
+    const auto kernel = sv::sample_kernel<LT, CUTS>;
     if (smem + sizeof(sv::SampleShared) > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(sv::sample_kernel<LT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(kSampleSmem));
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSampleSmem));
         if (e != cudaSuccess)
             return e;
     }
@@ -994,7 +996,7 @@ template <typename LT> cudaError_t sample_launch(const sv::SampleParams &P, size
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, sv::sample_kernel<LT>, P);
+    return cudaLaunchKernelEx(&cfg, kernel, P);
 }
 
 template <bool VEC> cudaError_t norm_launch(const sv::NormParams &P, int nseg, unsigned grid, cudaStream_t s)
@@ -1588,8 +1590,10 @@ sv_status_t sv_sample_logits(const void *logits, sv_dtype_t logits_dtype, const 
     P.c_lo = static_cast<float>(c - static_cast<double>(P.c_hi));
     P.cq = static_cast<float>(c / 32);
     P.dmin = static_cast<float>(-48 * 32 / c);
-    P.window = static_cast<float>(10 * 32 / c);
-    // (a temperature this far from 1 leaves no fp32 number for its window)
+    // 24 octaves of mass, and 16 of logits at least where top-k counts ids without mass
+    const double low = top_k > 0 ? 16.0 : 0.0, octaves = 24 * 32 / c;
+    P.bins = static_cast<float>(sv::kSmFirst / (octaves > low ? octaves : low));
+    // (a temperature so far from 1 that its factors leave the fp32 range)
     if (!std::isfinite(P.c_hi) || !std::isfinite(P.dmin) || !(P.cq > 0x1p-100f) || !(P.cq < 0x1p100f))
         return SV_EINVAL;
     if (rows > 0 && (!logits || !uniforms || !tokens))
@@ -1624,24 +1628,26 @@ sv_status_t sv_sample_logits(const void *logits, sv_dtype_t logits_dtype, const 
     // while the other works), and, for few rows, that the rows' clusters reach every
     // SM, down to 2048 ids a CTA.
     const int32_t es = static_cast<int32_t>(elem_size(logits_dtype)), pv = 16 / es;
+    const bool cuts = (top_k > 0 && top_k < V) || top_p < 1.0f;
+    const size_t more = cuts ? sizeof(sv::SampleBins) : 0;
     auto cut = [&](int32_t C) {
         P.C = C;
         P.slice = static_cast<int32_t>(ceil_div(ceil_div(static_cast<int64_t>(V) + pv, C), pv) * pv);
-        const int32_t part = static_cast<int32_t>(ceil_div(P.slice / pv, sv::kSmWarps)) * pv;
-        P.cap = part / 4 > 256 ? part / 4 : (part < 256 ? part : 256);
-        if (P.slice > 65536)
-            P.cap = 0; // a list's entries have 16 bits
-        return static_cast<size_t>(P.slice) * static_cast<size_t>(es) + static_cast<size_t>(P.cap) * 2 * sv::kSmWarps;
+        return static_cast<size_t>(P.slice) * static_cast<size_t>(es) + more;
     };
     int32_t C = 1;
-    while (C < sv::kSmMaxCtas && (cut(C) > 88 * 1024 || (rows * C * 2 <= 2 * kNominalSms && V / (2 * C) >= 2048)))
+    while (C < sv::kSmMaxCtas && (cut(C) > 111 * 1024 || (rows * C * 2 <= 2 * kNominalSms && V / (2 * C) >= 2048)))
         C *= 2;
     size_t smem = cut(C);
     P.staged = smem <= kSampleSmem;
     if (!P.staged)
-        smem = static_cast<size_t>(P.cap) * 2 * sv::kSmWarps;
+        smem = more;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = logits_dtype == SV_BF16 ? sample_launch<uint16_t>(P, smem, s) : sample_launch<float>(P, smem, s);
+    cudaError_t e;
+    if (logits_dtype == SV_BF16)
+        e = cuts ? sample_launch<uint16_t, true>(P, smem, s) : sample_launch<uint16_t, false>(P, smem, s);
+    else
+        e = cuts ? sample_launch<float, true>(P, smem, s) : sample_launch<float, false>(P, smem, s);
     return e == cudaSuccess ? SV_OK : SV_ECUDA;
 }
 

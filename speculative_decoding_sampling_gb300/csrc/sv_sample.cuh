@@ -13,24 +13,31 @@
 // a factor in two parts; fp32 logits give their difference in two parts too),
 //   e^((z - max) / T) = 2^(k / 32) (1 + x + x^2/2 + x^3/6),  x = r ln(2) / 32,
 // |x| <= 0.0109, the series' rest below 2^-30; 2^(j / 32) comes from a table of 32
-// whose entries lie in 32 different banks.  (exp2 in fp32 alone gives 2^-22: among
+// whose entries lie in different banks.  (exp2 in fp32 alone gives 2^-22: among
 // 10^5 ids a draw then falls on a neighbour once in some hundred rows.)
 //
 // A cluster of C CTAs (1, 2, 4 or 8) takes a row, each a slice of its ids, read
-// once from memory into shared memory (rows too long for eight stay in L2).
+// once from memory into shared memory (rows too long for eight stay in L2).  CTAs
+// exchange through distributed shared memory; a step ends with a cluster barrier.
 //  1. load, maximum;
-//  2. the mass of the whole row, where it is asked for (top-p without top-k, or
-//     no filter at all);
-//  3. with a filter: the ids above a window below the maximum are listed (id order
-//     within a warp's part); a window that does not hold the cut is widened, up to
-//     the whole row, which needs no list;
-//  4. the cut, digit by digit of the order key (512 bins a digit, counts and masses
-//     of the listed ids; one digit for a bf16 window of up to 512 values), and
-//     among equal keys the j-th id;
-//  5. the kept masses by warp and CTA, the draw inside the warp that holds it;
-//  6. q.
-// CTAs exchange through distributed shared memory, one cluster barrier a step.
+//  2. top-k, top-p: the ids are counted in 1024 bins from the maximum down (24
+//     octaves of mass, and 16 of logits at least for top-k); where top-p refers to
+//     the whole row its mass is formed in the same pass.  A scan finds top-k's bin;
+//     for top-p the counts and the bins' edges bound the running mass to 1.6 % and
+//     so the bins that its cut may lie in.  The ids down to the last of these bins
+//     are listed (up to 4096 a CTA; more are picked out of the slice each time), and
+//     nothing below them is looked at again;
+//  3. up to 256 listed ids are gathered by every CTA and ranked, which settles the
+//     row.  Of more, those of top-k's bin are; then masses are binned (four
+//     shared-memory additions an id) and the ids of top-p's bin gathered.  A bin of
+//     more than 256 is counted again digit by digit of the order key (512 bins a
+//     digit) down to one value, as is all below the bins when a cut lies there;
+//     among ids of one value the j-th in id order is found by an ordered count;
+//  4. the kept masses by warp and CTA, the draw inside the warp that holds it;
+//  5. q.
 #pragma once
+
+#include <type_traits>
 
 #include "sv_filter.cuh"
 
@@ -49,7 +56,7 @@ struct SampleParams {
     float c_hi, c_lo;    // 32 log2(e) / T
     float cq;            // log2(e) / T
     float dmin;          // differences below this have no mass: -48 T ln 2
-    float window;        // first window below the maximum, > 0: 10 T ln 2
+    float bins;          // bins of step 2 per unit of the logits
     double min_off;      // T ln(min_p) (min_p > 0)
     int32_t top_k;       // <= 0: off
     float top_p;         // >= 1: off
@@ -57,7 +64,6 @@ struct SampleParams {
     int32_t C;           // CTAs of a cluster
     int32_t slice;       // ids of a CTA, a multiple of 16 bytes of them
     int32_t staged;      // the slices fit in shared memory
-    int32_t cap;         // list entries of a warp (0: no lists)
     int32_t fix;         // fractional bits of the masses (at most 45, sums of a row below 2^62)
     int32_t piece;       // bits of a mass that a bin adds up in one 32-bit word
     int32_t vec_q;       // q's vectors lie as the logits' do
@@ -68,32 +74,50 @@ struct SampleParams {
     int32_t *status;     // or nullptr
 };
 
+constexpr int kSmFew = 256;    // ids gathered and ranked
+constexpr int kSmFirst = 1024; // bins of step 2
+constexpr int kSmList = 4096;  // ids a CTA lists
+
+// A cut: ids with a larger key, and of those with this key the ones up to `id`.
+struct SampleCutAt {
+    uint32_t key;
+    int32_t id;
+};
+
 struct SampleShared {
     float2 tab[32];                                  // 2^(j / 32) 2^27: as fp32, and as an integer less the shift's bits
     float cmax[kSmMaxCtas];
-    int cbad[kSmMaxCtas];
     unsigned long long cmass[4][kSmMaxCtas];         // exchanged sums, a row of slots for each use
     uint32_t ccnt[4][kSmMaxCtas];
-    uint32_t hist[2][4][kSmBins];                    // counts, masses in three pieces; two, alternating
     unsigned long long wmass[kSmWarps];
     uint32_t wcnt[kSmWarps];
+    float wmax[kSmWarps];
+};
+
+// What top-k and top-p need besides, behind the slice.
+struct SampleBins {
+    uint32_t first[4][kSmFirst];                     // step 2: counts, masses in three pieces
+    uint32_t hist[4][kSmBins];                       // step 3: the same
+    uint2 few[2][kSmFew];                            // this CTA's gathered (key, id): for top-k, for top-p
+    uint2 all[kSmFew];                               // every CTA's
+    unsigned long long mass[kSmFew];                 // and their masses
+    uint16_t list[kSmList];                          // positions in the slice, ascending
+    uint32_t nfew[2];
     unsigned long long smass[kSmWarps];              // scan of the bins
     uint32_t scnt[kSmWarps];
-    uint32_t nlist[kSmWarps];
-    float wmax[kSmWarps];
-    int bad;
-    uint32_t over;
-    // the bin that holds the target
+    // where a target was found: bin (or -1), and what lies before and in it
     int bin;
     unsigned long long bmass_before, bmass_at;
     uint32_t bcnt_before, bcnt_at;
     int32_t nth;
+    SampleCutAt cut;
+    unsigned long long upto;
 };
 
 __device__ __forceinline__ uint32_t sm_peer(const void *p, uint32_t rank)
 {
     uint32_t d;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_addr(p)), "r"(rank));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_addr(p)), "r"(rank));
     return d;
 }
 __device__ __forceinline__ void sm_put(const void *p, uint32_t rank, uint32_t v)
@@ -107,15 +131,19 @@ __device__ __forceinline__ void sm_put(const void *p, uint32_t rank, unsigned lo
 __device__ __forceinline__ uint32_t sm_get(const void *p, uint32_t rank)
 {
     uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(sm_peer(p, rank)) : "memory");
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(sm_peer(p, rank)));
+    return v;
+}
+__device__ __forceinline__ uint2 sm_get2(const void *p, uint32_t rank)
+{
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(sm_peer(p, rank)));
     return v;
 }
 __device__ __forceinline__ void sm_cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-
-constexpr uint32_t kSmFull = 1u << 22; // a full list's count: above every row's
 
 constexpr float kSmShift = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number
 constexpr uint32_t kSmShiftBits = 0x4B400000u;
@@ -164,13 +192,6 @@ __device__ __forceinline__ void sm_init_table(SampleShared &S)
     }
 }
 
-// A cut: ids with a larger key, and of those with this key the ones up to `id`.
-struct SampleCut {
-    uint32_t key;
-    int32_t id;
-    __device__ __forceinline__ bool keeps(uint32_t k, int32_t i) const { return k > key || (k == key && i <= id); }
-};
-
 // This CTA's slice of a row.  Position p (16-byte vectors of PV positions) holds
 // id first + p; positions outside the slice read as -inf.
 template <typename LT> struct SampleSlice {
@@ -181,12 +202,24 @@ template <typename LT> struct SampleSlice {
     int32_t first;     // id of position 0 (may be below the slice's first)
     int32_t lo, hi;    // ids of the slice
     int32_t nv;        // vectors
+    // -0 as +0, the same logit: the sum with +0
+    __device__ __forceinline__ static uint4 plain(const uint4 &w)
+    {
+        uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if constexpr (PV == 8)
+                asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(u[k]) : "r"(0u));
+            else
+                u[k] = __float_as_uint(__uint_as_float(u[k]) + 0.0f);
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
     // vector v straight from memory
     __device__ __forceinline__ uint4 fetch(int32_t v) const
     {
         const int32_t i = first + v * PV;
         if (i >= lo && i + PV <= hi)
-            return ld_stream_v4(row + i);
+            return plain(ld_stream_v4(row + i));
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -199,20 +232,9 @@ template <typename LT> struct SampleSlice {
                 w[k] = i + k >= lo && i + k < hi ? filter_bits<LT>(row, i + k) : E::kNegInf;
             }
         }
-        return make_uint4(w[0], w[1], w[2], w[3]);
+        return plain(make_uint4(w[0], w[1], w[2], w[3]));
     }
     __device__ __forceinline__ uint4 vec(int32_t v) const { return mem ? mem[v] : fetch(v); }
-    __device__ __forceinline__ uint32_t bits(int32_t p) const
-    {
-        if (!mem) {
-            const int32_t i = first + p;
-            return i >= lo && i < hi ? filter_bits<LT>(row, i) : E::kNegInf;
-        }
-        if constexpr (PV == 8)
-            return reinterpret_cast<const unsigned short *>(mem)[p];
-        else
-            return reinterpret_cast<const uint32_t *>(mem)[p];
-    }
     __device__ __forceinline__ static uint32_t of(const uint4 &w, int j)
     {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -222,32 +244,6 @@ template <typename LT> struct SampleSlice {
             return u[j];
     }
 };
-
-// The listed ids of a warp's part, or (no list) all of it: f(in, id, bits) is
-// called by whole warps, in ascending order of ids over the lanes of a call.
-struct SampleList {
-    const uint16_t *pos; // this warp's entries, or nullptr
-    uint32_t n;
-};
-
-template <typename LT, typename F>
-__device__ __forceinline__ void sm_each(const SampleSlice<LT> &X, const SampleList &L, int32_t v0, int32_t v1, F &&f)
-{
-    constexpr int PV = SampleSlice<LT>::PV;
-    const int lane = threadIdx.x & 31;
-    if (L.pos) {
-        for (uint32_t i = 0; i < L.n; i += 32) {
-            const bool in = i + lane < L.n;
-            const int32_t p = in ? L.pos[i + lane] : 0;
-            f(in, X.first + p, in ? X.bits(p) : FilterElem<LT>::kNegInf);
-        }
-    } else {
-        for (int32_t p = v0 * PV; p < v1 * PV; p += 32) {
-            const bool in = p + lane < v1 * PV;
-            f(in, X.first + p + lane, in ? X.bits(p + lane) : FilterElem<LT>::kNegInf);
-        }
-    }
-}
 
 // Every CTA's sums (mass and cnt, the same in all threads of one) in every CTA:
 // the row of slots that got them.  The rows are used in turn: between two uses of
@@ -286,144 +282,416 @@ __device__ __forceinline__ void sm_block_sum(SampleShared &S, unsigned long long
     }
 }
 
-// The cut where the running count (MASS false) or mass of the members reaches
-// `target`, from the largest key down; members: listed ids with keys in
-// [klo, khi] that `bound` keeps.  upto gets the mass through the cut.
+// Every thread's bins in order: where the running count (MASS false) or mass
+// reaches `target`, in S.bin, S.b*; cnt and mass: this thread's N bins, the first
+// of which is N threadIdx.x.  Returns the sums of all bins.
+template <bool MASS, int N>
+__device__ __forceinline__ void sm_scan(SampleBins &S, const uint32_t (&cnt)[N], const unsigned long long (&mass)[N],
+                                        unsigned long long target, uint32_t &cnt_all, unsigned long long &mass_all)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t c = 0;
+    unsigned long long m = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        c += cnt[i];
+        m += mass[i];
+    }
+    const unsigned long long mi = static_cast<unsigned long long>(warp_incl_scan_ll(static_cast<long long>(m), lane));
+    uint32_t ci = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t n = __shfl_up_sync(0xFFFFFFFFu, ci, o);
+        ci += lane >= o ? n : 0u;
+    }
+    __syncthreads(); // what was found before has been read
+    if (lane == 31) {
+        S.smass[warp] = mi;
+        S.scnt[warp] = ci;
+    }
+    if (threadIdx.x == 0)
+        S.bin = -1;
+    __syncthreads();
+    unsigned long long mb = mi - m;
+    uint32_t cb = ci - c;
+    mass_all = 0;
+    cnt_all = 0;
+#pragma unroll
+    for (int w = 0; w < kSmWarps; ++w) {
+        const unsigned long long sm = S.smass[w];
+        const uint32_t sc = S.scnt[w];
+        mb += w < warp ? sm : 0ull;
+        cb += w < warp ? sc : 0u;
+        mass_all += sm;
+        cnt_all += sc;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const unsigned long long before = MASS ? mb : cb, here = MASS ? mass[i] : cnt[i];
+        if (before < target && target <= before + here) {
+            S.bin = static_cast<int>(threadIdx.x) * N + i;
+            S.bcnt_before = cb;
+            S.bcnt_at = cnt[i];
+            S.bmass_before = mb;
+            S.bmass_at = mass[i];
+        }
+        mb += mass[i];
+        cb += cnt[i];
+    }
+    __syncthreads();
+}
+
+// A cut as it is found: all ids of larger keys, and the first j of the `ties` ids
+// with this one (or, `known`, those up to an id).
+struct SampleFound {
+    bool any;                 // whether there is a cut: the target was reached
+    bool known;
+    uint32_t key;
+    int32_t id;
+    uint32_t j, ties;
+    uint32_t below;           // of the ties, how many in the CTAs before this one
+    uint32_t mine;            // and in this one
+    unsigned long long upto;  // mass through the cut (through everything, without one)
+};
+
+// Step 2's bin of a logit, from 0 for the maximum up; kSmFirst or more for what lies
+// below the bins.  It never grows with the logit (a difference and a product, each
+// rounded), so a bin is a range of keys.
+__device__ __forceinline__ uint32_t sm_bin(const SampleRow &R, float z, float scale)
+{
+    return __float_as_uint(__fmaf_rn(R.m - z, scale, 8388608.0f)) - 0x4B000000u;
+}
+// The least key of bin b or one before, by bisection.
+template <typename LT> __device__ __forceinline__ uint32_t sm_first_key(const SampleRow &R, float scale, uint32_t b, uint32_t ktop)
+{
+    using E = FilterElem<LT>;
+    uint32_t lo = E::kKeyMin, hi = ktop; // (the maximum's bin is 0)
+    while (lo < hi) {
+        const uint32_t mid = lo + ((hi - lo) >> 1);
+        if (sm_bin(R, E::value(E::bits_of_key(mid)), scale) <= b)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    return lo;
+}
+
+// The largest logit of a vector.
+template <typename LT> __device__ __forceinline__ float sm_largest(const uint4 &w)
+{
+    if constexpr (sizeof(LT) == 2) {
+        uint32_t a, b;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w.x), "r"(w.y));
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w.z), "r"(w.w));
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+        return fmaxf(bf16_lo(a), bf16_hi(a));
+    } else {
+        return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+    }
+}
+
+// The ids of bins 0 .. last of step 2 in this CTA: listed, or picked out of the slice.
+template <typename LT> struct SampleSet {
+    const SampleSlice<LT> &X;
+    const SampleRow &R;
+    float scale;
+    uint32_t last;
+    const uint16_t *list; // or nullptr
+    uint32_t n;
+    __device__ __forceinline__ uint32_t bits(uint32_t i) const
+    {
+        if constexpr (sizeof(LT) == 2)
+            return reinterpret_cast<const unsigned short *>(X.mem)[list[i]];
+        else
+            return reinterpret_cast<const uint32_t *>(X.mem)[list[i]];
+    }
+    __device__ __forceinline__ int32_t id(uint32_t i) const { return X.first + list[i]; }
+    // f(bits, id, bin) for each, in no order
+    template <typename F> __device__ __forceinline__ void each(F &&f) const
+    {
+        using E = FilterElem<LT>;
+        if (list) {
+            for (uint32_t i = threadIdx.x; i < n; i += kSmThreads) {
+                const uint32_t b = bits(i);
+                f(b, id(i), sm_bin(R, E::value(b), scale));
+            }
+        } else {
+            for (int32_t v = threadIdx.x; v < X.nv; v += kSmThreads) {
+                const uint4 w = X.vec(v);
+                if (sm_bin(R, sm_largest<LT>(w), scale) > last)
+                    continue;
+#pragma unroll 1
+                for (int j = 0; j < E::kPerVec; ++j) {
+                    const uint32_t b = SampleSlice<LT>::of(w, j), bin = sm_bin(R, E::value(b), scale);
+                    if (bin <= last)
+                        f(b, X.first + v * E::kPerVec + j, bin);
+                }
+            }
+        }
+    }
+};
+
+// Every CTA's gathered ids (`use`: 0 or 1), and their masses, in S.all, S.mass; how many.
+template <typename LT>
+__device__ __forceinline__ uint32_t sm_collect(const SampleRow &R, int use, uint32_t C, SampleBins &S)
+{
+    using E = FilterElem<LT>;
+    sm_cluster_sync();
+    uint32_t n = 0;
+    for (uint32_t r = 0; r < C; ++r) {
+        const uint32_t c = min(sm_get(&S.nfew[use], r), static_cast<uint32_t>(kSmFew));
+        const uint32_t i = threadIdx.x - n;
+        if (threadIdx.x >= n && i < c && threadIdx.x < kSmFew) {
+            const uint2 e = sm_get2(&S.few[use][i], r);
+            S.all[threadIdx.x] = e;
+            S.mass[threadIdx.x] = R.mass<sizeof(LT) == 4>(E::value(E::bits_of_key(e.x)));
+        }
+        n += c;
+    }
+    __syncthreads();
+    return min(n, static_cast<uint32_t>(kSmFew));
+}
+
+// Whether a ranks before b.
+__device__ __forceinline__ bool sm_before(uint2 a, uint2 b) { return a.x > b.x || (a.x == b.x && a.y < b.y); }
+
+// The ids of bin `bin` that `bound` keeps, at most kSmFew in all: gathered by every
+// CTA and ranked; the cut where the running count or mass reaches target.
 template <typename LT, bool MASS>
-__device__ SampleCut sm_select(const SampleSlice<LT> &X, const SampleList &L, int32_t v0, int32_t v1, const SampleRow &R,
-                               uint32_t klo, uint32_t khi, bool bounded, SampleCut bound, unsigned long long target,
-                               unsigned long long &upto, int piece, int &buf, uint32_t C, uint32_t rank, SampleShared &S)
+__device__ SampleFound sm_gather(const SampleSet<LT> &Set, uint32_t bin, unsigned long long above,
+                                 unsigned long long target, SampleCutAt bound, int use, uint32_t C, SampleBins &S)
+{
+    Set.each([&](uint32_t bits, int32_t id, uint32_t b) {
+        const uint32_t k = FilterElem<LT>::key(bits);
+        if (b != bin || k < bound.key || (k == bound.key && id > bound.id))
+            return;
+        const uint32_t at = atomicAdd(&S.nfew[use], 1u);
+        if (at < kSmFew) // (the bin's count bounds it)
+            S.few[use][at] = make_uint2(k, static_cast<uint32_t>(id));
+    });
+    const uint32_t n = sm_collect<LT>(Set.R, use, C, S);
+    if (threadIdx.x == 0)
+        S.bin = -1;
+    __syncthreads();
+    if (threadIdx.x < n) {
+        const uint2 me = S.all[threadIdx.x];
+        uint32_t before = 0;
+        unsigned long long mass = 0;
+        for (uint32_t i = 0; i < n; ++i)
+            if (sm_before(S.all[i], me)) {
+                ++before;
+                mass += S.mass[i];
+            }
+        const unsigned long long w = S.mass[threadIdx.x];
+        const unsigned long long b = MASS ? mass : before, here = MASS ? w : 1;
+        if (b < target && target <= b + here) {
+            S.bin = 0;
+            S.cut = {me.x, static_cast<int32_t>(me.y)};
+            S.upto = mass + w;
+        }
+    }
+    __syncthreads();
+    SampleFound f = {};
+    f.any = S.bin == 0; // the target lies in the bin: found
+    f.known = true;
+    f.key = S.cut.key;
+    f.id = S.cut.id;
+    f.upto = above + S.upto;
+    __syncthreads();
+    return f;
+}
+
+// The cut among the ids with keys in [klo, khi], digit by digit.
+template <typename LT, bool MASS>
+__device__ SampleFound sm_narrow(const SampleSlice<LT> &X, const SampleRow &R, uint32_t klo, uint32_t khi,
+                                 unsigned long long above, unsigned long long target, int piece, uint32_t C, uint32_t rank,
+                                 SampleBins &S)
 {
     using E = FilterElem<LT>;
     constexpr bool F32 = sizeof(LT) == 4;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     static_assert(kSmThreads == kSmBins, "a thread for each bin");
     const uint32_t low = (1u << piece) - 1u;
-    unsigned long long above = 0;
+    SampleFound f = {};
     for (;;) {
         const uint32_t span = khi - klo;
         const int sh = span < kSmBins ? 0 : 32 - __clz(span) - 9;
-        uint32_t(&H)[4][kSmBins] = S.hist[buf];
-        buf ^= 1;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            H[k][threadIdx.x] = 0u;
+            S.hist[k][threadIdx.x] = 0u;
         __syncthreads();
-        sm_each<LT>(X, L, v0, v1, [&](bool in, int32_t id, uint32_t bits) {
-            const uint32_t k = E::key(bits);
-            if (!in || !E::finite(bits) || k < klo || k > khi || (bounded && !bound.keeps(k, id)))
-                return;
-            const uint32_t b = (khi - k) >> sh;
-            const unsigned long long w = R.mass<F32>(E::value(bits));
-            atomicAdd(&H[0][b], 1u);
-            if (w) {
-                atomicAdd(&H[1][b], static_cast<uint32_t>(w) & low);
-                atomicAdd(&H[2][b], static_cast<uint32_t>(w >> piece) & low);
-                atomicAdd(&H[3][b], static_cast<uint32_t>(w >> (2 * piece)));
-            }
-        });
-        sm_cluster_sync();
-        // bin threadIdx.x over the cluster
-        uint32_t cnt = 0;
-        unsigned long long mass = 0;
-        for (uint32_t r = 0; r < C; ++r) {
-            cnt += sm_get(&H[0][threadIdx.x], r);
-            mass += sm_get(&H[1][threadIdx.x], r);
-            mass += static_cast<unsigned long long>(sm_get(&H[2][threadIdx.x], r)) << piece;
-            mass += static_cast<unsigned long long>(sm_get(&H[3][threadIdx.x], r)) << (2 * piece);
-        }
-        const unsigned long long mi = static_cast<unsigned long long>(warp_incl_scan_ll(static_cast<long long>(mass), lane));
-        uint32_t ci = cnt;
+        for (int32_t v = threadIdx.x; v < X.nv; v += kSmThreads) {
+            const uint4 w = X.vec(v);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t n = __shfl_up_sync(0xFFFFFFFFu, ci, o);
-            ci += lane >= o ? n : 0u;
+            for (int j = 0; j < E::kPerVec; ++j) {
+                const uint32_t bits = SampleSlice<LT>::of(w, j), k = E::key(bits);
+                if (k >= klo && k <= khi && E::finite(bits)) {
+                    const uint32_t b = (khi - k) >> sh;
+                    const unsigned long long e = R.mass<F32>(E::value(bits));
+                    atomicAdd(&S.hist[0][b], 1u);
+                    if (e) {
+                        atomicAdd(&S.hist[1][b], static_cast<uint32_t>(e) & low);
+                        atomicAdd(&S.hist[2][b], static_cast<uint32_t>(e >> piece) & low);
+                        atomicAdd(&S.hist[3][b], static_cast<uint32_t>(e >> (2 * piece)));
+                    }
+                }
+            }
         }
-        if (lane == 31) {
-            S.smass[warp] = mi;
-            S.scnt[warp] = ci;
+        sm_cluster_sync();
+        uint32_t cnt[1] = {0};
+        unsigned long long mass[1] = {0};
+        for (uint32_t r = 0; r < C; ++r) {
+            cnt[0] += sm_get(&S.hist[0][threadIdx.x], r);
+            mass[0] += sm_get(&S.hist[1][threadIdx.x], r);
+            mass[0] += static_cast<unsigned long long>(sm_get(&S.hist[2][threadIdx.x], r)) << piece;
+            mass[0] += static_cast<unsigned long long>(sm_get(&S.hist[3][threadIdx.x], r)) << (2 * piece);
         }
-        if (threadIdx.x == 0)
-            S.bin = -1;
-        __syncthreads();
-        unsigned long long mb = mi - mass;
-        uint32_t cb = ci - cnt;
-        for (int w = 0; w < warp; ++w) {
-            mb += S.smass[w];
-            cb += S.scnt[w];
+        uint32_t cnt_all;
+        unsigned long long mass_all;
+        sm_scan<MASS>(S, cnt, mass, target, cnt_all, mass_all);
+        const int bin = S.bin;
+        f.any = bin >= 0;
+        if (!f.any) {
+            f.upto = above + mass_all;
+            sm_cluster_sync();
+            return f;
         }
-        const unsigned long long before = MASS ? mb : cb, here = MASS ? mass : cnt;
-        if (before < target && target <= before + here) {
-            S.bin = threadIdx.x;
-            S.bcnt_before = cb;
-            S.bcnt_at = cnt;
-            S.bmass_before = mb;
-            S.bmass_at = mass;
-        }
-        __syncthreads();
-        const int bin = S.bin; // the target is at most the members' sum: found
-        if (bin < 0)
-            return {0u, 0x7FFFFFFF};
         above += S.bmass_before;
         target -= MASS ? S.bmass_before : S.bcnt_before;
         khi -= static_cast<uint32_t>(bin) << sh;
         const uint32_t width = (1u << sh) - 1u;
         klo = khi - klo > width ? khi - width : klo;
-        const uint32_t ties = S.bcnt_at;
-        if (sh > 0 && klo != khi) {
-            __syncthreads();
-            continue;
-        }
-        // one value: the j-th of its ids
-        const unsigned long long w = R.mass<F32>(E::value(E::bits_of_key(khi)));
-        unsigned long long j = target;
-        if (MASS)
-            j = w ? (target + w - 1) / w : 1;
-        j = j < 1 ? 1 : (j > ties ? ties : j);
-        upto = above + j * w;
-        SampleCut cut = {khi, 0x7FFFFFFF};
-        if (j < ties) { // the same in every CTA
-            uint32_t below = 0; // ids of this value in the CTAs before
+        f.ties = S.bcnt_at;
+        if (klo == khi) {
             for (uint32_t r = 0; r < rank; ++r)
-                below += sm_get(&H[0][bin], r);
-            const uint32_t mine = sm_get(&H[0][bin], rank);
-            if (j <= below) {
-                cut.id = -1;
-            } else if (j - below < mine) {
-                const uint32_t want = static_cast<uint32_t>(j) - below; // of this CTA's
-                uint32_t n = 0;
-                auto member = [&](bool in, int32_t id, uint32_t bits) {
-                    const uint32_t k = E::key(bits);
-                    return in && k == khi && E::finite(bits) && (!bounded || bound.keeps(k, id));
-                };
-                sm_each<LT>(X, L, v0, v1, [&](bool in, int32_t id, uint32_t bits) {
-                    n += __popc(__ballot_sync(0xFFFFFFFFu, member(in, id, bits)));
-                });
-                if (lane == 0)
-                    S.scnt[warp] = n;
-                __syncthreads();
-                uint32_t at = 0;
-                for (int w2 = 0; w2 < warp; ++w2)
-                    at += S.scnt[w2];
-                if (at < want && want <= at + n) {
-                    sm_each<LT>(X, L, v0, v1, [&](bool in, int32_t id, uint32_t bits) {
-                        const uint32_t b = __ballot_sync(0xFFFFFFFFu, member(in, id, bits));
-                        const uint32_t upto_lane = at + __popc(b & ((2u << lane) - 1u));
-                        if ((b >> lane & 1u) && upto_lane == want)
-                            S.nth = id;
-                        at += __popc(b);
-                    });
-                }
-                __syncthreads();
-                cut.id = S.nth;
+                f.below += sm_get(&S.hist[0][bin], r);
+            f.mine = sm_get(&S.hist[0][bin], rank);
+        }
+        sm_cluster_sync(); // every CTA has read the bins
+        if (klo == khi)
+            break;
+    }
+    f.key = khi;
+    const unsigned long long w = R.mass<F32>(E::value(E::bits_of_key(khi)));
+    unsigned long long j = MASS ? (w ? (target + w - 1) / w : 1) : target;
+    f.j = static_cast<uint32_t>(j < 1 ? 1 : (j > f.ties ? f.ties : j));
+    f.upto = above + f.j * w;
+    return f;
+}
+
+// A found cut as every CTA compares with it: (key, id).
+template <typename LT>
+__device__ SampleCutAt sm_settle(const SampleSlice<LT> &X, const SampleFound &f, int32_t v0, int32_t v1, SampleBins &S)
+{
+    using E = FilterElem<LT>;
+    constexpr int PV = E::kPerVec;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (!f.any)
+        return {0u, 0x7FFFFFFF}; // everything finite
+    if (f.known)
+        return {f.key, f.id};
+    if (f.j >= f.below + f.mine)
+        return {f.key, 0x7FFFFFFF};
+    if (f.j <= f.below)
+        return {f.key, -1};
+    // this CTA's want-th id of the value, in id order
+    const uint32_t want = f.j - f.below;
+    auto hits = [&](int32_t v) {
+        uint32_t h = 0;
+        if (v < v1) {
+            const uint4 w = X.vec(v);
+#pragma unroll
+            for (int j = 0; j < PV; ++j) {
+                const uint32_t bits = SampleSlice<LT>::of(w, j);
+                h |= E::finite(bits) && E::key(bits) == f.key ? 1u << j : 0u;
             }
         }
-        __syncthreads();
-        return cut;
+        return h;
+    };
+    uint32_t n = 0;
+    for (int32_t v = v0 + lane; v < v1; v += 32)
+        n += __popc(hits(v));
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    if (lane == 0)
+        S.scnt[warp] = n;
+    __syncthreads();
+    uint32_t at = 0;
+    for (int w = 0; w < warp; ++w)
+        at += S.scnt[w];
+    if (at < want && want <= at + n) {
+        for (int32_t v = v0; v < v1; v += 32) {
+            uint32_t h = hits(v + lane);
+            const uint32_t c = __popc(h);
+            uint32_t incl = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                incl += lane >= o ? up : 0u;
+            }
+            const uint32_t before = at + incl - c;
+            if (before < want && want <= before + c) {
+                for (uint32_t i = want - before; i > 1; --i)
+                    h &= h - 1;
+                S.nth = X.first + (v + lane) * PV + __ffs(h) - 1;
+            }
+            at += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        }
+    }
+    __syncthreads();
+    const int32_t id = S.nth;
+    __syncthreads();
+    return {f.key, id};
+}
+
+// The processed distribution over this CTA's ids, Z its mass in units of 2^-fix.
+template <typename LT, bool CUTS>
+__device__ __forceinline__ void sm_write_q(const SampleSlice<LT> &X, const SampleRow &R, const SampleParams &P, float *qrow,
+                                           float zlo, SampleCutAt cut, unsigned long long Z)
+{
+    using E = FilterElem<LT>;
+    constexpr int PV = E::kPerVec;
+    if (!qrow)
+        return;
+    float least = zlo;
+    if (CUTS && cut.key)
+        least = fmaxf(least, E::value(E::bits_of_key(cut.key)));
+    const float scale = ldexpf(1.0f, P.fix) / static_cast<float>(Z);
+    const float cq = P.cq;
+    const bool filtered = CUTS || P.min_p;
+    for (int32_t v = threadIdx.x; v < X.nv; v += kSmThreads) {
+        const uint4 w = X.vec(v);
+        const int32_t i = X.first + v * PV;
+        float q[PV];
+        if (!filtered) { // (exp2 of -inf is 0)
+#pragma unroll
+            for (int j = 0; j < PV; ++j)
+                q[j] = ex2(__fmul_rn(E::value(SampleSlice<LT>::of(w, j)) - R.m, cq)) * scale;
+        } else if (sm_largest<LT>(w) >= least) {
+#pragma unroll
+            for (int j = 0; j < PV; ++j) {
+                const uint32_t b = SampleSlice<LT>::of(w, j);
+                const bool in = E::finite(b) && E::value(b) >= least && (!CUTS || E::key(b) != cut.key || i + j <= cut.id);
+                q[j] = in ? ex2(__fmul_rn(E::value(b) - R.m, cq)) * scale : 0.0f;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < PV; ++j)
+                q[j] = 0.0f;
+        }
+        if (P.vec_q && i >= X.lo && i + PV <= X.hi) {
+#pragma unroll
+            for (int j = 0; j < PV; j += 4)
+                __stcs(reinterpret_cast<float4 *>(qrow + i + j), make_float4(q[j], q[j + 1], q[j + 2], q[j + 3]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < PV; ++j)
+                if (i + j >= X.lo && i + j < X.hi)
+                    qrow[i + j] = q[j];
+        }
     }
 }
 
-template <typename LT>
+// CUTS: whether there is a top-k or a top-p.
+template <typename LT, bool CUTS>
 __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParams P)
 {
     using E = FilterElem<LT>;
@@ -439,6 +707,13 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
     // a CTA's shared memory may be written to once it has arrived here
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     sm_init_table(S);
+    SampleBins &H = *reinterpret_cast<SampleBins *>(sm_raw + (P.staged ? static_cast<size_t>(P.slice) * sizeof(LT) : 0));
+    if constexpr (CUTS) {
+        for (int i = threadIdx.x; i < 4 * kSmFirst; i += kSmThreads)
+            H.first[0][i] = 0u;
+        if (threadIdx.x < 2)
+            H.nfew[threadIdx.x] = 0u;
+    }
     pdl_wait_primary();
     pdl_launch_dependents();
 
@@ -532,156 +807,326 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
     const int32_t part = (X.nv + kSmWarps - 1) / kSmWarps;
     const int32_t v0 = min(X.nv, warp * part), v1 = min(X.nv, v0 + part);
 
-    SampleList list = {nullptr, 0};
-    SampleCut cut = {0u, 0x7FFFFFFF}; // everything finite
-    unsigned long long total = 0;
-    int buf = 0, turn = 0;
-    // 2. the whole row's mass
-    auto row_sums = [&](unsigned long long &mass, uint32_t &cnt) {
-        mass = 0;
-        cnt = 0;
-        for (int32_t v = v0 + lane; v < v1; v += 32) {
-            const uint4 w = X.vec(v);
+    SampleCutAt cut = {0u, 0x7FFFFFFF}; // everything finite
+    int turn = 0;
+    const uint16_t *list = nullptr; // of the ids that may be kept, with a cut
+    uint32_t nlist = 0;
+    if constexpr (CUTS) {
+        // 2. counts in bins; the whole row's mass
+        const uint32_t ktop = E::key(F32 ? __float_as_uint(mx) : __float_as_uint(mx) >> 16);
+        const bool whole = !use_k; // what top-p refers to
+        unsigned long long total = 0;
+        auto pass = [&](auto with_mass) {
+            constexpr bool kMass = decltype(with_mass)::value;
+            for (int32_t v = v0 + lane; v < v1; v += 32) {
+                const uint4 w = X.vec(v);
 #pragma unroll
-            for (int j = 0; j < PV; ++j) {
-                const uint32_t b = Slice::of(w, j);
-                cnt += E::finite(b) ? 1u : 0u;
-                mass += R.mass<F32>(E::value(b));
+                for (int j = 0; j < PV; ++j) {
+                    const float z = E::value(Slice::of(w, j));
+                    if (kMass)
+                        total += R.mass<F32>(z);
+                    const uint32_t b = sm_bin(R, z, P.bins);
+                    if (b < kSmFirst)
+                        atomicAdd(&H.first[0][b], 1u);
+                }
             }
-        }
-        sm_block_sum(S, mass, cnt);
-        const int use = sm_exchange(S, turn, C, rank, mass, cnt);
-        mass = 0;
-        cnt = 0;
+        };
+        if (whole)
+            pass(std::true_type{});
+        else
+            pass(std::false_type{});
+        uint32_t none = 0;
+        sm_block_sum(S, total, none);
+        int use = sm_exchange(S, turn, C, rank, total, 0);
+        total = 0;
+        for (uint32_t k = 0; k < C; ++k)
+            total += S.cmass[use][k];
+        auto tau = [&](unsigned long long base) {
+            const double x = ceil(static_cast<double>(P.top_p) * static_cast<double>(base));
+            return static_cast<unsigned long long>(x < 1.0 ? 1.0 : x);
+        };
+        // this thread's two bins over the cluster
+        static_assert(kSmFirst == 2 * kSmThreads, "two bins a thread");
+        uint32_t cnt[2] = {}, cnt_all;
+        unsigned long long mass[2] = {}, mass_all;
         for (uint32_t k = 0; k < C; ++k) {
-            mass += S.cmass[use][k];
-            cnt += S.ccnt[use][k];
+            const uint2 c = sm_get2(&H.first[0][2 * threadIdx.x], k);
+            cnt[0] += c.x;
+            cnt[1] += c.y;
         }
-    };
-    uint32_t finite = 0;
-    if (use_p && !use_k)
-        row_sums(total, finite);
-    auto mass_target = [&](unsigned long long base) {
-        const double tau = ceil(static_cast<double>(P.top_p) * static_cast<double>(base));
-        return static_cast<unsigned long long>(tau < 1.0 ? 1.0 : tau);
-    };
-    const bool filtered = use_k || use_p || P.min_p;
-    if (filtered) {
-        // 3. the ids of a window
-        uint16_t *const mine = reinterpret_cast<uint16_t *>(sm_raw + (P.staged ? static_cast<size_t>(P.slice) * sizeof(LT) : 0)) +
-                               static_cast<size_t>(warp) * P.cap;
-        bool whole = P.cap == 0;
-        float win = P.window, zc = -INFINITY;
-        while (!whole) {
-            zc = use_k || use_p ? mx - win : zlo;
-            uint32_t n = 0;
-            for (int32_t v = v0; v < v1; v += 32) {
-                uint32_t hit = 0;
-                if (v + lane < v1) {
-                    const uint4 w = X.vec(v + lane);
+        // bins b0 .. b1 that the cut may lie in; `deep`: it lies below the bins
+        const unsigned long long ktarget = static_cast<unsigned long long>(P.top_k);
+        uint32_t b0 = 0, b1 = kSmFirst - 1, down_to_b1;
+        bool deep = false;
+        unsigned long long kleft = 0; // of top-k, in its bin
+        uint32_t kties = 0;
+        if (use_k) {
+            sm_scan<false>(H, cnt, mass, ktarget, cnt_all, mass_all);
+            deep = H.bin < 0;
+            if (!deep) {
+                b1 = static_cast<uint32_t>(H.bin);
+                kleft = ktarget - H.bcnt_before;
+                kties = H.bcnt_at;
+            }
+            down_to_b1 = deep ? cnt_all : H.bcnt_before + H.bcnt_at;
+        } else {
+            // the running mass through a bin lies between its count's at the bins' edges (a
+            // fiftieth of a bin further, for the roundings of a bin's number)
+            const unsigned long long target = tau(total);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                mass[i] = cnt[i] * R.mass<F32>(fminf(mx, mx - (2 * threadIdx.x + i - 0.52f) / P.bins));
+            sm_scan<true>(H, cnt, mass, target, cnt_all, mass_all);
+            b0 = H.bin >= 0 ? static_cast<uint32_t>(H.bin) : kSmFirst;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                mass[i] = cnt[i] * R.mass<F32>(mx - (2 * threadIdx.x + i + 0.52f) / P.bins);
+            sm_scan<true>(H, cnt, mass, target, cnt_all, mass_all);
+            deep = H.bin < 0;
+            if (!deep)
+                b1 = static_cast<uint32_t>(H.bin);
+            down_to_b1 = deep ? cnt_all : H.bcnt_before + H.bcnt_at;
+        }
+        SampleSet<LT> Set = {X, R, P.bins, b1, nullptr, 0};
+        if (!deep && down_to_b1 <= kSmFew) {
+            // 3. few ids: the row is settled at once, by every CTA
+            Set.each([&](uint32_t bits, int32_t id, uint32_t) {
+                const uint32_t at = atomicAdd(&H.nfew[0], 1u);
+                if (at < kSmFew) // (the count bounds it)
+                    H.few[0][at] = make_uint2(E::key(bits), static_cast<uint32_t>(id));
+            });
+            const uint32_t m = sm_collect<LT>(R, 0, C, H);
+            const uint2 me = threadIdx.x < m ? H.all[threadIdx.x] : make_uint2(0u, 0u);
+            uint32_t before = 0;
+            unsigned long long through = threadIdx.x < m ? H.mass[threadIdx.x] : 0ull;
+            if (threadIdx.x < m)
+                for (uint32_t i = 0; i < m; ++i)
+                    if (sm_before(H.all[i], me)) {
+                        ++before;
+                        through += H.mass[i];
+                    }
+            // the last of the top-k set, the last of top-p's, the last that min-p keeps
+            const bool in_k = threadIdx.x < m && (!use_k || before < static_cast<uint32_t>(P.top_k));
+            if (use_k && threadIdx.x < m && before + 1 == min(static_cast<uint32_t>(P.top_k), m))
+                H.upto = through;
+            __syncthreads();
+            const unsigned long long target = use_p ? tau(use_k ? H.upto : total) : ~0ull;
+            const unsigned long long own = threadIdx.x < m ? H.mass[threadIdx.x] : 0ull;
+            const bool in = in_k && (!use_p || through - own < target) && E::value(E::bits_of_key(me.x)) >= zlo;
+            if (threadIdx.x < m)
+                H.mass[threadIdx.x] = in ? own : 0ull;
+            if (threadIdx.x == 0) {
+                H.cut = {ktop, -1};
+                H.bin = -1;
+            }
+            const uint32_t kept = static_cast<uint32_t>(__syncthreads_count(in));
+            if (in && before + 1 == kept) // (the kept are the first of the order)
+                H.cut = {me.x, static_cast<int32_t>(me.y)};
+            unsigned long long Z = 0, upto = 0;
+            if (threadIdx.x < m)
+                for (uint32_t i = 0; i < m; ++i) {
+                    const unsigned long long w = H.mass[i];
+                    Z += w;
+                    upto += H.all[i].y <= me.y ? w : 0ull;
+                }
+            if (threadIdx.x == 0)
+                H.upto = Z;
+            __syncthreads();
+            Z = H.upto;
+            cut = H.cut;
+            if (rank == 0) {
+                const unsigned long long t = static_cast<unsigned long long>(mul_floor(u, static_cast<long long>(Z)));
+                if (threadIdx.x == 0 && P.kept)
+                    P.kept[r] = static_cast<int32_t>(kept);
+                if (in && !bad_u && t < upto && t >= upto - own) {
+                    P.tokens[r] = static_cast<int32_t>(me.y);
+                    if (P.prob)
+                        P.prob[r] = static_cast<float>(static_cast<double>(own) / static_cast<double>(Z));
+                }
+            }
+            sm_write_q<LT, true>(X, R, P, qrow, zlo, cut, Z);
+            sm_cluster_sync(); // no CTA leaves while another may read it
+            return;
+        }
+        // the list: counted, then written, in order
+        if (X.mem && P.slice <= 65536) {
+            auto hits = [&](int32_t v) {
+                uint32_t h = 0;
+                const uint4 w = X.vec(v);
+                if (sm_bin(R, sm_largest<LT>(w), P.bins) <= b1) {
 #pragma unroll
                     for (int j = 0; j < PV; ++j)
-                        hit |= E::value(Slice::of(w, j)) >= zc ? 1u << j : 0u;
+                        h |= sm_bin(R, E::value(Slice::of(w, j)), P.bins) <= b1 ? 1u << j : 0u;
                 }
-                if (__any_sync(0xFFFFFFFFu, hit)) {
-                    const uint32_t own = __popc(hit);
-                    uint32_t at = own;
+                return h;
+            };
+            uint32_t c = 0;
+            for (int32_t v = v0 + lane; v < v1; v += 32)
+                c += __popc(hits(v));
+            unsigned long long no = 0;
+            sm_block_sum(S, no, c);
+            if (c <= kSmList) {
+                uint32_t at = 0;
+                for (int w = 0; w < warp; ++w)
+                    at += S.wcnt[w];
+                for (int32_t v = v0; v < v1; v += 32) {
+                    const uint32_t h = v + lane < v1 ? hits(v + lane) : 0u;
+                    if (!__any_sync(0xFFFFFFFFu, h))
+                        continue;
+                    uint32_t incl = __popc(h);
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
-                        const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, at, o);
-                        at += lane >= o ? up : 0u;
+                        const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                        incl += lane >= o ? up : 0u;
                     }
-                    const uint32_t sum = __shfl_sync(0xFFFFFFFFu, at, 31);
-                    at += n - own;
-                    for (uint32_t h = hit; h; h &= h - 1) {
-                        if (at < static_cast<uint32_t>(P.cap))
-                            mine[at] = static_cast<uint16_t>((v + lane) * PV + __ffs(h) - 1);
-                        ++at;
-                    }
-                    n += sum;
+                    uint32_t to = at + incl - __popc(h);
+                    for (uint32_t g = h; g; g &= g - 1)
+                        H.list[to++] = static_cast<uint16_t>((v + lane) * PV + __ffs(g) - 1);
+                    at += __shfl_sync(0xFFFFFFFFu, incl, 31);
                 }
+                Set.list = H.list;
+                Set.n = c;
+                __syncthreads();
             }
-            __syncwarp();
-            const bool full = n > static_cast<uint32_t>(P.cap);
-            list.pos = mine;
-            list.n = n;
-            unsigned long long have = 0;
-            if (use_p && !use_k && !full)
-                sm_each<LT>(X, list, v0, v1, [&](bool in, int32_t, uint32_t bits) {
-                    have += in ? R.mass<F32>(E::value(bits)) : 0ull;
-                });
-            uint32_t count = lane == 0 ? (full ? kSmFull : n) : 0u; // (a cluster's 128 of them add up in 32 bits)
-            sm_block_sum(S, have, count);
-            const int use = sm_exchange(S, turn, C, rank, have, count);
-            have = 0;
-            count = 0;
+        }
+        // the cut of a target inside a bin of `ties` ids
+        auto resolve = [&](auto by_mass, uint32_t bin, uint32_t ties, unsigned long long above, unsigned long long left, int few) {
+            constexpr bool MASS = decltype(by_mass)::value;
+            if (ties <= kSmFew)
+                return sm_gather<LT, MASS>(Set, bin, above, left, cut, few, C, H);
+            const uint32_t klo = sm_first_key<LT>(R, P.bins, bin, ktop);
+            const uint32_t khi = bin ? sm_first_key<LT>(R, P.bins, bin - 1, ktop) - 1 : ktop;
+            return sm_narrow<LT, MASS>(X, R, klo, khi, above, left, P.piece, C, rank, H);
+        };
+        // ... or below the bins
+        auto resolve_below = [&](auto by_mass, unsigned long long above, unsigned long long left) {
+            constexpr bool MASS = decltype(by_mass)::value;
+            const uint32_t khi = sm_first_key<LT>(R, P.bins, kSmFirst - 1, ktop) - 1;
+            if (khi < E::kKeyMin) {
+                SampleFound f = {};
+                f.upto = above;
+                return f;
+            }
+            return sm_narrow<LT, MASS>(X, R, E::kKeyMin, khi, above, left, P.piece, C, rank, H);
+        };
+        SampleFound f = {};
+        if (use_k) {
+            f = deep ? resolve_below(std::false_type{}, 0, ktarget - cnt_all)
+                     : resolve(std::false_type{}, b1, kties, 0, kleft, 0);
+            cut = sm_settle<LT>(X, f, v0, v1, H);
+        }
+        if (use_p) {
+            // masses: above those bins in one sum, in them by bin
+            sm_cluster_sync(); // the counts have been read by every CTA
+            for (int i = threadIdx.x; i < 4 * kSmFirst; i += kSmThreads)
+                H.first[0][i] = 0u;
+            __syncthreads();
+            const uint32_t low = (1u << P.piece) - 1u;
+            unsigned long long above = 0;
+            Set.each([&](uint32_t bits, int32_t id, uint32_t b) {
+                const uint32_t key = E::key(bits);
+                if (key < cut.key || (key == cut.key && id > cut.id))
+                    return;
+                const unsigned long long e = R.mass<F32>(E::value(bits));
+                if (b < b0) {
+                    above += e;
+                } else {
+                    atomicAdd(&H.first[0][b], 1u);
+                    atomicAdd(&H.first[1][b], static_cast<uint32_t>(e) & low);
+                    atomicAdd(&H.first[2][b], static_cast<uint32_t>(e >> P.piece) & low);
+                    atomicAdd(&H.first[3][b], static_cast<uint32_t>(e >> (2 * P.piece)));
+                }
+            });
+            sm_block_sum(S, above, none);
+            use = sm_exchange(S, turn, C, rank, above, 0);
+            above = 0;
+            for (uint32_t k = 0; k < C; ++k)
+                above += S.cmass[use][k];
+            cnt[0] = cnt[1] = 0;
+            mass[0] = mass[1] = 0;
             for (uint32_t k = 0; k < C; ++k) {
-                have += S.cmass[use][k];
-                count += S.ccnt[use][k];
+                const uint2 c = sm_get2(&H.first[0][2 * threadIdx.x], k), m0 = sm_get2(&H.first[1][2 * threadIdx.x], k),
+                            m1 = sm_get2(&H.first[2][2 * threadIdx.x], k), m2 = sm_get2(&H.first[3][2 * threadIdx.x], k);
+                cnt[0] += c.x;
+                cnt[1] += c.y;
+                mass[0] += m0.x + (static_cast<unsigned long long>(m1.x) << P.piece) +
+                           (static_cast<unsigned long long>(m2.x) << (2 * P.piece));
+                mass[1] += m0.y + (static_cast<unsigned long long>(m1.y) << P.piece) +
+                           (static_cast<unsigned long long>(m2.y) << (2 * P.piece));
             }
-            whole = count >= kSmFull; // some list is full
-            if (whole || (use_k ? count >= static_cast<uint32_t>(P.top_k) : !use_p || have >= mass_target(total)))
-                break;
-            win *= 2.0f;
-            whole = !(win < -P.dmin); // (what has no mass may still count for top-k)
+            if (use_k) { // the top-k set's
+                sm_scan<true>(H, cnt, mass, 1, cnt_all, mass_all);
+                total = mass_all + (deep ? f.upto : 0);
+            }
+            const unsigned long long target = tau(total);
+            const unsigned long long left = target > above ? target - above : 1;
+            sm_scan<true>(H, cnt, mass, left, cnt_all, mass_all);
+            if (H.bin >= 0) {
+                const unsigned long long before = H.bmass_before;
+                const uint32_t bin = static_cast<uint32_t>(H.bin), ties = H.bcnt_at;
+                f = resolve(std::true_type{}, bin, ties, above + before, left - before, 1);
+            } else {
+                f = resolve_below(std::true_type{}, above + mass_all, left - mass_all);
+                deep = true;
+            }
+            cut = sm_settle<LT>(X, f, v0, v1, H);
         }
-        if (whole) {
-            list.pos = nullptr;
-            zc = -INFINITY;
-        }
-        // 4. the cuts
-        if (use_k || use_p) {
-            const uint32_t ktop = E::key(F32 ? __float_as_uint(mx) : __float_as_uint(mx) >> 16);
-            uint32_t klow = E::kKeyMin;
-            if (!whole) { // the key of zc, rounded down to the logits' type
-                uint32_t b = __float_as_uint(zc);
-                if (!F32)
-                    b = (b >> 31 ? b + 0xFFFFu : b) >> 16;
-                klow = max(E::key(b), E::kKeyMin);
-            }
-            bool have_cut = false;
-            if (use_k) {
-                bool cuts = true;
-                if (whole) {
-                    row_sums(total, finite);
-                    cuts = finite > static_cast<uint32_t>(P.top_k);
-                }
-                if (cuts) {
-                    cut = sm_select<LT, false>(X, list, v0, v1, R, klow, ktop, false, cut,
-                                               static_cast<unsigned long long>(P.top_k), total, P.piece, buf,
-                                               C, rank, S);
-                    have_cut = true;
-                }
-            }
-            if (use_p) { // of the top-k set's mass, or the row's
-                unsigned long long upto = 0;
-                cut = sm_select<LT, true>(X, list, v0, v1, R, klow, ktop, have_cut, cut, mass_target(total), upto,
-                                          P.piece, buf, C, rank, S);
-            }
-        }
+        list = Set.list;
+        nlist = Set.n;
+        if (deep) // (it may reach below what is listed)
+            list = nullptr;
     }
-    // 5. the kept masses
+    // 4. the kept masses.  An id is kept from `least` on (min-p, and below the cut's
+    // value nothing is); of a vector that has none nothing else is looked at.
+    const bool filtered = CUTS || P.min_p;
+    float least = zlo;
+    if (cut.key)
+        least = fmaxf(least, E::value(E::bits_of_key(cut.key)));
     auto keeps = [&](uint32_t bits, int32_t id) {
-        return E::finite(bits) && E::value(bits) >= zlo && cut.keeps(E::key(bits), id);
+        return E::finite(bits) && E::value(bits) >= least && (!CUTS || E::key(bits) != cut.key || id <= cut.id);
     };
-    unsigned long long a = 0;
-    uint32_t n = 0;
-    if (filtered) {
-        sm_each<LT>(X, list, v0, v1, [&](bool in, int32_t id, uint32_t bits) {
-            const bool k = in && keeps(bits, id);
-            n += k ? 1u : 0u;
-            a += k ? R.mass<F32>(E::value(bits)) : 0ull;
-        });
-    } else {
-        for (int32_t v = v0 + lane; v < v1; v += 32) {
-            const uint4 w = X.vec(v);
+    // the kept mass of vector v, and how many ids
+    auto vec_mass = [&](int32_t v, uint32_t &n) {
+        const uint4 w = X.vec(v);
+        unsigned long long a = 0;
+        if (!filtered) {
 #pragma unroll
             for (int j = 0; j < PV; ++j) {
                 const uint32_t b = Slice::of(w, j);
                 n += E::finite(b) ? 1u : 0u;
                 a += R.mass<F32>(E::value(b));
             }
+        } else if (sm_largest<LT>(w) >= least) {
+#pragma unroll 1
+            for (int j = 0; j < PV; ++j) {
+                const uint32_t b = Slice::of(w, j);
+                if (keeps(b, X.first + v * PV + j)) {
+                    ++n;
+                    a += R.mass<F32>(E::value(b));
+                }
+            }
         }
+        return a;
+    };
+    const SampleSet<LT> Kept = {X, R, 0.0f, 0u, list, nlist};
+    auto entry_mass = [&](uint32_t i, uint32_t &n) {
+        const uint32_t b = Kept.bits(i);
+        if (!keeps(b, Kept.id(i)))
+            return 0ull;
+        ++n;
+        return R.mass<F32>(E::value(b));
+    };
+    // a warp's part of the list
+    const uint32_t lpart = (nlist + kSmWarps - 1) / kSmWarps;
+    const uint32_t l0 = min(nlist, warp * lpart), l1 = min(nlist, l0 + lpart);
+    unsigned long long a = 0;
+    uint32_t n = 0;
+    if (list) {
+        for (uint32_t i = l0 + lane; i < l1; i += 32)
+            a += entry_mass(i, n);
+    } else {
+        for (int32_t v = v0 + lane; v < v1; v += 32)
+            a += vec_mass(v, n);
     }
     sm_block_sum(S, a, n);
     const int use = sm_exchange(S, turn, C, rank, a, n);
@@ -705,53 +1150,47 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
             at += S.wmass[w];
         }
         if (warp == w) {
-            bool done = false;
-            sm_each<LT>(X, list, v0, v1, [&](bool in, int32_t id, uint32_t bits) {
-                if (done)
-                    return;
-                const bool k = in && keeps(bits, id);
-                const unsigned long long e = k ? R.mass<F32>(E::value(bits)) : 0ull;
+            auto draw = [&](int32_t id, unsigned long long one) {
+                P.tokens[r] = id;
+                if (P.prob)
+                    P.prob[r] = static_cast<float>(static_cast<double>(one) / static_cast<double>(Z));
+            };
+            const int32_t i0 = list ? static_cast<int32_t>(l0) : v0, i1 = list ? static_cast<int32_t>(l1) : v1;
+            for (int32_t i = i0; i < i1; i += 32) {
+                uint32_t cnt = 0;
+                const unsigned long long e =
+                    i + lane < i1 ? (list ? entry_mass(i + lane, cnt) : vec_mass(i + lane, cnt)) : 0ull;
                 const unsigned long long run =
                     at + static_cast<unsigned long long>(warp_incl_scan_ll(static_cast<long long>(e), lane));
                 const uint32_t b = __ballot_sync(0xFFFFFFFFu, t < run);
                 if (b) {
                     if (lane == __ffs(b) - 1) {
-                        P.tokens[r] = id;
-                        if (P.prob)
-                            P.prob[r] = static_cast<float>(static_cast<double>(e) / static_cast<double>(Z));
+                        if (list) {
+                            draw(Kept.id(i + lane), e);
+                        } else { // inside this lane's vector
+                            unsigned long long to = run - e;
+                            const uint4 x = X.vec(i + lane);
+#pragma unroll 1
+                            for (int j = 0; j < PV; ++j) {
+                                const uint32_t bits = Slice::of(x, j);
+                                const int32_t id = X.first + (i + lane) * PV + j;
+                                const unsigned long long one = keeps(bits, id) ? R.mass<F32>(E::value(bits)) : 0ull;
+                                to += one;
+                                if (t < to) {
+                                    draw(id, one);
+                                    break;
+                                }
+                            }
+                        }
                     }
-                    done = true;
+                    break;
                 }
                 at = __shfl_sync(0xFFFFFFFFu, run, 31);
-            });
-        }
-    }
-    // 6. q
-    if (qrow) {
-        const float scale = ldexpf(1.0f, P.fix) / static_cast<float>(Z);
-        const float cq = P.cq;
-        auto q_of = [&](uint32_t bits, int32_t id) {
-            return keeps(bits, id) ? ex2(__fmul_rn(E::value(bits) - mx, cq)) * scale : 0.0f;
-        };
-        for (int32_t v = threadIdx.x; v < X.nv; v += kSmThreads) {
-            const uint4 w = X.vec(v);
-            const int32_t i = X.first + v * PV;
-            float q[PV];
-#pragma unroll
-            for (int j = 0; j < PV; ++j)
-                q[j] = q_of(Slice::of(w, j), i + j);
-            if (P.vec_q && i >= X.lo && i + PV <= X.hi) {
-#pragma unroll
-                for (int j = 0; j < PV; j += 4)
-                    __stcs(reinterpret_cast<float4 *>(qrow + i + j), make_float4(q[j], q[j + 1], q[j + 2], q[j + 3]));
-            } else {
-#pragma unroll
-                for (int j = 0; j < PV; ++j)
-                    if (i + j >= X.lo && i + j < X.hi)
-                        qrow[i + j] = q[j];
             }
         }
     }
+    // 5. q
+    sm_write_q<LT, CUTS>(X, R, P, qrow, zlo, cut, Z);
     sm_cluster_sync(); // no CTA leaves while another may read it
 }
 
