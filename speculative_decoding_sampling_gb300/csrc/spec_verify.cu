@@ -972,10 +972,10 @@ cudaError_t dequantize_fp4_launch(const sv::Fp4BackParams &P, bool vec, cudaStre
 
 // ------------------------------------------------------- the draw of tokens
 
-template <typename LT, bool CUTS>
-cudaError_t sample_launch(const sv::SampleParams &P, size_t smem, cudaStream_t stream)
+template <typename LT, int NT, bool CUTS>
+cudaError_t sample_launch_as(const sv::SampleParams &P, size_t smem, cudaStream_t stream)
 {
-    const auto kernel = sv::sample_kernel<LT, CUTS>;
+    const auto kernel = sv::sample_kernel<LT, NT, CUTS>;
     if (smem + sizeof(sv::SampleShared) > 48 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSampleSmem));
@@ -991,12 +991,20 @@ cudaError_t sample_launch(const sv::SampleParams &P, size_t smem, cudaStream_t s
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(P.rows * P.C));
-    cfg.blockDim = dim3(sv::kSmThreads);
+    cfg.blockDim = dim3(NT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, P);
+}
+
+template <typename LT>
+cudaError_t sample_launch(const sv::SampleParams &P, int threads, bool cuts, size_t smem, cudaStream_t s)
+{
+    if (threads == 256)
+        return cuts ? sample_launch_as<LT, 256, true>(P, smem, s) : sample_launch_as<LT, 256, false>(P, smem, s);
+    return cuts ? sample_launch_as<LT, 512, true>(P, smem, s) : sample_launch_as<LT, 512, false>(P, smem, s);
 }
 
 template <bool VEC> cudaError_t norm_launch(const sv::NormParams &P, int nseg, unsigned grid, cudaStream_t s)
@@ -1590,9 +1598,10 @@ sv_status_t sv_sample_logits(const void *logits, sv_dtype_t logits_dtype, const 
     P.c_lo = static_cast<float>(c - static_cast<double>(P.c_hi));
     P.cq = static_cast<float>(c / 32);
     P.dmin = static_cast<float>(-48 * 32 / c);
-    // 24 octaves of mass, and 16 of logits at least where top-k counts ids without mass
-    const double low = top_k > 0 ? 16.0 : 0.0, octaves = 24 * 32 / c;
-    P.bins = static_cast<float>(sv::kSmFirst / (octaves > low ? octaves : low));
+    // 24 octaves of mass, and 12 of logits at least where top-k counts ids without mass
+    const double low = top_k > 0 ? 12.0 : 0.0, octaves = 24 * 32 / c, range = octaves > low ? octaves : low;
+    P.bins = static_cast<float>(sv::kSmBins / range);
+    P.width = static_cast<float>(range / sv::kSmBins);
     // (a temperature so far from 1 that its factors leave the fp32 range)
     if (!std::isfinite(P.c_hi) || !std::isfinite(P.dmin) || !(P.cq > 0x1p-100f) || !(P.cq < 0x1p100f))
         return SV_EINVAL;
@@ -1636,18 +1645,16 @@ sv_status_t sv_sample_logits(const void *logits, sv_dtype_t logits_dtype, const 
         return static_cast<size_t>(P.slice) * static_cast<size_t>(es) + more;
     };
     int32_t C = 1;
-    while (C < sv::kSmMaxCtas && (cut(C) > 111 * 1024 || (rows * C * 2 <= 2 * kNominalSms && V / (2 * C) >= 2048)))
+    while (C < sv::kSmMaxCtas && (cut(C) > 55 * 1024 || (rows * C * 2 <= 2 * kNominalSms && V / (2 * C) >= 2048)))
         C *= 2;
     size_t smem = cut(C);
+    const int threads = rows * C > 2 * kNominalSms && smem <= 55 * 1024 ? 256 : 512;
     P.staged = smem <= kSampleSmem;
     if (!P.staged)
         smem = more;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (logits_dtype == SV_BF16)
-        e = cuts ? sample_launch<uint16_t, true>(P, smem, s) : sample_launch<uint16_t, false>(P, smem, s);
-    else
-        e = cuts ? sample_launch<float, true>(P, smem, s) : sample_launch<float, false>(P, smem, s);
+    const cudaError_t e = logits_dtype == SV_BF16 ? sample_launch<uint16_t>(P, threads, cuts, smem, s)
+                                                  : sample_launch<float>(P, threads, cuts, smem, s);
     return e == cudaSuccess ? SV_OK : SV_ECUDA;
 }
 

@@ -20,12 +20,12 @@
 // once from memory into shared memory (rows too long for eight stay in L2).  CTAs
 // exchange through distributed shared memory; a step ends with a cluster barrier.
 //  1. load, maximum;
-//  2. top-k, top-p: the ids are counted in 1024 bins from the maximum down (24
-//     octaves of mass, and 16 of logits at least for top-k); where top-p refers to
+//  2. top-k, top-p: the ids are counted in 512 bins from the maximum down (24
+//     octaves of mass, and 12 of logits at least for top-k); where top-p refers to
 //     the whole row its mass is formed in the same pass.  A scan finds top-k's bin;
-//     for top-p the counts and the bins' edges bound the running mass to 1.6 % and
+//     for top-p the counts and the bins' edges bound the running mass to 3.3 % and
 //     so the bins that its cut may lie in.  The ids down to the last of these bins
-//     are listed (up to 4096 a CTA; more are picked out of the slice each time), and
+//     are listed (up to 2048 a CTA; more are picked out of the slice each time), and
 //     nothing below them is looked at again;
 //  3. up to 256 listed ids are gathered by every CTA and ranked, which settles the
 //     row.  Of more, those of top-k's bin are; then masses are binned (four
@@ -43,9 +43,7 @@
 
 namespace sv {
 
-constexpr int kSmThreads = 512;
-constexpr int kSmWarps = kSmThreads / 32;
-constexpr int kSmBins = 512;
+constexpr int kSmMaxWarps = 16; // CTAs of 256 or 512 threads (NT)
 constexpr int kSmMaxCtas = 8;
 
 struct SampleParams {
@@ -56,7 +54,7 @@ struct SampleParams {
     float c_hi, c_lo;    // 32 log2(e) / T
     float cq;            // log2(e) / T
     float dmin;          // differences below this have no mass: -48 T ln 2
-    float bins;          // bins of step 2 per unit of the logits
+    float bins, width;   // bins of step 2 per unit of the logits, and a bin's width
     double min_off;      // T ln(min_p) (min_p > 0)
     int32_t top_k;       // <= 0: off
     float top_p;         // >= 1: off
@@ -75,8 +73,8 @@ struct SampleParams {
 };
 
 constexpr int kSmFew = 256;    // ids gathered and ranked
-constexpr int kSmFirst = 1024; // bins of step 2
-constexpr int kSmList = 4096;  // ids a CTA lists
+constexpr int kSmBins = 512;   // bins of steps 2 and 3
+constexpr int kSmList = 2048;  // ids a CTA lists
 
 // A cut: ids with a larger key, and of those with this key the ones up to `id`.
 struct SampleCutAt {
@@ -89,22 +87,22 @@ struct SampleShared {
     float cmax[kSmMaxCtas];
     unsigned long long cmass[4][kSmMaxCtas];         // exchanged sums, a row of slots for each use
     uint32_t ccnt[4][kSmMaxCtas];
-    unsigned long long wmass[kSmWarps];
-    uint32_t wcnt[kSmWarps];
-    float wmax[kSmWarps];
+    unsigned long long wmass[kSmMaxWarps];
+    uint32_t wcnt[kSmMaxWarps];
+    float wmax[kSmMaxWarps];
 };
 
 // What top-k and top-p need besides, behind the slice.
 struct SampleBins {
-    uint32_t first[4][kSmFirst];                     // step 2: counts, masses in three pieces
-    uint32_t hist[4][kSmBins];                       // step 3: the same
+    uint32_t first[4][kSmBins];                      // counts, masses in three pieces
     uint2 few[2][kSmFew];                            // this CTA's gathered (key, id): for top-k, for top-p
     uint2 all[kSmFew];                               // every CTA's
     unsigned long long mass[kSmFew];                 // and their masses
-    uint16_t list[kSmList];                          // positions in the slice, ascending
+    uint16_t list[kSmList];                          // positions in the slice, in no order
+    uint32_t nlist;
     uint32_t nfew[2];
-    unsigned long long smass[kSmWarps];              // scan of the bins
-    uint32_t scnt[kSmWarps];
+    unsigned long long smass[kSmMaxWarps];           // scan of the bins
+    uint32_t scnt[kSmMaxWarps];
     // where a target was found: bin (or -1), and what lies before and in it
     int bin;
     unsigned long long bmass_before, bmass_at;
@@ -139,6 +137,34 @@ __device__ __forceinline__ uint2 sm_get2(const void *p, uint32_t rank)
     uint2 v;
     asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(sm_peer(p, rank)));
     return v;
+}
+// A pair of words summed over the cluster's CTAs (every load is on its way before
+// the first is used).
+__device__ __forceinline__ uint2 sm_sum2(const void *p, uint32_t C)
+{
+    uint2 t[kSmMaxCtas], s = make_uint2(0u, 0u);
+#pragma unroll
+    for (uint32_t k = 0; k < kSmMaxCtas; ++k)
+        t[k] = k < C ? sm_get2(p, k) : make_uint2(0u, 0u);
+#pragma unroll
+    for (uint32_t k = 0; k < kSmMaxCtas; ++k) {
+        s.x += t[k].x;
+        s.y += t[k].y;
+    }
+    return s;
+}
+// Two words of a mass in pieces, summed as 64-bit numbers.
+__device__ __forceinline__ void sm_add2(unsigned long long (&m)[2], const void *p, uint32_t C, int shift)
+{
+    uint2 t[kSmMaxCtas];
+#pragma unroll
+    for (uint32_t k = 0; k < kSmMaxCtas; ++k)
+        t[k] = k < C ? sm_get2(p, k) : make_uint2(0u, 0u);
+#pragma unroll
+    for (uint32_t k = 0; k < kSmMaxCtas; ++k) {
+        m[0] += static_cast<unsigned long long>(t[k].x) << shift;
+        m[1] += static_cast<unsigned long long>(t[k].y) << shift;
+    }
 }
 __device__ __forceinline__ void sm_cluster_sync()
 {
@@ -262,7 +288,7 @@ __device__ __forceinline__ int sm_exchange(SampleShared &S, int &turn, uint32_t 
 
 // Every thread gets the CTA's sums of (mass, cnt); each warp's own are left in
 // S.wmass, S.wcnt.
-__device__ __forceinline__ void sm_block_sum(SampleShared &S, unsigned long long &mass, uint32_t &cnt)
+template <int NT> __device__ __forceinline__ void sm_block_sum(SampleShared &S, unsigned long long &mass, uint32_t &cnt)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     mass = static_cast<unsigned long long>(warp_sum_ll(static_cast<long long>(mass)));
@@ -276,16 +302,16 @@ __device__ __forceinline__ void sm_block_sum(SampleShared &S, unsigned long long
     mass = 0;
     cnt = 0;
 #pragma unroll
-    for (int w = 0; w < kSmWarps; ++w) {
+    for (int w = 0; w < NT / 32; ++w) {
         mass += S.wmass[w];
         cnt += S.wcnt[w];
     }
 }
 
-// Every thread's bins in order: where the running count (MASS false) or mass
-// reaches `target`, in S.bin, S.b*; cnt and mass: this thread's N bins, the first
-// of which is N threadIdx.x.  Returns the sums of all bins.
-template <bool MASS, int N>
+// This thread's bins (the first is N threadIdx.x) in order: the bin where the
+// running count (MASS false; masses are then not looked at) or mass reaches
+// `target`, in S.bin, S.b*.  Also the sums of all bins.
+template <bool MASS, int NT, int N>
 __device__ __forceinline__ void sm_scan(SampleBins &S, const uint32_t (&cnt)[N], const unsigned long long (&mass)[N],
                                         unsigned long long target, uint32_t &cnt_all, unsigned long long &mass_all)
 {
@@ -295,14 +321,18 @@ __device__ __forceinline__ void sm_scan(SampleBins &S, const uint32_t (&cnt)[N],
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         c += cnt[i];
-        m += mass[i];
+        m += MASS ? mass[i] : 0ull;
     }
-    const unsigned long long mi = static_cast<unsigned long long>(warp_incl_scan_ll(static_cast<long long>(m), lane));
+    unsigned long long mi = m;
     uint32_t ci = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const uint32_t n = __shfl_up_sync(0xFFFFFFFFu, ci, o);
         ci += lane >= o ? n : 0u;
+        if (MASS) {
+            const unsigned long long k = __shfl_up_sync(0xFFFFFFFFu, mi, o);
+            mi += lane >= o ? k : 0ull;
+        }
     }
     __syncthreads(); // what was found before has been read
     if (lane == 31) {
@@ -317,13 +347,15 @@ __device__ __forceinline__ void sm_scan(SampleBins &S, const uint32_t (&cnt)[N],
     mass_all = 0;
     cnt_all = 0;
 #pragma unroll
-    for (int w = 0; w < kSmWarps; ++w) {
-        const unsigned long long sm = S.smass[w];
+    for (int w = 0; w < NT / 32; ++w) {
         const uint32_t sc = S.scnt[w];
-        mb += w < warp ? sm : 0ull;
         cb += w < warp ? sc : 0u;
-        mass_all += sm;
         cnt_all += sc;
+        if (MASS) {
+            const unsigned long long sm = S.smass[w];
+            mb += w < warp ? sm : 0ull;
+            mass_all += sm;
+        }
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -333,11 +365,82 @@ __device__ __forceinline__ void sm_scan(SampleBins &S, const uint32_t (&cnt)[N],
             S.bcnt_before = cb;
             S.bcnt_at = cnt[i];
             S.bmass_before = mb;
-            S.bmass_at = mass[i];
         }
-        mb += mass[i];
+        mb += MASS ? mass[i] : 0ull;
         cb += cnt[i];
     }
+    __syncthreads();
+}
+
+// This thread's bins of S.first over the cluster.
+template <int N> __device__ __forceinline__ void sm_counts(const SampleBins &S, uint32_t C, uint32_t (&cnt)[N])
+{
+    if constexpr (N == 2) {
+        const uint2 c = sm_sum2(&S.first[0][2 * threadIdx.x], C);
+        cnt[0] = c.x;
+        cnt[1] = c.y;
+    } else {
+        uint32_t t[kSmMaxCtas];
+#pragma unroll
+        for (uint32_t k = 0; k < kSmMaxCtas; ++k)
+            t[k] = k < C ? sm_get(&S.first[0][threadIdx.x], k) : 0u;
+        cnt[0] = 0;
+#pragma unroll
+        for (uint32_t k = 0; k < kSmMaxCtas; ++k)
+            cnt[0] += t[k];
+    }
+}
+template <int N>
+__device__ __forceinline__ void sm_masses(const SampleBins &S, uint32_t C, int piece, unsigned long long (&mass)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        mass[i] = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        if constexpr (N == 2) {
+            sm_add2(mass, &S.first[1 + i][2 * threadIdx.x], C, i * piece);
+        } else {
+            uint32_t t[kSmMaxCtas];
+#pragma unroll
+            for (uint32_t k = 0; k < kSmMaxCtas; ++k)
+                t[k] = k < C ? sm_get(&S.first[1 + i][threadIdx.x], k) : 0u;
+#pragma unroll
+            for (uint32_t k = 0; k < kSmMaxCtas; ++k)
+                mass[0] += static_cast<unsigned long long>(t[k]) << (i * piece);
+        }
+    }
+}
+
+// The same of this CTA alone.
+template <int N> __device__ __forceinline__ void sm_counts_here(const SampleBins &S, uint32_t (&cnt)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        cnt[i] = S.first[0][N * threadIdx.x + i];
+}
+template <int N>
+__device__ __forceinline__ void sm_masses_here(const SampleBins &S, int piece, unsigned long long (&mass)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        mass[i] = S.first[1][N * threadIdx.x + i] + (static_cast<unsigned long long>(S.first[2][N * threadIdx.x + i]) << piece) +
+                  (static_cast<unsigned long long>(S.first[3][N * threadIdx.x + i]) << (2 * piece));
+}
+
+// An id's mass into bin b.
+__device__ __forceinline__ void sm_add_mass(SampleBins &S, uint32_t b, unsigned long long e, int piece)
+{
+    const uint32_t low = (1u << piece) - 1u;
+    atomicAdd(&S.first[0][b], 1u);
+    atomicAdd(&S.first[1][b], static_cast<uint32_t>(e) & low);
+    atomicAdd(&S.first[2][b], static_cast<uint32_t>(e >> piece) & low);
+    atomicAdd(&S.first[3][b], static_cast<uint32_t>(e >> (2 * piece)));
+}
+template <int NT> __device__ __forceinline__ void sm_clear(SampleBins &S)
+{
+    for (int i = threadIdx.x; i < 4 * kSmBins; i += NT)
+        S.first[0][i] = 0u;
     __syncthreads();
 }
 
@@ -354,7 +457,7 @@ struct SampleFound {
     unsigned long long upto;  // mass through the cut (through everything, without one)
 };
 
-// Step 2's bin of a logit, from 0 for the maximum up; kSmFirst or more for what lies
+// Step 2's bin of a logit, from 0 for the maximum up; kSmBins or more for what lies
 // below the bins.  It never grows with the logit (a difference and a product, each
 // rounded), so a bin is a range of keys.
 __device__ __forceinline__ uint32_t sm_bin(const SampleRow &R, float z, float scale)
@@ -391,7 +494,7 @@ template <typename LT> __device__ __forceinline__ float sm_largest(const uint4 &
 }
 
 // The ids of bins 0 .. last of step 2 in this CTA: listed, or picked out of the slice.
-template <typename LT> struct SampleSet {
+template <typename LT, int NT> struct SampleSet {
     const SampleSlice<LT> &X;
     const SampleRow &R;
     float scale;
@@ -411,12 +514,12 @@ template <typename LT> struct SampleSet {
     {
         using E = FilterElem<LT>;
         if (list) {
-            for (uint32_t i = threadIdx.x; i < n; i += kSmThreads) {
+            for (uint32_t i = threadIdx.x; i < n; i += NT) {
                 const uint32_t b = bits(i);
                 f(b, id(i), sm_bin(R, E::value(b), scale));
             }
         } else {
-            for (int32_t v = threadIdx.x; v < X.nv; v += kSmThreads) {
+            for (int32_t v = threadIdx.x; v < X.nv; v += NT) {
                 const uint4 w = X.vec(v);
                 if (sm_bin(R, sm_largest<LT>(w), scale) > last)
                     continue;
@@ -437,28 +540,48 @@ __device__ __forceinline__ uint32_t sm_collect(const SampleRow &R, int use, uint
 {
     using E = FilterElem<LT>;
     sm_cluster_sync();
-    uint32_t n = 0;
-    for (uint32_t r = 0; r < C; ++r) {
-        const uint32_t c = min(sm_get(&S.nfew[use], r), static_cast<uint32_t>(kSmFew));
-        const uint32_t i = threadIdx.x - n;
-        if (threadIdx.x >= n && i < c && threadIdx.x < kSmFew) {
-            const uint2 e = sm_get2(&S.few[use][i], r);
-            S.all[threadIdx.x] = e;
-            S.mass[threadIdx.x] = R.mass<sizeof(LT) == 4>(E::value(E::bits_of_key(e.x)));
-        }
-        n += c;
+    // how many each CTA has, a lane each; then every thread its entry
+    const uint32_t lane = threadIdx.x & 31u;
+    const uint32_t c = lane < C ? min(sm_get(&S.nfew[use], lane), static_cast<uint32_t>(kSmFew)) : 0u;
+    uint32_t i = threadIdx.x, from = C, n = 0;
+#pragma unroll
+    for (uint32_t r = 0; r < kSmMaxCtas; ++r) {
+        const uint32_t cr = __shfl_sync(0xFFFFFFFFu, c, r);
+        if (from == C && i < cr)
+            from = r;
+        if (from == C)
+            i -= cr;
+        n += cr;
+    }
+    n = min(n, static_cast<uint32_t>(kSmFew));
+    if (threadIdx.x < n) {
+        const uint2 e = sm_get2(&S.few[use][i], from);
+        S.all[threadIdx.x] = e;
+        S.mass[threadIdx.x] = R.mass<sizeof(LT) == 4>(E::value(E::bits_of_key(e.x)));
     }
     __syncthreads();
-    return min(n, static_cast<uint32_t>(kSmFew));
+    return n;
 }
 
-// Whether a ranks before b.
-__device__ __forceinline__ bool sm_before(uint2 a, uint2 b) { return a.x > b.x || (a.x == b.x && a.y < b.y); }
+// How many of the n collected ids rank before `me`, and their mass.
+__device__ __forceinline__ void sm_rank(const SampleBins &S, uint32_t n, uint2 me, uint32_t &before, unsigned long long &mass)
+{
+    before = 0;
+    mass = 0;
+#pragma unroll 4
+    for (uint32_t i = 0; i < n; ++i) {
+        const uint2 o = S.all[i];
+        const bool b = o.x > me.x | (o.x == me.x & o.y < me.y);
+        const unsigned long long w = S.mass[i];
+        before += b ? 1u : 0u;
+        mass += b ? w : 0ull;
+    }
+}
 
 // The ids of bin `bin` that `bound` keeps, at most kSmFew in all: gathered by every
 // CTA and ranked; the cut where the running count or mass reaches target.
-template <typename LT, bool MASS>
-__device__ SampleFound sm_gather(const SampleSet<LT> &Set, uint32_t bin, unsigned long long above,
+template <typename LT, int NT, bool MASS>
+__device__ SampleFound sm_gather(const SampleSet<LT, NT> &Set, uint32_t bin, unsigned long long above,
                                  unsigned long long target, SampleCutAt bound, int use, uint32_t C, SampleBins &S)
 {
     Set.each([&](uint32_t bits, int32_t id, uint32_t b) {
@@ -475,13 +598,9 @@ __device__ SampleFound sm_gather(const SampleSet<LT> &Set, uint32_t bin, unsigne
     __syncthreads();
     if (threadIdx.x < n) {
         const uint2 me = S.all[threadIdx.x];
-        uint32_t before = 0;
-        unsigned long long mass = 0;
-        for (uint32_t i = 0; i < n; ++i)
-            if (sm_before(S.all[i], me)) {
-                ++before;
-                mass += S.mass[i];
-            }
+        uint32_t before;
+        unsigned long long mass;
+        sm_rank(S, n, me, before, mass);
         const unsigned long long w = S.mass[threadIdx.x];
         const unsigned long long b = MASS ? mass : before, here = MASS ? w : 1;
         if (b < target && target <= b + here) {
@@ -502,60 +621,59 @@ __device__ SampleFound sm_gather(const SampleSet<LT> &Set, uint32_t bin, unsigne
 }
 
 // The cut among the ids with keys in [klo, khi], digit by digit.
-template <typename LT, bool MASS>
+template <typename LT, int NT, bool MASS>
 __device__ SampleFound sm_narrow(const SampleSlice<LT> &X, const SampleRow &R, uint32_t klo, uint32_t khi,
                                  unsigned long long above, unsigned long long target, int piece, uint32_t C, uint32_t rank,
                                  SampleBins &S)
 {
     using E = FilterElem<LT>;
     constexpr bool F32 = sizeof(LT) == 4;
-    static_assert(kSmThreads == kSmBins, "a thread for each bin");
-    const uint32_t low = (1u << piece) - 1u;
+    constexpr int N = kSmBins / NT;
     SampleFound f = {};
     for (;;) {
         const uint32_t span = khi - klo;
         const int sh = span < kSmBins ? 0 : 32 - __clz(span) - 9;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            S.hist[k][threadIdx.x] = 0u;
-        __syncthreads();
-        for (int32_t v = threadIdx.x; v < X.nv; v += kSmThreads) {
+        sm_cluster_sync(); // every CTA has read the bins
+        sm_clear<NT>(S);
+        for (int32_t v = threadIdx.x; v < X.nv; v += NT) {
             const uint4 w = X.vec(v);
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < E::kPerVec; ++j) {
                 const uint32_t bits = SampleSlice<LT>::of(w, j), k = E::key(bits);
-                if (k >= klo && k <= khi && E::finite(bits)) {
-                    const uint32_t b = (khi - k) >> sh;
-                    const unsigned long long e = R.mass<F32>(E::value(bits));
-                    atomicAdd(&S.hist[0][b], 1u);
-                    if (e) {
-                        atomicAdd(&S.hist[1][b], static_cast<uint32_t>(e) & low);
-                        atomicAdd(&S.hist[2][b], static_cast<uint32_t>(e >> piece) & low);
-                        atomicAdd(&S.hist[3][b], static_cast<uint32_t>(e >> (2 * piece)));
-                    }
-                }
+                if (k >= klo && k <= khi && E::finite(bits))
+                    sm_add_mass(S, (khi - k) >> sh, R.mass<F32>(E::value(bits)), piece);
             }
         }
         sm_cluster_sync();
-        uint32_t cnt[1] = {0};
-        unsigned long long mass[1] = {0};
-        for (uint32_t r = 0; r < C; ++r) {
-            cnt[0] += sm_get(&S.hist[0][threadIdx.x], r);
-            mass[0] += sm_get(&S.hist[1][threadIdx.x], r);
-            mass[0] += static_cast<unsigned long long>(sm_get(&S.hist[2][threadIdx.x], r)) << piece;
-            mass[0] += static_cast<unsigned long long>(sm_get(&S.hist[3][threadIdx.x], r)) << (2 * piece);
+        uint32_t cnt[N], cnt_all;
+        unsigned long long mass[N], mass_all;
+        sm_counts(S, C, cnt);
+        sm_masses(S, C, piece, mass);
+        unsigned long long before = 0;
+        if (MASS) {
+            sm_scan<true, NT>(S, cnt, mass, target, cnt_all, mass_all);
+        } else { // and the mass before the bin
+            sm_scan<false, NT>(S, cnt, mass, target, cnt_all, mass_all);
+            const int bin = S.bin;
+            unsigned long long own = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                own += static_cast<int>(threadIdx.x) * N + i < bin || bin < 0 ? mass[i] : 0ull;
+            own = static_cast<unsigned long long>(warp_sum_ll(static_cast<long long>(own)));
+            if ((threadIdx.x & 31) == 0)
+                S.smass[threadIdx.x >> 5] = own;
+            __syncthreads();
+            for (int w = 0; w < NT / 32; ++w)
+                before += S.smass[w];
+            mass_all = before;
         }
-        uint32_t cnt_all;
-        unsigned long long mass_all;
-        sm_scan<MASS>(S, cnt, mass, target, cnt_all, mass_all);
         const int bin = S.bin;
         f.any = bin >= 0;
         if (!f.any) {
             f.upto = above + mass_all;
-            sm_cluster_sync();
             return f;
         }
-        above += S.bmass_before;
+        above += MASS ? S.bmass_before : before;
         target -= MASS ? S.bmass_before : S.bcnt_before;
         khi -= static_cast<uint32_t>(bin) << sh;
         const uint32_t width = (1u << sh) - 1u;
@@ -563,12 +681,10 @@ __device__ SampleFound sm_narrow(const SampleSlice<LT> &X, const SampleRow &R, u
         f.ties = S.bcnt_at;
         if (klo == khi) {
             for (uint32_t r = 0; r < rank; ++r)
-                f.below += sm_get(&S.hist[0][bin], r);
-            f.mine = sm_get(&S.hist[0][bin], rank);
-        }
-        sm_cluster_sync(); // every CTA has read the bins
-        if (klo == khi)
+                f.below += sm_get(&S.first[0][bin], r);
+            f.mine = sm_get(&S.first[0][bin], rank);
             break;
+        }
     }
     f.key = khi;
     const unsigned long long w = R.mass<F32>(E::value(E::bits_of_key(khi)));
@@ -643,7 +759,7 @@ __device__ SampleCutAt sm_settle(const SampleSlice<LT> &X, const SampleFound &f,
 }
 
 // The processed distribution over this CTA's ids, Z its mass in units of 2^-fix.
-template <typename LT, bool CUTS>
+template <typename LT, int NT, bool CUTS>
 __device__ __forceinline__ void sm_write_q(const SampleSlice<LT> &X, const SampleRow &R, const SampleParams &P, float *qrow,
                                            float zlo, SampleCutAt cut, unsigned long long Z)
 {
@@ -657,7 +773,7 @@ __device__ __forceinline__ void sm_write_q(const SampleSlice<LT> &X, const Sampl
     const float scale = ldexpf(1.0f, P.fix) / static_cast<float>(Z);
     const float cq = P.cq;
     const bool filtered = CUTS || P.min_p;
-    for (int32_t v = threadIdx.x; v < X.nv; v += kSmThreads) {
+    for (int32_t v = threadIdx.x; v < X.nv; v += NT) {
         const uint4 w = X.vec(v);
         const int32_t i = X.first + v * PV;
         float q[PV];
@@ -691,8 +807,8 @@ __device__ __forceinline__ void sm_write_q(const SampleSlice<LT> &X, const Sampl
 }
 
 // CUTS: whether there is a top-k or a top-p.
-template <typename LT, bool CUTS>
-__global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParams P)
+template <typename LT, int NT, bool CUTS>
+__global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleParams P)
 {
     using E = FilterElem<LT>;
     using Slice = SampleSlice<LT>;
@@ -709,10 +825,12 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
     sm_init_table(S);
     SampleBins &H = *reinterpret_cast<SampleBins *>(sm_raw + (P.staged ? static_cast<size_t>(P.slice) * sizeof(LT) : 0));
     if constexpr (CUTS) {
-        for (int i = threadIdx.x; i < 4 * kSmFirst; i += kSmThreads)
+        for (int i = threadIdx.x; i < 4 * kSmBins; i += NT)
             H.first[0][i] = 0u;
         if (threadIdx.x < 2)
             H.nfew[threadIdx.x] = 0u;
+        if (threadIdx.x == 0)
+            H.nlist = 0u;
     }
     pdl_wait_primary();
     pdl_launch_dependents();
@@ -747,18 +865,18 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
             }
         };
         constexpr int U = 8;
-        for (int32_t v = threadIdx.x; v < X.nv; v += U * kSmThreads) {
+        for (int32_t v = threadIdx.x; v < X.nv; v += U * NT) {
             uint4 w[U];
 #pragma unroll
             for (int t = 0; t < U; ++t)
-                if (v + t * kSmThreads < X.nv)
-                    w[t] = X.fetch(v + t * kSmThreads);
+                if (v + t * NT < X.nv)
+                    w[t] = X.fetch(v + t * NT);
 #pragma unroll
             for (int t = 0; t < U; ++t)
-                if (v + t * kSmThreads < X.nv) {
+                if (v + t * NT < X.nv) {
                     fold(w[t]);
                     if (P.staged)
-                        stage[v + t * kSmThreads] = w[t];
+                        stage[v + t * NT] = w[t];
                 }
         }
 #pragma unroll
@@ -769,7 +887,7 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
         __syncthreads();
         mx = S.wmax[0];
 #pragma unroll
-        for (int w = 1; w < kSmWarps; ++w)
+        for (int w = 1; w < NT / 32; ++w)
             asm("max.NaN.f32 %0, %1, %2;" : "=f"(mx) : "f"(mx), "f"(S.wmax[w]));
         asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
         if (threadIdx.x < C)
@@ -794,7 +912,7 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
     }
     if (bad_row) { // the same in every CTA
         if (qrow)
-            for (int32_t i = X.lo + threadIdx.x; i < X.hi; i += kSmThreads)
+            for (int32_t i = X.lo + threadIdx.x; i < X.hi; i += NT)
                 qrow[i] = 0.0f;
         sm_cluster_sync(); // no CTA leaves while another may write to it
         return;
@@ -804,7 +922,7 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
     const float zlo = P.min_p ? __double2float_ru(static_cast<double>(mx) + P.min_off) : -INFINITY;
     const bool use_k = P.top_k > 0 && P.top_k < P.V, use_p = P.top_p < 1.0f;
     // a warp's part of the slice
-    const int32_t part = (X.nv + kSmWarps - 1) / kSmWarps;
+    const int32_t part = (X.nv + NT / 32 - 1) / (NT / 32);
     const int32_t v0 = min(X.nv, warp * part), v1 = min(X.nv, v0 + part);
 
     SampleCutAt cut = {0u, 0x7FFFFFFF}; // everything finite
@@ -826,7 +944,7 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
                     if (kMass)
                         total += R.mass<F32>(z);
                     const uint32_t b = sm_bin(R, z, P.bins);
-                    if (b < kSmFirst)
+                    if (b < kSmBins)
                         atomicAdd(&H.first[0][b], 1u);
                 }
             }
@@ -836,7 +954,7 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
         else
             pass(std::false_type{});
         uint32_t none = 0;
-        sm_block_sum(S, total, none);
+        sm_block_sum<NT>(S, total, none);
         int use = sm_exchange(S, turn, C, rank, total, 0);
         total = 0;
         for (uint32_t k = 0; k < C; ++k)
@@ -845,23 +963,19 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
             const double x = ceil(static_cast<double>(P.top_p) * static_cast<double>(base));
             return static_cast<unsigned long long>(x < 1.0 ? 1.0 : x);
         };
-        // this thread's two bins over the cluster
-        static_assert(kSmFirst == 2 * kSmThreads, "two bins a thread");
-        uint32_t cnt[2] = {}, cnt_all;
-        unsigned long long mass[2] = {}, mass_all;
-        for (uint32_t k = 0; k < C; ++k) {
-            const uint2 c = sm_get2(&H.first[0][2 * threadIdx.x], k);
-            cnt[0] += c.x;
-            cnt[1] += c.y;
-        }
+        // this thread's bins over the cluster
+        constexpr int N = kSmBins / NT;
+        uint32_t cnt[N], cnt_all;
+        unsigned long long mass[N], mass_all;
+        sm_counts(H, C, cnt);
         // bins b0 .. b1 that the cut may lie in; `deep`: it lies below the bins
         const unsigned long long ktarget = static_cast<unsigned long long>(P.top_k);
-        uint32_t b0 = 0, b1 = kSmFirst - 1, down_to_b1;
+        uint32_t b0 = 0, b1 = kSmBins - 1, down_to_b1;
         bool deep = false;
         unsigned long long kleft = 0; // of top-k, in its bin
         uint32_t kties = 0;
         if (use_k) {
-            sm_scan<false>(H, cnt, mass, ktarget, cnt_all, mass_all);
+            sm_scan<false, NT>(H, cnt, mass, ktarget, cnt_all, mass_all);
             deep = H.bin < 0;
             if (!deep) {
                 b1 = static_cast<uint32_t>(H.bin);
@@ -874,20 +988,20 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
             // fiftieth of a bin further, for the roundings of a bin's number)
             const unsigned long long target = tau(total);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                mass[i] = cnt[i] * R.mass<F32>(fminf(mx, mx - (2 * threadIdx.x + i - 0.52f) / P.bins));
-            sm_scan<true>(H, cnt, mass, target, cnt_all, mass_all);
-            b0 = H.bin >= 0 ? static_cast<uint32_t>(H.bin) : kSmFirst;
+            for (int i = 0; i < N; ++i)
+                mass[i] = cnt[i] * R.mass<F32>(fminf(mx, mx - (N * threadIdx.x + i - 0.52f) * P.width));
+            sm_scan<true, NT>(H, cnt, mass, target, cnt_all, mass_all);
+            b0 = H.bin >= 0 ? static_cast<uint32_t>(H.bin) : kSmBins;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                mass[i] = cnt[i] * R.mass<F32>(mx - (2 * threadIdx.x + i + 0.52f) / P.bins);
-            sm_scan<true>(H, cnt, mass, target, cnt_all, mass_all);
+            for (int i = 0; i < N; ++i)
+                mass[i] = cnt[i] * R.mass<F32>(mx - (N * threadIdx.x + i + 0.52f) * P.width);
+            sm_scan<true, NT>(H, cnt, mass, target, cnt_all, mass_all);
             deep = H.bin < 0;
             if (!deep)
                 b1 = static_cast<uint32_t>(H.bin);
             down_to_b1 = deep ? cnt_all : H.bcnt_before + H.bcnt_at;
         }
-        SampleSet<LT> Set = {X, R, P.bins, b1, nullptr, 0};
+        SampleSet<LT, NT> Set = {X, R, P.bins, b1, nullptr, 0};
         if (!deep && down_to_b1 <= kSmFew) {
             // 3. few ids: the row is settled at once, by every CTA
             Set.each([&](uint32_t bits, int32_t id, uint32_t) {
@@ -898,13 +1012,11 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
             const uint32_t m = sm_collect<LT>(R, 0, C, H);
             const uint2 me = threadIdx.x < m ? H.all[threadIdx.x] : make_uint2(0u, 0u);
             uint32_t before = 0;
-            unsigned long long through = threadIdx.x < m ? H.mass[threadIdx.x] : 0ull;
-            if (threadIdx.x < m)
-                for (uint32_t i = 0; i < m; ++i)
-                    if (sm_before(H.all[i], me)) {
-                        ++before;
-                        through += H.mass[i];
-                    }
+            unsigned long long through = 0;
+            if (threadIdx.x < m) {
+                sm_rank(H, m, me, before, through);
+                through += H.mass[threadIdx.x];
+            }
             // the last of the top-k set, the last of top-p's, the last that min-p keeps
             const bool in_k = threadIdx.x < m && (!use_k || before < static_cast<uint32_t>(P.top_k));
             if (use_k && threadIdx.x < m && before + 1 == min(static_cast<uint32_t>(P.top_k), m))
@@ -924,6 +1036,7 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
                 H.cut = {me.x, static_cast<int32_t>(me.y)};
             unsigned long long Z = 0, upto = 0;
             if (threadIdx.x < m)
+#pragma unroll 4
                 for (uint32_t i = 0; i < m; ++i) {
                     const unsigned long long w = H.mass[i];
                     Z += w;
@@ -944,70 +1057,50 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
                         P.prob[r] = static_cast<float>(static_cast<double>(own) / static_cast<double>(Z));
                 }
             }
-            sm_write_q<LT, true>(X, R, P, qrow, zlo, cut, Z);
+            sm_write_q<LT, NT, true>(X, R, P, qrow, zlo, cut, Z);
             sm_cluster_sync(); // no CTA leaves while another may read it
             return;
         }
-        // the list: counted, then written, in order
+        // the list
         if (X.mem && P.slice <= 65536) {
-            auto hits = [&](int32_t v) {
-                uint32_t h = 0;
+            for (int32_t v = threadIdx.x; v < X.nv; v += NT) {
                 const uint4 w = X.vec(v);
-                if (sm_bin(R, sm_largest<LT>(w), P.bins) <= b1) {
+                if (sm_bin(R, sm_largest<LT>(w), P.bins) > b1)
+                    continue;
+                uint32_t h = 0;
 #pragma unroll
-                    for (int j = 0; j < PV; ++j)
-                        h |= sm_bin(R, E::value(Slice::of(w, j)), P.bins) <= b1 ? 1u << j : 0u;
-                }
-                return h;
-            };
-            uint32_t c = 0;
-            for (int32_t v = v0 + lane; v < v1; v += 32)
-                c += __popc(hits(v));
-            unsigned long long no = 0;
-            sm_block_sum(S, no, c);
-            if (c <= kSmList) {
-                uint32_t at = 0;
-                for (int w = 0; w < warp; ++w)
-                    at += S.wcnt[w];
-                for (int32_t v = v0; v < v1; v += 32) {
-                    const uint32_t h = v + lane < v1 ? hits(v + lane) : 0u;
-                    if (!__any_sync(0xFFFFFFFFu, h))
-                        continue;
-                    uint32_t incl = __popc(h);
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                        incl += lane >= o ? up : 0u;
-                    }
-                    uint32_t to = at + incl - __popc(h);
-                    for (uint32_t g = h; g; g &= g - 1)
-                        H.list[to++] = static_cast<uint16_t>((v + lane) * PV + __ffs(g) - 1);
-                    at += __shfl_sync(0xFFFFFFFFu, incl, 31);
-                }
+                for (int j = 0; j < PV; ++j)
+                    h |= sm_bin(R, E::value(Slice::of(w, j)), P.bins) <= b1 ? 1u << j : 0u;
+                uint32_t at = atomicAdd(&H.nlist, static_cast<uint32_t>(__popc(h)));
+                for (; h; h &= h - 1, ++at)
+                    if (at < kSmList)
+                        H.list[at] = static_cast<uint16_t>(v * PV + __ffs(h) - 1);
+            }
+            __syncthreads();
+            if (H.nlist <= kSmList) {
                 Set.list = H.list;
-                Set.n = c;
-                __syncthreads();
+                Set.n = H.nlist;
             }
         }
         // the cut of a target inside a bin of `ties` ids
         auto resolve = [&](auto by_mass, uint32_t bin, uint32_t ties, unsigned long long above, unsigned long long left, int few) {
             constexpr bool MASS = decltype(by_mass)::value;
             if (ties <= kSmFew)
-                return sm_gather<LT, MASS>(Set, bin, above, left, cut, few, C, H);
+                return sm_gather<LT, NT, MASS>(Set, bin, above, left, cut, few, C, H);
             const uint32_t klo = sm_first_key<LT>(R, P.bins, bin, ktop);
             const uint32_t khi = bin ? sm_first_key<LT>(R, P.bins, bin - 1, ktop) - 1 : ktop;
-            return sm_narrow<LT, MASS>(X, R, klo, khi, above, left, P.piece, C, rank, H);
+            return sm_narrow<LT, NT, MASS>(X, R, klo, khi, above, left, P.piece, C, rank, H);
         };
         // ... or below the bins
         auto resolve_below = [&](auto by_mass, unsigned long long above, unsigned long long left) {
             constexpr bool MASS = decltype(by_mass)::value;
-            const uint32_t khi = sm_first_key<LT>(R, P.bins, kSmFirst - 1, ktop) - 1;
+            const uint32_t khi = sm_first_key<LT>(R, P.bins, kSmBins - 1, ktop) - 1;
             if (khi < E::kKeyMin) {
                 SampleFound f = {};
                 f.upto = above;
                 return f;
             }
-            return sm_narrow<LT, MASS>(X, R, E::kKeyMin, khi, above, left, P.piece, C, rank, H);
+            return sm_narrow<LT, NT, MASS>(X, R, E::kKeyMin, khi, above, left, P.piece, C, rank, H);
         };
         SampleFound f = {};
         if (use_k) {
@@ -1017,11 +1110,8 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
         }
         if (use_p) {
             // masses: above those bins in one sum, in them by bin
-            sm_cluster_sync(); // the counts have been read by every CTA
-            for (int i = threadIdx.x; i < 4 * kSmFirst; i += kSmThreads)
-                H.first[0][i] = 0u;
-            __syncthreads();
-            const uint32_t low = (1u << P.piece) - 1u;
+            sm_cluster_sync(); // the bins have been read by every CTA
+            sm_clear<NT>(H);
             unsigned long long above = 0;
             Set.each([&](uint32_t bits, int32_t id, uint32_t b) {
                 const uint32_t key = E::key(bits);
@@ -1031,36 +1121,23 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
                 if (b < b0) {
                     above += e;
                 } else {
-                    atomicAdd(&H.first[0][b], 1u);
-                    atomicAdd(&H.first[1][b], static_cast<uint32_t>(e) & low);
-                    atomicAdd(&H.first[2][b], static_cast<uint32_t>(e >> P.piece) & low);
-                    atomicAdd(&H.first[3][b], static_cast<uint32_t>(e >> (2 * P.piece)));
+                    sm_add_mass(H, b, e, P.piece);
                 }
             });
-            sm_block_sum(S, above, none);
+            sm_block_sum<NT>(S, above, none);
             use = sm_exchange(S, turn, C, rank, above, 0);
             above = 0;
             for (uint32_t k = 0; k < C; ++k)
                 above += S.cmass[use][k];
-            cnt[0] = cnt[1] = 0;
-            mass[0] = mass[1] = 0;
-            for (uint32_t k = 0; k < C; ++k) {
-                const uint2 c = sm_get2(&H.first[0][2 * threadIdx.x], k), m0 = sm_get2(&H.first[1][2 * threadIdx.x], k),
-                            m1 = sm_get2(&H.first[2][2 * threadIdx.x], k), m2 = sm_get2(&H.first[3][2 * threadIdx.x], k);
-                cnt[0] += c.x;
-                cnt[1] += c.y;
-                mass[0] += m0.x + (static_cast<unsigned long long>(m1.x) << P.piece) +
-                           (static_cast<unsigned long long>(m2.x) << (2 * P.piece));
-                mass[1] += m0.y + (static_cast<unsigned long long>(m1.y) << P.piece) +
-                           (static_cast<unsigned long long>(m2.y) << (2 * P.piece));
-            }
+            sm_counts(H, C, cnt);
+            sm_masses(H, C, P.piece, mass);
             if (use_k) { // the top-k set's
-                sm_scan<true>(H, cnt, mass, 1, cnt_all, mass_all);
+                sm_scan<true, NT>(H, cnt, mass, 1, cnt_all, mass_all);
                 total = mass_all + (deep ? f.upto : 0);
             }
             const unsigned long long target = tau(total);
             const unsigned long long left = target > above ? target - above : 1;
-            sm_scan<true>(H, cnt, mass, left, cnt_all, mass_all);
+            sm_scan<true, NT>(H, cnt, mass, left, cnt_all, mass_all);
             if (H.bin >= 0) {
                 const unsigned long long before = H.bmass_before;
                 const uint32_t bin = static_cast<uint32_t>(H.bin), ties = H.bcnt_at;
@@ -1108,7 +1185,7 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
         }
         return a;
     };
-    const SampleSet<LT> Kept = {X, R, 0.0f, 0u, list, nlist};
+    const SampleSet<LT, NT> Kept = {X, R, 0.0f, 0u, list, nlist};
     auto entry_mass = [&](uint32_t i, uint32_t &n) {
         const uint32_t b = Kept.bits(i);
         if (!keeps(b, Kept.id(i)))
@@ -1116,19 +1193,16 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
         ++n;
         return R.mass<F32>(E::value(b));
     };
-    // a warp's part of the list
-    const uint32_t lpart = (nlist + kSmWarps - 1) / kSmWarps;
-    const uint32_t l0 = min(nlist, warp * lpart), l1 = min(nlist, l0 + lpart);
     unsigned long long a = 0;
     uint32_t n = 0;
     if (list) {
-        for (uint32_t i = l0 + lane; i < l1; i += 32)
+        for (uint32_t i = threadIdx.x; i < nlist; i += NT)
             a += entry_mass(i, n);
     } else {
         for (int32_t v = v0 + lane; v < v1; v += 32)
             a += vec_mass(v, n);
     }
-    sm_block_sum(S, a, n);
+    sm_block_sum<NT>(S, a, n);
     const int use = sm_exchange(S, turn, C, rank, a, n);
     uint32_t kept = 0;
     unsigned long long Z = 0, below = 0;
@@ -1142,44 +1216,65 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
         P.kept[r] = static_cast<int32_t>(kept);
     const unsigned long long t = static_cast<unsigned long long>(mul_floor(u, static_cast<long long>(Z)));
     if (!bad_u && t >= below && t < below + a) { // this CTA's: the first id whose running mass exceeds t
+        // vectors i0 .. i1 - 1 hold it, `at` the mass before them
         unsigned long long at = below;
-        int w = 0;
-        for (; w < kSmWarps - 1; ++w) {
-            if (t < at + S.wmass[w])
-                break;
-            at += S.wmass[w];
+        int32_t i0 = v0, i1 = v1;
+        bool here;
+        if (CUTS && list) { // the listed masses by runs of vectors, of which there are at most as many as bins
+            if constexpr (CUTS) {
+                constexpr int N = kSmBins / NT;
+                const int32_t run = (X.nv + kSmBins - 1) / kSmBins;
+                SampleBins &H = *reinterpret_cast<SampleBins *>(sm_raw + (P.staged ? static_cast<size_t>(P.slice) * sizeof(LT) : 0));
+                // (no other CTA reads the bins any more: each has arrived at the barrier above)
+                sm_clear<NT>(H);
+                for (uint32_t i = threadIdx.x; i < nlist; i += NT) {
+                    uint32_t no = 0;
+                    const unsigned long long e = entry_mass(i, no);
+                    if (e)
+                        sm_add_mass(H, (list[i] / PV) / run, e, P.piece);
+                }
+                __syncthreads();
+                uint32_t cnt[N], no;
+                unsigned long long mass[N], none;
+                sm_counts_here(H, cnt);
+                sm_masses_here(H, P.piece, mass);
+                sm_scan<true, NT>(H, cnt, mass, t - below + 1, no, none);
+                i0 = H.bin * run;
+                i1 = min(X.nv, i0 + run);
+                at += H.bmass_before;
+            }
+            here = warp == 0;
+        } else { // by warps' parts
+            int w = 0;
+            for (; w < NT / 32 - 1; ++w) {
+                if (t < at + S.wmass[w])
+                    break;
+                at += S.wmass[w];
+            }
+            here = warp == w;
         }
-        if (warp == w) {
-            auto draw = [&](int32_t id, unsigned long long one) {
-                P.tokens[r] = id;
-                if (P.prob)
-                    P.prob[r] = static_cast<float>(static_cast<double>(one) / static_cast<double>(Z));
-            };
-            const int32_t i0 = list ? static_cast<int32_t>(l0) : v0, i1 = list ? static_cast<int32_t>(l1) : v1;
+        if (here) {
             for (int32_t i = i0; i < i1; i += 32) {
-                uint32_t cnt = 0;
-                const unsigned long long e =
-                    i + lane < i1 ? (list ? entry_mass(i + lane, cnt) : vec_mass(i + lane, cnt)) : 0ull;
+                uint32_t no = 0;
+                const unsigned long long e = i + lane < i1 ? vec_mass(i + lane, no) : 0ull;
                 const unsigned long long run =
                     at + static_cast<unsigned long long>(warp_incl_scan_ll(static_cast<long long>(e), lane));
                 const uint32_t b = __ballot_sync(0xFFFFFFFFu, t < run);
                 if (b) {
-                    if (lane == __ffs(b) - 1) {
-                        if (list) {
-                            draw(Kept.id(i + lane), e);
-                        } else { // inside this lane's vector
-                            unsigned long long to = run - e;
-                            const uint4 x = X.vec(i + lane);
+                    if (lane == __ffs(b) - 1) { // inside this lane's vector
+                        unsigned long long to = run - e;
+                        const uint4 x = X.vec(i + lane);
 #pragma unroll 1
-                            for (int j = 0; j < PV; ++j) {
-                                const uint32_t bits = Slice::of(x, j);
-                                const int32_t id = X.first + (i + lane) * PV + j;
-                                const unsigned long long one = keeps(bits, id) ? R.mass<F32>(E::value(bits)) : 0ull;
-                                to += one;
-                                if (t < to) {
-                                    draw(id, one);
-                                    break;
-                                }
+                        for (int j = 0; j < PV; ++j) {
+                            const uint32_t bits = Slice::of(x, j);
+                            const int32_t id = X.first + (i + lane) * PV + j;
+                            const unsigned long long one = keeps(bits, id) ? R.mass<F32>(E::value(bits)) : 0ull;
+                            to += one;
+                            if (t < to) {
+                                P.tokens[r] = id;
+                                if (P.prob)
+                                    P.prob[r] = static_cast<float>(static_cast<double>(one) / static_cast<double>(Z));
+                                break;
                             }
                         }
                     }
@@ -1190,7 +1285,7 @@ __global__ void __launch_bounds__(kSmThreads, 2) sample_kernel(const SampleParam
         }
     }
     // 5. q
-    sm_write_q<LT, CUTS>(X, R, P, qrow, zlo, cut, Z);
+    sm_write_q<LT, NT, CUTS>(X, R, P, qrow, zlo, cut, Z);
     sm_cluster_sync(); // no CTA leaves while another may read it
 }
 
