@@ -790,10 +790,12 @@ bool lm4_scale_map(CUtensorMap *map, const void *base, int64_t tiles, uint32_t b
 // How a product is cut: a function of (M, V).  A stage (256 hidden dims) of a tile
 // costs an SM the largest of
 //   the MMAs' time, 2 cycles an id (4 steps of 64 dims);
-//   what it loads: a row of h or of W is 128 bytes with 16 of scales, at about 50
+//   what it loads: a row of h or of W is 128 bytes with 16 of scales, at about 45
 //   bytes a cycle from L2 -- and with one row tile, where W comes from memory
 //   once, 23 bytes a cycle and SM for W.
-// Narrower tiles on ties: they reach more SMs.
+// Pairs load half as much of W a row; lone CTAs do not keep half of a pair idle
+// where the rows end in its first half.  Narrower tiles on ties: they reach more
+// SMs.
 struct Lm4Plan {
     bool pair;
     int32_t MT, NT, NB;
@@ -802,20 +804,29 @@ struct Lm4Plan {
 Lm4Plan lm4_plan(int64_t M, int32_t V)
 {
     Lm4Plan p = {};
-    p.pair = M > sv::kLmBM;
-    const int64_t units = p.pair ? kNominalSms / 2 : kNominalSms;
-    p.MT = static_cast<int32_t>(ceil_div(M > 0 ? M : 1, p.pair ? 2 * sv::kLmBM : sv::kLmBM));
     const int64_t rows = M < sv::kLmBM ? M : sv::kLmBM;
     int64_t best = INT64_MAX;
-    for (int32_t nb = sv::kL4MaxNB; nb >= 64; nb -= 64) {
-        const int64_t w = 144 * (p.pair ? nb / 2 : nb), loads = (144 * rows + w) / 50;
-        int64_t stage = p.MT == 1 ? w / 23 : 0;
-        stage = stage > loads ? stage : loads;
-        stage = stage > 2 * nb ? stage : 2 * nb;
-        const int64_t cost = ceil_div(p.MT * ceil_div(V, nb), units) * (stage + 40);
-        if (cost <= best) {
-            best = cost;
-            p.NB = nb;
+    for (int pair = M > sv::kLmBM ? 1 : 0; pair >= 0; --pair) {
+        const int64_t units = pair ? kNominalSms / 2 : kNominalSms;
+        const int32_t mt = static_cast<int32_t>(ceil_div(M > 0 ? M : 1, pair ? 2 * sv::kLmBM : sv::kLmBM));
+        int64_t low = INT64_MAX;
+        int32_t NB = 0;
+        for (int32_t nb = sv::kL4MaxNB; nb >= 64; nb -= 64) {
+            const int64_t w = 144 * (pair ? nb / 2 : nb), loads = (144 * rows + w) / 45;
+            int64_t stage = mt == 1 ? w / 23 : 0;
+            stage = stage > loads ? stage : loads;
+            stage = stage > 2 * nb ? stage : 2 * nb;
+            const int64_t cost = ceil_div(mt * ceil_div(V, nb), units) * (stage + 40);
+            if (cost <= low) {
+                low = cost;
+                NB = nb;
+            }
+        }
+        if (low < best) { // a pair on ties
+            best = low;
+            p.pair = pair != 0;
+            p.MT = mt;
+            p.NB = NB;
         }
     }
     p.NT = static_cast<int32_t>(ceil_div(V, p.NB));
@@ -957,7 +968,9 @@ int32_t fp4_warps(int32_t octets)
 template <int BLOCK, typename XT>
 cudaError_t quantize_fp4_launch(const sv::Fp4Params &P, bool vec, cudaStream_t s)
 {
-    const unsigned grid = static_cast<unsigned>(ceil_div(P.Mpad, sv::kF4Threads / 32 / P.WPR));
+    const int64_t rows = ceil_div(P.Mpad, sv::kF4Threads / 32 / P.WPR);
+    const int64_t stay = static_cast<int64_t>(kNominalSms) * sv::kF4Ctas<XT>;
+    const unsigned grid = static_cast<unsigned>(rows < stay ? rows : stay);
     return launch_behind(vec ? sv::quantize_fp4_kernel<BLOCK, XT, true> : sv::quantize_fp4_kernel<BLOCK, XT, false>, grid,
                          sv::kF4Threads, 0, s, P);
 }

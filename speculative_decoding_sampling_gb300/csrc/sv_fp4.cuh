@@ -19,7 +19,8 @@
 // Work is cut in octets (8 values of a row, one lane): 16-byte loads of bf16,
 // 4-byte stores, both whole lines a warp; a block is 2 or 4 neighbouring lanes.
 // A row belongs to WPR warps, whose lanes keep its octets in registers between
-// the row's maximum and the values (longer rows are read again).
+// the row's maximum and the values (of longer rows the rest is read again), and
+// have the next row's on their way meanwhile.
 #pragma once
 
 #include "sv_device.cuh"
@@ -28,6 +29,8 @@ namespace sv {
 
 constexpr int kF4Threads = 256;
 constexpr int kF4Regs = 4; // octets a lane keeps between the two passes
+// CTAs of an SM that stay and walk the rows, the next row's octets on their way
+template <typename XT> constexpr int kF4Ctas = sizeof(XT) == 2 ? 3 : 2;
 
 struct Fp4Params {
     const void *x;        // [M, d]
@@ -189,26 +192,24 @@ __device__ __forceinline__ uint32_t f4_outer(uint32_t amax)
 }
 
 template <int BLOCK, typename XT, bool VEC>
-__global__ void __launch_bounds__(kF4Threads) quantize_fp4_kernel(const Fp4Params P)
+__global__ void __launch_bounds__(kF4Threads, kF4Ctas<XT>) quantize_fp4_kernel(const Fp4Params P)
 {
     constexpr int L = BLOCK / 8; // lanes of a block
-    __shared__ uint32_t wmax[kF4Threads / 32];
+    __shared__ uint32_t wmax[2][kF4Threads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = kF4Threads / 32 / P.WPR; // rows of a CTA
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * per + warp / P.WPR;
+    const int per = kF4Threads / 32 / P.WPR; // rows of a CTA at a time (128 is a multiple)
     const int first = (warp & (P.WPR - 1)) * 32 + lane, stride = P.WPR * 32;
-    const bool real = row < P.M;
     pdl_wait_primary();
     pdl_launch_dependents();
-    const XT *x = static_cast<const XT *>(P.x) + (real ? row : 0) * P.d;
-    auto fetch = [&](F4Octet<XT> &o, int32_t i) {
-        const int32_t left = real ? P.d - i * 8 : 0;
+    auto fetch = [&](F4Octet<XT> &o, int64_t row, int32_t i) {
+        const int32_t left = row < P.M ? P.d - i * 8 : 0;
+        const XT *x = static_cast<const XT *>(P.x) + row * P.d + i * 8;
         if (left <= 0)
             o.zero();
         else if (VEC)
-            o.load(x + i * 8);
+            o.load(x);
         else
-            o.load_some(x + i * 8, left);
+            o.load_some(x, left);
     };
     auto block_max = [&](const F4Octet<XT> &o) {
         uint32_t m = o.amax();
@@ -219,89 +220,105 @@ __global__ void __launch_bounds__(kF4Threads) quantize_fp4_kernel(const Fp4Param
     };
     // every warp's lanes take the same number of steps (the shuffles)
     const int steps = static_cast<int>((P.octets + stride - 1) / stride);
+    const int64_t step_rows = static_cast<int64_t>(gridDim.x) * per;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * per + warp / P.WPR;
     F4Octet<XT> keep[kF4Regs];
-    uint32_t amax[kF4Regs];
-    uint32_t top = 0;
-    if (BLOCK == 16 || steps <= kF4Regs) {
 #pragma unroll
-        for (int t = 0; t < kF4Regs; ++t)
-            if (t < steps)
-                fetch(keep[t], first + t * stride);
+    for (int t = 0; t < kF4Regs; ++t)
+        if (t < steps)
+            fetch(keep[t], row, first + t * stride);
+    uint32_t parity = 0;
+    for (; row < P.Mpad; row += step_rows, parity ^= 1u) { // (all warps of a CTA together)
+        uint32_t amax[kF4Regs];
+        uint32_t top = 0;
 #pragma unroll
         for (int t = 0; t < kF4Regs; ++t)
             if (t < steps) {
                 amax[t] = block_max(keep[t]);
                 top = max(top, amax[t] < 0x7F800000u ? amax[t] : 0u);
             }
-    }
-    uint32_t ge = 127u; // the row's biased exponent
-    if (BLOCK == 16) {
-        for (int t = kF4Regs; t < steps; ++t) {
-            F4Octet<XT> o;
-            fetch(o, first + t * stride);
-            const uint32_t m = block_max(o);
-            top = max(top, m < 0x7F800000u ? m : 0u);
-        }
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-        if (P.WPR > 1) {
-            if (lane == 0)
-                wmax[warp] = top;
-            __syncthreads();
-            for (int w = 0; w < P.WPR; ++w)
-                top = max(top, wmax[(warp & ~(P.WPR - 1)) + w]);
-        }
-        ge = f4_outer(top);
-        if (real && first == 0)
-            P.g[row] = __uint_as_float(ge << 23);
-    }
-    auto finish = [&](const F4Octet<XT> &o, uint32_t m, int32_t i) {
-        const bool bad = m >= 0x7F800000u;
-        float f[8];
-        o.values(f);
-        uint32_t byte;
+        F4Octet<XT> next[kF4Regs];
+#pragma unroll
+        for (int t = 0; t < kF4Regs; ++t)
+            if (t < steps)
+                fetch(next[t], row + step_rows, first + t * stride);
+        uint32_t ge = 127u; // the row's biased exponent
         if (BLOCK == 16) {
-            const float ginv = __uint_as_float((254u - ge) << 23);
-            byte = f4_to_e4m3(__fdiv_rn(__fmul_rn(__uint_as_float(m), ginv), 6.0f));
-            byte = bad ? 0x7Fu : (m ? max(byte, 1u) : 0u);
-            const float s = f4_e4m3(byte);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                f[k] = (bad || !m) ? 0.0f : __fdiv_rn(__fmul_rn(f[k], ginv), s);
-        } else {
-            const int e = static_cast<int>(m >> 23) - 2;
-            byte = bad ? 0xFFu : static_cast<uint32_t>(e > 0 ? e : 0);
-            const float sinv = __uint_as_float((254u - byte) << 23);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                f[k] = bad ? 0.0f : __fmul_rn(f[k], sinv);
+            for (int t = kF4Regs; t < steps; ++t) {
+                F4Octet<XT> o;
+                fetch(o, row, first + t * stride);
+                const uint32_t m = block_max(o);
+                top = max(top, m < 0x7F800000u ? m : 0u);
+            }
+            top = __reduce_max_sync(0xFFFFFFFFu, top);
+            if (P.WPR > 1) {
+                if (lane == 0)
+                    wmax[parity][warp] = top;
+                __syncthreads();
+                for (int w = 0; w < P.WPR; ++w)
+                    top = max(top, wmax[parity][(warp & ~(P.WPR - 1)) + w]);
+            }
+            ge = f4_outer(top);
+            if (row < P.M && first == 0)
+                P.g[row] = __uint_as_float(ge << 23);
         }
-        const uint32_t packed = f4_pack(f);
-        if (i >= P.octets || row >= P.Mpad)
-            return;
-        if (lane % L == 0)
-            P.s[f4_scale_at(row, i / L, P.KT)] = static_cast<uint8_t>(byte);
-        const int32_t left = real ? P.d - i * 8 : 0;
-        uint8_t *v = P.v + row * (P.d >> 1) + i * 4;
-        if (VEC) {
-            if (left > 0)
-                *reinterpret_cast<uint32_t *>(v) = packed;
-        } else {
+        auto finish = [&](const F4Octet<XT> &o, uint32_t m, int32_t i) {
+            const bool bad = m >= 0x7F800000u;
+            float f[8];
+            o.values(f);
+            uint32_t byte;
+            if (BLOCK == 16) {
+                const float ginv = __uint_as_float((254u - ge) << 23);
+                // x / g is exact.  Quotients by 6 and by s from a rounded reciprocal and one
+                // correction, which rounds correctly (Markstein 1990): q = y r, q + (y - q s) r.
+                const float y = __fmul_rn(__uint_as_float(m), ginv), q6 = __fmul_rn(y, 1.0f / 6.0f);
+                byte = f4_to_e4m3(__fmaf_rn(__fmaf_rn(q6, -6.0f, y), 1.0f / 6.0f, q6));
+                byte = bad ? 0x7Fu : (m ? max(byte, 1u) : 0u);
+                const bool zero = bad || !m;
+                const float s = zero ? 1.0f : f4_e4m3(byte), r = __frcp_rn(s), scale = zero ? 0.0f : ginv;
+                const unsigned long long gg = pack2(scale, scale), rr = pack2(r, r), ss = pack2(-s, -s);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (2 * k < left)
-                    v[k] = static_cast<uint8_t>(packed >> (8 * k));
-        }
-    };
-    if (BLOCK == 16 || steps <= kF4Regs) {
+                for (int k = 0; k < 8; k += 2) {
+                    const unsigned long long y2 = mul2(pack2(bad ? 0.0f : f[k], bad ? 0.0f : f[k + 1]), gg), q = mul2(y2, rr);
+                    unpack2(fma2(fma2(q, ss, y2), rr, q), f[k], f[k + 1]);
+                }
+            } else {
+                const int e = static_cast<int>(m >> 23) - 2;
+                byte = bad ? 0xFFu : static_cast<uint32_t>(e > 0 ? e : 0);
+                const float sinv = __uint_as_float((254u - byte) << 23);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    f[k] = bad ? 0.0f : __fmul_rn(f[k], sinv);
+            }
+            const uint32_t packed = f4_pack(f);
+            if (i >= P.octets)
+                return;
+            if (lane % L == 0)
+                P.s[f4_scale_at(row, i / L, P.KT)] = static_cast<uint8_t>(byte);
+            const int32_t left = row < P.M ? P.d - i * 8 : 0;
+            uint8_t *v = P.v + row * (P.d >> 1) + i * 4;
+            if (VEC) {
+                if (left > 0)
+                    *reinterpret_cast<uint32_t *>(v) = packed;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (2 * k < left)
+                        v[k] = static_cast<uint8_t>(packed >> (8 * k));
+            }
+        };
 #pragma unroll
         for (int t = 0; t < kF4Regs; ++t)
             if (t < steps)
                 finish(keep[t], amax[t], first + t * stride);
-    }
-    for (int t = (BLOCK == 16 || steps <= kF4Regs) ? kF4Regs : 0; t < steps; ++t) {
-        F4Octet<XT> o;
-        fetch(o, first + t * stride);
-        finish(o, block_max(o), first + t * stride);
+        for (int t = kF4Regs; t < steps; ++t) {
+            F4Octet<XT> o;
+            fetch(o, row, first + t * stride);
+            finish(o, block_max(o), first + t * stride);
+        }
+#pragma unroll
+        for (int t = 0; t < kF4Regs; ++t)
+            keep[t] = next[t];
     }
 }
 

@@ -19,8 +19,8 @@
 // issues: the stage's scale tiles from shared into tensor memory (tcgen05.cp,
 // the four lane quarters get copies), then an MMA for each 64 dims.  Copies and
 // MMAs of one thread run in order, and two sets of scale columns alternate.
-// Warps 2..5 are the epilogue: two accumulators, so that a tile is read, scaled
-// and stored (through shared memory, as for e4m3) while the next is formed.
+// Warps 2..9 are the epilogue, two for each 32 rows: two accumulators, so that a
+// tile is read, scaled and stored (through shared memory, as for e4m3) while the next is formed.
 // 512 tensor-memory columns: 2 x 192 of sums, 2 x 64 of scales, hence NB <= 192.
 // Ids start at a multiple of 64 of their scale tile: two columns.
 // Every wait is bounded (l8_wait), with lm_head_kernel's teardown.
@@ -32,20 +32,21 @@ namespace sv {
 
 constexpr int kL4BK = 256;                 // hidden dims of a stage
 constexpr int kL4MaxNB = 192;
-constexpr int kL4Threads = 192;
+constexpr int kL4EpiWarps = 8;             // two a lane quarter, each half of a tile's columns
+constexpr int kL4Threads = 64 + 32 * kL4EpiWarps;
 constexpr int kL4MaxStages = 8;
 constexpr uint32_t kL4TmemCols = 512;
 constexpr uint32_t kL4ScaleCol = 2 * kL4MaxNB; // first of 2 x 64 scale columns
-constexpr int kL4StgBytes = kL4MaxNB / 32 * kL8BoxBytes; // an epilogue warp's 32 rows of a tile
+constexpr int kL4StgBytes = kL4MaxNB / 64 * kL8BoxBytes; // an epilogue warp's 32 rows of half a tile
 constexpr int kL4RingBytes = 172 * 1024;
-// l8_store_rows reads whole half tiles of 4 boxes (what lies past a tile's ids is
-// not used): the last warp's second half ends past its boxes and the factors.
-constexpr int kL4Behind = 4 * kL4MaxNB * 4 + 1024;
-static_assert(3 * kL4StgBytes + 8 * kL8BoxBytes <= 4 * kL4StgBytes + kL4Behind, "staged rows read behind the boxes");
-constexpr int kL4Smem = 1024 + kL4RingBytes + 4 * kL4StgBytes + kL4Behind;
+// l8_store_rows reads 4 boxes whatever a warp has (what lies past its ids is not
+// used): the last warp's end past its boxes, in the ids' factors.
+constexpr int kL4Behind = kL4EpiWarps * kL4MaxNB / 2 * 4;
+static_assert(4 * kL8BoxBytes <= kL4StgBytes + kL4Behind, "staged rows read behind the boxes");
+constexpr int kL4Smem = 1024 + kL4RingBytes + kL4EpiWarps * kL4StgBytes + kL4Behind;
 static_assert(kL4Smem <= 227 * 1024 - 512, "shared memory of a CTA, less the barriers");
 // the MMA's 128 rows may run past the rows a stage has: never past the memory
-static_assert(4 * kL4StgBytes >= kLmBM * 128, "rows read behind the ring");
+static_assert(kL4EpiWarps * kL4StgBytes >= kLmBM * 128, "rows read behind the ring");
 
 struct Lm4Params {
     Lm8Params t;              // M, N, tiles, logits, status (its own scales and sums unused)
@@ -117,8 +118,8 @@ __device__ __forceinline__ float4 l4_lds4(uint32_t addr)
 // x, NaN if it is infinite: -inf is a masked token to what reads the logits.
 __device__ __forceinline__ float l4_finite(float x) { return __fmaf_rn(x, 0.0f, x); }
 
-// The epilogue warps: warp w holds the tile's rows of tensor-memory lane
-// quarter w mod 4.
+// The epilogue warps: warp w holds the tile's rows of tensor-memory lane quarter
+// w mod 4, and the first or the second half of its ids.
 template <bool PAIR>
 __device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMap *map, uint32_t stg0, uint32_t gws0,
                                             uint32_t tbase, uint32_t tfull, uint32_t tempty, int *stop, uint32_t rank,
@@ -126,21 +127,22 @@ __device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMa
 {
     const Lm8Params &T = P.t;
     const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31u), lq = warp & 3;
-    const uint32_t stg = stg0 + static_cast<uint32_t>(lq) * kL4StgBytes;
-    const uint32_t gws = gws0 + static_cast<uint32_t>(lq) * (kL4MaxNB * 4);
-    const int G = T.NB / 32;
+    const int half = (warp - 2) >> 2, G = T.NB / 64; // groups of 32 ids: 1, 2 or 3
+    const uint32_t stg = stg0 + static_cast<uint32_t>(warp - 2) * kL4StgBytes;
+    const uint32_t gws = gws0 + static_cast<uint32_t>(warp - 2) * (kL4MaxNB / 2 * 4);
     const uint32_t te = PAIR ? lm_mapa(tempty, 0) : tempty;
     bool alive = true;
     uint32_t i = 0;
     for (uint32_t t = unit; t < ntiles; t += units, ++i) {
         const uint32_t a = i & 1u;
-        const int row0 = l8_row0<PAIR>(T, t, rank, lq), n0 = static_cast<int>(l8_tile_n(T, t)) * T.NB;
+        const int row0 = l8_row0<PAIR>(T, t, rank, lq);
+        const int n0 = static_cast<int>(l8_tile_n(T, t)) * T.NB + half * G * 32;
         // the rows' and ids' factors, while the tile is formed
         float gh = 1.0f;
         if (P.gh) {
             gh = row0 + lane < T.M ? __ldg(P.gh + row0 + lane) : 0.0f;
             __syncwarp();
-            for (int c = lane; c < T.NB; c += 32) {
+            for (int c = lane; c < G * 32; c += 32) {
                 const float g = n0 + c < T.N ? __ldg(P.gw + n0 + c) : 0.0f;
                 asm volatile("st.shared.f32 [%0], %1;" ::"r"(gws + static_cast<uint32_t>(c) * 4u), "f"(g) : "memory");
             }
@@ -150,27 +152,31 @@ __device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMa
         if (!alive)
             break;
         lm_tc_after();
+        const bool in = row0 < T.M && n0 < T.N;
+        const uint32_t tl = tbase + (static_cast<uint32_t>(lq) << 21) + a * kL4MaxNB + static_cast<uint32_t>(half * G * 32);
+        uint32_t v[2][32]; // the next group is on its way while one is scaled
+        if (in)
+            l8_ld_start(tl, v[0]);
         if (T.tma && i > 0) // the last tile's stores have read this warp's shared memory
             l8_stores_read();
         __syncwarp();
-        const bool rows_in = row0 < T.M;
-        const uint32_t tl = tbase + (static_cast<uint32_t>(lq) << 21) + a * kL4MaxNB;
-#pragma unroll 1
-        for (int g = 0; g < G; ++g) {
-            if (rows_in) {
-                uint32_t v[32];
-                l8_ld_start(tl + 32 * g, v);
-                l8_ld_wait(v);
+#pragma unroll
+        for (int g = 0; g < kL4MaxNB / 64; ++g) {
+            if (in && g < G) {
+                uint32_t(&x)[32] = v[g & 1];
+                l8_ld_wait(x);
+                if (g + 1 < G)
+                    l8_ld_start(tl + 32 * (g + 1), v[(g + 1) & 1]);
                 uint32_t pk[16];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     float4 w = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
                     if (P.gh)
                         w = l4_lds4(gws + static_cast<uint32_t>(32 * g + 4 * k) * 4u);
-                    const float x0 = l4_finite(__fmul_rn(__uint_as_float(v[4 * k]), __fmul_rn(gh, w.x)));
-                    const float x1 = l4_finite(__fmul_rn(__uint_as_float(v[4 * k + 1]), __fmul_rn(gh, w.y)));
-                    const float x2 = l4_finite(__fmul_rn(__uint_as_float(v[4 * k + 2]), __fmul_rn(gh, w.z)));
-                    const float x3 = l4_finite(__fmul_rn(__uint_as_float(v[4 * k + 3]), __fmul_rn(gh, w.w)));
+                    const float x0 = l4_finite(__fmul_rn(__uint_as_float(x[4 * k]), __fmul_rn(gh, w.x)));
+                    const float x1 = l4_finite(__fmul_rn(__uint_as_float(x[4 * k + 1]), __fmul_rn(gh, w.y)));
+                    const float x2 = l4_finite(__fmul_rn(__uint_as_float(x[4 * k + 2]), __fmul_rn(gh, w.z)));
+                    const float x3 = l4_finite(__fmul_rn(__uint_as_float(x[4 * k + 3]), __fmul_rn(gh, w.w)));
                     pk[2 * k] = bf16_rn_pair(x0, x1);
                     pk[2 * k + 1] = bf16_rn_pair(x2, x3);
                 }
@@ -181,7 +187,7 @@ __device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMa
         __syncwarp();
         if (lane == 0) // this warp has read the accumulator
             l8_arrive(te + a * 8u);
-        if (!rows_in)
+        if (!in)
             continue;
         if (T.tma) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -193,12 +199,9 @@ __device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMa
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
         } else {
-            const int ncols = T.N - n0 < T.NB ? T.N - n0 : T.NB;
             uint32_t boxes = stg;
             l8_staged_now(boxes);
-            l8_store_rows(T, boxes, row0, n0, ncols < 128 ? ncols : 128, lane);
-            if (ncols > 128)
-                l8_store_rows(T, boxes + 4 * kL8BoxBytes, row0, n0 + 128, ncols - 128, lane);
+            l8_store_rows(T, boxes, row0, n0, T.N - n0 < G * 32 ? T.N - n0 : G * 32, lane);
             __syncwarp();
         }
     }
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(kL4Threads, 1)
         }
         for (int a = 0; a < 2; ++a) {
             lm_mbar_init(smem_addr(&tfull[a]), 1);
-            lm_mbar_init(smem_addr(&tempty[a]), kCtas * 4);
+            lm_mbar_init(smem_addr(&tempty[a]), kCtas * kL4EpiWarps);
         }
         lm_mbar_init(smem_addr(&drain), 1);
         stop = 0;
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(kL4Threads, 1)
                 l8_fail(T, &stop);
         }
     } else {
-        l4_epilogue<PAIR>(P, &tmC, sbase + kL4RingBytes, sbase + kL4RingBytes + 4 * kL4StgBytes, tbase,
+        l4_epilogue<PAIR>(P, &tmC, sbase + kL4RingBytes, sbase + kL4RingBytes + kL4EpiWarps * kL4StgBytes, tbase,
                           smem_addr(&tfull[0]), smem_addr(&tempty[0]), &stop, rank, unit, units, ntiles);
     }
     // ---- teardown: copies and MMAs in flight complete before the memory goes
