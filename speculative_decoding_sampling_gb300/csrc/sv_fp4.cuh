@@ -201,15 +201,20 @@ __global__ void __launch_bounds__(kF4Threads, kF4Ctas<XT>) quantize_fp4_kernel(c
     const int first = (warp & (P.WPR - 1)) * 32 + lane, stride = P.WPR * 32;
     pdl_wait_primary();
     pdl_launch_dependents();
-    auto fetch = [&](F4Octet<XT> &o, int64_t row, int32_t i) {
-        const int32_t left = row < P.M ? P.d - i * 8 : 0;
-        const XT *x = static_cast<const XT *>(P.x) + row * P.d + i * 8;
+    // every warp's lanes take the same number of steps (the shuffles)
+    const int steps = static_cast<int>((P.octets + stride - 1) / stride);
+    const int64_t step_rows = static_cast<int64_t>(gridDim.x) * per;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * per + warp / P.WPR;
+    const XT *x = static_cast<const XT *>(P.x) + row * P.d + first * 8; // this lane's first octet of the row
+    const int64_t x_step = step_rows * P.d;
+    auto fetch = [&](F4Octet<XT> &o, const XT *from, bool real, int t) {
+        const int32_t left = real ? P.d - (first + t * stride) * 8 : 0;
         if (left <= 0)
             o.zero();
         else if (VEC)
-            o.load(x);
+            o.load(from + t * stride * 8);
         else
-            o.load_some(x, left);
+            o.load_some(from + t * stride * 8, left);
     };
     auto block_max = [&](const F4Octet<XT> &o) {
         uint32_t m = o.amax();
@@ -218,17 +223,14 @@ __global__ void __launch_bounds__(kF4Threads, kF4Ctas<XT>) quantize_fp4_kernel(c
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
         return m;
     };
-    // every warp's lanes take the same number of steps (the shuffles)
-    const int steps = static_cast<int>((P.octets + stride - 1) / stride);
-    const int64_t step_rows = static_cast<int64_t>(gridDim.x) * per;
-    int64_t row = static_cast<int64_t>(blockIdx.x) * per + warp / P.WPR;
     F4Octet<XT> keep[kF4Regs];
 #pragma unroll
     for (int t = 0; t < kF4Regs; ++t)
         if (t < steps)
-            fetch(keep[t], row, first + t * stride);
+            fetch(keep[t], x, row < P.M, t);
     uint32_t parity = 0;
-    for (; row < P.Mpad; row += step_rows, parity ^= 1u) { // (all warps of a CTA together)
+    for (; row < P.Mpad; row += step_rows, x += x_step, parity ^= 1u) { // (all warps of a CTA together)
+        const bool real = row < P.M;
         uint32_t amax[kF4Regs];
         uint32_t top = 0;
 #pragma unroll
@@ -241,12 +243,12 @@ __global__ void __launch_bounds__(kF4Threads, kF4Ctas<XT>) quantize_fp4_kernel(c
 #pragma unroll
         for (int t = 0; t < kF4Regs; ++t)
             if (t < steps)
-                fetch(next[t], row + step_rows, first + t * stride);
+                fetch(next[t], x + x_step, row + step_rows < P.M, t);
         uint32_t ge = 127u; // the row's biased exponent
         if (BLOCK == 16) {
             for (int t = kF4Regs; t < steps; ++t) {
                 F4Octet<XT> o;
-                fetch(o, row, first + t * stride);
+                fetch(o, x, real, t);
                 const uint32_t m = block_max(o);
                 top = max(top, m < 0x7F800000u ? m : 0u);
             }
@@ -259,44 +261,53 @@ __global__ void __launch_bounds__(kF4Threads, kF4Ctas<XT>) quantize_fp4_kernel(c
                     top = max(top, wmax[parity][(warp & ~(P.WPR - 1)) + w]);
             }
             ge = f4_outer(top);
-            if (row < P.M && first == 0)
+            if (real && first == 0)
                 P.g[row] = __uint_as_float(ge << 23);
         }
-        auto finish = [&](const F4Octet<XT> &o, uint32_t m, int32_t i) {
-            const bool bad = m >= 0x7F800000u;
+        // this lane's first scale and values; a step further lies a whole number of tiles
+        uint8_t *const s0 = P.s + f4_scale_at(row, first / L, P.KT);
+        uint8_t *const v0 = P.v + row * (P.d >> 1) + first * 4;
+        const float ginv = __uint_as_float((254u - ge) << 23);
+        auto finish = [&](const F4Octet<XT> &o, uint32_t m, int t) {
             float f[8];
             o.values(f);
             uint32_t byte;
             if (BLOCK == 16) {
-                const float ginv = __uint_as_float((254u - ge) << 23);
-                // x / g is exact.  Quotients by 6 and by s from a rounded reciprocal and one
-                // correction, which rounds correctly (Markstein 1990): q = y r, q + (y - q s) r.
+                // x / g is exact.  Quotients by 6 and by s from a rounded reciprocal r and one
+                // correction, which rounds correctly, and r itself from the unit's approximation
+                // and one of its own (Markstein 1990): q = y r, q + (y - q s) r.
                 const float y = __fmul_rn(__uint_as_float(m), ginv), q6 = __fmul_rn(y, 1.0f / 6.0f);
                 byte = f4_to_e4m3(__fmaf_rn(__fmaf_rn(q6, -6.0f, y), 1.0f / 6.0f, q6));
-                byte = bad ? 0x7Fu : (m ? max(byte, 1u) : 0u);
-                const bool zero = bad || !m;
-                const float s = zero ? 1.0f : f4_e4m3(byte), r = __frcp_rn(s), scale = zero ? 0.0f : ginv;
-                const unsigned long long gg = pack2(scale, scale), rr = pack2(r, r), ss = pack2(-s, -s);
+                byte = m ? max(byte, 1u) : 0u;
+                const float s = m ? f4_e4m3(byte) : 1.0f;
+                float r;
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+                r = __fmaf_rn(__fmaf_rn(-s, r, 1.0f), r, r);
+                const unsigned long long gg = pack2(ginv, ginv), rr = pack2(r, r), ss = pack2(-s, -s);
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) {
-                    const unsigned long long y2 = mul2(pack2(bad ? 0.0f : f[k], bad ? 0.0f : f[k + 1]), gg), q = mul2(y2, rr);
+                    const unsigned long long y2 = mul2(pack2(f[k], f[k + 1]), gg), q = mul2(y2, rr);
                     unpack2(fma2(fma2(q, ss, y2), rr, q), f[k], f[k + 1]);
                 }
             } else {
                 const int e = static_cast<int>(m >> 23) - 2;
-                byte = bad ? 0xFFu : static_cast<uint32_t>(e > 0 ? e : 0);
+                byte = static_cast<uint32_t>(e > 0 ? e : 0);
                 const float sinv = __uint_as_float((254u - byte) << 23);
+                const unsigned long long ss = pack2(sinv, sinv);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    f[k] = bad ? 0.0f : __fmul_rn(f[k], sinv);
+                for (int k = 0; k < 8; k += 2)
+                    unpack2(mul2(pack2(f[k], f[k + 1]), ss), f[k], f[k + 1]);
             }
-            const uint32_t packed = f4_pack(f);
-            if (i >= P.octets)
-                return;
-            if (lane % L == 0)
-                P.s[f4_scale_at(row, i / L, P.KT)] = static_cast<uint8_t>(byte);
-            const int32_t left = row < P.M ? P.d - i * 8 : 0;
-            uint8_t *v = P.v + row * (P.d >> 1) + i * 4;
+            uint32_t packed = f4_pack(f);
+            if (m >= 0x7F800000u) { // a NaN or an infinity
+                packed = 0;
+                byte = BLOCK == 16 ? 0x7Fu : 0xFFu;
+            }
+            const int32_t i = first + t * stride;
+            if (lane % L == 0 && i < P.octets)
+                s0[t * (stride / (4 * L)) * 512] = static_cast<uint8_t>(byte);
+            const int32_t left = real ? P.d - i * 8 : 0;
+            uint8_t *v = v0 + t * stride * 4;
             if (VEC) {
                 if (left > 0)
                     *reinterpret_cast<uint32_t *>(v) = packed;
@@ -310,11 +321,11 @@ __global__ void __launch_bounds__(kF4Threads, kF4Ctas<XT>) quantize_fp4_kernel(c
 #pragma unroll
         for (int t = 0; t < kF4Regs; ++t)
             if (t < steps)
-                finish(keep[t], amax[t], first + t * stride);
+                finish(keep[t], amax[t], t);
         for (int t = kF4Regs; t < steps; ++t) {
             F4Octet<XT> o;
-            fetch(o, row, first + t * stride);
-            finish(o, block_max(o), first + t * stride);
+            fetch(o, x, real, t);
+            finish(o, block_max(o), t);
         }
 #pragma unroll
         for (int t = 0; t < kF4Regs; ++t)
