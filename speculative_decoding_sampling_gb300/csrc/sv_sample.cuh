@@ -173,39 +173,59 @@ __device__ __forceinline__ void sm_cluster_sync()
 
 constexpr float kSmShift = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number
 constexpr uint32_t kSmShiftBits = 0x4B400000u;
+constexpr float kSmLn1 = 0.021660849392498290f, kSmLn2 = kSmLn1 * kSmLn1 / 2, kSmLn3 = kSmLn1 * kSmLn1 * kSmLn1 / 6; // ln(2) / 32
 
 // What a row's masses are formed with.
 struct SampleRow {
     float m, c_hi, c_lo, dmin;
-    uint32_t tab; // shared-memory address of the table
-    int up;       // fix - 27
-    // the mass of logit z <= m, in 2^-fix of the maximum's, rounded; 0 for -inf
+    uint32_t tab;  // shared-memory address of the table
+    int down;      // 59 - fix, and the shift's bits beside k's octaves
+    // The masses of two logits z <= m, in 2^-fix of the maximum's, rounded; 0 for -inf.
+    // (Pairs: the arithmetic is packed.)
+    template <bool F32>
+    __device__ __forceinline__ void masses(float z0, float z1, unsigned long long &w0, unsigned long long &w1) const
+    {
+        const unsigned long long z = pack2(z0, z1), mm = pack2(-m, -m);
+        const unsigned long long df = add2(z, mm);
+        float d0, d1, dl0 = 0.0f, dl1 = 0.0f;
+        unpack2(df, d0, d1);
+        if (F32) { // what the differences lost (Knuth's two-sum); nothing of one without mass
+            const float b0 = d0 - z0, b1 = d1 - z1;
+            dl0 = d0 > dmin ? (z0 - (d0 - b0)) + (-m - b0) : 0.0f;
+            dl1 = d1 > dmin ? (z1 - (d1 - b1)) + (-m - b1) : 0.0f;
+        }
+        const unsigned long long d = pack2(fmaxf(d0, dmin), fmaxf(d1, dmin));
+        const unsigned long long t = fma2(d, pack2(c_hi, c_hi), pack2(kSmShift, kSmShift));
+        const unsigned long long k = add2(t, pack2(-kSmShift, -kSmShift));
+        unsigned long long r = fma2(d, pack2(c_hi, c_hi), mul2(k, pack2(-1.0f, -1.0f)));
+        r = fma2(d, pack2(c_lo, c_lo), r);
+        if (F32)
+            r = fma2(pack2(dl0, dl1), pack2(c_hi, c_hi), r);
+        // e^x - 1, x = r ln(2) / 32: x + x^2 / 2 + x^3 / 6
+        unsigned long long p = fma2(r, pack2(kSmLn3, kSmLn3), pack2(kSmLn2, kSmLn2));
+        p = mul2(fma2(r, p, pack2(kSmLn1, kSmLn1)), r);
+        float t0, t1, p0, p1;
+        unpack2(t, t0, t1);
+        unpack2(p, p0, p1);
+        w0 = whole(t0, p0);
+        w1 = whole(t1, p1);
+    }
+    __device__ __forceinline__ unsigned long long whole(float t, float p) const
+    {
+        const uint32_t bits = __float_as_uint(t); // k beside the shift's bits
+        float2 e;
+        asm("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(e.x), "=f"(e.y) : "r"(tab + ((bits & 31u) << 3)));
+        const int s = down - static_cast<int>(bits >> 5); // 59 - fix + octaves below the maximum: 14 or more
+        uint32_t half; // half a unit of the result, where bits are lost (a shift by a negative number gives 0)
+        asm("shl.b32 %0, 1, %1;" : "=r"(half) : "r"(s - 33));
+        const uint32_t E = __float_as_uint(e.y) + __float_as_uint(__fmaf_rn(e.x, p, kSmShift)) + half;
+        return (static_cast<unsigned long long>(E) << 32) >> s;
+    }
     template <bool F32> __device__ __forceinline__ unsigned long long mass(float z) const
     {
-        float d = z - m, dl = 0.0f;
-        if (F32) { // what the difference lost (Knuth's two-sum)
-            const float bb = d - z;
-            dl = (z - (d - bb)) + (-m - bb);
-        }
-        const bool in = d > dmin;
-        d = in ? d : 0.0f;
-        const float t = __fmaf_rn(d, c_hi, kSmShift);
-        const float k = t - kSmShift;
-        float r = __fmaf_rn(d, c_hi, -k);
-        r = __fmaf_rn(d, c_lo, r);
-        if (F32)
-            r = __fmaf_rn(dl, c_hi, r);
-        const float x = __fmul_rn(r, 0.021660849392498290f); // ln(2) / 32
-        const float p = __fmaf_rn(__fmul_rn(x, x), __fmaf_rn(x, 0.16666667f, 0.5f), x);
-        const int kb = static_cast<int>(__float_as_uint(t) - kSmShiftBits); // k, at most 0
-        float2 e;
-        asm("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(e.x), "=f"(e.y) : "r"(tab + ((static_cast<uint32_t>(kb) & 31u) << 3)));
-        const int down = -(kb >> 5);
-        uint32_t half; // half a unit of the result, where bits are lost (a shift by a negative number gives 0)
-        asm("shl.b32 %0, 1, %1;" : "=r"(half) : "r"(down - up - 1));
-        const uint32_t E = __float_as_uint(e.y) + __float_as_uint(__fmaf_rn(e.x, p, kSmShift)) + half;
-        const unsigned long long w = (static_cast<unsigned long long>(E) << up) >> down;
-        return in ? w : 0ull;
+        unsigned long long w0, w1;
+        masses<F32>(z, z, w0, w1);
+        return w0;
     }
 };
 
@@ -493,6 +513,20 @@ template <typename LT> __device__ __forceinline__ float sm_largest(const uint4 &
     }
 }
 
+// ... and its smallest.
+template <typename LT> __device__ __forceinline__ float sm_smallest(const uint4 &w)
+{
+    if constexpr (sizeof(LT) == 2) {
+        uint32_t a, b;
+        asm("min.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w.x), "r"(w.y));
+        asm("min.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w.z), "r"(w.w));
+        asm("min.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+        return fminf(bf16_lo(a), bf16_hi(a));
+    } else {
+        return fminf(fminf(__uint_as_float(w.x), __uint_as_float(w.y)), fminf(__uint_as_float(w.z), __uint_as_float(w.w)));
+    }
+}
+
 // The ids of bins 0 .. last of step 2 in this CTA: listed, or picked out of the slice.
 template <typename LT, int NT> struct SampleSet {
     const SampleSlice<LT> &X;
@@ -770,8 +804,7 @@ __device__ __forceinline__ void sm_write_q(const SampleSlice<LT> &X, const Sampl
     float least = zlo;
     if (CUTS && cut.key)
         least = fmaxf(least, E::value(E::bits_of_key(cut.key)));
-    const float scale = ldexpf(1.0f, P.fix) / static_cast<float>(Z);
-    const float cq = P.cq;
+    const float cq = P.cq, lz = static_cast<float>(P.fix) - __log2f(static_cast<float>(Z)); // log2(2^fix / Z)
     const bool filtered = CUTS || P.min_p;
     for (int32_t v = threadIdx.x; v < X.nv; v += NT) {
         const uint4 w = X.vec(v);
@@ -780,13 +813,13 @@ __device__ __forceinline__ void sm_write_q(const SampleSlice<LT> &X, const Sampl
         if (!filtered) { // (exp2 of -inf is 0)
 #pragma unroll
             for (int j = 0; j < PV; ++j)
-                q[j] = ex2(__fmul_rn(E::value(SampleSlice<LT>::of(w, j)) - R.m, cq)) * scale;
+                q[j] = ex2(__fmaf_rn(E::value(SampleSlice<LT>::of(w, j)) - R.m, cq, lz));
         } else if (sm_largest<LT>(w) >= least) {
 #pragma unroll
             for (int j = 0; j < PV; ++j) {
                 const uint32_t b = SampleSlice<LT>::of(w, j);
                 const bool in = E::finite(b) && E::value(b) >= least && (!CUTS || E::key(b) != cut.key || i + j <= cut.id);
-                q[j] = in ? ex2(__fmul_rn(E::value(b) - R.m, cq)) * scale : 0.0f;
+                q[j] = in ? ex2(__fmaf_rn(E::value(b) - R.m, cq, lz)) : 0.0f;
             }
         } else {
 #pragma unroll
@@ -917,7 +950,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleParam
         sm_cluster_sync(); // no CTA leaves while another may write to it
         return;
     }
-    SampleRow R = {mx, P.c_hi, P.c_lo, P.dmin, smem_addr(S.tab), P.fix - 27};
+    SampleRow R = {mx, P.c_hi, P.c_lo, P.dmin, smem_addr(S.tab), 59 - P.fix + static_cast<int>(kSmShiftBits >> 5)};
     // min-p: the least logit kept (p >= min_p max p, in logits)
     const float zlo = P.min_p ? __double2float_ru(static_cast<double>(mx) + P.min_off) : -INFINITY;
     const bool use_k = P.top_k > 0 && P.top_k < P.V, use_p = P.top_p < 1.0f;
@@ -939,13 +972,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleParam
             for (int32_t v = v0 + lane; v < v1; v += 32) {
                 const uint4 w = X.vec(v);
 #pragma unroll
-                for (int j = 0; j < PV; ++j) {
-                    const float z = E::value(Slice::of(w, j));
-                    if (kMass)
-                        total += R.mass<F32>(z);
-                    const uint32_t b = sm_bin(R, z, P.bins);
-                    if (b < kSmBins)
-                        atomicAdd(&H.first[0][b], 1u);
+                for (int j = 0; j < PV; j += 2) {
+                    const float z0 = E::value(Slice::of(w, j)), z1 = E::value(Slice::of(w, j + 1));
+                    if (kMass) {
+                        unsigned long long e0, e1;
+                        R.masses<F32>(z0, z1, e0, e1);
+                        total += e0 + e1;
+                    }
+                    const uint32_t b0 = sm_bin(R, z0, P.bins), b1 = sm_bin(R, z1, P.bins);
+                    if (b0 < kSmBins)
+                        atomicAdd(&H.first[0][b0], 1u);
+                    if (b1 < kSmBins)
+                        atomicAdd(&H.first[0][b1], 1u);
                 }
             }
         };
@@ -1168,11 +1206,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleParam
         unsigned long long a = 0;
         if (!filtered) {
 #pragma unroll
-            for (int j = 0; j < PV; ++j) {
-                const uint32_t b = Slice::of(w, j);
-                n += E::finite(b) ? 1u : 0u;
-                a += R.mass<F32>(E::value(b));
+            for (int j = 0; j < PV; j += 2) {
+                unsigned long long e0, e1;
+                R.masses<F32>(E::value(Slice::of(w, j)), E::value(Slice::of(w, j + 1)), e0, e1);
+                a += e0 + e1;
             }
+            n += PV;
+            if (sm_smallest<LT>(w) == -INFINITY)
+#pragma unroll 1
+                for (int j = 0; j < PV; ++j)
+                    n -= E::finite(Slice::of(w, j)) ? 0u : 1u;
         } else if (sm_largest<LT>(w) >= least) {
 #pragma unroll 1
             for (int j = 0; j < PV; ++j) {
