@@ -166,6 +166,12 @@ __device__ __forceinline__ void sm_add2(unsigned long long (&m)[2], const void *
         m[1] += static_cast<unsigned long long>(t[k].y) << shift;
     }
 }
+// The last barrier of a CTA: it has no word left to read in another, or for another
+// to write.  Nothing is handed over, so it does not wait for q's stores.
+__device__ __forceinline__ void sm_cluster_leave()
+{
+    asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
+}
 __device__ __forceinline__ void sm_cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
@@ -841,7 +847,7 @@ __device__ __forceinline__ void sm_write_q(const SampleSlice<LT> &X, const Sampl
 
 // CUTS: whether there is a top-k or a top-p.
 template <typename LT, int NT, bool CUTS>
-__global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleParams P)
+__global__ void __launch_bounds__(NT, (CUTS ? 1024 : 1280) / NT) sample_kernel(const SampleParams P)
 {
     using E = FilterElem<LT>;
     using Slice = SampleSlice<LT>;
@@ -947,7 +953,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleParam
         if (qrow)
             for (int32_t i = X.lo + threadIdx.x; i < X.hi; i += NT)
                 qrow[i] = 0.0f;
-        sm_cluster_sync(); // no CTA leaves while another may write to it
+        sm_cluster_leave();
         return;
     }
     SampleRow R = {mx, P.c_hi, P.c_lo, P.dmin, smem_addr(S.tab), 59 - P.fix + static_cast<int>(kSmShiftBits >> 5)};
@@ -1096,7 +1102,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleParam
                 }
             }
             sm_write_q<LT, NT, true>(X, R, P, qrow, zlo, cut, Z);
-            sm_cluster_sync(); // no CTA leaves while another may read it
+            sm_cluster_leave();
             return;
         }
         // the list
@@ -1329,7 +1335,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleParam
     }
     // 5. q
     sm_write_q<LT, NT, CUTS>(X, R, P, qrow, zlo, cut, Z);
-    sm_cluster_sync(); // no CTA leaves while another may read it
+    sm_cluster_leave();
 }
 
 } // namespace sv
