@@ -989,7 +989,7 @@ template <typename LT, int NT, bool CUTS>
 cudaError_t sample_launch_as(const sv::SampleParams &P, size_t smem, cudaStream_t stream)
 {
     const auto kernel = sv::sample_kernel<LT, NT, CUTS>;
-    if (smem + sizeof(sv::SampleShared) > 48 * 1024) {
+    if (smem > 40 * 1024) { // (48 KiB without it, the kernel's own structures among them)
         const cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSampleSmem));
         if (e != cudaSuccess)
@@ -1611,8 +1611,8 @@ sv_status_t sv_sample_logits(const void *logits, sv_dtype_t logits_dtype, const 
     P.c_lo = static_cast<float>(c - static_cast<double>(P.c_hi));
     P.cq = static_cast<float>(c / 32);
     P.dmin = static_cast<float>(-48 * 32 / c);
-    // 24 octaves of mass, and 12 of logits at least where top-k counts ids without mass
-    const double low = top_k > 0 ? 12.0 : 0.0, octaves = 24 * 32 / c, range = octaves > low ? octaves : low;
+    // 24 octaves of mass, and 16 of logits at least where top-k counts ids without mass
+    const double low = top_k > 0 ? 16.0 : 0.0, octaves = 24 * 32 / c, range = octaves > low ? octaves : low;
     P.bins = static_cast<float>(sv::kSmBins / range);
     P.width = static_cast<float>(range / sv::kSmBins);
     // (a temperature so far from 1 that its factors leave the fp32 range)
@@ -1651,17 +1651,22 @@ sv_status_t sv_sample_logits(const void *logits, sv_dtype_t logits_dtype, const 
     // SM, down to 2048 ids a CTA.
     const int32_t es = static_cast<int32_t>(elem_size(logits_dtype)), pv = 16 / es;
     const bool cuts = (top_k > 0 && top_k < V) || top_p < 1.0f;
-    const size_t more = cuts ? sizeof(sv::SampleBins) : 0;
+    // a large batch's CTAs have 256 threads, four of them (five without cuts) an SM
+    const size_t bins = cuts ? sizeof(sv::SampleBins) : 0, slim = 1152 * sizeof(uint16_t), wide = 4096 * sizeof(uint16_t);
+    constexpr size_t kQuarter = 227 * 1024 / 4 - sizeof(sv::SampleShared) - 1024 - 256;
     auto cut = [&](int32_t C) {
         P.C = C;
         P.slice = static_cast<int32_t>(ceil_div(ceil_div(static_cast<int64_t>(V) + pv, C), pv) * pv);
-        return static_cast<size_t>(P.slice) * static_cast<size_t>(es) + more;
+        return static_cast<size_t>(P.slice) * static_cast<size_t>(es) + bins + (cuts ? slim : 0);
     };
     int32_t C = 1;
-    while (C < sv::kSmMaxCtas && (cut(C) > 55 * 1024 || (rows * C * 2 <= 2 * kNominalSms && V / (2 * C) >= 2048)))
+    while (C < sv::kSmMaxCtas && (cut(C) > kQuarter || (rows * C * 2 <= 2 * kNominalSms && V / (2 * C) >= 2048)))
         C *= 2;
     size_t smem = cut(C);
-    const int threads = rows * C > 2 * kNominalSms && smem <= 55 * 1024 ? 256 : 512;
+    const int threads = rows * C > 2 * kNominalSms && smem <= kQuarter ? 256 : 512;
+    P.cap = threads == 256 ? 1152 : 4096;
+    const size_t more = bins + (cuts ? (threads == 256 ? slim : wide) : 0);
+    smem = static_cast<size_t>(P.slice) * static_cast<size_t>(es) + more;
     P.staged = smem <= kSampleSmem;
     if (!P.staged)
         smem = more;

@@ -21,15 +21,18 @@
 // exchange through distributed shared memory; a step ends with a cluster barrier.
 //  1. load, maximum;
 //  2. top-k, top-p: the ids are counted in 512 bins from the maximum down (24
-//     octaves of mass, and 12 of logits at least for top-k); where top-p refers to
+//     octaves of mass, and 16 of logits at least for top-k); where top-p refers to
 //     the whole row its mass is formed in the same pass.  A scan finds top-k's bin;
 //     for top-p the counts and the bins' edges bound the running mass to 3.3 % and
 //     so the bins that its cut may lie in.  The ids down to the last of these bins
-//     are listed (up to 2048 a CTA; more are picked out of the slice each time), and
+//     are listed (up to 1152 or 4096 a CTA; more are picked out of the slice each time), and
 //     nothing below them is looked at again;
 //  3. up to 256 listed ids are gathered by every CTA and ranked, which settles the
-//     row.  Of more, those of top-k's bin are; then masses are binned (four
-//     shared-memory additions an id) and the ids of top-p's bin gathered.  A bin of
+//     row.  Up to 1024 go, in a large batch, to the cluster's first CTA, which settles
+//     the row alone as all would together: the ids of top-k's bin are ranked; then masses are
+//     binned (four shared-memory additions an id) and the ids of top-p's bin ranked;
+//     the draw finds its run of ids by such bins too.  (Of more, the ranked ones are
+//     gathered by every CTA.)  A bin of
 //     more than 256 is counted again digit by digit of the order key (512 bins a
 //     digit) down to one value, as is all below the bins when a cut lies there;
 //     among ids of one value the j-th in id order is found by an ordered count;
@@ -61,6 +64,7 @@ struct SampleParams {
     int32_t min_p;       // whether min_off counts
     int32_t C;           // CTAs of a cluster
     int32_t slice;       // ids of a CTA, a multiple of 16 bytes of them
+    int32_t cap;         // ids a CTA lists (at least kSmOne)
     int32_t staged;      // the slices fit in shared memory
     int32_t fix;         // fractional bits of the masses (at most 45, sums of a row below 2^62)
     int32_t piece;       // bits of a mass that a bin adds up in one 32-bit word
@@ -74,7 +78,7 @@ struct SampleParams {
 
 constexpr int kSmFew = 256;    // ids gathered and ranked
 constexpr int kSmBins = 512;   // bins of steps 2 and 3
-constexpr int kSmList = 2048;  // ids a CTA lists
+constexpr int kSmOne = 1024;   // ids that one CTA settles
 
 // A cut: ids with a larger key, and of those with this key the ones up to `id`.
 struct SampleCutAt {
@@ -95,12 +99,18 @@ struct SampleShared {
 // What top-k and top-p need besides, behind the slice.
 struct SampleBins {
     uint32_t first[4][kSmBins];                      // counts, masses in three pieces
-    uint2 few[2][kSmFew];                            // this CTA's gathered (key, id): for top-k, for top-p
+    union {
+        uint2 few[2][kSmFew];                        // this CTA's gathered (key, id): for top-k, for top-p
+        uint2 ent[kSmOne];                           // every CTA's listed ones, in the first CTA
+    };
     uint2 all[kSmFew];                               // every CTA's
     unsigned long long mass[kSmFew];                 // and their masses
-    uint16_t list[kSmList];                          // positions in the slice, in no order
-    uint32_t nlist;
+    uint32_t nlist, nent, base;
     uint32_t nfew[2];
+    // what the first CTA found: whether it did, the cut, the kept mass
+    int settled;
+    SampleCutAt rcut;
+    unsigned long long rmass;
     unsigned long long smass[kSmMaxWarps];           // scan of the bins
     uint32_t scnt[kSmMaxWarps];
     // where a target was found: bin (or -1), and what lies before and in it
@@ -110,6 +120,7 @@ struct SampleBins {
     int32_t nth;
     SampleCutAt cut;
     unsigned long long upto;
+    uint16_t list[1];                                // (P.cap) positions in the slice, in no order
 };
 
 __device__ __forceinline__ uint32_t sm_peer(const void *p, uint32_t rank)
@@ -734,6 +745,149 @@ __device__ SampleFound sm_narrow(const SampleSlice<LT> &X, const SampleRow &R, u
     return f;
 }
 
+// An entry's place in S.all, with its mass.
+__device__ __forceinline__ void sm_keep(SampleBins &S, uint2 e, unsigned long long w)
+{
+    const uint32_t at = atomicAdd(&S.nfew[0], 1u);
+    if (at < kSmFew) { // (the bin's count bounds it)
+        S.all[at] = e;
+        S.mass[at] = w;
+    }
+}
+
+// The first CTA settles a row from the n (key, id) in S.ent, the ids of bins 0 .. b1:
+// the cuts (top-k's among the kties ids of bin b1, at the kleft-th; top-p's in bins
+// b0 .. b1), the token, its probability, how many are kept.  False where a bin
+// holds more ids than are ranked; nothing has been written then.
+template <typename LT, int NT>
+__device__ bool sm_settle_row(const SampleParams &P, const SampleRow &R, SampleShared &Sh, SampleBins &S, uint32_t n, uint32_t b0,
+                              uint32_t b1, uint32_t kties, unsigned long long kleft, unsigned long long total, float zlo,
+                              float u, int64_t r, SampleCutAt &cut, unsigned long long &Z)
+{
+    using E = FilterElem<LT>;
+    constexpr bool F32 = sizeof(LT) == 4;
+    constexpr int N = kSmBins / NT;
+    const bool use_k = P.top_k > 0 && P.top_k < P.V, use_p = P.top_p < 1.0f;
+    auto value = [&](uint2 e) { return E::value(E::bits_of_key(e.x)); };
+    auto within = [](uint2 e, SampleCutAt c) { return e.x > c.key || (e.x == c.key && static_cast<int32_t>(e.y) <= c.id); };
+    cut = {0u, 0x7FFFFFFF};
+    auto rank_all = [&](auto by_mass, uint32_t m, unsigned long long target) { // the cut among S.all's m
+        constexpr bool MASS = decltype(by_mass)::value;
+        __syncthreads();
+        if (threadIdx.x < m) {
+            const uint2 me = S.all[threadIdx.x];
+            uint32_t before;
+            unsigned long long mass;
+            sm_rank(S, m, me, before, mass);
+            const unsigned long long w = S.mass[threadIdx.x], b = MASS ? mass : before, here = MASS ? w : 1;
+            if (b < target && target <= b + here)
+                S.cut = {me.x, static_cast<int32_t>(me.y)};
+        }
+        if (threadIdx.x == 0)
+            S.nfew[0] = 0u;
+        __syncthreads();
+        cut = S.cut;
+    };
+    if (use_k) {
+        if (kties > kSmFew)
+            return false;
+        for (uint32_t i = threadIdx.x; i < n; i += NT) {
+            const uint2 e = S.ent[i];
+            if (sm_bin(R, value(e), P.bins) == b1)
+                sm_keep(S, e, 0ull);
+        }
+        rank_all(std::false_type{}, kties, kleft);
+    }
+    uint32_t cnt[N], cnt_all;
+    unsigned long long mass[N], mass_all;
+    if (use_p) {
+        sm_clear<NT>(S);
+        unsigned long long above = 0;
+        uint32_t none = 0;
+        for (uint32_t i = threadIdx.x; i < n; i += NT) {
+            const uint2 e = S.ent[i];
+            if (!within(e, cut))
+                continue;
+            const float z = value(e);
+            const unsigned long long w = R.mass<F32>(z);
+            const uint32_t b = sm_bin(R, z, P.bins);
+            if (b < b0)
+                above += w;
+            else
+                sm_add_mass(S, b, w, P.piece);
+        }
+        sm_block_sum<NT>(Sh, above, none);
+        sm_counts_here(S, cnt);
+        sm_masses_here(S, P.piece, mass);
+        if (use_k) {
+            sm_scan<true, NT>(S, cnt, mass, 1, cnt_all, mass_all);
+            total = mass_all;
+        }
+        const double x = ceil(static_cast<double>(P.top_p) * static_cast<double>(total));
+        const unsigned long long target = static_cast<unsigned long long>(x < 1.0 ? 1.0 : x);
+        const unsigned long long left = target > above ? target - above : 1;
+        sm_scan<true, NT>(S, cnt, mass, left, cnt_all, mass_all);
+        const uint32_t bin = static_cast<uint32_t>(S.bin), ties = S.bcnt_at;
+        const unsigned long long before = S.bmass_before;
+        if (S.bin < 0 || ties > kSmFew)
+            return false;
+        for (uint32_t i = threadIdx.x; i < n; i += NT) {
+            const uint2 e = S.ent[i];
+            const float z = value(e);
+            if (sm_bin(R, z, P.bins) == bin && within(e, cut))
+                sm_keep(S, e, R.mass<F32>(z));
+        }
+        rank_all(std::true_type{}, ties, left - before);
+    }
+    // the kept masses by runs of ids
+    const uint32_t run = (static_cast<uint32_t>(P.V) + kSmBins - 1) / kSmBins;
+    sm_clear<NT>(S);
+    Z = 0;
+    uint32_t kept = 0;
+    for (uint32_t i = threadIdx.x; i < n; i += NT) {
+        const uint2 e = S.ent[i];
+        const float z = value(e);
+        if (!within(e, cut) || z < zlo)
+            continue;
+        const unsigned long long w = R.mass<F32>(z);
+        Z += w;
+        ++kept;
+        sm_add_mass(S, e.y / run, w, P.piece);
+    }
+    sm_block_sum<NT>(Sh, Z, kept);
+    sm_counts_here(S, cnt);
+    sm_masses_here(S, P.piece, mass);
+    const bool good = u >= 0.0f && u < 1.0f;
+    const unsigned long long t = static_cast<unsigned long long>(mul_floor(good ? u : 0.0f, static_cast<long long>(Z)));
+    sm_scan<true, NT>(S, cnt, mass, t + 1, cnt_all, mass_all);
+    const uint32_t at = static_cast<uint32_t>(S.bin), m = S.bcnt_at;
+    const unsigned long long before = S.bmass_before;
+    if (m > kSmFew)
+        return false;
+    for (uint32_t i = threadIdx.x; i < n; i += NT) {
+        const uint2 e = S.ent[i];
+        const float z = value(e);
+        if (e.y / run == at && within(e, cut) && z >= zlo)
+            sm_keep(S, e, R.mass<F32>(z));
+    }
+    __syncthreads();
+    if (threadIdx.x < m && good) {
+        const uint2 me = S.all[threadIdx.x];
+        unsigned long long upto = before;
+        for (uint32_t i = 0; i < m; ++i)
+            upto += S.all[i].y <= me.y ? S.mass[i] : 0ull;
+        const unsigned long long w = S.mass[threadIdx.x];
+        if (t < upto && t >= upto - w) {
+            P.tokens[r] = static_cast<int32_t>(me.y);
+            if (P.prob)
+                P.prob[r] = static_cast<float>(static_cast<double>(w) / static_cast<double>(Z));
+        }
+    }
+    if (threadIdx.x == 0 && P.kept)
+        P.kept[r] = static_cast<int32_t>(kept);
+    return true;
+}
+
 // A found cut as every CTA compares with it: (key, id).
 template <typename LT>
 __device__ SampleCutAt sm_settle(const SampleSlice<LT> &X, const SampleFound &f, int32_t v0, int32_t v1, SampleBins &S)
@@ -869,7 +1023,7 @@ __global__ void __launch_bounds__(NT, (CUTS ? 1024 : 1280) / NT) sample_kernel(c
         if (threadIdx.x < 2)
             H.nfew[threadIdx.x] = 0u;
         if (threadIdx.x == 0)
-            H.nlist = 0u;
+            H.nlist = H.nent = 0u;
     }
     pdl_wait_primary();
     pdl_launch_dependents();
@@ -1117,13 +1271,53 @@ __global__ void __launch_bounds__(NT, (CUTS ? 1024 : 1280) / NT) sample_kernel(c
                     h |= sm_bin(R, E::value(Slice::of(w, j)), P.bins) <= b1 ? 1u << j : 0u;
                 uint32_t at = atomicAdd(&H.nlist, static_cast<uint32_t>(__popc(h)));
                 for (; h; h &= h - 1, ++at)
-                    if (at < kSmList)
+                    if (at < static_cast<uint32_t>(P.cap))
                         H.list[at] = static_cast<uint16_t>(v * PV + __ffs(h) - 1);
             }
             __syncthreads();
-            if (H.nlist <= kSmList) {
+            if (H.nlist <= static_cast<uint32_t>(P.cap)) {
                 Set.list = H.list;
                 Set.n = H.nlist;
+            }
+        }
+        // (clusters of a large batch work at the same time, and one CTA's work leaves the
+        // SMs to them: 190 -> 154 us for 256 rows of 128256; 8 rows are settled sooner by all
+        // CTAs together, 31 against 38 us)
+        if (NT == 256 && Set.list && !deep && down_to_b1 <= kSmOne) {
+            if (threadIdx.x == 0) {
+                uint32_t base;
+                asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
+                             : "=r"(base)
+                             : "r"(sm_peer(&H.nent, 0)), "r"(Set.n)
+                             : "memory");
+                H.base = base;
+            }
+            __syncthreads();
+            const uint32_t base = H.base, to = sm_peer(&H.ent[0], 0);
+            for (uint32_t i = threadIdx.x; i < Set.n; i += NT)
+                asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(to + (base + i) * 8u), "r"(E::key(Set.bits(i))),
+                             "r"(static_cast<uint32_t>(Set.id(i)))
+                             : "memory");
+            sm_cluster_sync();
+            if (rank == 0) {
+                unsigned long long Z = 0;
+                SampleCutAt found;
+                const bool done = sm_settle_row<LT, NT>(P, R, S, H, down_to_b1, b0, b1, kties, kleft, total, zlo, u, r, found, Z);
+                __syncthreads();
+                if (threadIdx.x < C) {
+                    sm_put(&H.rcut.key, threadIdx.x, found.key);
+                    sm_put(&H.rcut.id, threadIdx.x, static_cast<uint32_t>(found.id));
+                    sm_put(&H.rmass, threadIdx.x, Z);
+                    sm_put(&H.settled, threadIdx.x, done ? 1u : 0u);
+                }
+                if (threadIdx.x == 0)
+                    H.nfew[0] = 0u;
+            }
+            sm_cluster_sync();
+            if (H.settled) {
+                sm_write_q<LT, NT, true>(X, R, P, qrow, zlo, H.rcut, H.rmass);
+                sm_cluster_leave();
+                return;
             }
         }
         // the cut of a target inside a bin of `ties` ids
