@@ -798,7 +798,9 @@ bool lm4_scale_map(CUtensorMap *map, const void *base, int64_t tiles, uint32_t b
 // SMs.
 struct Lm4Plan {
     bool pair;
-    int32_t MT, NT, NB;
+    int32_t H;          // row tiles that share a pair's tile of W
+    int32_t RT, MT;     // row tiles, groups of H of them
+    int32_t NT, NB;
 };
 
 Lm4Plan lm4_plan(int64_t M, int32_t V)
@@ -806,25 +808,30 @@ Lm4Plan lm4_plan(int64_t M, int32_t V)
     Lm4Plan p = {};
     const int64_t rows = M < sv::kLmBM ? M : sv::kLmBM;
     int64_t best = INT64_MAX;
-    for (int pair = M > sv::kLmBM ? 1 : 0; pair >= 0; --pair) {
+    for (int shape = M > 2 * sv::kLmBM ? 2 : (M > sv::kLmBM ? 1 : 0); shape >= 0; --shape) { // H 2, pair, lone CTA
+        const bool pair = shape > 0;
+        const int32_t H = shape == 2 ? 2 : 1;
         const int64_t units = pair ? kNominalSms / 2 : kNominalSms;
-        const int32_t mt = static_cast<int32_t>(ceil_div(M > 0 ? M : 1, pair ? 2 * sv::kLmBM : sv::kLmBM));
+        const int32_t rt = static_cast<int32_t>(ceil_div(M > 0 ? M : 1, pair ? 2 * sv::kLmBM : sv::kLmBM));
+        const int32_t mt = static_cast<int32_t>(ceil_div(rt, H));
         int64_t low = INT64_MAX;
         int32_t NB = 0;
         for (int32_t nb = sv::kL4MaxNB; nb >= 64; nb -= 64) {
-            const int64_t w = 144 * (pair ? nb / 2 : nb), loads = (144 * rows + w) / 45;
+            const int64_t w = 144 * (pair ? nb / 2 : nb), loads = (H * 144 * rows + w) / 45;
             int64_t stage = mt == 1 ? w / 23 : 0;
             stage = stage > loads ? stage : loads;
-            stage = stage > 2 * nb ? stage : 2 * nb;
+            stage = stage > 2 * nb * H ? stage : 2 * nb * H;
             const int64_t cost = ceil_div(mt * ceil_div(V, nb), units) * (stage + 40);
             if (cost <= low) {
                 low = cost;
                 NB = nb;
             }
         }
-        if (low < best) { // a pair on ties
+        if (low < best) { // two row tiles, then a pair, on ties
             best = low;
-            p.pair = pair != 0;
+            p.pair = pair;
+            p.H = H;
+            p.RT = rt;
             p.MT = mt;
             p.NB = NB;
         }
@@ -833,7 +840,7 @@ Lm4Plan lm4_plan(int64_t M, int32_t V)
     return p;
 }
 
-template <bool PAIR, int BLOCK> cudaError_t lm4_units(int &units)
+template <bool PAIR, int H, int BLOCK> cudaError_t lm4_units(int &units)
 {
     struct Entry {
         int units;
@@ -850,7 +857,7 @@ template <bool PAIR, int BLOCK> cudaError_t lm4_units(int &units)
     const unsigned long long ctx = current_context_id();
     std::lock_guard<std::mutex> lock(mu);
     if (cache[dev].units == 0 || cache[dev].ctx == 0 || cache[dev].ctx != ctx) {
-        const auto kernel = sv::lm_head_fp4_kernel<PAIR, BLOCK>;
+        const auto kernel = sv::lm_head_fp4_kernel<PAIR, H, BLOCK>;
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sv::kL4Smem);
         if (e != cudaSuccess)
             return e;
@@ -884,11 +891,11 @@ template <bool PAIR, int BLOCK> cudaError_t lm4_units(int &units)
     return cudaSuccess;
 }
 
-template <bool PAIR, int BLOCK>
+template <bool PAIR, int H, int BLOCK>
 cudaError_t lm4_launch_as(const CUtensorMap (&m)[5], const sv::Lm4Params &L, cudaStream_t stream)
 {
     int units = 0;
-    const cudaError_t e = lm4_units<PAIR, BLOCK>(units);
+    const cudaError_t e = lm4_units<PAIR, H, BLOCK>(units);
     if (e != cudaSuccess)
         return e;
     const int64_t tiles = static_cast<int64_t>(L.t.MT) * L.t.NT; // below 2^31 (sv_lm_head_logits_fp4)
@@ -907,7 +914,15 @@ cudaError_t lm4_launch_as(const CUtensorMap (&m)[5], const sv::Lm4Params &L, cud
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, sv::lm_head_fp4_kernel<PAIR, BLOCK>, m[0], m[1], m[2], m[3], m[4], L);
+    return cudaLaunchKernelEx(&cfg, sv::lm_head_fp4_kernel<PAIR, H, BLOCK>, m[0], m[1], m[2], m[3], m[4], L);
+}
+
+template <int BLOCK>
+cudaError_t lm4_launch_shape(const Lm4Plan &p, const CUtensorMap (&m)[5], const sv::Lm4Params &L, cudaStream_t stream)
+{
+    if (!p.pair)
+        return lm4_launch_as<false, 1, BLOCK>(m, L, stream);
+    return p.H == 2 ? lm4_launch_as<true, 2, BLOCK>(m, L, stream) : lm4_launch_as<true, 1, BLOCK>(m, L, stream);
 }
 
 cudaError_t lm4_launch(const void *hidden, const void *hidden_scales, const float *gh, const void *lm_head,
@@ -923,11 +938,14 @@ cudaError_t lm4_launch(const void *hidden, const void *hidden_scales, const floa
     L.KT = fp4_tiles(d, block);
     const int32_t per_stage = sv::kL4BK / (4 * block); // scale tiles
     L.blocks = p.NB > 128 ? 2 : 1;
-    L.t.stage_bytes = static_cast<int32_t>((L.t.a_rows + brows) * 128 + per_stage * 512 * (1 + L.blocks));
+    L.t.stage_bytes = static_cast<int32_t>((p.H * L.t.a_rows + brows) * 128 + per_stage * 512 * (p.H + L.blocks));
     L.t.stage_bytes = (L.t.stage_bytes + 1023) / 1024 * 1024;
     L.t.stages = sv::kL4RingBytes / L.t.stage_bytes;
     if (L.t.stages > sv::kL4MaxStages)
         L.t.stages = sv::kL4MaxStages;
+    // (the last stage's first rows and what the MMA reads behind them lie in the ring)
+    while ((L.t.stages - 1) * L.t.stage_bytes + (p.H - 1) * L.t.a_rows * 128 + sv::kLmBM * 128 > sv::kL4RingBytes)
+        --L.t.stages;
     CUtensorMap m[5] = {};
     if (!lm_tensor_map(&m[0], hidden, M, d / 2, static_cast<uint32_t>(L.t.a_rows), true) ||
         !lm_tensor_map(&m[1], lm_head, V, d / 2, static_cast<uint32_t>(brows), true) ||
@@ -939,6 +957,7 @@ cudaError_t lm4_launch(const void *hidden, const void *hidden_scales, const floa
     L.t.KB = static_cast<int32_t>(ceil_div(d, sv::kL4BK));
     L.t.mt_inv = p.MT > 1 ? UINT64_MAX / static_cast<uint64_t>(p.MT) + 1 : 0;
     L.t.MT = p.MT;
+    L.RT = p.RT;
     L.t.NT = p.NT;
     L.t.NB = p.NB;
     L.t.logits = static_cast<uint16_t *>(logits);
@@ -950,9 +969,7 @@ cudaError_t lm4_launch(const void *hidden, const void *hidden_scales, const floa
     L.idesc = sv::l4_idesc(p.pair ? 2 * sv::kLmBM : sv::kLmBM, p.NB, block);
     L.gh = gh;
     L.gw = gw;
-    if (block == 16)
-        return p.pair ? lm4_launch_as<true, 16>(m, L, stream) : lm4_launch_as<false, 16>(m, L, stream);
-    return p.pair ? lm4_launch_as<true, 32>(m, L, stream) : lm4_launch_as<false, 32>(m, L, stream);
+    return block == 16 ? lm4_launch_shape<16>(p, m, L, stream) : lm4_launch_shape<32>(p, m, L, stream);
 }
 
 // Warps of a row of `octets` octets: as many as it takes for each lane to keep

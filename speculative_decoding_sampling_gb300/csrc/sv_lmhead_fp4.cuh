@@ -11,7 +11,11 @@
 // Two shapes of one kernel, as for e4m3.  PAIR false (M <= 128): a CTA per SM,
 // tiles of 128 rows x NB ids; W streams through.  PAIR true: a cluster of two
 // CTAs on a pair of SMs, tiles of 256 rows x NB ids, each CTA loading its 128
-// rows of h and half of the tile of W.  Tiles are walked rows fastest.
+// rows of h and half of the tile of W.  What bounds many rows is what the SMs take
+// from L2 (about 83 bytes a nanosecond each, all of them at once; with three
+// quarters of the MMAs left out the kernel was 13 % faster): where it pays, a pair
+// forms two such tiles of rows at a time from one tile of W, one in each accumulator
+// (H 2).  Tiles are walked rows fastest.
 //
 // Warp 0 loads: a stage is 256 hidden dims, one 128-byte swizzle row of 4-bit
 // values, with the 512-byte scale tiles that belong to it (both CTAs of a pair
@@ -22,7 +26,8 @@
 // Warps 2..9 are the epilogue, two for each 32 rows: two accumulators, so that a
 // tile is read, scaled and stored (through shared memory, as for e4m3) while the next is formed.
 // 512 tensor-memory columns: 2 x 192 of sums, 2 x 64 of scales, hence NB <= 192.
-// Ids start at a multiple of 64 of their scale tile: two columns.
+// (A set: 16 columns for each row tile, 32 for the ids.)  Ids start at a multiple of
+// 64 of their scale tile: two columns.
 // Every wait is bounded (l8_wait), with lm_head_kernel's teardown.
 #pragma once
 
@@ -37,19 +42,18 @@ constexpr int kL4Threads = 64 + 32 * kL4EpiWarps;
 constexpr int kL4MaxStages = 8;
 constexpr uint32_t kL4TmemCols = 512;
 constexpr uint32_t kL4ScaleCol = 2 * kL4MaxNB; // first of 2 x 64 scale columns
-constexpr int kL4StgBytes = kL4MaxNB / 64 * kL8BoxBytes; // an epilogue warp's 32 rows of half a tile
-constexpr int kL4RingBytes = 172 * 1024;
-// l8_store_rows reads 4 boxes whatever a warp has (what lies past its ids is not
-// used): the last warp's end past its boxes, in the ids' factors.
-constexpr int kL4Behind = kL4EpiWarps * kL4MaxNB / 2 * 4;
-static_assert(4 * kL8BoxBytes <= kL4StgBytes + kL4Behind, "staged rows read behind the boxes");
-constexpr int kL4Smem = 1024 + kL4RingBytes + kL4EpiWarps * kL4StgBytes + kL4Behind;
-static_assert(kL4Smem <= 227 * 1024 - 512, "shared memory of a CTA, less the barriers");
-// the MMA's 128 rows may run past the rows a stage has: never past the memory
-static_assert(kL4EpiWarps * kL4StgBytes >= kLmBM * 128, "rows read behind the ring");
+// Shared memory: a box of 32 rows x 32 logits and 32 factors for each epilogue warp,
+// then the ring, behind whose last stage lm4_launch leaves what the MMA reads of its
+// 128 rows where a stage has fewer.
+constexpr int kL4StgBytes = kL8BoxBytes;
+constexpr int kL4Front = kL4EpiWarps * (kL4StgBytes + 128);
+constexpr int kL4RingBytes = 208 * 1024;
+constexpr int kL4Smem = 1024 + kL4Front + kL4RingBytes;
+static_assert(kL4Front % 1024 == 0 && kL4Smem <= 227 * 1024 - 512, "shared memory of a CTA, less the barriers");
 
 struct Lm4Params {
-    Lm8Params t;              // M, N, tiles, logits, status (its own scales and sums unused)
+    Lm8Params t;              // M, N, tiles (MT: groups of row tiles), logits, status (its own scales and sums unused)
+    int32_t RT;               // row tiles
     int32_t d;                // hidden dims
     int32_t KT;               // scale tiles along d
     int32_t blocks;           // scale tiles across a tile's ids: 1 or 2
@@ -118,35 +122,73 @@ __device__ __forceinline__ float4 l4_lds4(uint32_t addr)
 // x, NaN if it is infinite: -inf is a masked token to what reads the logits.
 __device__ __forceinline__ float l4_finite(float x) { return __fmaf_rn(x, 0.0f, x); }
 
+// A staged box (ncols <= 32 ids of rows row0 ..) by plain stores, at whatever
+// alignment its rows have: their whole 16-byte units, 4 lanes a row, each shifted
+// out of two staged units; then the logits before the first and behind the last
+// unit (8 a row, or up to 14 where the vocabulary ends), 8 lanes a row.
+__device__ __forceinline__ void l4_store_box(const Lm8Params &T, uint32_t box, int row0, int n, int ncols, int lane)
+{
+    const int rows = T.M - row0 < 32 ? T.M - row0 : 32;
+    uint16_t *const dst0 = T.logits + static_cast<int64_t>(row0) * T.N + n;
+    auto columns_before_unit = [&](const uint16_t *dst) {
+        return (8 - static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 1)) & 7;
+    };
+    const int u = (lane & 3) * 8;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int r = it * 8 + (lane >> 2);
+        const uint4 lo = l8_staged4(l8_staged_at(box, r, u)), hi = l8_staged4(l8_staged_at(box, r, u < 24 ? u + 8 : u));
+        uint16_t *dst = dst0 + static_cast<int64_t>(r) * T.N;
+        const int lead = columns_before_unit(dst);
+        if (r < rows && u + lead + 8 <= ncols)
+            *reinterpret_cast<uint4 *>(dst + u + lead) = l8_shift(lo, hi, lead);
+    }
+    const int c = lane & 7;
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+        const int r = it * 4 + (lane >> 3);
+        uint16_t *dst = dst0 + static_cast<int64_t>(r) * T.N;
+        const int lead = columns_before_unit(dst);
+        const int units = ncols > lead ? (ncols - lead) >> 3 : 0, edges = ncols - units * 8, first = lead < ncols ? lead : ncols;
+        if (r < rows && c < edges) {
+            const int p = c < first ? c : units * 8 + c;
+            dst[p] = l8_staged1(l8_staged_at(box, r, p));
+        }
+        if (r < rows && c + 8 < edges) {
+            const int p = c + 8 < first ? c + 8 : units * 8 + c + 8;
+            dst[p] = l8_staged1(l8_staged_at(box, r, p));
+        }
+    }
+}
+
 // The epilogue warps: warp w holds the tile's rows of tensor-memory lane quarter
 // w mod 4, and the first or the second half of its ids.
-template <bool PAIR>
-__device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMap *map, uint32_t stg0, uint32_t gws0,
-                                            uint32_t tbase, uint32_t tfull, uint32_t tempty, int *stop, uint32_t rank,
-                                            uint32_t unit, uint32_t units, uint32_t ntiles)
+template <bool PAIR, int H>
+__device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMap *map, uint32_t stg0, uint32_t tbase,
+                                            uint32_t tfull, uint32_t tempty, int *stop, uint32_t rank, uint32_t unit,
+                                            uint32_t units, uint32_t ntiles)
 {
     const Lm8Params &T = P.t;
     const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31u), lq = warp & 3;
     const int half = (warp - 2) >> 2, G = T.NB / 64; // groups of 32 ids: 1, 2 or 3
     const uint32_t stg = stg0 + static_cast<uint32_t>(warp - 2) * kL4StgBytes;
-    const uint32_t gws = gws0 + static_cast<uint32_t>(warp - 2) * (kL4MaxNB / 2 * 4);
+    const uint32_t gws = stg0 + kL4EpiWarps * kL4StgBytes + static_cast<uint32_t>(warp - 2) * 128u;
     const uint32_t te = PAIR ? lm_mapa(tempty, 0) : tempty;
-    bool alive = true;
-    uint32_t i = 0;
-    for (uint32_t t = unit; t < ntiles; t += units, ++i) {
+    bool alive = true, sent = false;
+    uint32_t i = 0; // row tiles so far: accumulator i mod 2
+    uint32_t t = unit, sub = 0;
+    for (; t < ntiles; ++i) {
         const uint32_t a = i & 1u;
-        const int row0 = l8_row0<PAIR>(T, t, rank, lq);
+        const uint32_t m = l8_tile_m(T, t) * H + sub; // row tile
+        const int row0 = static_cast<int>((m * (PAIR ? 2u : 1u) + rank) * kLmBM) + lq * 32;
         const int n0 = static_cast<int>(l8_tile_n(T, t)) * T.NB + half * G * 32;
         // the rows' and ids' factors, while the tile is formed
-        float gh = 1.0f;
+        float gh = 1.0f, gw[kL4MaxNB / 64];
         if (P.gh) {
             gh = row0 + lane < T.M ? __ldg(P.gh + row0 + lane) : 0.0f;
-            __syncwarp();
-            for (int c = lane; c < G * 32; c += 32) {
-                const float g = n0 + c < T.N ? __ldg(P.gw + n0 + c) : 0.0f;
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(gws + static_cast<uint32_t>(c) * 4u), "f"(g) : "memory");
-            }
-            __syncwarp();
+#pragma unroll
+            for (int g = 0; g < kL4MaxNB / 64; ++g)
+                gw[g] = g < G && n0 + 32 * g + lane < T.N ? __ldg(P.gw + n0 + 32 * g + lane) : 0.0f;
         }
         alive = __all_sync(0xFFFFFFFFu, l8_wait(tfull + a * 8u, (i >> 1) & 1u));
         if (!alive)
@@ -157,22 +199,30 @@ __device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMa
         uint32_t v[2][32]; // the next group is on its way while one is scaled
         if (in)
             l8_ld_start(tl, v[0]);
-        if (T.tma && i > 0) // the last tile's stores have read this warp's shared memory
-            l8_stores_read();
-        __syncwarp();
 #pragma unroll
         for (int g = 0; g < kL4MaxNB / 64; ++g) {
             if (in && g < G) {
                 uint32_t(&x)[32] = v[g & 1];
+                if (P.gh) {
+                    __syncwarp();
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(gws + static_cast<uint32_t>(lane) * 4u), "f"(gw[g]) : "memory");
+                    __syncwarp();
+                }
                 l8_ld_wait(x);
-                if (g + 1 < G)
+                if (g + 1 < G) {
                     l8_ld_start(tl + 32 * (g + 1), v[(g + 1) & 1]);
+                } else { // this warp has read the accumulator
+                    lm_tc_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        l8_arrive(te + a * 8u);
+                }
                 uint32_t pk[16];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     float4 w = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
                     if (P.gh)
-                        w = l4_lds4(gws + static_cast<uint32_t>(32 * g + 4 * k) * 4u);
+                        w = l4_lds4(gws + static_cast<uint32_t>(4 * k) * 4u);
                     const float x0 = l4_finite(__fmul_rn(__uint_as_float(x[4 * k]), __fmul_rn(gh, w.x)));
                     const float x1 = l4_finite(__fmul_rn(__uint_as_float(x[4 * k + 1]), __fmul_rn(gh, w.y)));
                     const float x2 = l4_finite(__fmul_rn(__uint_as_float(x[4 * k + 2]), __fmul_rn(gh, w.z)));
@@ -180,29 +230,38 @@ __device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMa
                     pk[2 * k] = bf16_rn_pair(x0, x1);
                     pk[2 * k + 1] = bf16_rn_pair(x2, x3);
                 }
-                l8_stage(stg + g * kL8BoxBytes, pk, lane);
+                if (T.tma && sent) // the last store has read the box
+                    l8_stores_read();
+                __syncwarp();
+                l8_stage(stg, pk, lane);
+                const int n = n0 + 32 * g;
+                if (T.tma) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (l8_elect() && n < T.N) {
+                        l8_send(map, stg, n, row0);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                    sent = true;
+                } else {
+                    __syncwarp();
+                    uint32_t boxes = stg;
+                    l8_staged_now(boxes);
+                    if (n < T.N)
+                        l4_store_box(T, boxes, row0, n, T.N - n < 32 ? T.N - n : 32, lane);
+                    __syncwarp();
+                }
             }
         }
-        lm_tc_before();
-        __syncwarp();
-        if (lane == 0) // this warp has read the accumulator
-            l8_arrive(te + a * 8u);
-        if (!in)
-            continue;
-        if (T.tma) {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (!in) {
+            lm_tc_before();
             __syncwarp();
-            if (l8_elect()) {
-                for (int g = 0; g < G; ++g)
-                    if (n0 + 32 * g < T.N)
-                        l8_send(map, stg + g * kL8BoxBytes, n0 + 32 * g, row0);
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            }
-        } else {
-            uint32_t boxes = stg;
-            l8_staged_now(boxes);
-            l8_store_rows(T, boxes, row0, n0, T.N - n0 < G * 32 ? T.N - n0 : G * 32, lane);
-            __syncwarp();
+            if (lane == 0)
+                l8_arrive(te + a * 8u);
+        }
+        if (++sub == H || m + 1 == static_cast<uint32_t>(P.RT)) {
+            sub = 0;
+            t += units;
         }
     }
     if (!alive && lane == 0)
@@ -211,7 +270,7 @@ __device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMa
 }
 
 // Unit u (a pair of SMs, or one) takes tiles u, u + units, ...
-template <bool PAIR, int BLOCK>
+template <bool PAIR, int H, int BLOCK>
 __global__ void __launch_bounds__(kL4Threads, 1)
     lm_head_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
@@ -226,7 +285,7 @@ __global__ void __launch_bounds__(kL4Threads, 1)
     __shared__ int stop;
     const Lm8Params &T = P.t;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(lm_smem_raw) + 1023) & ~uintptr_t{1023});
-    const uint32_t sbase = smem_addr(smem);
+    const uint32_t front = smem_addr(smem), sbase = front + kL4Front;
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? lm_cluster_rank() : 0u;
     const bool leader = rank == 0;
@@ -262,11 +321,11 @@ __global__ void __launch_bounds__(kL4Threads, 1)
         uint32_t ph = 0;
         bool wrapped = false, ok = true;
         const uint32_t fb0 = PAIR ? lm_mapa(smem_addr(&full[0]), 0) : smem_addr(&full[0]);
-        const uint32_t bytes = kCtas * (abytes + bbytes + static_cast<uint32_t>(kTiles * 512 * (1 + P.blocks)));
         for (uint32_t t = unit; t < ntiles && ok; t += units) {
-            const int mt = static_cast<int>(l8_tile_m(T, t) * kCtas + rank);
-            const int n0 = static_cast<int>(l8_tile_n(T, t)) * T.NB;
-            const int sa0 = mt * P.KT, sb0 = (n0 >> 7) * P.KT;
+            const int m = static_cast<int>(l8_tile_m(T, t)) * H, n0 = static_cast<int>(l8_tile_n(T, t)) * T.NB;
+            const int subs = P.RT - m < H ? P.RT - m : H; // row tiles of this group
+            const int sb0 = (n0 >> 7) * P.KT;
+            const uint32_t bytes = kCtas * (subs * (abytes + kTiles * 512) + bbytes + static_cast<uint32_t>(kTiles * 512 * P.blocks));
             for (int kb = 0; kb < T.KB; ++kb) {
                 if (wrapped && !__all_sync(0xFFFFFFFFu, l8_wait(smem_addr(&empty[s]), ph ^ 1u))) {
                     ok = false;
@@ -277,12 +336,15 @@ __global__ void __launch_bounds__(kL4Threads, 1)
                     const uint32_t fb = fb0 + static_cast<uint32_t>(s * 8);
                     if (leader)
                         lm_mbar_expect(smem_addr(&full[s]), bytes);
-                    l8_tma_2d<PAIR>(dst, &tmA, kb * 128, mt * kLmBM, fb);
-                    dst += abytes;
+                    for (int h = 0; h < subs; ++h)
+                        l8_tma_2d<PAIR>(dst + h * abytes, &tmA, kb * 128, ((m + h) * kCtas + static_cast<int>(rank)) * kLmBM, fb);
+                    dst += H * abytes;
                     l8_tma_2d<PAIR>(dst, &tmB, kb * 128, n0 + static_cast<int>(rank) * (T.NB / kCtas), fb);
                     dst += bbytes;
-                    l8_tma_2d<PAIR>(dst, &tmSA, 0, sa0 + kb * kTiles, fb);
-                    dst += kTiles * 512;
+                    for (int h = 0; h < subs; ++h)
+                        l8_tma_2d<PAIR>(dst + h * kTiles * 512, &tmSA, 0,
+                                        ((m + h) * kCtas + static_cast<int>(rank)) * P.KT + kb * kTiles, fb);
+                    dst += H * kTiles * 512;
                     l8_tma_2d<PAIR>(dst, &tmSB, 0, sb0 + kb * kTiles, fb);
                     if (P.blocks == 2)
                         l8_tma_2d<PAIR>(dst + kTiles * 512, &tmSB, 0, sb0 + P.KT + kb * kTiles, fb);
@@ -313,66 +375,79 @@ __global__ void __launch_bounds__(kL4Threads, 1)
             l8_fail(T, &stop);
     } else if (warp == 1) {
         if (leader) {
-            const uint64_t ad0 = lm_desc(sbase), bd0 = lm_desc(sbase + abytes);
-            const uint64_t sd0 = l4_scale_desc(sbase + abytes + bbytes);
+            const uint64_t ad0 = lm_desc(sbase), bd0 = lm_desc(sbase + H * abytes);
+            const uint64_t sd0 = l4_scale_desc(sbase + H * abytes + bbytes);
             int s = 0;
-            uint32_t ph = 0, i = 0, set = 0;
+            uint32_t ph = 0, i = 0, set = 0; // i: row tiles so far, accumulator i mod 2
             bool ok = true;
-            for (uint32_t t = unit; t < ntiles && ok; t += units, ++i) {
-                const uint32_t a = i & 1u;
-                if (i >= 2 && !__all_sync(0xFFFFFFFFu, l8_wait(smem_addr(&tempty[a]), ((i >> 1) & 1u) ^ 1u))) {
-                    ok = false;
-                    break;
-                }
-                lm_tc_after();
-                const uint32_t tacc = tbase + a * kL4MaxNB;
+            for (uint32_t t = unit; t < ntiles && ok; t += units) {
+                const int m = static_cast<int>(l8_tile_m(T, t)) * H;
+                const int subs = P.RT - m < H ? P.RT - m : H;
                 const uint32_t shift = ((l8_tile_n(T, t) * static_cast<uint32_t>(T.NB)) & 127u) >> 5; // 0 or 2 columns
-                for (int kb = 0; kb < T.KB; ++kb) {
+                for (int kb = 0; kb < T.KB && ok; ++kb) {
                     if (!__all_sync(0xFFFFFFFFu, l8_wait(smem_addr(&full[s]), ph))) {
                         ok = false;
                         break;
                     }
-                    lm_tc_after();
-                    if (l8_elect()) {
-                        const uint64_t so = static_cast<uint64_t>((s * T.stage_bytes) >> 4);
-                        const uint32_t sa = tbase + kL4ScaleCol + set * 64u, sb = sa + kTiles * 4u;
-                        const int left = P.d - kb * kL4BK; // hidden dims from here on
-#pragma unroll
-                        for (int k = 0; k < kTiles; ++k) {
-                            l4_copy_scales<PAIR>(sa + 4 * k, sd0 + so + static_cast<uint64_t>(k * 32));
-                            l4_copy_scales<PAIR>(sb + 4 * P.blocks * k, sd0 + so + static_cast<uint64_t>((kTiles + k) * 32));
-                            if (P.blocks == 2)
-                                l4_copy_scales<PAIR>(sb + 8 * k + 4, sd0 + so + static_cast<uint64_t>((2 * kTiles + k) * 32));
+                    const uint64_t so = static_cast<uint64_t>((s * T.stage_bytes) >> 4);
+                    const uint32_t sa0 = tbase + kL4ScaleCol + set * 64u, sb = sa0 + H * kTiles * 4u;
+                    #pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        if (h >= subs)
+                            break;
+                        const uint32_t j = i + h, a = j & 1u;
+                        if (kb == 0 && j >= 2 &&
+                            !__all_sync(0xFFFFFFFFu, l8_wait(smem_addr(&tempty[a]), ((j >> 1) & 1u) ^ 1u))) {
+                            ok = false;
+                            break;
                         }
+                        lm_tc_after();
+                        if (l8_elect()) {
+                            const uint32_t sa = sa0 + h * kTiles * 4u, tacc = tbase + a * kL4MaxNB;
+                            const uint64_t ad = ad0 + so + static_cast<uint64_t>(h * static_cast<int>(abytes >> 4));
+                            const uint64_t sd = sd0 + so;
+                            const int left = P.d - kb * kL4BK; // hidden dims from here on
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if (k * 64 >= left)
-                                break;
-                            const int tile = k * 64 / kDimsPerTile; // of the stage's scale tiles
-                            // two scales a row and MMA: the first or the second half of the word
-                            const uint32_t half = BLOCK == 32 && (k & 1) ? (2u << 29) | (2u << 4) : 0u;
-                            l4_mma<PAIR, BLOCK>(tacc, ad0 + so + static_cast<uint64_t>(k * 2),
-                                                bd0 + so + static_cast<uint64_t>(k * 2), P.idesc | half, sa + 4 * tile,
-                                                sb + 4 * P.blocks * tile + shift, (kb | k) ? 1u : 0u);
+                            for (int k = 0; k < kTiles; ++k) {
+                                l4_copy_scales<PAIR>(sa + 4 * k, sd + static_cast<uint64_t>((h * kTiles + k) * 32));
+                                if (h == 0) {
+                                    l4_copy_scales<PAIR>(sb + 4 * P.blocks * k, sd + static_cast<uint64_t>((H * kTiles + k) * 32));
+                                    if (P.blocks == 2)
+                                        l4_copy_scales<PAIR>(sb + 8 * k + 4, sd + static_cast<uint64_t>(((H + 1) * kTiles + k) * 32));
+                                }
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if (k * 64 >= left)
+                                    break;
+                                const int tile = k * 64 / kDimsPerTile; // of the stage's scale tiles
+                                // two scales a row and MMA: the first or the second half of the word
+                                const uint32_t half = BLOCK == 32 && (k & 1) ? (2u << 29) | (2u << 4) : 0u;
+                                l4_mma<PAIR, BLOCK>(tacc, ad + static_cast<uint64_t>(k * 2),
+                                                    bd0 + so + static_cast<uint64_t>(k * 2), P.idesc | half, sa + 4 * tile,
+                                                    sb + 4 * P.blocks * tile + shift, (kb | k) ? 1u : 0u);
+                            }
+                            if (h == subs - 1)
+                                l8_commit<PAIR>(smem_addr(&empty[s]));
+                            if (kb == T.KB - 1)
+                                l8_commit<PAIR>(smem_addr(&tfull[a]));
                         }
-                        l8_commit<PAIR>(smem_addr(&empty[s]));
-                        if (kb == T.KB - 1)
-                            l8_commit<PAIR>(smem_addr(&tfull[a]));
+                        __syncwarp();
                     }
-                    __syncwarp();
                     set ^= 1u;
                     if (++s == T.stages) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
+                i += subs;
             }
             if (!ok && lane == 0)
                 l8_fail(T, &stop);
         }
     } else {
-        l4_epilogue<PAIR>(P, &tmC, sbase + kL4RingBytes, sbase + kL4RingBytes + kL4EpiWarps * kL4StgBytes, tbase,
-                          smem_addr(&tfull[0]), smem_addr(&tempty[0]), &stop, rank, unit, units, ntiles);
+        l4_epilogue<PAIR, H>(P, &tmC, front, tbase, smem_addr(&tfull[0]), smem_addr(&tempty[0]), &stop, rank, unit, units,
+                             ntiles);
     }
     // ---- teardown: copies and MMAs in flight complete before the memory goes
     lm_tc_before();

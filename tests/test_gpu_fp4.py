@@ -137,11 +137,11 @@ def _head(M, V, d, block, seed=0, exact=False):
     return z.cpu().double().numpy(), want, mag
 
 
-# tiles of 64, 128 and 192 ids, alone and in pairs; rows that fill no tile; vocabularies that end inside a tile and are
+# tiles of 64, 128 and 192 ids, alone, in pairs and with two row tiles a pair; rows that fill no tile; vocabularies that end inside a tile and are
 # no multiple of 8; a last stage of 32 to 224 dims
 SHAPES = [(1, 100, 32), (1, 5000, 256), (5, 1, 64), (8, 777, 96), (17, 2048, 1024), (64, 4100, 288), (127, 300, 544),
           (128, 20000, 256), (129, 1000, 480), (131, 3203, 1056), (200, 30000, 128), (257, 4096, 512), (513, 515, 224),
-          (300, 15001, 64)]
+          (300, 15001, 64), (600, 9000, 288), (1030, 21000, 64), (520, 30001, 512)]
 
 
 @pytest.mark.parametrize("block", [16, 32])
