@@ -462,7 +462,7 @@ sv_status_t sv_dequantize_fp4(const void *values, const void *scales,
  *   logits         [M, V] bf16 out (16-byte aligned with V % 8 == 0 for the
  *                  fast stores);
  *   status_dev     as for sv_lm_head_logits;
- *   d a multiple of 32 (the rows' 16-byte stride).
+ *   d a multiple of 32 (the rows' 16-byte stride), at most 2^20.
  * M <= 2^30, V <= SV_MAX_V.  Returns SV_EINVAL / SV_EUNSUPPORTED on bad sizes or
  * pointers, SV_ECUDA when a launch (or the tensor-map set-up) fails.  One launch
  * on `stream`; allocates nothing. */

@@ -672,23 +672,25 @@ class Fp4Tensor:
 
 def _fp4_check(t: Fp4Tensor, name: str) -> tuple[torch.device, int, int, int]:
     """(device, block, rows, d) of t."""
-    block = _SCALE_TYPES.get(t.scales.dtype)
+    v, sc, rs = t.values, t.scales, t.row_scales
+    block = _SCALE_TYPES.get(sc.dtype)
     if block is None:
-        raise TypeError(f"{name}.scales: expected float8_e4m3fn or float8_e8m0fnu, got {t.scales.dtype}")
-    if t.values.dtype is not torch.uint8:
-        raise TypeError(f"{name}.values: expected uint8, got {t.values.dtype}")
-    dev = _cuda(t.values, f"{name}.values")
-    shape = t.values.shape
+        raise TypeError(f"{name}.scales: expected float8_e4m3fn or float8_e8m0fnu, got {sc.dtype}")
+    if v.dtype is not torch.uint8:
+        raise TypeError(f"{name}.values: expected uint8, got {v.dtype}")
+    dev = _cuda(v, name)
+    shape = v.shape
     if len(shape) < 1 or shape[-1] < 1:
         raise ValueError(f"{name}.values must be [..., d / 2]")
-    d = 2 * shape[-1]
+    half = shape[-1]
+    d = 2 * half
     _fits(d)
-    rows = t.values.numel() // shape[-1]
-    _need(t.scales, f"{name}.scales", t.scales.dtype, _fp4_scale_shape(rows, d, block), dev)
-    if (t.row_scales is None) != (block == 32):
+    rows = v.numel() // half
+    _need(sc, name, sc.dtype, _fp4_scale_shape(rows, d, block), dev)
+    if (rs is None) != (block == 32):
         raise ValueError(f"{name}.row_scales: blocks of 16 have them, blocks of 32 do not")
-    if block == 16:
-        _need(t.row_scales, f"{name}.row_scales", _F32, shape[:-1], dev)
+    if rs is not None:
+        _need(rs, name, _F32, shape[:-1], dev)
     return dev, block, rows, d
 
 
@@ -808,23 +810,29 @@ def sv_sample_logits(logits: torch.Tensor, uniforms: torch.Tensor, temperature: 
     _need(uniforms, "uniforms", _F32, lead, dev)
     if status is not None:
         _need(status, "status", torch.int32, (1,), dev)
-    top_k = min(max(int(top_k), 0), 0x7FFFFFFF)
+    top_k = min(max(int(top_k), 0), 0x7FFFFFFF)  # (more than every row has, for what a 32-bit number does not hold)
     with _on(dev, stream) as s:
-        o = {}
-        for name, dtype, oshape in (("tokens", torch.int32, lead), ("prob", _F32, lead), ("kept", torch.int32, lead),
-                                    ("probs", _F32, shape)):
-            given = out.get(name) if out else None
-            if given is not None:
-                _need(given, name, dtype, oshape, dev)
-            elif name != "probs" or want_probs:
-                given = torch.empty(oshape, dtype=dtype, device=dev)
-            o[name] = given
-        rc = N.lib().sv_sample_logits(logits.data_ptr(), dt, uniforms.data_ptr(), float(temperature), top_k,
-                                      float(top_p), float(min_p), rows, V, o["tokens"].data_ptr(), o["prob"].data_ptr(),
-                                      o["kept"].data_ptr(), _ptr(o["probs"]), _ptr(status), s)
+        tokens = prob = kept = probs = None
+        if out:
+            tokens, prob, kept, probs = (out.get(k) for k in ("tokens", "prob", "kept", "probs"))
+            for t, name, dtype, oshape in ((tokens, "tokens", torch.int32, lead), (prob, "prob", _F32, lead),
+                                           (kept, "kept", torch.int32, lead), (probs, "probs", _F32, shape)):
+                if t is not None:
+                    _need(t, name, dtype, oshape, dev)
+        if tokens is None:
+            tokens = torch.empty(lead, dtype=torch.int32, device=dev)
+        if prob is None:
+            prob = torch.empty(lead, dtype=_F32, device=dev)
+        if kept is None:
+            kept = torch.empty(lead, dtype=torch.int32, device=dev)
+        if probs is None and want_probs:
+            probs = torch.empty(shape, dtype=_F32, device=dev)
+        rc = N.lib().sv_sample_logits(logits.data_ptr(), dt, uniforms.data_ptr(), float(temperature), top_k, float(top_p),
+                                      float(min_p), rows, V,
+                                      tokens.data_ptr(), prob.data_ptr(), kept.data_ptr(), _ptr(probs), _ptr(status), s)
     if rc != N.SV_OK:
         raise SpecVerifyError(rc)
-    return SampleResult(o["tokens"], o["prob"], o["kept"], o["probs"], status)
+    return SampleResult(tokens, prob, kept, probs, status)
 
 
 # ------------------------------------------------------------- trees

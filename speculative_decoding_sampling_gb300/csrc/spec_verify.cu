@@ -1540,6 +1540,7 @@ sv_status_t sv_quantize_fp4(const void *x, sv_dtype_t x_dtype, int64_t rows, int
     P.KT = fp4_tiles(d, block);
     P.octets = static_cast<int32_t>(P.KT * (block / 2)); // 4 blocks a tile
     P.WPR = fp4_warps(P.octets);
+    P.pairs = aligned(x, 2 * elem_size(x_dtype));
     P.v = static_cast<uint8_t *>(values);
     P.s = static_cast<uint8_t *>(scales);
     P.g = row_scales;
@@ -1574,6 +1575,7 @@ sv_status_t sv_dequantize_fp4(const void *values, const void *scales, const floa
     P.octets = static_cast<int32_t>(ceil_div(d, 8));
     P.KT = fp4_tiles(d, block);
     P.WPR = fp4_warps(P.octets);
+    P.pairs = aligned(out, 2 * elem_size(out_dtype));
     P.out = out;
     const bool vec = d % 8 == 0 && aligned(values, 4) && aligned(out, 16);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1592,9 +1594,10 @@ sv_status_t sv_lm_head_logits_fp4(const void *hidden, const void *hidden_scales,
 {
     if (M < 0 || d < 32 || d % 32 != 0 || V < 1 || (block != 16 && block != 32) || !aligned(status_dev, 4))
         return SV_EINVAL;
-    if (V > SV_MAX_V || M > kLmMaxRows)
+    // (a tile's sum over d is one bounded wait)
+    if (V > SV_MAX_V || M > kLmMaxRows || d > (1 << 20))
         return SV_EUNSUPPORTED;
-    // tiles, their steps and the scale tiles are counted in 32 bits
+    // tiles and scale tiles are counted in 32 bits
     const Lm4Plan p = lm4_plan(M, V);
     const int64_t tiles = static_cast<int64_t>(p.MT) * p.NT, kt = fp4_tiles(d, block);
     if (tiles > INT32_MAX || ceil_div(M, 128) > INT32_MAX / kt - 4 || ceil_div(V, 128) > INT32_MAX / kt - 4)

@@ -39,6 +39,7 @@ struct Fp4Params {
     int32_t octets;       // of a row, the padded blocks' included (4 blocks a tile)
     int32_t KT;           // scale tiles along d
     int32_t WPR;          // warps of a row: 1, 2, 4 or 8
+    int32_t pairs;        // x is aligned to two of its elements (and so are all rows)
     uint8_t *v;           // [M, d / 2]
     uint8_t *s;           // [Mpad / 128, KT, 512]
     float *g;             // [M] (block 16)
@@ -49,6 +50,7 @@ struct Fp4BackParams {
     const float *g;       // [M] or nullptr
     int64_t M;
     int32_t d, octets, KT, WPR;
+    int32_t pairs;        // out is aligned to two of its elements
     void *out;            // [M, d] bf16 or fp32
 };
 
@@ -123,13 +125,15 @@ template <> struct F4Octet<uint16_t> {
     uint4 w;
     __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void load(const uint16_t *p) { w = ld_stream_v4(p); }
-    __device__ __forceinline__ void load_some(const uint16_t *p, int n)
+    // the first n (even), the others 0
+    __device__ __forceinline__ void load_some(const uint16_t *p, int n, bool pairs)
     {
         uint32_t u[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n)
-                u[i >> 1] |= static_cast<uint32_t>(__ldg(p + i)) << (16 * (i & 1));
+        for (int i = 0; i < 4; ++i)
+            if (2 * i < n)
+                u[i] = pairs ? __ldg(reinterpret_cast<const uint32_t *>(p) + i)
+                             : __ldg(p + 2 * i) | static_cast<uint32_t>(__ldg(p + 2 * i + 1)) << 16;
         w = make_uint4(u[0], u[1], u[2], u[3]);
     }
     // the largest magnitude, as fp32 bits
@@ -157,14 +161,17 @@ template <> struct F4Octet<float> {
         a = ld_stream_v4(p);
         b = ld_stream_v4(p + 4);
     }
-    __device__ __forceinline__ void load_some(const float *p, int n)
+    __device__ __forceinline__ void load_some(const float *p, int n, bool pairs)
     {
-        uint32_t u[8];
+        float2 f[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            u[i] = i < n ? __float_as_uint(__ldg(p + i)) : 0u;
-        a = make_uint4(u[0], u[1], u[2], u[3]);
-        b = make_uint4(u[4], u[5], u[6], u[7]);
+        for (int i = 0; i < 4; ++i) {
+            f[i] = make_float2(0.0f, 0.0f);
+            if (2 * i < n)
+                f[i] = pairs ? __ldg(reinterpret_cast<const float2 *>(p) + i) : make_float2(__ldg(p + 2 * i), __ldg(p + 2 * i + 1));
+        }
+        a = make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+        b = make_uint4(__float_as_uint(f[2].x), __float_as_uint(f[2].y), __float_as_uint(f[3].x), __float_as_uint(f[3].y));
     }
     __device__ __forceinline__ uint32_t amax() const
     {
@@ -179,6 +186,40 @@ template <> struct F4Octet<float> {
             f[i] = __uint_as_float(u[i]);
     }
 };
+
+// The first n (even) values of an octet's 4 bytes, in pieces as large as the address
+// allows (the same for a whole row).
+__device__ __forceinline__ void f4_store_some(uint8_t *v, uint32_t packed, int n)
+{
+    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(v));
+    if ((at & 3u) == 0 && n >= 8) {
+        *reinterpret_cast<uint32_t *>(v) = packed;
+    } else if ((at & 1u) == 0 && n >= 8) {
+        reinterpret_cast<uint16_t *>(v)[0] = static_cast<uint16_t>(packed);
+        reinterpret_cast<uint16_t *>(v)[1] = static_cast<uint16_t>(packed >> 16);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (2 * k < n)
+                v[k] = static_cast<uint8_t>(packed >> (8 * k));
+    }
+}
+__device__ __forceinline__ uint32_t f4_load_some(const uint8_t *v, int n)
+{
+    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(v));
+    uint32_t p = 0;
+    if ((at & 3u) == 0 && n >= 8) {
+        p = __ldg(reinterpret_cast<const uint32_t *>(v));
+    } else if ((at & 1u) == 0 && n >= 8) {
+        p = __ldg(reinterpret_cast<const uint16_t *>(v)) | static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(v) + 1)) << 16;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (2 * k < n)
+                p |= static_cast<uint32_t>(__ldg(v + k)) << (8 * k);
+    }
+    return p;
+}
 
 // The row's power of two from its largest magnitude's bits: biased exponent
 // of the least 2^k with amax <= 2688 * 2^k (2688 = 1.3125 * 2^11); 2^0 for a
@@ -214,7 +255,7 @@ __global__ void __launch_bounds__(kF4Threads, kF4Ctas<XT>) quantize_fp4_kernel(c
         else if (VEC)
             o.load(from + t * stride * 8);
         else
-            o.load_some(from + t * stride * 8, left);
+            o.load_some(from + t * stride * 8, left, P.pairs);
     };
     auto block_max = [&](const F4Octet<XT> &o) {
         uint32_t m = o.amax();
@@ -312,10 +353,7 @@ __global__ void __launch_bounds__(kF4Threads, kF4Ctas<XT>) quantize_fp4_kernel(c
                 if (left > 0)
                     *reinterpret_cast<uint32_t *>(v) = packed;
             } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (2 * k < left)
-                        v[k] = static_cast<uint8_t>(packed >> (8 * k));
+                f4_store_some(v, packed, left);
             }
         };
 #pragma unroll
@@ -356,10 +394,7 @@ __global__ void __launch_bounds__(kF4Threads) dequantize_fp4_kernel(const Fp4Bac
         if (VEC) {
             p = __ldg(reinterpret_cast<const uint32_t *>(v + i * 4));
         } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (2 * k < left)
-                    p |= static_cast<uint32_t>(__ldg(v + i * 4 + k)) << (8 * k);
+            p = f4_load_some(v + i * 4, left);
         }
         const uint32_t byte = __ldg(P.s + f4_scale_at(row, i / L, P.KT));
         const float s = BLOCK == 16 ? f4_e4m3(byte) : f4_e8m0(byte);
@@ -379,9 +414,15 @@ __global__ void __launch_bounds__(kF4Threads) dequantize_fp4_kernel(const Fp4Bac
                 reinterpret_cast<float4 *>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
             } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < left)
-                        o[k] = f[k];
+                for (int k = 0; k < 8; k += 2)
+                    if (k < left) { // (left is even)
+                        if (P.pairs) {
+                            *reinterpret_cast<float2 *>(o + k) = make_float2(f[k], f[k + 1]);
+                        } else {
+                            o[k] = f[k];
+                            o[k + 1] = f[k + 1];
+                        }
+                    }
             }
         } else {
             uint16_t *o = static_cast<uint16_t *>(P.out) + row * P.d + i * 8;
@@ -393,9 +434,15 @@ __global__ void __launch_bounds__(kF4Threads) dequantize_fp4_kernel(const Fp4Bac
                 *reinterpret_cast<uint4 *>(o) = make_uint4(u[0], u[1], u[2], u[3]);
             } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < left)
-                        o[k] = static_cast<uint16_t>(u[k >> 1] >> (16 * (k & 1)));
+                for (int k = 0; k < 4; ++k)
+                    if (2 * k < left) {
+                        if (P.pairs) {
+                            reinterpret_cast<uint32_t *>(o)[k] = u[k];
+                        } else {
+                            o[2 * k] = static_cast<uint16_t>(u[k]);
+                            o[2 * k + 1] = static_cast<uint16_t>(u[k] >> 16);
+                        }
+                    }
             }
         }
     }

@@ -265,24 +265,12 @@ template <typename LT> struct SampleSlice {
     int32_t first;     // id of position 0 (may be below the slice's first)
     int32_t lo, hi;    // ids of the slice
     int32_t nv;        // vectors
-    // -0 as +0, the same logit: the sum with +0
-    __device__ __forceinline__ static uint4 plain(const uint4 &w)
-    {
-        uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if constexpr (PV == 8)
-                asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(u[k]) : "r"(0u));
-            else
-                u[k] = __float_as_uint(__uint_as_float(u[k]) + 0.0f);
-        return make_uint4(u[0], u[1], u[2], u[3]);
-    }
     // vector v straight from memory
     __device__ __forceinline__ uint4 fetch(int32_t v) const
     {
         const int32_t i = first + v * PV;
         if (i >= lo && i + PV <= hi)
-            return plain(ld_stream_v4(row + i));
+            return ld_stream_v4(row + i);
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -295,7 +283,7 @@ template <typename LT> struct SampleSlice {
                 w[k] = i + k >= lo && i + k < hi ? filter_bits<LT>(row, i + k) : E::kNegInf;
             }
         }
-        return plain(make_uint4(w[0], w[1], w[2], w[3]));
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
     __device__ __forceinline__ uint4 vec(int32_t v) const { return mem ? mem[v] : fetch(v); }
     __device__ __forceinline__ static uint32_t of(const uint4 &w, int j)
@@ -964,7 +952,7 @@ __device__ __forceinline__ void sm_write_q(const SampleSlice<LT> &X, const Sampl
     float least = zlo;
     if (CUTS && cut.key)
         least = fmaxf(least, E::value(E::bits_of_key(cut.key)));
-    const float cq = P.cq, lz = static_cast<float>(P.fix) - __log2f(static_cast<float>(Z)); // log2(2^fix / Z)
+    const float cq = P.cq, scale = ldexpf(1.0f, P.fix) / static_cast<float>(Z);
     const bool filtered = CUTS || P.min_p;
     for (int32_t v = threadIdx.x; v < X.nv; v += NT) {
         const uint4 w = X.vec(v);
@@ -973,13 +961,13 @@ __device__ __forceinline__ void sm_write_q(const SampleSlice<LT> &X, const Sampl
         if (!filtered) { // (exp2 of -inf is 0)
 #pragma unroll
             for (int j = 0; j < PV; ++j)
-                q[j] = ex2(__fmaf_rn(E::value(SampleSlice<LT>::of(w, j)) - R.m, cq, lz));
+                q[j] = ex2(__fmul_rn(E::value(SampleSlice<LT>::of(w, j)) - R.m, cq)) * scale;
         } else if (sm_largest<LT>(w) >= least) {
 #pragma unroll
             for (int j = 0; j < PV; ++j) {
                 const uint32_t b = SampleSlice<LT>::of(w, j);
                 const bool in = E::finite(b) && E::value(b) >= least && (!CUTS || E::key(b) != cut.key || i + j <= cut.id);
-                q[j] = in ? ex2(__fmaf_rn(E::value(b) - R.m, cq, lz)) : 0.0f;
+                q[j] = in ? ex2(__fmul_rn(E::value(b) - R.m, cq)) * scale : 0.0f;
             }
         } else {
 #pragma unroll
@@ -1057,20 +1045,23 @@ __global__ void __launch_bounds__(NT, (CUTS ? 1024 : 1280) / NT) sample_kernel(c
                     asm("max.NaN.f32 %0, %1, %2;" : "=f"(mx) : "f"(mx), "f"(__uint_as_float(u[k])));
             }
         };
-        constexpr int U = 8;
-        for (int32_t v = threadIdx.x; v < X.nv; v += U * NT) {
-            uint4 w[U];
-#pragma unroll
-            for (int t = 0; t < U; ++t)
-                if (v + t * NT < X.nv)
-                    w[t] = X.fetch(v + t * NT);
-#pragma unroll
-            for (int t = 0; t < U; ++t)
-                if (v + t * NT < X.nv) {
-                    fold(w[t]);
-                    if (P.staged)
-                        stage[v + t * NT] = w[t];
-                }
+        if (P.staged) {
+            // every vector on its way at once; a slice's ragged ends by way of registers
+            for (int32_t v = threadIdx.x; v < X.nv; v += NT) {
+                const int32_t i = X.first + v * PV;
+                if (i >= X.lo && i + PV <= X.hi)
+                    cp_async16(stage + v, row + i);
+                else
+                    stage[v] = X.fetch(v);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory"); // (a thread folds what it copied)
+#pragma unroll 4
+            for (int32_t v = threadIdx.x; v < X.nv; v += NT)
+                fold(lds_v4(stage + v));
+        } else {
+#pragma unroll 4
+            for (int32_t v = threadIdx.x; v < X.nv; v += NT)
+                fold(X.fetch(v));
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)

@@ -72,10 +72,11 @@ def test_head_host_checks(kw):
 def test_head_sizes():
     assert _call("sv_lm_head_logits_fp4", HEAD, dict(V=N.SV_MAX_V + 1)) == N.SV_EUNSUPPORTED
     assert _call("sv_lm_head_logits_fp4", HEAD, dict(M=(1 << 30) + 1)) == N.SV_EUNSUPPORTED
+    assert _call("sv_lm_head_logits_fp4", HEAD, dict(d=(1 << 20) + 32)) == N.SV_EUNSUPPORTED
     assert _call("sv_lm_head_logits_fp4", HEAD, dict(M=0, h=None)) == N.SV_OK
     # more tiles of logits, or of scales, than are counted in 32 bits
     assert _call("sv_lm_head_logits_fp4", HEAD, dict(M=1 << 30, V=N.SV_MAX_V)) == N.SV_EUNSUPPORTED
-    assert _call("sv_lm_head_logits_fp4", HEAD, dict(M=1 << 22, V=64, d=(1 << 31) - 32)) == N.SV_EUNSUPPORTED
+    assert _call("sv_lm_head_logits_fp4", HEAD, dict(M=1 << 30, V=64, d=1 << 20)) == N.SV_EUNSUPPORTED
 
 
 SAMPLE = dict(z=FAKE, zt=N.SV_BF16, u=FAKE, T=1.0, top_k=0, top_p=1.0, min_p=0.0, rows=4, V=1000, tokens=FAKE, prob=None,

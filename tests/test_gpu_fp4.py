@@ -86,6 +86,18 @@ def test_quantize_alignment_leading_dims_and_out():
     odd = buf[1:].view(15, 64)
     odd.copy_(x.view(15, 64))
     assert torch.equal(sv.sv_quantize_fp4(odd).values, t.values.view(15, 32))
+    # ... and so for rows that are no whole octets, in and out
+    for dtype in (BF, F32):
+        y = _x(9, 214, dtype, seed=2)
+        buf = torch.zeros(9 * 214 + 1, dtype=dtype, device=DEV)
+        odd = buf[1:].view(9, 214)
+        odd.copy_(y)
+        q = sv.sv_quantize_fp4(odd)
+        _check_quantized(y, 16, q)
+        shifted = torch.zeros(9 * 214 + 3, dtype=dtype, device=DEV)
+        sv.sv_dequantize_fp4(q, dtype, out=shifted[1:-2].view(9, 214))
+        assert torch.equal(shifted[1:-2].view(9, 214), sv.sv_dequantize_fp4(q, dtype))
+        assert not shifted[0] and not shifted[-2:].any()
     again = sv.sv_quantize_fp4(2 * x, out=t)
     assert again is t
     _check_quantized(2 * x.cpu().view(15, 64), 16, t)

@@ -72,11 +72,13 @@ def test_sizes(dtype, V):
     _check(z, u, 0.9, top_p=0.95, min_p=0.001)
 
 
-@pytest.mark.parametrize("rows", [1, 2, 37, 300])
+@pytest.mark.parametrize("rows", [1, 2, 37, 300, 400])
 def test_row_counts(rows):
     z = _logits(rows, 5000, BF, 3.0, seed=rows)
     u = np.random.default_rng(rows).random(rows, dtype=np.float32)
     _check(z, u, 0.7, top_k=100, top_p=0.9)
+    _check(z, u, 0.7, top_k=900, top_p=0.95)
+    _check(z, u, 0.7, top_p=0.99)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
@@ -197,6 +199,32 @@ def test_rows_do_not_depend_on_the_batch():
         b = sv.sv_sample_logits(z[i:i + 1], u[i:i + 1], 0.8, 0, 0.9, want_probs=True)
         assert torch.equal(a.tokens[i:i + 1], b.tokens) and torch.equal(a.probs[i:i + 1], b.probs)
         assert torch.equal(a.prob[i:i + 1], b.prob) and torch.equal(a.kept[i:i + 1], b.kept)
+
+
+@pytest.mark.parametrize("filt", FILTERS + [dict(top_k=700), dict(top_k=900, top_p=0.97), dict(top_p=0.98, min_p=1e-4)],
+                         ids=lambda f: ",".join(f"{k}={v}" for k, v in f.items()) or "none")
+@pytest.mark.parametrize("dtype,V", [(BF, 4099), (BF, 50001), (F32, 12000)], ids=["bf16-4099", "bf16-50001", "fp32-12000"])
+def test_large_batches(dtype, V, filt):
+    """Many rows (CTAs of another size, another division of the work) against the same rows in small calls, which the
+    plain form above checks: bit for bit.  Among them flat, tied, masked and bad rows."""
+    rows = 330
+    z = _logits(rows, V, dtype, 3.0, seed=V)
+    z[3], z[4, :] = 0.0, -1.25
+    z[5] = (z[5] / 3).round()                     # a few values, many times each
+    z[6, 20:] = -np.inf
+    z[7] = z[7].sort(descending=True).values      # the largest in one CTA
+    z[8, 0] = 200.0                               # all mass in one id
+    z[9] *= 0.05
+    z[10, 7], z[11, :] = float("nan"), -np.inf
+    zd = z.to(DEV)
+    u = torch.from_numpy(np.random.default_rng(V).random(rows, dtype=np.float32)).to(DEV)
+    u[12] = 1.0
+    a = sv.sv_sample_logits(zd, u, 0.8, filt.get("top_k", 0), filt.get("top_p", 1.0), filt.get("min_p", 0.0), want_probs=True)
+    for i in range(0, rows, 30):
+        b = sv.sv_sample_logits(zd[i:i + 30], u[i:i + 30], 0.8, filt.get("top_k", 0), filt.get("top_p", 1.0),
+                                filt.get("min_p", 0.0), want_probs=True)
+        for name in ("tokens", "prob", "kept", "probs"):
+            assert torch.equal(getattr(a, name)[i:i + 30], getattr(b, name)), (name, i)
 
 
 def test_distribution_of_draws():
