@@ -21,6 +21,12 @@
 // A row belongs to WPR warps, whose lanes keep its octets in registers between
 // the row's maximum and the values (of longer rows the rest is read again), and
 // have the next row's on their way meanwhile.
+//
+// Measured (replayed; GB300) at 128256 x 4096 bf16: quantising in blocks of 16 319
+// us = 4.2 TB/s, of 32 226 us = 5.9 TB/s; reading back 208 us = 6.5 TB/s and 241 us.
+// Blocks of 16 are bound by instructions (about 100 an octet, the ALU pipe first);
+// with divisions by the compiler and addresses by octet it was 500 us, 375 with
+// corrected reciprocals, 319 with addresses by row.
 #pragma once
 
 #include "sv_device.cuh"

@@ -8,14 +8,14 @@
 // scales in (tcgen05, kind mxf4nvf4, block_scale), so the whole sum over d stays
 // in tensor memory in fp32 and only the rows' factors are left to the epilogue.
 //
-// Two shapes of one kernel, as for e4m3.  PAIR false (M <= 128): a CTA per SM,
-// tiles of 128 rows x NB ids; W streams through.  PAIR true: a cluster of two
-// CTAs on a pair of SMs, tiles of 256 rows x NB ids, each CTA loading its 128
-// rows of h and half of the tile of W.  What bounds many rows is what the SMs take
-// from L2 (about 83 bytes a nanosecond each, all of them at once; with three
-// quarters of the MMAs left out the kernel was 13 % faster): where it pays, a pair
-// forms two such tiles of rows at a time from one tile of W, one in each accumulator
-// (H 2).  Tiles are walked rows fastest.
+// Two shapes of one kernel, as for e4m3.  PAIR false (M <= 128, and where a pair's
+// second CTA would have few rows): a CTA per SM, tiles of 128 rows x NB ids; W
+// streams through.  PAIR true: a cluster of two CTAs on a pair of SMs, tiles of 256
+// rows x NB ids, each CTA loading its 128 rows of h and half of the tile of W.  With
+// many rows what bounds a stage is the round trip of its shared memory (MMA, commit,
+// wait, load from L2, wait: about 2 us) over the stages that fit; a pair then forms
+// two tiles of rows at a time from one tile of W, one in each accumulator (H 2),
+// which halves what W takes of a stage.  Tiles are walked rows fastest.
 //
 // Warp 0 loads: a stage is 256 hidden dims, one 128-byte swizzle row of 4-bit
 // values, with the 512-byte scale tiles that belong to it (both CTAs of a pair
@@ -24,11 +24,22 @@
 // the four lane quarters get copies), then an MMA for each 64 dims.  Copies and
 // MMAs of one thread run in order, and two sets of scale columns alternate.
 // Warps 2..9 are the epilogue, two for each 32 rows: two accumulators, so that a
-// tile is read, scaled and stored (through shared memory, as for e4m3) while the next is formed.
+// tile is read, scaled and stored (box by box through shared memory, as for e4m3)
+// while the next is formed.
 // 512 tensor-memory columns: 2 x 192 of sums, 2 x 64 of scales, hence NB <= 192.
 // (A set: 16 columns for each row tile, 32 for the ids.)  Ids start at a multiple of
 // 64 of their scale tile: two columns.
 // Every wait is bounded (l8_wait), with lm_head_kernel's teardown.
+//
+// Measured (replayed; GB300): M 2304, V 151936, d 4096: 497 us = 5.8 PFLOP/s (the
+// tensor pipe was 75 % active at 5.0 PFLOP/s, so 64 dims an MMA give it 6.7 at
+// most); 532 with one row tile a pair and five stages.  M 64, V 128256, d 2048: 27 us
+// = 5.7 TB/s; M 1, V 32000, d 4096: 16 us = 4.5 TB/s, bound by the weights' bytes and
+// some 5 us of launch, first loads and last tile.  M 131, V 32003, d 1056: 19 us,
+// three tiles a pair and odd rows' plain stores (16.6 with 96 ids staged at a time,
+// for which the ring that many rows want leaves no room).
+// With three quarters of the MMAs left out the first case took 463 instead of 532 us,
+// without the scales' copies 496, with one stage's lines loaded again and again 508.
 #pragma once
 
 #include "sv_lmhead_fp8.cuh"

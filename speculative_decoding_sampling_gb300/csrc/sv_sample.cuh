@@ -25,19 +25,31 @@
 //     the whole row its mass is formed in the same pass.  A scan finds top-k's bin;
 //     for top-p the counts and the bins' edges bound the running mass to 3.3 % and
 //     so the bins that its cut may lie in.  The ids down to the last of these bins
-//     are listed (up to 1152 or 4096 a CTA; more are picked out of the slice each time), and
-//     nothing below them is looked at again;
+//     are listed (up to 1152 or 4096 a CTA; more are picked out of the slice each
+//     time), and nothing below them is looked at again;
 //  3. up to 256 listed ids are gathered by every CTA and ranked, which settles the
-//     row.  Up to 1024 go, in a large batch, to the cluster's first CTA, which settles
-//     the row alone as all would together: the ids of top-k's bin are ranked; then masses are
-//     binned (four shared-memory additions an id) and the ids of top-p's bin ranked;
-//     the draw finds its run of ids by such bins too.  (Of more, the ranked ones are
-//     gathered by every CTA.)  A bin of
-//     more than 256 is counted again digit by digit of the order key (512 bins a
-//     digit) down to one value, as is all below the bins when a cut lies there;
+//     row.  Up to 1024 go, in a large batch, to the cluster's first CTA, which
+//     settles the row alone as all would together: the ids of top-k's bin are ranked;
+//     then masses are binned (four shared-memory additions an id) and the ids of
+//     top-p's bin ranked; the draw finds its run of ids by such bins too.  (Of more
+//     than 1024, and in small batches, the ranked ones are gathered by every CTA.)  A
+//     bin of more than 256 is counted again digit by digit of the order key (512 bins
+//     a digit) down to one value, as is all below the bins when a cut lies there;
 //     among ids of one value the j-th in id order is found by an ordered count;
 //  4. the kept masses by warp and CTA, the draw inside the warp that holds it;
 //  5. q.
+//
+// Measured (calls replayed from a graph; GB300): 1 row of 32000 fp32, k 50, p 0.95:
+// 11 us; 8 rows of 128256 bf16, p 0.9: 30 us; 256 rows of 128256 bf16, k 1000, p
+// 0.9, min-p 0.01, with q: 137 us; 256 rows of 151936 bf16 at temperature alone, with
+// q: 80 us = 2.9 TB/s.  Without cuts bound by issue (43 % of the slots, some 40
+// instructions an id, half of them the mass) and the waves of clusters; with cuts by
+// the chain of steps of a row (about 25 us: 5 load, 5 counts, 3 list, 9 one CTA's
+// settling, 3 q, the rest barriers of 0.7 us each), four CTAs an SM.
+// What the parts were worth on 256 rows of 128256 with every filter: 614 us as first
+// built (masses in bins, digit by digit over a list); 572 -> 369 bins of the value
+// instead of digits of the key; 284 counts first, masses only where the cut may lie;
+// 184 lists and ranked candidates; 151 one CTA settling; 137 asynchronous copies.
 #pragma once
 
 #include <type_traits>
@@ -115,7 +127,7 @@ struct SampleBins {
     uint32_t scnt[kSmMaxWarps];
     // where a target was found: bin (or -1), and what lies before and in it
     int bin;
-    unsigned long long bmass_before, bmass_at;
+    unsigned long long bmass_before;
     uint32_t bcnt_before, bcnt_at;
     int32_t nth;
     SampleCutAt cut;
