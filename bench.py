@@ -81,7 +81,8 @@ def kernel_source_hash(only: str | None = None) -> str:
     """Hash of device code, with // comments, trailing blanks and empty lines
     removed (they do not change a kernel).  Default: the verification
     kernels, i.e. every .cuh file but those of the top-k / top-p filter, the
-    LM head (bf16 and e4m3), the last norms and the tree walk (the C ABI's
+    LM head (bf16, e4m3 and 4-bit), the last norms, 4-bit quantisation, the draw
+    of tokens and the tree walk (the C ABI's
     host code in spec_verify.cu is left out).  only="sv_lmhead.cuh" (or another of those files): that file
     and the verification kernels it includes."""
     h = hashlib.sha256()

@@ -789,13 +789,17 @@ bool lm4_scale_map(CUtensorMap *map, const void *base, int64_t tiles, uint32_t b
 
 // How a product is cut: a function of (M, V).  A stage (256 hidden dims) of a tile
 // costs an SM the largest of
-//   the MMAs' time, 2 cycles an id (4 steps of 64 dims);
-//   what it loads: a row of h or of W is 128 bytes with 16 of scales, at about 45
-//   bytes a cycle from L2 -- and with one row tile, where W comes from memory
-//   once, 23 bytes a cycle and SM for W.
-// Pairs load half as much of W a row; lone CTAs do not keep half of a pair idle
-// where the rows end in its first half.  Narrower tiles on ties: they reach more
-// SMs.
+//   the MMAs' time, 2 cycles an id and row tile (4 steps of 64 dims);
+//   what it loads, 128 bytes and 16 of scales for each row of h and of W, at the rate
+//   that was measured of each shape: 55 bytes a cycle for lone CTAs, 45 for pairs, 42
+//   for pairs with two row tiles (whose accumulators are not read behind the next
+//   tile's MMAs: half a tile more at the end);
+//   with one row tile, where W comes from memory once, 23 bytes a cycle for W.
+// Narrower tiles on ties: they reach more SMs.  The three shapes, replayed, d 4096
+// (two row tiles, pairs, lone CTAs; the rule's choice starred):
+//   V 128256: M 384 98* 105 101 us; M 576 182 154 149*; M 1024 184* 204 244; M 2304 397* 462 519;
+//   V 32000: M 257 37 35 31*; M 576 48 44* 45; M 1024 60 56* 65; M 2304 113* 116 135;
+//   M 131, V 128256: pairs 59*, lone CTAs 69.
 struct Lm4Plan {
     bool pair;
     int32_t H;          // row tiles that share a pair's tile of W
@@ -811,17 +815,23 @@ Lm4Plan lm4_plan(int64_t M, int32_t V)
     for (int shape = M > 2 * sv::kLmBM ? 2 : (M > sv::kLmBM ? 1 : 0); shape >= 0; --shape) { // H 2, pair, lone CTA
         const bool pair = shape > 0;
         const int32_t H = shape == 2 ? 2 : 1;
-        const int64_t units = pair ? kNominalSms / 2 : kNominalSms;
+        const int64_t units = pair ? kNominalSms / 2 : kNominalSms, rate = shape == 2 ? 42 : (pair ? 45 : 55);
         const int32_t rt = static_cast<int32_t>(ceil_div(M > 0 ? M : 1, pair ? 2 * sv::kLmBM : sv::kLmBM));
         const int32_t mt = static_cast<int32_t>(ceil_div(rt, H));
         int64_t low = INT64_MAX;
         int32_t NB = 0;
         for (int32_t nb = sv::kL4MaxNB; nb >= 64; nb -= 64) {
-            const int64_t w = 144 * (pair ? nb / 2 : nb), loads = (H * 144 * rows + w) / 45;
-            int64_t stage = mt == 1 ? w / 23 : 0;
-            stage = stage > loads ? stage : loads;
-            stage = stage > 2 * nb * H ? stage : 2 * nb * H;
-            const int64_t cost = ceil_div(mt * ceil_div(V, nb), units) * (stage + 40);
+            const int64_t w = 144 * (pair ? nb / 2 : nb);
+            auto stage = [&](int64_t h) { // of a group of h row tiles
+                int64_t c = (h * 144 * rows + w) / rate;
+                c = c > 2 * nb * h ? c : 2 * nb * h;
+                return mt == 1 && c < w / 23 ? w / 23 : c;
+            };
+            // the mean of a unit's tiles; where the units are a multiple of the groups, some units
+            // get full groups only
+            const int64_t tile =
+                (units % mt == 0 ? stage(H) : (rt / H * stage(H) + (rt % H ? stage(1) : 0)) / mt) + 40;
+            const int64_t cost = ceil_div(mt * ceil_div(V, nb), units) * tile + (H == 2 ? tile / 2 : 0);
             if (cost <= low) {
                 low = cost;
                 NB = nb;
@@ -940,11 +950,14 @@ cudaError_t lm4_launch(const void *hidden, const void *hidden_scales, const floa
     L.blocks = p.NB > 128 ? 2 : 1;
     L.t.stage_bytes = static_cast<int32_t>((p.H * L.t.a_rows + brows) * 128 + per_stage * 512 * (p.H + L.blocks));
     L.t.stage_bytes = (L.t.stage_bytes + 1023) / 1024 * 1024;
-    L.t.stages = sv::kL4RingBytes / L.t.stage_bytes;
+    L.t.tma = (V % 8 == 0 && aligned(logits, 16)) ? 1 : 0;
+    L.front = sv::l4_front(L.t.tma != 0);
+    const int32_t ring = sv::kL4Bytes - L.front;
+    L.t.stages = ring / L.t.stage_bytes;
     if (L.t.stages > sv::kL4MaxStages)
         L.t.stages = sv::kL4MaxStages;
     // (the last stage's first rows and what the MMA reads behind them lie in the ring)
-    while ((L.t.stages - 1) * L.t.stage_bytes + (p.H - 1) * L.t.a_rows * 128 + sv::kLmBM * 128 > sv::kL4RingBytes)
+    while ((L.t.stages - 1) * L.t.stage_bytes + (p.H - 1) * L.t.a_rows * 128 + sv::kLmBM * 128 > ring)
         --L.t.stages;
     CUtensorMap m[5] = {};
     if (!lm_tensor_map(&m[0], hidden, M, d / 2, static_cast<uint32_t>(L.t.a_rows), true) ||
@@ -961,7 +974,6 @@ cudaError_t lm4_launch(const void *hidden, const void *hidden_scales, const floa
     L.t.NT = p.NT;
     L.t.NB = p.NB;
     L.t.logits = static_cast<uint16_t *>(logits);
-    L.t.tma = (V % 8 == 0 && aligned(logits, 16)) ? 1 : 0;
     if (L.t.tma && !lm_tensor_map(&m[4], logits, M, V, 32, false, 32))
         return cudaErrorInvalidValue;
     L.t.status = status;
@@ -1630,7 +1642,9 @@ sv_status_t sv_sample_logits(const void *logits, sv_dtype_t logits_dtype, const 
     P.c_hi = static_cast<float>(c);
     P.c_lo = static_cast<float>(c - static_cast<double>(P.c_hi));
     P.cq = static_cast<float>(c / 32);
-    P.dmin = static_cast<float>(-48 * 32 / c);
+    const int fb = 62 - ceil_log2_u64(static_cast<uint64_t>(V) + 1);
+    P.fix = fb < 45 ? fb : 45;
+    P.dmin = static_cast<float>(-(P.fix + 3) * 32 / c); // (a shift by 62 bits: nothing is left)
     // 24 octaves of mass, and 16 of logits at least where top-k counts ids without mass
     const double low = top_k > 0 ? 16.0 : 0.0, octaves = 24 * 32 / c, range = octaves > low ? octaves : low;
     P.bins = static_cast<float>(sv::kSmBins / range);
@@ -1661,8 +1675,6 @@ sv_status_t sv_sample_logits(const void *logits, sv_dtype_t logits_dtype, const 
     P.probs = probs;
     P.status = status_dev;
     P.vec_q = aligned(logits, 16) && aligned(probs, 16);
-    const int fb = 62 - ceil_log2_u64(static_cast<uint64_t>(V) + 1);
-    P.fix = fb < 45 ? fb : 45;
     // a CTA's ids of a bin add up in 32 bits: 15 bits of up to 2^16 ids each, or (rows
     // of more than 2^19, up to 2^18 a CTA, and then fix <= 42) 14
     P.piece = V <= (1 << 19) ? 15 : 14;

@@ -35,9 +35,8 @@
 // tensor pipe was 75 % active at 5.0 PFLOP/s, so 64 dims an MMA give it 6.7 at
 // most); 532 with one row tile a pair and five stages.  M 64, V 128256, d 2048: 27 us
 // = 5.7 TB/s; M 1, V 32000, d 4096: 16 us = 4.5 TB/s, bound by the weights' bytes and
-// some 5 us of launch, first loads and last tile.  M 131, V 32003, d 1056: 19 us,
-// three tiles a pair and odd rows' plain stores (16.6 with 96 ids staged at a time,
-// for which the ring that many rows want leaves no room).
+// some 5 us of launch, first loads and last tile.  M 131, V 32003, d 1056: 17 us,
+// three tiles a pair and odd rows' plain stores.
 // With three quarters of the MMAs left out the first case took 463 instead of 532 us,
 // without the scales' copies 496, with one stage's lines loaded again and again 508.
 #pragma once
@@ -53,18 +52,25 @@ constexpr int kL4Threads = 64 + 32 * kL4EpiWarps;
 constexpr int kL4MaxStages = 8;
 constexpr uint32_t kL4TmemCols = 512;
 constexpr uint32_t kL4ScaleCol = 2 * kL4MaxNB; // first of 2 x 64 scale columns
-// Shared memory: a box of 32 rows x 32 logits and 32 factors for each epilogue warp,
-// then the ring, behind whose last stage lm4_launch leaves what the MMA reads of its
-// 128 rows where a stage has fewer.
-constexpr int kL4StgBytes = kL8BoxBytes;
-constexpr int kL4Front = kL4EpiWarps * (kL4StgBytes + 128);
-constexpr int kL4RingBytes = 208 * 1024;
-constexpr int kL4Smem = 1024 + kL4Front + kL4RingBytes;
-static_assert(kL4Front % 1024 == 0 && kL4Smem <= 227 * 1024 - 512, "shared memory of a CTA, less the barriers");
+// Shared memory: what the epilogue warps stage, 32 factors for each of them, then the
+// ring, behind whose last stage lm4_launch leaves what the MMA reads of its 128 rows
+// where a stage has fewer.  Tensor stores take a box of 32 rows x 32 logits at a time;
+// rows that are no whole 16-byte units leave by plain stores (l8_store_rows), half a
+// tile's 96 logits at a time, since each row's two ends go logit by logit (box by box
+// 19.0 instead of 16.6 us at M 131, V 32003), and the ring has 32 KiB less.
+constexpr int kL4Gws = kL4EpiWarps * 128;
+constexpr int kL4StgTma = kL8BoxBytes, kL4StgPlain = kL4MaxNB / 64 * kL8BoxBytes; // of a warp
+constexpr int kL4Bytes = 225 * 1024;                                              // staged, factors, ring
+constexpr int kL4Smem = 1024 + kL4Bytes;
+static_assert(kL4Smem <= 227 * 1024 - 512, "shared memory of a CTA, less the barriers");
+// the ring's place: a multiple of 1024
+inline int l4_front(bool tma) { return kL4EpiWarps * (tma ? kL4StgTma : kL4StgPlain) + kL4Gws; }
+static_assert(kL4EpiWarps * kL4StgTma % 1024 == 0 && kL4EpiWarps * kL4StgPlain % 1024 == 0 && kL4Gws == 1024, "swizzled tiles");
 
 struct Lm4Params {
     Lm8Params t;              // M, N, tiles (MT: groups of row tiles), logits, status (its own scales and sums unused)
     int32_t RT;               // row tiles
+    int32_t front;            // bytes of shared memory before the ring
     int32_t d;                // hidden dims
     int32_t KT;               // scale tiles along d
     int32_t blocks;           // scale tiles across a tile's ids: 1 or 2
@@ -133,45 +139,6 @@ __device__ __forceinline__ float4 l4_lds4(uint32_t addr)
 // x, NaN if it is infinite: -inf is a masked token to what reads the logits.
 __device__ __forceinline__ float l4_finite(float x) { return __fmaf_rn(x, 0.0f, x); }
 
-// A staged box (ncols <= 32 ids of rows row0 ..) by plain stores, at whatever
-// alignment its rows have: their whole 16-byte units, 4 lanes a row, each shifted
-// out of two staged units; then the logits before the first and behind the last
-// unit (8 a row, or up to 14 where the vocabulary ends), 8 lanes a row.
-__device__ __forceinline__ void l4_store_box(const Lm8Params &T, uint32_t box, int row0, int n, int ncols, int lane)
-{
-    const int rows = T.M - row0 < 32 ? T.M - row0 : 32;
-    uint16_t *const dst0 = T.logits + static_cast<int64_t>(row0) * T.N + n;
-    auto columns_before_unit = [&](const uint16_t *dst) {
-        return (8 - static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 1)) & 7;
-    };
-    const int u = (lane & 3) * 8;
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-        const int r = it * 8 + (lane >> 2);
-        const uint4 lo = l8_staged4(l8_staged_at(box, r, u)), hi = l8_staged4(l8_staged_at(box, r, u < 24 ? u + 8 : u));
-        uint16_t *dst = dst0 + static_cast<int64_t>(r) * T.N;
-        const int lead = columns_before_unit(dst);
-        if (r < rows && u + lead + 8 <= ncols)
-            *reinterpret_cast<uint4 *>(dst + u + lead) = l8_shift(lo, hi, lead);
-    }
-    const int c = lane & 7;
-#pragma unroll
-    for (int it = 0; it < 8; ++it) {
-        const int r = it * 4 + (lane >> 3);
-        uint16_t *dst = dst0 + static_cast<int64_t>(r) * T.N;
-        const int lead = columns_before_unit(dst);
-        const int units = ncols > lead ? (ncols - lead) >> 3 : 0, edges = ncols - units * 8, first = lead < ncols ? lead : ncols;
-        if (r < rows && c < edges) {
-            const int p = c < first ? c : units * 8 + c;
-            dst[p] = l8_staged1(l8_staged_at(box, r, p));
-        }
-        if (r < rows && c + 8 < edges) {
-            const int p = c + 8 < first ? c + 8 : units * 8 + c + 8;
-            dst[p] = l8_staged1(l8_staged_at(box, r, p));
-        }
-    }
-}
-
 // The epilogue warps: warp w holds the tile's rows of tensor-memory lane quarter
 // w mod 4, and the first or the second half of its ids.
 template <bool PAIR, int H>
@@ -182,8 +149,8 @@ __device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMa
     const Lm8Params &T = P.t;
     const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31u), lq = warp & 3;
     const int half = (warp - 2) >> 2, G = T.NB / 64; // groups of 32 ids: 1, 2 or 3
-    const uint32_t stg = stg0 + static_cast<uint32_t>(warp - 2) * kL4StgBytes;
-    const uint32_t gws = stg0 + kL4EpiWarps * kL4StgBytes + static_cast<uint32_t>(warp - 2) * 128u;
+    const uint32_t stg = stg0 + static_cast<uint32_t>((warp - 2) * (T.tma ? kL4StgTma : kL4StgPlain));
+    const uint32_t gws = stg0 + static_cast<uint32_t>(P.front - kL4Gws + (warp - 2) * 128);
     const uint32_t te = PAIR ? lm_mapa(tempty, 0) : tempty;
     bool alive = true, sent = false;
     uint32_t i = 0; // row tiles so far: accumulator i mod 2
@@ -244,7 +211,7 @@ __device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMa
                 if (T.tma && sent) // the last store has read the box
                     l8_stores_read();
                 __syncwarp();
-                l8_stage(stg, pk, lane);
+                l8_stage(T.tma ? stg : stg + g * kL8BoxBytes, pk, lane);
                 const int n = n0 + 32 * g;
                 if (T.tma) {
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -254,15 +221,15 @@ __device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMa
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     }
                     sent = true;
-                } else {
-                    __syncwarp();
-                    uint32_t boxes = stg;
-                    l8_staged_now(boxes);
-                    if (n < T.N)
-                        l4_store_box(T, boxes, row0, n, T.N - n < 32 ? T.N - n : 32, lane);
-                    __syncwarp();
                 }
             }
+        }
+        if (in && !T.tma) {
+            __syncwarp();
+            uint32_t boxes = stg;
+            l8_staged_now(boxes);
+            l8_store_rows(T, boxes, row0, n0, T.N - n0 < G * 32 ? T.N - n0 : G * 32, lane);
+            __syncwarp();
         }
         if (!in) {
             lm_tc_before();
@@ -296,7 +263,7 @@ __global__ void __launch_bounds__(kL4Threads, 1)
     __shared__ int stop;
     const Lm8Params &T = P.t;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(lm_smem_raw) + 1023) & ~uintptr_t{1023});
-    const uint32_t front = smem_addr(smem), sbase = front + kL4Front;
+    const uint32_t front = smem_addr(smem), sbase = front + static_cast<uint32_t>(P.front);
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? lm_cluster_rank() : 0u;
     const bool leader = rank == 0;

@@ -68,7 +68,7 @@ struct SampleParams {
     const float *u;      // [rows]
     float c_hi, c_lo;    // 32 log2(e) / T
     float cq;            // log2(e) / T
-    float dmin;          // differences below this have no mass: -48 T ln 2
+    float dmin;          // differences below this have no mass: -(fix + 3) T ln 2
     float bins, width;   // bins of step 2 per unit of the logits, and a bin's width
     double min_off;      // T ln(min_p) (min_p > 0)
     int32_t top_k;       // <= 0: off

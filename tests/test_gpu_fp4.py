@@ -105,6 +105,27 @@ def test_quantize_alignment_leading_dims_and_out():
     assert sv.sv_dequantize_fp4(t, F32, out=back) is back and torch.equal(back, sv.sv_dequantize_fp4(t, F32))
 
 
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("M,d", [(5, 30), (130, 256), (3, 9000)])
+def test_nothing_is_written_beside_the_outputs(block, M, d):
+    x = _x(M, d, BF).to(DEV)
+    n = -(-M // 128) * -(-d // (4 * block)) * 512
+    v = torch.full((M * (d // 2) + 128,), 0xA5, dtype=torch.uint8, device=DEV)
+    s = torch.full((n + 128,), 0xA5, dtype=torch.uint8, device=DEV)
+    g = torch.full((M + 2,), 77.0, device=DEV)
+    t = sv.Fp4Tensor(v[64:-64].view(M, d // 2),
+                     s[64:-64].view(torch.float8_e4m3fn if block == 16 else torch.float8_e8m0fnu).view(
+                         -(-M // 128), -(-d // (4 * block)), 32, 4, 4), g[1:-1] if block == 16 else None)
+    sv.sv_quantize_fp4(x, block, out=t)
+    _check_quantized(x.cpu(), block, t)
+    for b in (v, s):
+        assert (b[:64] == 0xA5).all() and (b[-64:] == 0xA5).all()
+    assert g[0] == 77 and g[-1] == 77
+    out = torch.full((M * d + 16,), 77.0, dtype=BF, device=DEV)
+    sv.sv_dequantize_fp4(t, out=out[8:-8].view(M, d))
+    assert (out[:8] == 77).all() and (out[-8:] == 77).all()
+
+
 def test_no_rows():
     for block in (16, 32):
         t = sv.sv_quantize_fp4(torch.empty((0, 64), device=DEV), block)

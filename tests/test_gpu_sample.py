@@ -191,6 +191,25 @@ def test_given_outputs_leading_dims_and_no_rows():
     assert e.tokens.shape == (0, 4)
 
 
+@pytest.mark.parametrize("rows,V", [(3, 4099), (330, 4099), (2, 151936)])
+def test_nothing_is_written_beside_the_outputs(rows, V):
+    z = _logits(rows, V, BF, 3.0, seed=rows)
+    z[1] = float("nan")
+    buf = {"tokens": torch.full((rows + 2,), -77, dtype=torch.int32, device=DEV),
+           "kept": torch.full((rows + 2,), -77, dtype=torch.int32, device=DEV),
+           "prob": torch.full((rows + 2,), -77.0, device=DEV), "probs": torch.full((rows * V + 2 * 64,), -77.0, device=DEV)}
+    o = {k: v[1:-1] for k, v in buf.items() if k != "probs"}
+    o["probs"] = buf["probs"][64:-64].view(rows, V)
+    zd, u = z.to(DEV), torch.rand(rows, device=DEV)
+    before = zd.clone()
+    for f in (dict(), dict(top_k=50), dict(top_k=600, top_p=0.9), dict(top_p=0.99), dict(min_p=0.1)):
+        sv.sv_sample_logits(zd, u, 0.8, out=o, **f)
+        for k, v in buf.items():
+            edge = 64 if k == "probs" else 1
+            assert (v[:edge] == -77).all() and (v[-edge:] == -77).all() and not (o[k] == -77).any(), k
+    assert torch.equal(zd.view(torch.int16), before.view(torch.int16))
+
+
 def test_rows_do_not_depend_on_the_batch():
     z = _logits(200, 4000, BF, seed=12).to(DEV)
     u = torch.rand(200, device=DEV)
