@@ -235,6 +235,9 @@ def test_large_batches(dtype, V, filt):
     z[8, 0] = 200.0                               # all mass in one id
     z[9] *= 0.05
     z[10, 7], z[11, :] = float("nan"), -np.inf
+    z[13], z[14] = -50.0, -50.0
+    z[13, 1:1 + 600 * (V // 700):V // 700] = 5.0  # more equal ids than are ranked, fewer than one CTA settles
+    z[14, :700] = torch.linspace(3.0, 3.02, 700).to(dtype)   # as many in one bin or two
     zd = z.to(DEV)
     u = torch.from_numpy(np.random.default_rng(V).random(rows, dtype=np.float32)).to(DEV)
     u[12] = 1.0
