@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kF4Threads, kF4Ctas<XT>) quantize_fp4_kernel(c
             }
             const int32_t i = first + t * stride;
             if (lane % L == 0 && i < P.octets)
-                s0[t * (stride / (4 * L)) * 512] = static_cast<uint8_t>(byte);
+                s0[static_cast<int64_t>(t) * ((stride / (4 * L)) * 512)] = static_cast<uint8_t>(byte);
             const int32_t left = real ? P.d - i * 8 : 0;
             uint8_t *v = v0 + t * stride * 4;
             if (VEC) {
