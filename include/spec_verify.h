@@ -437,6 +437,7 @@ sv_status_t sv_quantize_fp8(const void *x, sv_dtype_t x_dtype, int64_t rows,
  *   row_scales [rows] fp32 out (block 16), NULL for block 32.
  * sv_dequantize_fp4 reads the form back: value * scale * row scale, in fp32,
  * rounded to out_dtype (bf16 or fp32); row_scales there may be any numbers.
+ * Rows and d are at most 2^31 - 128 and 2^31 - 1025 (SV_EUNSUPPORTED beyond);
  * sv_fp4_scale_bytes is 0 for sizes that are refused.  One launch each on
  * `stream`; allocate nothing. */
 size_t sv_fp4_scale_bytes(int64_t rows, int32_t d, int32_t block);

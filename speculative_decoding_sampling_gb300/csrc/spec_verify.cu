@@ -777,6 +777,10 @@ constexpr size_t kSampleSmem = 227 * 1024 - sizeof(sv::SampleShared) - 1024;
 
 // ------------------------------------------------------- 4-bit operands
 
+// A row's steps and a matrix's rows of tiles are counted in 32 bits.
+constexpr int64_t kFp4MaxRows = INT32_MAX - 127;
+constexpr int32_t kFp4MaxD = INT32_MAX - 1024;
+
 // Scale tiles (128 rows x 4 blocks) along d.
 int32_t fp4_tiles(int32_t d, int32_t block) { return static_cast<int32_t>(ceil_div(d, 4 * static_cast<int64_t>(block))); }
 
@@ -1527,7 +1531,7 @@ sv_status_t sv_quantize_fp8(const void *x, sv_dtype_t x_dtype, int64_t rows, int
 
 size_t sv_fp4_scale_bytes(int64_t rows, int32_t d, int32_t block)
 {
-    if (rows < 0 || rows > INT32_MAX || d < 2 || d % 2 != 0 || (block != 16 && block != 32))
+    if (rows < 0 || rows > kFp4MaxRows || d < 2 || d > kFp4MaxD || d % 2 != 0 || (block != 16 && block != 32))
         return 0;
     return static_cast<size_t>(ceil_div(rows, 128)) * static_cast<size_t>(fp4_tiles(d, block)) * 512;
 }
@@ -1537,7 +1541,7 @@ sv_status_t sv_quantize_fp4(const void *x, sv_dtype_t x_dtype, int64_t rows, int
 {
     if (rows < 0 || d < 2 || d % 2 != 0 || !is_bf16_or_fp32(x_dtype) || (block != 16 && block != 32))
         return SV_EINVAL;
-    if (rows > INT32_MAX - 127 || d > INT32_MAX - 1024)
+    if (rows > kFp4MaxRows || d > kFp4MaxD)
         return SV_EUNSUPPORTED;
     if (rows == 0)
         return SV_OK;
@@ -1571,7 +1575,7 @@ sv_status_t sv_dequantize_fp4(const void *values, const void *scales, const floa
 {
     if (rows < 0 || d < 2 || d % 2 != 0 || !is_bf16_or_fp32(out_dtype) || (block != 16 && block != 32))
         return SV_EINVAL;
-    if (rows > INT32_MAX - 127 || d > INT32_MAX - 1024)
+    if (rows > kFp4MaxRows || d > kFp4MaxD)
         return SV_EUNSUPPORTED;
     if (rows == 0)
         return SV_OK;
