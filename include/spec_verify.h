@@ -456,8 +456,8 @@ sv_status_t sv_dequantize_fp4(const void *values, const void *scales,
  * block scales exact, the order of summation theirs), the row scales (any fp32
  * numbers; NULL for block 32) multiplied to it in fp32, and the result rounded
  * once to bf16, nearest even.  A NaN scale gives NaN logits in the rows or ids
- * it belongs to, and a result outside the fp32 range is NaN, never infinite (-inf
- * is a masked token); verification and draw report such a row as SV_BAD_ROW.
+ * it belongs to, and a result that rounds to no finite bf16 value is NaN, never
+ * infinite (-inf is a masked token); verification and draw report such a row as SV_BAD_ROW.
  *   hidden         [M, d / 2] bytes, hidden_scales its tiles, both 16-byte
  *                  aligned; lm_head [V, d / 2] and lm_head_scales likewise;
  *   logits         [M, V] bf16 out (16-byte aligned with V % 8 == 0 for the

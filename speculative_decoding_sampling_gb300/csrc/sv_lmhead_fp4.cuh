@@ -136,8 +136,16 @@ __device__ __forceinline__ float4 l4_lds4(uint32_t addr)
     return r;
 }
 
-// x, NaN if it is infinite: -inf is a masked token to what reads the logits.
-__device__ __forceinline__ float l4_finite(float x) { return __fmaf_rn(x, 0.0f, x); }
+// Two logits, NaN where bf16 cannot hold them (-inf is a masked token to what reads
+// them): an infinity, of the product or of its rounding, times 0 is NaN, and x * 0 + x
+// is x for the others.
+__device__ __forceinline__ uint32_t l4_round(float x0, float x1)
+{
+    const uint32_t p = bf16_rn_pair(x0, x1);
+    uint32_t r;
+    asm("{\n\t.reg .b32 z;\n\tmov.b32 z, 0;\n\tfma.rn.bf16x2 %0, %1, z, %1;\n\t}" : "=r"(r) : "r"(p));
+    return r;
+}
 
 // The epilogue warps: warp w holds the tile's rows of tensor-memory lane quarter
 // w mod 4, and the first or the second half of its ids.
@@ -201,12 +209,12 @@ __device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMa
                     float4 w = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
                     if (P.gh)
                         w = l4_lds4(gws + static_cast<uint32_t>(4 * k) * 4u);
-                    const float x0 = l4_finite(__fmul_rn(__uint_as_float(x[4 * k]), __fmul_rn(gh, w.x)));
-                    const float x1 = l4_finite(__fmul_rn(__uint_as_float(x[4 * k + 1]), __fmul_rn(gh, w.y)));
-                    const float x2 = l4_finite(__fmul_rn(__uint_as_float(x[4 * k + 2]), __fmul_rn(gh, w.z)));
-                    const float x3 = l4_finite(__fmul_rn(__uint_as_float(x[4 * k + 3]), __fmul_rn(gh, w.w)));
-                    pk[2 * k] = bf16_rn_pair(x0, x1);
-                    pk[2 * k + 1] = bf16_rn_pair(x2, x3);
+                    const float x0 = __fmul_rn(__uint_as_float(x[4 * k]), __fmul_rn(gh, w.x));
+                    const float x1 = __fmul_rn(__uint_as_float(x[4 * k + 1]), __fmul_rn(gh, w.y));
+                    const float x2 = __fmul_rn(__uint_as_float(x[4 * k + 2]), __fmul_rn(gh, w.z));
+                    const float x3 = __fmul_rn(__uint_as_float(x[4 * k + 3]), __fmul_rn(gh, w.w));
+                    pk[2 * k] = l4_round(x0, x1);
+                    pk[2 * k + 1] = l4_round(x2, x3);
                 }
                 if (T.tma && sent) // the last store has read the box
                     l8_stores_read();
