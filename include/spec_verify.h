@@ -454,8 +454,9 @@ sv_status_t sv_dequantize_fp4(const void *values, const void *scales,
  *       * sum_k (hidden * its scale)[m, k] * (lm_head * its scale)[v, k]
  * The sum over all of d is formed by the tensor cores in fp32 (products and
  * block scales exact, the order of summation theirs), the row scales (any fp32
- * numbers; NULL for block 32) multiplied to it in fp32, and the result rounded
- * once to bf16, nearest even.  A NaN scale gives NaN logits in the rows or ids
+ * numbers; NULL for block 32) multiplied to it with two roundings to fp32 at
+ * most, whatever the product of the two scales alone comes to, and the result
+ * rounded once to bf16, nearest even.  A NaN scale gives NaN logits in the rows or ids
  * it belongs to, and a result that rounds to no finite bf16 value is NaN, never
  * infinite (-inf is a masked token); verification and draw report such a row as SV_BAD_ROW.
  *   hidden         [M, d / 2] bytes, hidden_scales its tiles, both 16-byte

@@ -26,6 +26,8 @@
 // Warps 2..9 are the epilogue, two for each 32 rows: two accumulators, so that a
 // tile is read, scaled and stored (box by box through shared memory, as for e4m3)
 // while the next is formed.
+// Where a product of two factors may leave fp32's range a tile goes a way of its own
+// (by way of fp64; inside the usual one it took M 131 from 16.3 to 17.3 us).
 // 512 tensor-memory columns: 2 x 192 of sums, 2 x 64 of scales, hence NB <= 192.
 // (A set: 16 columns for each row tile, 32 for the ids.)  Ids start at a multiple of
 // 64 of their scale tile: two columns.
@@ -40,6 +42,8 @@
 // With three quarters of the MMAs left out the first case took 463 instead of 532 us,
 // without the scales' copies 496, with one stage's lines loaded again and again 508.
 #pragma once
+
+#include <type_traits>
 
 #include "sv_lmhead_fp8.cuh"
 
@@ -147,6 +151,23 @@ __device__ __forceinline__ uint32_t l4_round(float x0, float x1)
     return r;
 }
 
+// Whether a factor is 0 or in [2^-63, 2^64): the product of two such is 0 by a factor or
+// in fp32's normal range.
+__device__ __forceinline__ bool l4_mild(float f)
+{
+    const uint32_t b = __float_as_uint(f) & 0x7FFFFFFFu;
+    return b == 0 || b - 0x20000000u < 0x3F800000u;
+}
+// x gh gw.  WIDE: where gh gw leaves that range although the whole need not, by way of
+// fp64, in which the product of the factors is exact; elsewhere what the short way gives.
+template <bool WIDE> __device__ __forceinline__ float l4_scaled(float x, float gh, float gw)
+{
+    const float p = __fmul_rn(gh, gw);
+    if (WIDE && (__float_as_uint(p) & 0x7FFFFFFFu) - 0x00800000u >= 0x7F000000u)
+        return static_cast<float>(static_cast<double>(x) * (static_cast<double>(gh) * static_cast<double>(gw)));
+    return __fmul_rn(x, p);
+}
+
 // The epilogue warps: warp w holds the tile's rows of tensor-memory lane quarter
 // w mod 4, and the first or the second half of its ids.
 template <bool PAIR, int H>
@@ -181,56 +202,86 @@ __device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMa
             break;
         lm_tc_after();
         const bool in = row0 < T.M && n0 < T.N;
+        bool mild = true;
+        if (P.gh) {
+            mild = l4_mild(gh);
+#pragma unroll
+            for (int g = 0; g < kL4MaxNB / 64; ++g)
+                mild = mild && l4_mild(gw[g]);
+            mild = __all_sync(0xFFFFFFFFu, mild);
+        }
         const uint32_t tl = tbase + (static_cast<uint32_t>(lq) << 21) + a * kL4MaxNB + static_cast<uint32_t>(half * G * 32);
         uint32_t v[2][32]; // the next group is on its way while one is scaled
-        if (in)
+        // the ids' factors of a group, read by every lane
+        auto put_factors = [&](float f) {
+            if (P.gh) {
+                __syncwarp();
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(gws + static_cast<uint32_t>(lane) * 4u), "f"(f) : "memory");
+                __syncwarp();
+            }
+        };
+        auto release = [&] { // this warp has read the accumulator
+            lm_tc_before();
+            __syncwarp();
+            if (lane == 0)
+                l8_arrive(te + a * 8u);
+        };
+        // group g's sums times their factors (in WIDE form where the product of two may leave
+        // fp32's range), rounded, staged and sent
+        auto group = [&](int g, const uint32_t (&x)[32], auto wide) {
+            constexpr bool WIDE = decltype(wide)::value;
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float4 w = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+                if (P.gh)
+                    w = l4_lds4(gws + static_cast<uint32_t>(4 * k) * 4u);
+                pk[2 * k] = l4_round(l4_scaled<WIDE>(__uint_as_float(x[4 * k]), gh, w.x),
+                                     l4_scaled<WIDE>(__uint_as_float(x[4 * k + 1]), gh, w.y));
+                pk[2 * k + 1] = l4_round(l4_scaled<WIDE>(__uint_as_float(x[4 * k + 2]), gh, w.z),
+                                         l4_scaled<WIDE>(__uint_as_float(x[4 * k + 3]), gh, w.w));
+            }
+            if (T.tma && sent) // the last store has read the box
+                l8_stores_read();
+            __syncwarp();
+            l8_stage(T.tma ? stg : stg + g * kL8BoxBytes, pk, lane);
+            const int n = n0 + 32 * g;
+            if (T.tma) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (l8_elect() && n < T.N) {
+                    l8_send(map, stg, n, row0);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                }
+                sent = true;
+            }
+        };
+        if (in && mild) {
             l8_ld_start(tl, v[0]);
 #pragma unroll
-        for (int g = 0; g < kL4MaxNB / 64; ++g) {
-            if (in && g < G) {
-                uint32_t(&x)[32] = v[g & 1];
-                if (P.gh) {
-                    __syncwarp();
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(gws + static_cast<uint32_t>(lane) * 4u), "f"(gw[g]) : "memory");
-                    __syncwarp();
-                }
-                l8_ld_wait(x);
-                if (g + 1 < G) {
-                    l8_ld_start(tl + 32 * (g + 1), v[(g + 1) & 1]);
-                } else { // this warp has read the accumulator
-                    lm_tc_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        l8_arrive(te + a * 8u);
-                }
-                uint32_t pk[16];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    float4 w = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-                    if (P.gh)
-                        w = l4_lds4(gws + static_cast<uint32_t>(4 * k) * 4u);
-                    const float x0 = __fmul_rn(__uint_as_float(x[4 * k]), __fmul_rn(gh, w.x));
-                    const float x1 = __fmul_rn(__uint_as_float(x[4 * k + 1]), __fmul_rn(gh, w.y));
-                    const float x2 = __fmul_rn(__uint_as_float(x[4 * k + 2]), __fmul_rn(gh, w.z));
-                    const float x3 = __fmul_rn(__uint_as_float(x[4 * k + 3]), __fmul_rn(gh, w.w));
-                    pk[2 * k] = l4_round(x0, x1);
-                    pk[2 * k + 1] = l4_round(x2, x3);
-                }
-                if (T.tma && sent) // the last store has read the box
-                    l8_stores_read();
-                __syncwarp();
-                l8_stage(T.tma ? stg : stg + g * kL8BoxBytes, pk, lane);
-                const int n = n0 + 32 * g;
-                if (T.tma) {
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (l8_elect() && n < T.N) {
-                        l8_send(map, stg, n, row0);
-                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    }
-                    sent = true;
+            for (int g = 0; g < kL4MaxNB / 64; ++g) {
+                if (g < G) {
+                    put_factors(gw[g]);
+                    l8_ld_wait(v[g & 1]);
+                    if (g + 1 < G)
+                        l8_ld_start(tl + 32 * (g + 1), v[(g + 1) & 1]);
+                    else
+                        release();
+                    group(g, v[g & 1], std::false_type{});
                 }
             }
+        } else if (in) {
+#pragma unroll 1
+            for (int g = 0; g < G; ++g) {
+                put_factors(g == 0 ? gw[0] : (g == 1 ? gw[1] : gw[2]));
+                l8_ld_start(tl + 32 * g, v[0]);
+                l8_ld_wait(v[0]);
+                if (g + 1 == G)
+                    release();
+                group(g, v[0], std::true_type{});
+            }
+        } else {
+            release();
         }
         if (in && !T.tma) {
             __syncwarp();
@@ -238,12 +289,6 @@ __device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMa
             l8_staged_now(boxes);
             l8_store_rows(T, boxes, row0, n0, T.N - n0 < G * 32 ? T.N - n0 : G * 32, lane);
             __syncwarp();
-        }
-        if (!in) {
-            lm_tc_before();
-            __syncwarp();
-            if (lane == 0)
-                l8_arrive(te + a * 8u);
         }
         if (++sub == H || m + 1 == static_cast<uint32_t>(P.RT)) {
             sub = 0;
