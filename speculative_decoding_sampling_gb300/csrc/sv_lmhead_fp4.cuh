@@ -287,7 +287,7 @@ __device__ __forceinline__ void l4_epilogue(const Lm4Params &P, const CUtensorMa
             __syncwarp();
             uint32_t boxes = stg;
             l8_staged_now(boxes);
-            l8_store_rows(T, boxes, row0, n0, T.N - n0 < G * 32 ? T.N - n0 : G * 32, lane);
+            l8_store_rows<kL4MaxNB / 64>(T, boxes, row0, n0, T.N - n0 < G * 32 ? T.N - n0 : G * 32, lane);
             __syncwarp();
         }
         if (++sub == H || m + 1 == static_cast<uint32_t>(P.RT)) {

@@ -496,13 +496,16 @@ __device__ __forceinline__ uint4 l8_shift(uint4 u, uint4 v, int a)
                       __byte_perm(w[3], w[4], sel));
 }
 
-// A half tile's staged rows (ncols <= 128 ids from n on) by plain stores, at
-// whatever alignment they have: first their whole 16-byte units, 16 lanes a
+// Staged rows (ncols ids from n on, in BOXES boxes of 32; nothing else is read) by plain
+// stores, at whatever alignment they have: first their whole 16-byte units, 16 lanes a
 // row, each shifted out of two staged units; then the logits before the first
 // and behind the last unit (8 a row, or up to 14 where the vocabulary ends),
 // 8 lanes a row.
+template <int BOXES>
 __device__ __forceinline__ void l8_store_rows(const Lm8Params &P, uint32_t boxes, int row0, int n, int ncols, int lane)
 {
+    constexpr int kCols = 32 * BOXES;
+    static_assert(BOXES <= 4, "16 lanes of 8 columns a row");
     const int rows = P.M - row0 < 32 ? P.M - row0 : 32;
     uint16_t *const dst0 = P.logits + static_cast<int64_t>(row0) * P.N + n;
     auto columns_before_unit = [&](const uint16_t *dst) {
@@ -510,13 +513,14 @@ __device__ __forceinline__ void l8_store_rows(const Lm8Params &P, uint32_t boxes
     };
     {
         const int u = (lane & 15) * 8;
+        const int u0 = BOXES == 4 || u < kCols ? u : 0, u1 = u < kCols - 8 ? u + 8 : u0; // (u >= kCols stores nothing)
 #pragma unroll 1
         for (int r0 = lane >> 4; r0 < rows; r0 += 4) {
             uint4 lo[2], hi[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                lo[i] = l8_staged4(l8_staged_at(boxes, (r0 + 2 * i) & 31, u));
-                hi[i] = l8_staged4(l8_staged_at(boxes, (r0 + 2 * i) & 31, u < 120 ? u + 8 : u));
+                lo[i] = l8_staged4(l8_staged_at(boxes, (r0 + 2 * i) & 31, u0));
+                hi[i] = l8_staged4(l8_staged_at(boxes, (r0 + 2 * i) & 31, u1));
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -536,7 +540,7 @@ __device__ __forceinline__ void l8_store_rows(const Lm8Params &P, uint32_t boxes
             const int lead = columns_before_unit(dst0 + static_cast<int64_t>(r0 + 4 * i) * P.N);
             const int units = ncols > lead ? (ncols - lead) >> 3 : 0; // whole units
             const int first = lead < ncols ? lead : ncols, p = c < first ? c : units * 8 + c;
-            v[i] = l8_staged1(l8_staged_at(boxes, (r0 + 4 * i) & 31, p < 128 ? p : 0));
+            v[i] = l8_staged1(l8_staged_at(boxes, (r0 + 4 * i) & 31, p < kCols ? p : 0));
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -604,9 +608,9 @@ __device__ __forceinline__ void l8_finish(const Lm8Params &P, uint32_t tabs, uin
         const int ncols = P.N - n0 < P.NB ? P.N - n0 : P.NB; // at least 1
         if (row0 < P.M) {
             if (!P.tma) {
-                l8_store_rows(P, half0, row0, n0, ncols < 128 ? ncols : 128, lane);
+                l8_store_rows<4>(P, half0, row0, n0, ncols < 128 ? ncols : 128, lane);
                 if (ncols > 128)
-                    l8_store_rows(P, half1, row0, n0 + 128, ncols - 128, lane);
+                    l8_store_rows<4>(P, half1, row0, n0 + 128, ncols - 128, lane);
             }
             if (P.part) {
                 const float2 ms = l8_statistics(P, half0, half1, lane, ncols);
