@@ -499,10 +499,11 @@ sv_status_t sv_lm_head_logits_fp4(
  *             -1, prob and kept 0, probs zeros), SV_BAD_U for a uniform outside
  *             [0, 1) (token -1, prob 0; kept and probs are the row's); may be
  *             NULL.
- * Masses are whole multiples of 2^-45 of the largest (2^-40 at V = SV_MAX_V), right to about 2^-28 of
- * themselves and summed exactly: an id below half a unit may be kept but
- * is never drawn.  A cut or a draw differs from exact arithmetic only where it
- * lies within about 2^-30 of an id's boundary.  Results do not depend on the other
+ * Masses are whole multiples of about 2^-45 of the largest (2^-40 at V =
+ * SV_MAX_V), right to 2^-26 of themselves (2^-28 as a rule) whatever the logits'
+ * sizes, and summed exactly: an id below half a unit may be kept but is never
+ * drawn.  A cut or a draw differs from exact arithmetic only where it lies within
+ * 2^-27 (as a rule 2^-30) of the mass from an id's boundary.  Results do not depend on the other
  * rows of a call.
  * Returns SV_EINVAL (NULL or misaligned pointer, rows < 0, V < 1, T not finite or
  * <= 0 or too far from 1, top_p <= 0 or NaN, min_p outside [0, 1], unknown

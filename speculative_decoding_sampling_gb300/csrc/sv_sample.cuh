@@ -9,10 +9,14 @@
 // first id with u Z < C(id) over the kept masses in id order.
 //
 // Masses are integers, so sums are exact and free of order.  They carry 2^-28 of
-// each value: with t = (z - max) 32 log2(e) / T and k = round(t), r = t - k (t from
-// a factor in two parts; fp32 logits give their difference in two parts too),
-//   e^((z - max) / T) = 2^(k / 32) (1 + x + x^2/2 + x^3/6),  x = r ln(2) / 32,
-// |x| <= 0.0109, the series' rest below 2^-30; 2^(j / 32) comes from a table of 32
+// each value: with c = 32 log2(e) / T, k = round(z c) and r = z c - k,
+//   e^(z / T) = 2^(k / 32) (1 + x + x^2/2 + x^3/6),  x = r ln(2) / 32,
+// of which 2^(k / 32) counts from the whole number next above max c on.  z c - k is
+// one multiply-add with c's high part and one with its low: z - max is not formed,
+// which fp32 cannot hold where the two differ much in size.  Where max c is 2^21 or
+// more the same is done with z - max, which is exact then wherever there is mass (z
+// lies within a factor of 2 of the maximum).
+// |x| <= 0.0122, the series' rest below 2^-30; 2^(j / 32) comes from a table of 32
 // whose entries lie in different banks.  (exp2 in fp32 alone gives 2^-22: among
 // 10^5 ids a draw then falls on a neighbour once in some hundred rows.)
 //
@@ -206,30 +210,37 @@ constexpr float kSmLn1 = 0.021660849392498290f, kSmLn2 = kSmLn1 * kSmLn1 / 2, kS
 
 // What a row's masses are formed with.
 struct SampleRow {
-    float m, c_hi, c_lo, dmin;
-    uint32_t tab;  // shared-memory address of the table
-    int down;      // 59 - fix, and the shift's bits beside k's octaves
-    // The masses of two logits z <= m, in 2^-fix of the maximum's, rounded; 0 for -inf.
+    float m;          // the maximum
+    float off;        // what is taken off a logit first: 0 (or m, rows whose m c is 2^21 or more)
+    float low;        // the least difference that is looked at: below it nothing has mass
+    float shift;      // kSmShift less the whole number next above m c (0 with off m)
+    float c_hi, c_lo;
+    uint32_t tab;     // shared-memory address of the table
+    int down;         // 59 - fix, and the shift's bits beside k's octaves
+    // m and the constants of a call.  c = c_hi + c_lo to 2^-48 of itself.
+    __device__ __forceinline__ void set(float mx, float hi, float lo, float dmin)
+    {
+        m = mx;
+        c_hi = hi;
+        c_lo = lo;
+        const float mc = __fmaf_rn(mx, hi, __fmul_rn(mx, lo));
+        const bool near = fabsf(mc) < 2097152.0f;
+        off = near ? 0.0f : mx;
+        low = near ? mx + dmin : dmin;
+        shift = near ? kSmShift - ceilf(mc) : kSmShift;
+    }
+    // The masses of two logits z <= m, in units of 2^-fix, rounded; 0 for -inf.  The
+    // maximum's is 1 (with off m), or less by at most the 32nd part of an octave.
     // (Pairs: the arithmetic is packed.)
-    template <bool F32>
     __device__ __forceinline__ void masses(float z0, float z1, unsigned long long &w0, unsigned long long &w1) const
     {
-        const unsigned long long z = pack2(z0, z1), mm = pack2(-m, -m);
-        const unsigned long long df = add2(z, mm);
-        float d0, d1, dl0 = 0.0f, dl1 = 0.0f;
-        unpack2(df, d0, d1);
-        if (F32) { // what the differences lost (Knuth's two-sum); nothing of one without mass
-            const float b0 = d0 - z0, b1 = d1 - z1;
-            dl0 = d0 > dmin ? (z0 - (d0 - b0)) + (-m - b0) : 0.0f;
-            dl1 = d1 > dmin ? (z1 - (d1 - b1)) + (-m - b1) : 0.0f;
-        }
-        const unsigned long long d = pack2(fmaxf(d0, dmin), fmaxf(d1, dmin));
-        const unsigned long long t = fma2(d, pack2(c_hi, c_hi), pack2(kSmShift, kSmShift));
-        const unsigned long long k = add2(t, pack2(-kSmShift, -kSmShift));
-        unsigned long long r = fma2(d, pack2(c_hi, c_hi), mul2(k, pack2(-1.0f, -1.0f)));
+        float d0, d1;
+        unpack2(add2(pack2(z0, z1), pack2(-off, -off)), d0, d1);
+        const unsigned long long d = pack2(fmaxf(d0, low), fmaxf(d1, low)), S = pack2(shift, shift);
+        const unsigned long long t = fma2(d, pack2(c_hi, c_hi), S);
+        // d c less the whole number in t: the product's high part is not rounded before
+        unsigned long long r = fma2(d, pack2(c_hi, c_hi), fma2(t, pack2(-1.0f, -1.0f), S));
         r = fma2(d, pack2(c_lo, c_lo), r);
-        if (F32)
-            r = fma2(pack2(dl0, dl1), pack2(c_hi, c_hi), r);
         // e^x - 1, x = r ln(2) / 32: x + x^2 / 2 + x^3 / 6
         unsigned long long p = fma2(r, pack2(kSmLn3, kSmLn3), pack2(kSmLn2, kSmLn2));
         p = mul2(fma2(r, p, pack2(kSmLn1, kSmLn1)), r);
@@ -250,10 +261,10 @@ struct SampleRow {
         const uint32_t E = __float_as_uint(e.y) + __float_as_uint(__fmaf_rn(e.x, p, kSmShift)) + half;
         return (static_cast<unsigned long long>(E) << 32) >> s;
     }
-    template <bool F32> __device__ __forceinline__ unsigned long long mass(float z) const
+    __device__ __forceinline__ unsigned long long mass(float z) const
     {
         unsigned long long w0, w1;
-        masses<F32>(z, z, w0, w1);
+        masses(z, z, w0, w1);
         return w0;
     }
 };
@@ -608,7 +619,7 @@ __device__ __forceinline__ uint32_t sm_collect(const SampleRow &R, int use, uint
     if (threadIdx.x < n) {
         const uint2 e = sm_get2(&S.few[use][i], from);
         S.all[threadIdx.x] = e;
-        S.mass[threadIdx.x] = R.mass<sizeof(LT) == 4>(E::value(E::bits_of_key(e.x)));
+        S.mass[threadIdx.x] = R.mass(E::value(E::bits_of_key(e.x)));
     }
     __syncthreads();
     return n;
@@ -678,7 +689,6 @@ __device__ SampleFound sm_narrow(const SampleSlice<LT> &X, const SampleRow &R, u
                                  SampleBins &S)
 {
     using E = FilterElem<LT>;
-    constexpr bool F32 = sizeof(LT) == 4;
     constexpr int N = kSmBins / NT;
     SampleFound f = {};
     for (;;) {
@@ -692,7 +702,7 @@ __device__ SampleFound sm_narrow(const SampleSlice<LT> &X, const SampleRow &R, u
             for (int j = 0; j < E::kPerVec; ++j) {
                 const uint32_t bits = SampleSlice<LT>::of(w, j), k = E::key(bits);
                 if (k >= klo && k <= khi && E::finite(bits))
-                    sm_add_mass(S, (khi - k) >> sh, R.mass<F32>(E::value(bits)), piece);
+                    sm_add_mass(S, (khi - k) >> sh, R.mass(E::value(bits)), piece);
             }
         }
         sm_cluster_sync();
@@ -738,7 +748,7 @@ __device__ SampleFound sm_narrow(const SampleSlice<LT> &X, const SampleRow &R, u
         }
     }
     f.key = khi;
-    const unsigned long long w = R.mass<F32>(E::value(E::bits_of_key(khi)));
+    const unsigned long long w = R.mass(E::value(E::bits_of_key(khi)));
     unsigned long long j = MASS ? (w ? (target + w - 1) / w : 1) : target;
     f.j = static_cast<uint32_t>(j < 1 ? 1 : (j > f.ties ? f.ties : j));
     f.upto = above + f.j * w;
@@ -765,7 +775,6 @@ __device__ bool sm_settle_row(const SampleParams &P, const SampleRow &R, SampleS
                               float u, int64_t r, SampleCutAt &cut, unsigned long long &Z)
 {
     using E = FilterElem<LT>;
-    constexpr bool F32 = sizeof(LT) == 4;
     constexpr int N = kSmBins / NT;
     const bool use_k = P.top_k > 0 && P.top_k < P.V, use_p = P.top_p < 1.0f;
     auto value = [&](uint2 e) { return E::value(E::bits_of_key(e.x)); };
@@ -809,7 +818,7 @@ __device__ bool sm_settle_row(const SampleParams &P, const SampleRow &R, SampleS
             if (!within(e, cut))
                 continue;
             const float z = value(e);
-            const unsigned long long w = R.mass<F32>(z);
+            const unsigned long long w = R.mass(z);
             const uint32_t b = sm_bin(R, z, P.bins);
             if (b < b0)
                 above += w;
@@ -835,7 +844,7 @@ __device__ bool sm_settle_row(const SampleParams &P, const SampleRow &R, SampleS
             const uint2 e = S.ent[i];
             const float z = value(e);
             if (sm_bin(R, z, P.bins) == bin && within(e, cut))
-                sm_keep(S, e, R.mass<F32>(z));
+                sm_keep(S, e, R.mass(z));
         }
         rank_all(std::true_type{}, ties, left - before);
     }
@@ -849,7 +858,7 @@ __device__ bool sm_settle_row(const SampleParams &P, const SampleRow &R, SampleS
         const float z = value(e);
         if (!within(e, cut) || z < zlo)
             continue;
-        const unsigned long long w = R.mass<F32>(z);
+        const unsigned long long w = R.mass(z);
         Z += w;
         ++kept;
         sm_add_mass(S, e.y / run, w, P.piece);
@@ -868,7 +877,7 @@ __device__ bool sm_settle_row(const SampleParams &P, const SampleRow &R, SampleS
         const uint2 e = S.ent[i];
         const float z = value(e);
         if (e.y / run == at && within(e, cut) && z >= zlo)
-            sm_keep(S, e, R.mass<F32>(z));
+            sm_keep(S, e, R.mass(z));
     }
     __syncthreads();
     if (threadIdx.x < m && good) {
@@ -964,7 +973,7 @@ __device__ __forceinline__ void sm_write_q(const SampleSlice<LT> &X, const Sampl
     float least = zlo;
     if (CUTS && cut.key)
         least = fmaxf(least, E::value(E::bits_of_key(cut.key)));
-    const float cq = P.cq, scale = ldexpf(1.0f, P.fix) / static_cast<float>(Z);
+    const float cq = P.cq, scale = static_cast<float>(R.mass(R.m)) / static_cast<float>(Z);
     const bool filtered = CUTS || P.min_p;
     for (int32_t v = threadIdx.x; v < X.nv; v += NT) {
         const uint4 w = X.vec(v);
@@ -1113,7 +1122,10 @@ __global__ void __launch_bounds__(NT, (CUTS ? 1024 : 1280) / NT) sample_kernel(c
         sm_cluster_leave();
         return;
     }
-    SampleRow R = {mx, P.c_hi, P.c_lo, P.dmin, smem_addr(S.tab), 59 - P.fix + static_cast<int>(kSmShiftBits >> 5)};
+    SampleRow R;
+    R.set(mx, P.c_hi, P.c_lo, P.dmin);
+    R.tab = smem_addr(S.tab);
+    R.down = 59 - P.fix + static_cast<int>(kSmShiftBits >> 5);
     // min-p: the least logit kept (p >= min_p max p, in logits)
     const float zlo = P.min_p ? __double2float_ru(static_cast<double>(mx) + P.min_off) : -INFINITY;
     const bool use_k = P.top_k > 0 && P.top_k < P.V, use_p = P.top_p < 1.0f;
@@ -1139,7 +1151,7 @@ __global__ void __launch_bounds__(NT, (CUTS ? 1024 : 1280) / NT) sample_kernel(c
                     const float z0 = E::value(Slice::of(w, j)), z1 = E::value(Slice::of(w, j + 1));
                     if (kMass) {
                         unsigned long long e0, e1;
-                        R.masses<F32>(z0, z1, e0, e1);
+                        R.masses(z0, z1, e0, e1);
                         total += e0 + e1;
                     }
                     const uint32_t b0 = sm_bin(R, z0, P.bins), b1 = sm_bin(R, z1, P.bins);
@@ -1190,12 +1202,12 @@ __global__ void __launch_bounds__(NT, (CUTS ? 1024 : 1280) / NT) sample_kernel(c
             const unsigned long long target = tau(total);
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                mass[i] = cnt[i] * R.mass<F32>(fminf(mx, mx - (N * threadIdx.x + i - 0.52f) * P.width));
+                mass[i] = cnt[i] * R.mass(fminf(mx, mx - (N * threadIdx.x + i - 0.52f) * P.width));
             sm_scan<true, NT>(H, cnt, mass, target, cnt_all, mass_all);
             b0 = H.bin >= 0 ? static_cast<uint32_t>(H.bin) : kSmBins;
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                mass[i] = cnt[i] * R.mass<F32>(mx - (N * threadIdx.x + i + 0.52f) * P.width);
+                mass[i] = cnt[i] * R.mass(mx - (N * threadIdx.x + i + 0.52f) * P.width);
             sm_scan<true, NT>(H, cnt, mass, target, cnt_all, mass_all);
             deep = H.bin < 0;
             if (!deep)
@@ -1358,7 +1370,7 @@ __global__ void __launch_bounds__(NT, (CUTS ? 1024 : 1280) / NT) sample_kernel(c
                 const uint32_t key = E::key(bits);
                 if (key < cut.key || (key == cut.key && id > cut.id))
                     return;
-                const unsigned long long e = R.mass<F32>(E::value(bits));
+                const unsigned long long e = R.mass(E::value(bits));
                 if (b < b0) {
                     above += e;
                 } else {
@@ -1411,7 +1423,7 @@ __global__ void __launch_bounds__(NT, (CUTS ? 1024 : 1280) / NT) sample_kernel(c
 #pragma unroll
             for (int j = 0; j < PV; j += 2) {
                 unsigned long long e0, e1;
-                R.masses<F32>(E::value(Slice::of(w, j)), E::value(Slice::of(w, j + 1)), e0, e1);
+                R.masses(E::value(Slice::of(w, j)), E::value(Slice::of(w, j + 1)), e0, e1);
                 a += e0 + e1;
             }
             n += PV;
@@ -1425,7 +1437,7 @@ __global__ void __launch_bounds__(NT, (CUTS ? 1024 : 1280) / NT) sample_kernel(c
                 const uint32_t b = Slice::of(w, j);
                 if (keeps(b, X.first + v * PV + j)) {
                     ++n;
-                    a += R.mass<F32>(E::value(b));
+                    a += R.mass(E::value(b));
                 }
             }
         }
@@ -1437,7 +1449,7 @@ __global__ void __launch_bounds__(NT, (CUTS ? 1024 : 1280) / NT) sample_kernel(c
         if (!keeps(b, Kept.id(i)))
             return 0ull;
         ++n;
-        return R.mass<F32>(E::value(b));
+        return R.mass(E::value(b));
     };
     unsigned long long a = 0;
     uint32_t n = 0;
@@ -1514,7 +1526,7 @@ __global__ void __launch_bounds__(NT, (CUTS ? 1024 : 1280) / NT) sample_kernel(c
                         for (int j = 0; j < PV; ++j) {
                             const uint32_t bits = Slice::of(x, j);
                             const int32_t id = X.first + (i + lane) * PV + j;
-                            const unsigned long long one = keeps(bits, id) ? R.mass<F32>(E::value(bits)) : 0ull;
+                            const unsigned long long one = keeps(bits, id) ? R.mass(E::value(bits)) : 0ull;
                             to += one;
                             if (t < to) {
                                 P.tokens[r] = id;
