@@ -16,7 +16,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 def _inputs() -> list[str]:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)
-             if f.endswith((".cu", ".cuh"))]
+             if f.endswith((".cu", ".cuh", ".h"))]
     files.append(os.path.join(INCLUDE, "spec_verify.h"))
     return files
 

@@ -20,6 +20,7 @@
 #include "sv_fp4.cuh"
 #include "sv_lmhead.cuh"
 #include "sv_lmhead_fp4.cuh"
+#include "sv_lmhead_fp4_plan.h"
 #include "sv_lmhead_fp8.cuh"
 #include "sv_sample.cuh"
 #include "sv_tree.cuh"
@@ -791,69 +792,6 @@ bool lm4_scale_map(CUtensorMap *map, const void *base, int64_t tiles, uint32_t b
                             CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// How a product is cut: a function of (M, V).  A stage (256 hidden dims) of a tile
-// costs an SM the largest of
-//   the MMAs' time, 2 cycles an id and row tile (4 steps of 64 dims);
-//   what it loads, 128 bytes and 16 of scales for each row of h and of W, at the rate
-//   that was measured of each shape: 55 bytes a cycle for lone CTAs, 45 for pairs, 42
-//   for pairs with two row tiles (whose accumulators are not read behind the next
-//   tile's MMAs: half a tile more at the end);
-//   with one row tile, where W comes from memory once, 23 bytes a cycle for W.
-// Narrower tiles on ties: they reach more SMs.  The three shapes, replayed, d 4096
-// (two row tiles, pairs, lone CTAs; the rule's choice starred):
-//   V 128256: M 384 98* 105 101 us; M 576 182 154 149*; M 1024 184* 204 244; M 2304 397* 462 519;
-//   V 32000: M 257 37 35 31*; M 576 48 44* 45; M 1024 60 56* 65; M 2304 113* 116 135;
-//   M 131, V 128256: pairs 59*, lone CTAs 69.
-struct Lm4Plan {
-    bool pair;
-    int32_t H;          // row tiles that share a pair's tile of W
-    int32_t RT, MT;     // row tiles, groups of H of them
-    int32_t NT, NB;
-};
-
-Lm4Plan lm4_plan(int64_t M, int32_t V)
-{
-    Lm4Plan p = {};
-    const int64_t rows = M < sv::kLmBM ? M : sv::kLmBM;
-    int64_t best = INT64_MAX;
-    for (int shape = M > 2 * sv::kLmBM ? 2 : (M > sv::kLmBM ? 1 : 0); shape >= 0; --shape) { // H 2, pair, lone CTA
-        const bool pair = shape > 0;
-        const int32_t H = shape == 2 ? 2 : 1;
-        const int64_t units = pair ? kNominalSms / 2 : kNominalSms, rate = shape == 2 ? 42 : (pair ? 45 : 55);
-        const int32_t rt = static_cast<int32_t>(ceil_div(M > 0 ? M : 1, pair ? 2 * sv::kLmBM : sv::kLmBM));
-        const int32_t mt = static_cast<int32_t>(ceil_div(rt, H));
-        int64_t low = INT64_MAX;
-        int32_t NB = 0;
-        for (int32_t nb = sv::kL4MaxNB; nb >= 64; nb -= 64) {
-            const int64_t w = 144 * (pair ? nb / 2 : nb);
-            auto stage = [&](int64_t h) { // of a group of h row tiles
-                int64_t c = (h * 144 * rows + w) / rate;
-                c = c > 2 * nb * h ? c : 2 * nb * h;
-                return mt == 1 && c < w / 23 ? w / 23 : c;
-            };
-            // the mean of a unit's tiles; where the units are a multiple of the groups, some units
-            // get full groups only
-            const int64_t tile =
-                (units % mt == 0 ? stage(H) : (rt / H * stage(H) + (rt % H ? stage(1) : 0)) / mt) + 40;
-            const int64_t cost = ceil_div(mt * ceil_div(V, nb), units) * tile + (H == 2 ? tile / 2 : 0);
-            if (cost <= low) {
-                low = cost;
-                NB = nb;
-            }
-        }
-        if (low < best) { // two row tiles, then a pair, on ties
-            best = low;
-            p.pair = pair;
-            p.H = H;
-            p.RT = rt;
-            p.MT = mt;
-            p.NB = NB;
-        }
-    }
-    p.NT = static_cast<int32_t>(ceil_div(V, p.NB));
-    return p;
-}
-
 template <bool PAIR, int H, int BLOCK> cudaError_t lm4_units(int &units)
 {
     struct Entry {
@@ -932,7 +870,7 @@ cudaError_t lm4_launch_as(const CUtensorMap (&m)[5], const sv::Lm4Params &L, cud
 }
 
 template <int BLOCK>
-cudaError_t lm4_launch_shape(const Lm4Plan &p, const CUtensorMap (&m)[5], const sv::Lm4Params &L, cudaStream_t stream)
+cudaError_t lm4_launch_shape(const sv::Lm4Plan &p, const CUtensorMap (&m)[5], const sv::Lm4Params &L, cudaStream_t stream)
 {
     if (!p.pair)
         return lm4_launch_as<false, 1, BLOCK>(m, L, stream);
@@ -943,7 +881,7 @@ cudaError_t lm4_launch(const void *hidden, const void *hidden_scales, const floa
                        const void *lm_head_scales, const float *gw, int32_t block, int64_t M, int32_t d, int32_t V,
                        void *logits, int32_t *status, cudaStream_t stream)
 {
-    const Lm4Plan p = lm4_plan(M, V);
+    const sv::Lm4Plan p = sv::lm4_plan(M, V, kNominalSms);
     sv::Lm4Params L = {};
     const int32_t brows = p.pair ? p.NB / 2 : p.NB; // ids of a tile that one CTA loads
     // A stage holds the rows of h that exist, in 8s (a swizzle group): the MMA's
@@ -1614,7 +1552,7 @@ sv_status_t sv_lm_head_logits_fp4(const void *hidden, const void *hidden_scales,
     if (V > SV_MAX_V || M > kLmMaxRows || d > (1 << 20))
         return SV_EUNSUPPORTED;
     // tiles and scale tiles are counted in 32 bits
-    const Lm4Plan p = lm4_plan(M, V);
+    const sv::Lm4Plan p = sv::lm4_plan(M, V, kNominalSms);
     const int64_t tiles = static_cast<int64_t>(p.MT) * p.NT, kt = fp4_tiles(d, block);
     if (tiles > INT32_MAX || ceil_div(M, 128) > INT32_MAX / kt - 4 || ceil_div(V, 128) > INT32_MAX / kt - 4)
         return SV_EUNSUPPORTED;

@@ -45,12 +45,13 @@
 
 #include <type_traits>
 
+#include "sv_lmhead_fp4_plan.h"
 #include "sv_lmhead_fp8.cuh"
 
 namespace sv {
 
 constexpr int kL4BK = 256;                 // hidden dims of a stage
-constexpr int kL4MaxNB = 192;
+static_assert(kL4Rows == kLmBM, "rows of a tile");
 constexpr int kL4EpiWarps = 8;             // two a lane quarter, each half of a tile's columns
 constexpr int kL4Threads = 64 + 32 * kL4EpiWarps;
 constexpr int kL4MaxStages = 8;
