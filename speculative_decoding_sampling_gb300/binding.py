@@ -657,7 +657,10 @@ def spec_verify_lm_head_fp8(hidden: torch.Tensor, hidden_scales: torch.Tensor, l
 
 # ------------------------------------------------------------- the draft's step in 4-bit floating point
 
-_SCALE_TYPES = {torch.float8_e4m3fn: 16, torch.float8_e8m0fnu: 32}  # values of a block, by its scales' type
+_E8M0 = getattr(torch, "float8_e8m0fnu", None)  # younger than every other type here: without it, no blocks of 32
+_SCALE_TYPES = {torch.float8_e4m3fn: 16}        # values of a block, by its scales' type
+if _E8M0 is not None:
+    _SCALE_TYPES[_E8M0] = 32
 
 
 @dataclass
@@ -709,6 +712,8 @@ def sv_quantize_fp4(x: torch.Tensor, block: int = 16, *, out: Fp4Tensor | None =
     shape = x.shape
     if block not in (16, 32):
         raise ValueError("block must be 16 or 32")
+    if block == 32 and _E8M0 is None:
+        raise TypeError("blocks of 32 need a torch that has float8_e8m0fnu")
     if len(shape) < 1 or shape[-1] < 2 or shape[-1] % 2:
         raise ValueError("x must be [..., d], d even")
     d = shape[-1]
@@ -716,7 +721,7 @@ def sv_quantize_fp4(x: torch.Tensor, block: int = 16, *, out: Fp4Tensor | None =
     rows = x.numel() // d
     with _on(dev, stream) as s:
         if out is None:
-            st = torch.float8_e4m3fn if block == 16 else torch.float8_e8m0fnu
+            st = torch.float8_e4m3fn if block == 16 else _E8M0
             out = Fp4Tensor(torch.empty(shape[:-1] + (d // 2,), dtype=torch.uint8, device=dev),
                             torch.empty(_fp4_scale_shape(rows, d, block), dtype=st, device=dev),
                             torch.empty(shape[:-1], dtype=_F32, device=dev) if block == 16 else None)
