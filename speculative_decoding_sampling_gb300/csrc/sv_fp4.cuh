@@ -322,7 +322,8 @@ __global__ void __launch_bounds__(kF4Threads, kF4Ctas<XT>) quantize_fp4_kernel(c
             if (BLOCK == 16) {
                 // x / g is exact.  Quotients by 6 and by s from a rounded reciprocal r and one
                 // correction, which rounds correctly, and r itself from the unit's approximation
-                // and one of its own (Markstein 1990): q = y r, q + (y - q s) r.
+                // and one of its own (Markstein 1990): q = y r, q - (q s - y) r.  (That way round, and
+                // y negative to begin with, a zero keeps its sign.)
                 const float y = __fmul_rn(__uint_as_float(m), ginv), q6 = __fmul_rn(y, 1.0f / 6.0f);
                 byte = f4_to_e4m3(__fmaf_rn(__fmaf_rn(q6, -6.0f, y), 1.0f / 6.0f, q6));
                 byte = m ? max(byte, 1u) : 0u;
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(kF4Threads, kF4Ctas<XT>) quantize_fp4_kernel(c
                 float r;
                 asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
                 r = __fmaf_rn(__fmaf_rn(-s, r, 1.0f), r, r);
-                const unsigned long long gg = pack2(ginv, ginv), rr = pack2(r, r), ss = pack2(-s, -s);
+                const unsigned long long gg = pack2(-ginv, -ginv), rr = pack2(-r, -r), ss = pack2(s, s);
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) {
                     const unsigned long long y2 = mul2(pack2(f[k], f[k + 1]), gg), q = mul2(y2, rr);

@@ -1,5 +1,5 @@
-"""The 4-bit LM head at the ends of the floating-point ranges: what bf16 cannot
-hold, row scales whose product leaves fp32's range."""
+"""4-bit operands at the ends of the floating-point ranges: signs of zeros, logits that
+bf16 cannot hold, row scales whose product leaves fp32's range."""
 import numpy as np
 import pytest
 import torch
@@ -10,6 +10,24 @@ import speculative_decoding_sampling_gb300 as sv
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 BF = torch.bfloat16
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("dtype", [BF, torch.float32], ids=["bf16", "fp32"])
+def test_zeros_keep_their_sign(block, dtype):
+    """-0 and negative values that round to zero are e2m1's -0, in both kinds of blocks; reading back keeps it."""
+    x = torch.randn((40, 96), generator=torch.Generator().manual_seed(8)).to(dtype)
+    x[:, ::5] = 0.0
+    x[:, ::7] = -0.0
+    x[:, 3::11] = -1e-6
+    x[5] = -0.0
+    t = sv.sv_quantize_fp4(x.to(DEV), block)
+    code = torch.stack((t.values & 15, t.values >> 4), -1).view(40, 96).cpu()
+    assert torch.equal(code > 7, torch.signbit(x))
+    v, _, _ = R.quantize(x.double().numpy(), block)
+    assert np.array_equal(R.unpack(t.values.cpu().numpy()), v)
+    for out in (BF, torch.float32):
+        assert torch.equal(torch.signbit(sv.sv_dequantize_fp4(t, out).cpu()), torch.signbit(x))
 
 
 def _single(products, gh, gw):
