@@ -494,7 +494,9 @@ sv_status_t sv_lm_head_logits_fp4(
  *   prob      [rows] fp32 out, the token's probability; may be NULL;
  *   kept      [rows] int32 out, ids kept; may be NULL;
  *   probs     [rows, V] fp32 out, the processed distribution (0 for ids that are
- *             not kept); may be NULL.  No output may overlap the logits.
+ *             not kept); may be NULL.  Its entries come from exp2 in fp32, prob from
+ *             the masses below: the two agree to 2^-17, not bit for bit.  No output
+ *             may overlap the logits.
  *   status_dev  SV_BAD_ROW for a row with NaN, +inf or no finite logit (token
  *             -1, prob and kept 0, probs zeros), SV_BAD_U for a uniform outside
  *             [0, 1) (token -1, prob 0; kept and probs are the row's); may be

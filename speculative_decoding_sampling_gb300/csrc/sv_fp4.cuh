@@ -22,10 +22,11 @@
 // the row's maximum and the values (of longer rows the rest is read again), and
 // have the next row's on their way meanwhile.
 //
-// Measured (replayed; GB300) at 128256 x 4096 bf16: quantising in blocks of 16 319
-// us = 4.2 TB/s, of 32 226 us = 5.9 TB/s; reading back 208 us = 6.5 TB/s and 241 us.
-// Blocks of 16 are bound by instructions (about 100 an octet, the ALU pipe first);
-// with divisions by the compiler and addresses by octet it was 500 us, 375 with
+// Measured (replayed; GB300) at 128256 x 4096: quantising bf16 in blocks of 16 315 us =
+// 4.3 TB/s, of 32 226 us = 5.9 TB/s, fp32 375 and 368 us = 6.4 TB/s; reading back to bf16
+// 207 us = 6.5 TB/s and 241 us, to fp32 502 and 476 us = 4.8 and 5.0 TB/s.  Blocks of 16 are
+// bound by instructions (136 an octet and lane, 70 % of the issue slots, the ALU pipe
+// first); with divisions by the compiler and addresses by octet it was 500 us, 375 with
 // corrected reciprocals, 319 with addresses by row.
 #pragma once
 

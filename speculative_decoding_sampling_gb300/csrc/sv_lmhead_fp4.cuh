@@ -33,14 +33,16 @@
 // 64 of their scale tile: two columns.
 // Every wait is bounded (l8_wait), with lm_head_kernel's teardown.
 //
-// Measured (replayed; GB300): M 2304, V 151936, d 4096: 497 us = 5.8 PFLOP/s (the
-// tensor pipe was 75 % active at 5.0 PFLOP/s, so 64 dims an MMA give it 6.7 at
-// most); 532 with one row tile a pair and five stages.  M 64, V 128256, d 2048: 27 us
-// = 5.7 TB/s; M 1, V 32000, d 4096: 16 us = 4.5 TB/s, bound by the weights' bytes and
-// some 5 us of launch, first loads and last tile.  M 131, V 32003, d 1056: 17 us,
-// three tiles a pair and odd rows' plain stores.
-// With three quarters of the MMAs left out the first case took 463 instead of 532 us,
-// without the scales' copies 496, with one stage's lines loaded again and again 508.
+// Measured (replayed; GB300): M 2304, V 151936, d 4096: 471 to 493 us = 5.8 to 6.1
+// PFLOP/s; 532 with one row tile a pair and five stages.  In blocks of 32: 462 us.  M 64,
+// V 128256, d 2048, blocks of 32: 27 us = 5.8 TB/s; M 1, V 32000, d 4096: 16 us = 4.5 TB/s,
+// bound by the weights' bytes and some 5 us of launch, first loads and last tile.  M 131,
+// V 32003, d 1056: 16 us, three tiles a pair and odd rows' plain stores.
+// What bounds many rows is a stage's round trip, no single unit: at M 2304, V 32768 (117
+// us) the tensor pipe is active 56 % of the time, which fits MMAs of 64 dims at 2 cycles an
+// id (9.4 PFLOP/s if they never paused), L2 44 %, memory 20 %.  The first case took 380
+// instead of 484 us with three quarters of the MMAs left out, 457 without the scales'
+// copies, 472 with the first lines loaded again and again.
 #pragma once
 
 #include <type_traits>

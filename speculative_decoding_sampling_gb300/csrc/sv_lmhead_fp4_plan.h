@@ -19,7 +19,9 @@ inline int64_t l4_ceil(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //   for pairs with two row tiles (whose accumulators are not read behind the next
 //   tile's MMAs: half a tile more at the end);
 //   with one row tile, where W comes from memory once, 23 bytes a cycle for W.
-// Narrower tiles on ties: they reach more SMs.  The three shapes, replayed, d 4096
+// d is not looked at: what a tile costs besides its stages (40 cycles a stage here) was
+// fitted at d 4096, and weighs more at small d, where the choice was measured at M 1024,
+// V 32003, d 1056 only.  Narrower tiles on ties: they reach more SMs.  The three shapes, replayed, d 4096
 // (two row tiles, pairs, lone CTAs; the rule's choice starred):
 //   V 128256: M 384 98* 105 101 us; M 576 182 154 149*; M 1024 184* 204 244; M 2304 397* 462 519;
 //   V 32000: M 257 37 35 31*; M 576 48 44 45*; M 1024 60 56* 65; M 2304 113* 116 135;

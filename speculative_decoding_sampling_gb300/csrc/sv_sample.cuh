@@ -44,12 +44,14 @@
 //  5. q.
 //
 // Measured (calls replayed from a graph; GB300): 1 row of 32000 fp32, k 50, p 0.95:
-// 11 us; 8 rows of 128256 bf16, p 0.9: 30 us; 256 rows of 128256 bf16, k 1000, p
-// 0.9, min-p 0.01, with q: 137 us; 256 rows of 151936 bf16 at temperature alone, with
-// q: 80 us = 2.9 TB/s.  Without cuts bound by issue (43 % of the slots, some 40
-// instructions an id, half of them the mass) and the waves of clusters; with cuts by
-// the chain of steps of a row (about 25 us: 5 load, 5 counts, 3 list, 9 one CTA's
-// settling, 3 q, the rest barriers of 0.7 us each), four CTAs an SM.
+// 11 us; 8 rows of 128256 bf16, p 0.9: 30 us; 133 rows of 32003 fp32, min-p: 11 us; 256
+// rows of 128256 bf16, k 1000, p 0.9, min-p 0.01, with q: 135 us; 256 rows of 151936
+// bf16 at temperature alone, with q: 80 us = 2.9 TB/s.  Without cuts a row's CTAs load,
+// wait, form masses, wait and write (16 us: 3 load, 2 barrier, 4 masses, 3 exchange and
+// draw, 2 q) and nothing of the next row is on its way: 59 % of the issue slots and 27 %
+// of the memory's rate are used, neither is the bound.  With cuts it is the chain of a
+// row's steps (about 26 us: 4 load and barrier, 5 counts, 2 scan, 4 list, 9 one CTA's
+// settling, 2 q), four CTAs an SM, 33 % of the issue slots.
 // What the parts were worth on 256 rows of 128256 with every filter: 614 us as first
 // built (masses in bins, digit by digit over a list); 572 -> 369 bins of the value
 // instead of digits of the key; 284 counts first, masses only where the cut may lie;
